@@ -23,7 +23,7 @@ from ._lib import Fp8Error  # noqa: F401
 
 __all__ = ["quantize", "quantize_dual", "quantize_tensors", "amax", "scaled_gemm", "blockscaled_gemm", "AmaxHistory", "Diag",
            "QuantResult", "Fp8Error", "FORMATS", "GRANULARITIES", "group_grid", "kv_store", "kv_load",
-           "KVTensorCache", "KVCache", "grouped_gemm", "workspace"]
+           "KVTensorCache", "KVCache", "grouped_gemm", "workspace", "kv_attention", "kv_evict"]
 
 FORMATS = {"e4m3": _lib.FP8_E4M3, "e5m2": _lib.FP8_E5M2}
 GRANULARITIES = {"tensor": _lib.FP8_GRAN_TENSOR, "row": _lib.FP8_GRAN_ROW,
@@ -547,6 +547,221 @@ def kv_load(cache: torch.Tensor, scale_inv: Optional[torch.Tensor], n: Optional[
     return out
 
 
+# ---------------------------------------- attention over the cache, eviction --
+def _kv_pair(k_cache, v_cache, page_table, lens, page_size, k_scale_inv, v_scale_inv, k_storage, v_storage, scaling,
+             max_len):
+    """The fp8_kv_pair of a layer's K and V caches and a batch's pages; raises
+    before any launch if a buffer is not what the library would read."""
+    if k_cache.dim() != 3 or not k_cache.is_cuda:
+        raise ValueError("k_cache must be a [capacity, heads, head_dim] device tensor")
+    capacity, heads, head_dim = k_cache.shape
+    dev = k_cache.device
+    if v_cache.shape != k_cache.shape:
+        raise ValueError("k_cache and v_cache must have one shape, got %s and %s"
+                         % (tuple(k_cache.shape), tuple(v_cache.shape)))
+    for cache, st, name in ((k_cache, k_storage, "k_cache"), (v_cache, v_storage, "v_cache")):
+        want = torch.bfloat16 if st == "bf16" else torch.uint8
+        if cache.dtype != want or not cache.is_contiguous() or cache.device != dev:
+            raise ValueError("%s must be a contiguous %s tensor on %s" % (name, want, dev))
+    if page_table.dim() != 2 or page_table.dtype != torch.int32 or page_table.device != dev:
+        raise ValueError("page_table must be an int32 [batch, pages] tensor on %s" % dev)
+    batch, pages = page_table.shape
+    if pages > 1 and page_table.stride(1) != 1:
+        raise ValueError("page_table must have a contiguous last dimension")
+    page_ld = page_table.stride(0) if batch > 1 else pages
+    if page_ld < pages:
+        raise ValueError("page_table must not overlap itself")
+    if max_len is None:
+        max_len = pages * page_size
+    elif max_len > pages * page_size:
+        raise ValueError("max_len=%d needs more than the %d pages of page_table" % (max_len, pages))
+    return _lib.Fp8KvPair(
+        k_cache.data_ptr(), v_cache.data_ptr(), _kv_scales(k_scale_inv, k_storage, scaling, capacity, heads, dev),
+        _kv_scales(v_scale_inv, v_storage, scaling, capacity, heads, dev), capacity, page_table.data_ptr(), page_ld,
+        _buf(lens, batch, torch.int32, dev, "lens"), max_len, KV_STORAGE[k_storage], KV_STORAGE[v_storage],
+        KV_SCALING[scaling], heads, head_dim, page_size, batch, 0)
+
+
+def _kv_weights(weights, batch: int, heads: int, least: int, device, name: str) -> int:
+    """Leading dimension of fp32 weights [batch, heads, >= least]."""
+    if not isinstance(weights, torch.Tensor) or weights.device != device:
+        raise ValueError("%s must be a tensor on %s" % (name, device))
+    if weights.dtype != torch.float32:
+        raise TypeError("%s must be torch.float32, got %s" % (name, weights.dtype))
+    if weights.dim() != 3 or tuple(weights.shape[:2]) != (batch, heads) or weights.shape[2] < least:
+        raise ValueError("%s must be [%d, %d, >= %d], got shape %s" % (name, batch, heads, least,
+                                                                       tuple(weights.shape)))
+    ld = weights.shape[2]
+    if heads > 1:
+        ld = weights.stride(1)
+    elif batch > 1:
+        ld = weights.stride(0)
+    if ((weights.shape[2] > 1 and weights.stride(2) != 1) or ld < weights.shape[2]
+            or (batch > 1 and weights.stride(0) != heads * ld)):
+        raise ValueError("%s must be rows of one pitch with a contiguous last dimension" % name)
+    return max(ld, 1)
+
+
+def _heads_matrix(x, head_dim: int, name: str):
+    """(rows, heads, row pitch) of a [n, heads, head_dim] bf16 device tensor with packed heads."""
+    if x.dtype != torch.bfloat16:
+        raise TypeError("%s must be torch.bfloat16, got %s" % (name, x.dtype))
+    if x.dim() != 3 or x.shape[2] != head_dim:
+        raise ValueError("%s must be [n, heads, %d], got shape %s" % (name, head_dim, tuple(x.shape)))
+    n, heads, _ = x.shape
+    if x.stride(2) != 1 or (heads > 1 and x.stride(1) != head_dim):
+        raise ValueError("%s must have packed heads" % name)
+    return n, heads, x.stride(0) if n > 1 else heads * head_dim
+
+
+class _on_device:
+    """Launch on a tensor's device whatever the current one is."""
+
+    def __init__(self, device):
+        self.index, self.back = device.index, None
+
+    def __enter__(self):
+        current = torch.cuda.current_device()
+        if self.index is not None and self.index != current:
+            self.back = current
+            torch.cuda.set_device(self.index)
+
+    def __exit__(self, *_):
+        if self.back is not None:
+            torch.cuda.set_device(self.back)
+
+
+def kv_attention(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor, page_table: torch.Tensor,
+                 lens: torch.Tensor, page_size: int, k_scale_inv: Optional[torch.Tensor] = None,
+                 v_scale_inv: Optional[torch.Tensor] = None, k_storage="e4m3", v_storage=None,
+                 scaling="token_head", q_offsets: Optional[torch.Tensor] = None, max_len: Optional[int] = None,
+                 window: int = 0, sinks: int = 0, scale: Optional[float] = None,
+                 weights: Optional[torch.Tensor] = None, return_lse: bool = False,
+                 out: Optional[torch.Tensor] = None, lse: Optional[torch.Tensor] = None,
+                 workspace: Optional[torch.Tensor] = None):
+    """Attention of a batch's newest tokens over one layer's paged cache,
+    read in place (fp8_kv_attention).
+
+    q: bf16 [total_q, q_heads, head_dim], the sequences' new tokens one after
+    the other; their K and V are already stored.  Every sequence has
+    total_q / batch of them (one: a decode step), or those q_offsets (int32
+    device tensor [batch + 1]) gives.  k_cache, v_cache: [capacity, heads,
+    head_dim] as kv_store fills them, with their scales; v_storage defaults to
+    k_storage.  page_table: int32 [batch, pages]: token j of sequence b is in
+    cache row page_table[b, j // page_size] * page_size + j % page_size (rows
+    outside the cache are not there).  lens: int32 [batch], cached tokens
+    including the new ones; max_len: an upper bound of them known on the host
+    (default: what page_table holds).
+
+    Causal; with window > 0 a token sees the last `window` tokens, itself
+    included, and the first `sinks`.  scale: default head_dim ** -0.5.
+    weights: fp32 [batch, heads, >= max_len], to which the call adds what each
+    cached token receives (the input of kv_evict).  workspace: a uint8 device
+    tensor for callers that may not allocate (fp8_kv_attention_workspace
+    bytes).
+
+    Returns out [total_q, q_heads, head_dim] bf16, with return_lse (or lse
+    given) also the fp32 log-sum-exp of the scores [total_q, q_heads]."""
+    if v_storage is None:
+        v_storage = k_storage
+    pair = _kv_pair(k_cache, v_cache, page_table, lens, page_size, k_scale_inv, v_scale_inv, k_storage, v_storage,
+                    scaling, max_len)
+    dev = k_cache.device
+    _same_device(q, dev, "q")
+    n, q_heads, ldq = _heads_matrix(q, pair.head_dim, "q")
+    if out is None:
+        out = torch.empty((n, q_heads, pair.head_dim), dtype=torch.bfloat16, device=dev)
+        ldo = q_heads * pair.head_dim
+    else:
+        _same_device(out, dev, "out")
+        n2, h2, ldo = _heads_matrix(out, pair.head_dim, "out")
+        if (n2, h2) != (n, q_heads):
+            raise ValueError("out must have shape %s, got %s" % (tuple(q.shape), tuple(out.shape)))
+    want_lse = return_lse or lse is not None
+    if lse is not None:
+        _buf(lse, n * q_heads, torch.float32, dev, "lse")
+    elif want_lse or weights is not None:
+        lse = torch.empty((n, q_heads), dtype=torch.float32, device=dev)
+    offsets = None
+    if q_offsets is not None:
+        offsets = _buf(q_offsets, pair.batch + 1, torch.int32, dev, "q_offsets")
+    ldw = 0
+    if weights is not None:
+        ldw = _kv_weights(weights, pair.batch, pair.heads, pair.max_len, dev, "weights")
+    L = _lib.lib()
+    ws_bytes = 0
+    if q_offsets is None and n == pair.batch:
+        ws_bytes = L.fp8_kv_attention_workspace(ctypes.byref(pair), n, q_heads, 0, window, sinks)
+    if workspace is not None:
+        if not isinstance(workspace, torch.Tensor) or workspace.device != dev or not workspace.is_contiguous():
+            raise ValueError("workspace must be a contiguous tensor on %s" % dev)
+        ws_bytes = workspace.numel() * workspace.element_size()
+    elif ws_bytes > 0:
+        workspace = torch.empty(ws_bytes, dtype=torch.uint8, device=dev)
+    if scale is None:
+        scale = pair.head_dim ** -0.5
+    with _on_device(dev):
+        st = L.fp8_kv_attention(
+            ctypes.byref(pair), q.data_ptr(), ldq, n, q_heads, offsets, scale, window, sinks, out.data_ptr(), ldo,
+            _ptr(lse), _ptr(weights), ldw, _ptr(workspace), ws_bytes, _stream(dev))
+    _lib.check(st, "fp8_kv_attention")
+    return (out, lse) if want_lse else out
+
+
+def kv_evict(k_cache: torch.Tensor, v_cache: torch.Tensor, weights: torch.Tensor, page_table: torch.Tensor,
+             lens: torch.Tensor, page_size: int, budget: int, sinks: int = 0, recent: int = 0,
+             k_scale_inv: Optional[torch.Tensor] = None, v_scale_inv: Optional[torch.Tensor] = None,
+             k_storage="e4m3", v_storage=None, scaling="token_head", max_len: Optional[int] = None,
+             dst_page_table: Optional[torch.Tensor] = None, weights_out: Optional[torch.Tensor] = None,
+             kept: Optional[torch.Tensor] = None, new_lens: Optional[torch.Tensor] = None):
+    """Cut every sequence of more than `budget` tokens to `budget`
+    (fp8_kv_evict): each KV head keeps the first `sinks` tokens, the last
+    `recent` and the heaviest of those between by weights [batch, heads, >=
+    max_len] (the lower position among equals), moved together in their order.
+    Without dst_page_table the cache, its scales and the weights are changed in
+    place; with it (int32 [batch, pages] other pages of the same caches) the
+    kept tokens are copied there.  weights_out [batch, heads, >= budget]: the
+    kept tokens' weights go there instead of into weights.
+
+    Returns (kept, new_lens): int32 [batch, heads, budget] positions kept, -1
+    behind the last, and int32 [batch] the new lengths.  lens is not changed:
+    every layer of a model evicts with the same one."""
+    if v_storage is None:
+        v_storage = k_storage
+    pair = _kv_pair(k_cache, v_cache, page_table, lens, page_size, k_scale_inv, v_scale_inv, k_storage, v_storage,
+                    scaling, max_len)
+    dev = k_cache.device
+    if budget < 1:
+        raise ValueError("budget must be >= 1, got %d" % budget)
+    ldw = _kv_weights(weights, pair.batch, pair.heads, pair.max_len, dev, "weights")
+    ldwo = 0
+    if weights_out is not None:
+        ldwo = _kv_weights(weights_out, pair.batch, pair.heads, budget, dev, "weights_out")
+    dst, dst_ld = None, 0
+    if dst_page_table is not None:
+        if (dst_page_table.dim() != 2 or dst_page_table.dtype != torch.int32 or dst_page_table.device != dev
+                or dst_page_table.shape[0] != pair.batch
+                or (dst_page_table.shape[1] > 1 and dst_page_table.stride(1) != 1)):
+            raise ValueError("dst_page_table must be an int32 [%d, pages] tensor on %s with a contiguous last "
+                             "dimension" % (pair.batch, dev))
+        if dst_page_table.shape[1] * page_size < budget:
+            raise ValueError("dst_page_table holds fewer than budget=%d tokens" % budget)
+        dst = dst_page_table.data_ptr()
+        dst_ld = dst_page_table.stride(0) if pair.batch > 1 else dst_page_table.shape[1]
+    if kept is None:
+        kept = torch.empty((pair.batch, pair.heads, budget), dtype=torch.int32, device=dev)
+    _buf(kept, pair.batch * pair.heads * budget, torch.int32, dev, "kept")
+    if new_lens is None:
+        new_lens = torch.empty(pair.batch, dtype=torch.int32, device=dev)
+    _buf(new_lens, pair.batch, torch.int32, dev, "new_lens")
+    with _on_device(dev):
+        st = _lib.lib().fp8_kv_evict(
+            ctypes.byref(pair), weights.data_ptr(), ldw, budget, sinks, recent, dst, dst_ld, _ptr(weights_out),
+            ldwo, kept.data_ptr(), new_lens.data_ptr(), _stream(dev))
+    _lib.check(st, "fp8_kv_evict")
+    return kept, new_lens
+
+
 class KVTensorCache:
     """One layer's K (or V) cache: `data` [capacity, heads, head_dim] (uint8
     codes; bf16 for the "bf16" storage) and `scale_inv` ([capacity, heads] for
@@ -615,3 +830,20 @@ class KVCache:
     def load(self, layer: int, n: Optional[int] = None, slots: Optional[torch.Tensor] = None,
              out_dtype=torch.bfloat16):
         return (self.k[layer].load(n, slots, out_dtype), self.v[layer].load(n, slots, out_dtype))
+
+    def _layer(self, layer: int) -> dict:
+        k, v = self.k[layer], self.v[layer]
+        return {"k_scale_inv": k.scale_inv, "v_scale_inv": v.scale_inv, "k_storage": k.storage,
+                "v_storage": v.storage, "scaling": k.scaling}
+
+    def attend(self, layer: int, q: torch.Tensor, page_table: torch.Tensor, lens: torch.Tensor, page_size: int,
+               **options):
+        """kv_attention of q over a layer's caches (options: its keywords)."""
+        return kv_attention(q, self.k[layer].data, self.v[layer].data, page_table, lens, page_size,
+                            **self._layer(layer), **options)
+
+    def evict(self, layer: int, weights: torch.Tensor, page_table: torch.Tensor, lens: torch.Tensor, page_size: int,
+              budget: int, sinks: int = 0, recent: int = 0, **options):
+        """kv_evict of a layer's caches (options: its keywords)."""
+        return kv_evict(self.k[layer].data, self.v[layer].data, weights, page_table, lens, page_size, budget, sinks,
+                        recent, **self._layer(layer), **options)

@@ -49,6 +49,14 @@ class Fp8Tensor(ctypes.Structure):
                 ("diag", _P)]
 
 
+class Fp8KvPair(ctypes.Structure):
+    """fp8_kv_pair, a layer's caches with the pages of a batch (104 bytes)."""
+    _fields_ = [("k", _P), ("v", _P), ("k_scale_inv", _P), ("v_scale_inv", _P), ("capacity", _I64),
+                ("page_table", _P), ("page_ld", _I64), ("lens", _P), ("max_len", _I64), ("k_storage", _I32),
+                ("v_storage", _I32), ("scaling", _I32), ("heads", _I32), ("head_dim", _I32), ("page_size", _I32),
+                ("batch", _I32), ("reserved", _I32)]
+
+
 # name -> (restype, argtypes); must match include/fp8mi.h
 SIGNATURES = {
     "fp8_abi_version": (_INT, []),
@@ -72,6 +80,10 @@ SIGNATURES = {
                                 _P, _INT, _P, _INT, _I64, _P, _I64, _P]),
     "fp8_kv_store": (_INT, [_P, _INT, _I64, _I64, _I32, _I32, _P, _INT, _INT, _U32, _P, _P, _I64, _P, _P]),
     "fp8_kv_load": (_INT, [_P, _INT, _INT, _P, _I64, _I32, _I32, _P, _I64, _INT, _P, _I64, _P]),
+    "fp8_kv_attention": (_INT, [_P, _P, _I64, _I64, _I32, _P, ctypes.c_float, _I32, _I32, _P, _I64, _P, _P, _I64,
+                                _P, _I64, _P]),
+    "fp8_kv_attention_workspace": (_I64, [_P, _I64, _I32, _I32, _I32, _I32]),
+    "fp8_kv_evict": (_INT, [_P, _P, _I64, _I32, _I32, _I32, _P, _I64, _P, _I64, _P, _P, _P]),
 }
 
 

@@ -20,9 +20,9 @@ CSRC = os.path.join(PKG, "csrc")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libfp8mi.so")
 PROBE_LIB = os.path.join(PKG, "libfp8probe.so")
-SOURCES = ["quantize.hip", "gemm.hip", "kvcache.hip", "api.cpp"]
+SOURCES = ["quantize.hip", "gemm.hip", "kvcache.hip", "attn_decode.hip", "attn_extend.hip", "evict.hip", "api.cpp"]
 PROBE_SOURCES = ["stream_probe.hip"]
-HEADERS = ["device_common.hpp", "cast_unit.hpp", "launch.hpp"]
+HEADERS = ["device_common.hpp", "cast_unit.hpp", "attention.hpp", "launch.hpp"]
 
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 FLAGS = [

@@ -526,4 +526,178 @@ fp8_status fp8_kv_load(const void* cache, fp8_kv_storage storage, fp8_kv_scaling
     return launch_result(fp8mi::launch_kv_load(a), "fp8_kv_load");
 }
 
+// Shape and alignment rules of fp8_kv_attention and fp8_kv_evict.  `sizes`:
+// sizes only (the workspace query reads no pointer).
+static_assert(sizeof(fp8_kv_pair) == 104, "fp8_kv_pair layout");
+
+static fp8_status check_kv_pair(const fp8_kv_pair* c, bool sizes, fp8mi::KvView* out) {
+    if (c == nullptr) return fail(FP8_ERR_INVALID_ARG, "cache is NULL");
+    if (c->reserved != 0) return fail(FP8_ERR_INVALID_ARG, "reserved=%d must be 0", (int)c->reserved);
+    if (c->head_dim % 16 != 0 || c->head_dim < 16 || c->head_dim > 256)
+        return fail(FP8_ERR_UNSUPPORTED_SHAPE, "head_dim=%d must be a multiple of 16 in 16..256", (int)c->head_dim);
+    if (c->heads < 1 || c->heads > 65535)
+        return fail(FP8_ERR_INVALID_ARG, "heads=%d must be in 1..65535", (int)c->heads);
+    if (c->batch < 0 || c->max_len < 0)
+        return fail(FP8_ERR_INVALID_ARG, "negative size batch=%d max_len=%lld", (int)c->batch, (long long)c->max_len);
+    if (c->batch > 65535) return fail(FP8_ERR_UNSUPPORTED_SHAPE, "batch=%d must be <= 65535", (int)c->batch);
+    if (c->max_len >= (int64_t(1) << 31) || c->capacity >= (int64_t(1) << 31))
+        return fail(FP8_ERR_UNSUPPORTED_SHAPE, "max_len and capacity must be < 2^31");
+    const int32_t ps = c->page_size;
+    if (ps < 1 || ps > (1 << 20) || (ps & (ps - 1)) != 0)
+        return fail(FP8_ERR_UNSUPPORTED_SHAPE, "page_size=%d must be a power of two <= 2^20", (int)ps);
+    const int64_t pages = (c->max_len + ps - 1) / ps;
+    if (c->page_ld < pages)
+        return fail(FP8_ERR_INVALID_ARG, "page_ld=%lld must be >= max_len / page_size = %lld", (long long)c->page_ld,
+                    (long long)pages);
+    if (!sizes) {
+        // a cache without rows has no per-(token, head) scales
+        static const float none = 0.0f;
+        const float* least = c->capacity == 0 && c->scaling == FP8_KV_PER_TOKEN_HEAD ? &none : nullptr;
+        fp8_status st = check_kv_common(c->k, c->k_storage, c->scaling, c->k_scale_inv ? c->k_scale_inv : least,
+                                        c->capacity, c->heads, c->head_dim, 0);
+        if (st != FP8_OK) return st;
+        st = check_kv_common(c->v, c->v_storage, c->scaling, c->v_scale_inv ? c->v_scale_inv : least, c->capacity,
+                             c->heads, c->head_dim, 0);
+        if (st != FP8_OK) return st;
+        if (c->batch > 0 && c->lens == nullptr) return fail(FP8_ERR_INVALID_ARG, "lens is NULL");
+        if (c->batch > 0 && pages > 0 && c->page_table == nullptr)
+            return fail(FP8_ERR_INVALID_ARG, "page_table is NULL");
+        if (!is_aligned(c->lens, 4) || !is_aligned(c->page_table, 4))
+            return fail(FP8_ERR_MISALIGNED, "lens and page_table must be 4-byte aligned");
+    }
+    out->k = c->k; out->v = c->v;
+    out->k_scale = c->k_storage == FP8_KV_BF16 ? nullptr : c->k_scale_inv;
+    out->v_scale = c->v_storage == FP8_KV_BF16 ? nullptr : c->v_scale_inv;
+    out->k_st = c->k_storage; out->v_st = c->v_storage; out->per_head = c->scaling == FP8_KV_PER_HEAD;
+    out->heads = c->heads; out->head_dim = c->head_dim; out->capacity = c->capacity;
+    out->table = c->page_table; out->table_ld = c->page_ld; out->page_shift = __builtin_ctz((unsigned)ps);
+    out->lens = c->lens; out->batch = c->batch; out->max_len = c->max_len;
+    return FP8_OK;
+}
+
+static fp8_status attention_args(const fp8_kv_pair* cache, bool sizes, int64_t total_q, int32_t q_heads, bool ragged,
+                                 int32_t window, int32_t sinks, fp8mi::AttnArgs* a) {
+    fp8_status st = check_kv_pair(cache, sizes, &a->kv);
+    if (st != FP8_OK) return st;
+    if (total_q < 0) return fail(FP8_ERR_INVALID_ARG, "negative size total_q=%lld", (long long)total_q);
+    if (q_heads < 1 || q_heads % cache->heads != 0)
+        return fail(FP8_ERR_INVALID_ARG, "q_heads=%d must be a multiple of heads=%d", (int)q_heads,
+                    (int)cache->heads);
+    if (total_q >= (int64_t(1) << 31) / q_heads || q_heads > 65535)
+        return fail(FP8_ERR_UNSUPPORTED_SHAPE, "total_q * q_heads must be < 2^31 and q_heads <= 65535");
+    if (total_q > 0 && cache->batch == 0) return fail(FP8_ERR_INVALID_ARG, "total_q=%lld with batch=0", (long long)total_q);
+    if (!ragged && cache->batch > 0 && total_q % cache->batch != 0)
+        return fail(FP8_ERR_INVALID_ARG, "total_q=%lld must be a multiple of batch=%d without q_offsets",
+                    (long long)total_q, (int)cache->batch);
+    if (window < 0 || sinks < 0)
+        return fail(FP8_ERR_INVALID_ARG, "window=%d and sinks=%d must be >= 0", (int)window, (int)sinks);
+    a->total_q = total_q; a->q_heads = q_heads;
+    // a window that reaches every token is none; sinks past the end are all
+    a->window = window >= cache->max_len ? 0 : window;
+    a->sinks = sinks > cache->max_len ? (int)cache->max_len : sinks;
+    return FP8_OK;
+}
+
+static bool one_each(const fp8mi::AttnArgs& a, bool ragged) { return !ragged && a.total_q == a.kv.batch; }
+
+int64_t fp8_kv_attention_workspace(const fp8_kv_pair* cache, int64_t total_q, int32_t q_heads, int32_t ragged,
+                                   int32_t window, int32_t sinks) {
+    fp8mi::AttnArgs a;
+    if (attention_args(cache, true, total_q, q_heads, ragged != 0, window, sinks, &a) != FP8_OK) return -1;
+    ok();
+    return total_q > 0 && one_each(a, ragged != 0) ? fp8mi::decode_workspace(a) : 0;
+}
+
+fp8_status fp8_kv_attention(const fp8_kv_pair* cache, const void* q, int64_t ldq, int64_t total_q, int32_t q_heads,
+                            const int32_t* q_offsets, float scale, int32_t window, int32_t sinks, void* out,
+                            int64_t ldo, float* lse, float* weights, int64_t ldw, void* workspace,
+                            int64_t workspace_bytes, void* stream) {
+    fp8mi::AttnArgs a;
+    const bool ragged = q_offsets != nullptr;
+    fp8_status st = attention_args(cache, false, total_q, q_heads, ragged, window, sinks, &a);
+    if (st != FP8_OK) return st;
+    const int64_t width = (int64_t)q_heads * cache->head_dim;
+    if (ldq < width || ldo < width)
+        return fail(FP8_ERR_INVALID_ARG, "ldq=%lld and ldo=%lld must be >= q_heads*head_dim=%lld", (long long)ldq,
+                    (long long)ldo, (long long)width);
+    if (ldq % 8 != 0 || ldo % 8 != 0)
+        return fail(FP8_ERR_MISALIGNED, "ldq=%lld and ldo=%lld must be multiples of 8", (long long)ldq,
+                    (long long)ldo);
+    if (total_q > 0 && q == nullptr) return fail(FP8_ERR_INVALID_ARG, "q is NULL");
+    if (total_q > 0 && out == nullptr) return fail(FP8_ERR_INVALID_ARG, "out is NULL");
+    if (!is_aligned(q, 16) || !is_aligned(out, 16))
+        return fail(FP8_ERR_MISALIGNED, "q and out must be 16-byte aligned");
+    if (!is_aligned(q_offsets, 4) || !is_aligned(lse, 4) || !is_aligned(weights, 4))
+        return fail(FP8_ERR_MISALIGNED, "q_offsets, lse and weights must be 4-byte aligned");
+    if (!(scale > -3.4e38f && scale < 3.4e38f)) return fail(FP8_ERR_INVALID_ARG, "scale must be finite");
+    if (weights != nullptr && lse == nullptr) return fail(FP8_ERR_INVALID_ARG, "lse is NULL (weights need it)");
+    if (weights != nullptr && ldw < cache->max_len)
+        return fail(FP8_ERR_INVALID_ARG, "ldw=%lld must be >= max_len=%lld", (long long)ldw,
+                    (long long)cache->max_len);
+    const bool decode = one_each(a, ragged);
+    const int64_t need = total_q > 0 && decode ? fp8mi::decode_workspace(a) : 0;
+    if (need > 0) {
+        if (workspace == nullptr)
+            return fail(FP8_ERR_INVALID_ARG, "workspace is NULL (this call needs %lld bytes)", (long long)need);
+        if (workspace_bytes < need)
+            return fail(FP8_ERR_INVALID_ARG, "workspace_bytes=%lld is below the %lld this call needs",
+                        (long long)workspace_bytes, (long long)need);
+        if (!is_aligned(workspace, 16)) return fail(FP8_ERR_MISALIGNED, "workspace must be 16-byte aligned");
+    }
+    int cus = 0;
+    st = check_device(&cus);
+    if (st != FP8_OK) return st;
+    if (total_q == 0) return ok();
+    a.q = static_cast<const uint16_t*>(q); a.ldq = ldq; a.q_offsets = q_offsets; a.scale = scale;
+    a.out = static_cast<uint16_t*>(out); a.ldo = ldo; a.lse = lse; a.weights = weights; a.ldw = ldw;
+    a.workspace = static_cast<uint8_t*>(workspace); a.stream = (hipStream_t)stream;
+    st = launch_result(decode ? fp8mi::launch_decode(a) : fp8mi::launch_extend(a), "fp8_kv_attention");
+    if (st != FP8_OK || weights == nullptr) return st;
+    return launch_result(fp8mi::launch_attention_weights(a), "fp8_kv_attention (weights)");
+}
+
+fp8_status fp8_kv_evict(const fp8_kv_pair* cache, float* weights, int64_t ldw, int32_t budget, int32_t sinks,
+                        int32_t recent, const int32_t* dst_page_table, int64_t dst_page_ld, float* weights_out,
+                        int64_t ldwo, int32_t* kept, int32_t* new_lens, void* stream) {
+    fp8mi::EvictArgs a;
+    fp8_status st = check_kv_pair(cache, false, &a.kv);
+    if (st != FP8_OK) return st;
+    if (budget < 1) return fail(FP8_ERR_INVALID_ARG, "budget=%d must be >= 1", (int)budget);
+    if (sinks < 0 || recent < 0 || (int64_t)sinks + recent > budget)
+        return fail(FP8_ERR_INVALID_ARG, "sinks=%d and recent=%d must be >= 0 and together <= budget=%d", (int)sinks,
+                    (int)recent, (int)budget);
+    if (cache->batch > 0 && weights == nullptr) return fail(FP8_ERR_INVALID_ARG, "weights is NULL");
+    if (ldw < cache->max_len || ldw < 1)
+        return fail(FP8_ERR_INVALID_ARG, "ldw=%lld must be >= max(max_len, 1)=%lld", (long long)ldw,
+                    (long long)cache->max_len);
+    if (weights_out != nullptr && weights_out != weights && ldwo < budget)
+        return fail(FP8_ERR_INVALID_ARG, "ldwo=%lld must be >= budget=%d", (long long)ldwo, (int)budget);
+    if (weights_out == weights && weights_out != nullptr && ldwo != ldw)
+        return fail(FP8_ERR_INVALID_ARG, "ldwo=%lld must be ldw=%lld when weights_out is weights", (long long)ldwo,
+                    (long long)ldw);
+    if (dst_page_table != nullptr) {
+        if (dst_page_ld < 1 || dst_page_ld < ((int64_t)budget + cache->page_size - 1) / cache->page_size)
+            return fail(FP8_ERR_INVALID_ARG, "dst_page_ld=%lld holds fewer than budget=%d tokens",
+                        (long long)dst_page_ld, (int)budget);
+        if (dst_page_table == cache->page_table)
+            return fail(FP8_ERR_INVALID_ARG, "dst_page_table is page_table (NULL moves in place)");
+    }
+    if (cache->batch > 0 && kept == nullptr) return fail(FP8_ERR_INVALID_ARG, "kept is NULL");
+    if (cache->batch > 0 && new_lens == nullptr) return fail(FP8_ERR_INVALID_ARG, "new_lens is NULL");
+    if (new_lens != nullptr && new_lens == cache->lens)
+        return fail(FP8_ERR_INVALID_ARG, "new_lens is lens (which the call still reads)");
+    if (!is_aligned(weights, 4) || !is_aligned(weights_out, 4) || !is_aligned(kept, 4) || !is_aligned(new_lens, 4) ||
+        !is_aligned(dst_page_table, 4))
+        return fail(FP8_ERR_MISALIGNED, "weights, weights_out, kept, new_lens and dst_page_table must be 4-byte aligned");
+    int cus = 0;
+    st = check_device(&cus);
+    if (st != FP8_OK) return st;
+    if (cache->batch == 0) return ok();
+    a.weights = weights; a.ldw = ldw;
+    a.weights_out = weights_out ? weights_out : weights; a.ldwo = weights_out ? ldwo : ldw;
+    a.budget = budget; a.sinks = sinks; a.recent = recent; a.dst_table = dst_page_table; a.dst_ld = dst_page_ld;
+    a.kept = kept; a.new_lens = new_lens; a.stream = (hipStream_t)stream;
+    return launch_result(fp8mi::launch_evict(a), "fp8_kv_evict");
+}
+
 }  // extern "C"

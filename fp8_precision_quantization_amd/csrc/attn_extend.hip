@@ -1,0 +1,602 @@
+// attn_extend.hip -- attention of several tokens per sequence (prompts,
+// chunks, drafted tokens) over the paged KV cache on gfx950, and the weights
+// every cached token receives from a call's queries.
+//
+// k_extend.  The query heads of one KV head share its keys, so a sequence's
+// rows are (token, head in the group), token-major; a block takes 128
+// consecutive rows (32 a wave) of one KV head and walks the cached tokens any
+// of them sees in steps of 64, with a running maximum and sum per row.
+// A step's K and V go through registers into LDS as bf16 (decoded once for
+// all waves) while the step before is computed on.  Scores are
+// S^T = K Q^T (32x32x16 bf16 products, queries as columns): a lane holds one
+// row's scores for half of the step's tokens, so maxima and sums need one
+// exchange (lanes l and l + 32), and the weights are already the B operand of
+// O^T = V^T P^T when that product numbers its 16 tokens as the accumulator
+// rows lie.  V^T is read from the row-major LDS tile by transposing reads.
+// FP8 scales multiply the fp32 score and the fp32 weight; the weight is then
+// rounded once to bf16 (relative error 2^-8 at most, each token its own, so
+// the sum's is smaller than the output's own bf16 rounding).
+//
+// LDS rows are padded (K by 16 bytes, V by 32) so that the 16-byte reads of
+// 8 K rows, and the transposing reads of 4 V rows, fall into different banks.
+//
+// Values that are not finite in V: a product with weight 0 would turn a token
+// that one row does not see into NaN for that row.  Staging takes such values
+// out of the tile and notes the token; the block then adds them by hand to
+// the rows that do see it.
+//
+// k_weights.  weights[b, h, j] += sum over the rows of 2^(x_ij - lse_i): a
+// block owns 128 tokens of a (sequence, KV head) with their K in registers
+// and walks the rows that see them, so every weight has one writer and the
+// sums have a fixed order.
+#include <hip/hip_runtime.h>
+
+#include "attention.hpp"
+
+namespace fp8mi {
+namespace {
+
+using namespace attn;
+
+constexpr int kStep = 64;        // cached tokens of one step
+constexpr int kWaves = 4;
+constexpr int kThreads = 64 * kWaves;
+constexpr int kRows = 32 * kWaves;
+
+struct ExtendParams {
+    KvView kv;
+    const uint16_t* q;
+    int64_t ldq, total_q;
+    int q_heads, group;
+    const int32_t* q_offsets;
+    float scale_log2;
+    int window, sinks;
+    uint16_t* out;
+    int64_t ldo;
+    float* lse;
+    float* weights;
+    int64_t ldw;
+};
+
+// Queries of sequence b: the first and their number, inside [0, total_q].
+__device__ __forceinline__ void queries_of(const ExtendParams& a, int b, int64_t* first, int* n) {
+    if (a.q_offsets == nullptr) {
+        const int64_t each = a.total_q / a.kv.batch;
+        *first = b * each;
+        *n = (int)each;
+    } else {
+        int64_t lo = a.q_offsets[b], hi = a.q_offsets[b + 1];
+        lo = lo < 0 ? 0 : lo > a.total_q ? a.total_q : lo;
+        hi = hi < lo ? lo : hi > a.total_q ? a.total_q : hi;
+        *first = lo;
+        *n = (int)(hi - lo);
+    }
+}
+
+// Slot of the first row tile of sequence b when a sequence's tiles start at
+// floor(first row / kRows) + b: increasing in b, and no two sequences share a
+// slot, without a prefix sum over the sequences.
+__device__ __forceinline__ int64_t first_slot(const ExtendParams& a, int b) {
+    if (a.q_offsets == nullptr) {
+        const int64_t each = a.total_q / a.kv.batch;
+        return b * ((each * a.group + kRows - 1) / kRows);
+    }
+    int64_t lo = a.q_offsets[b];
+    lo = lo < 0 ? 0 : lo > a.total_q ? a.total_q : lo;
+    return lo * a.group / kRows + b;
+}
+
+template <int DP>
+struct Lds {
+    static constexpr int kK = DP * 2 + 16, kV = DP * 2 + 32;     // bytes of a padded row
+    struct Buf {
+        alignas(16) uint8_t k[kStep * kK];
+        alignas(16) uint8_t v[kStep * kV];
+        alignas(16) float ks[kStep];
+        alignas(16) float vs[kStep];
+    };
+    Buf buf[2];
+    alignas(16) int row[3][kStep];
+    uint64_t bad[3];
+};
+
+// Words of w that hold a value that is not finite, and the same words with
+// these values cleared.
+template <int ST>
+__device__ __forceinline__ uint32_t not_finite(uint32_t w) {
+    uint32_t t;     // the top bit of every element that is not finite
+    if constexpr (ST == kE4M3) t = ((w & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u;
+    else if constexpr (ST == kE5M2) t = ((w & 0x7C7C7C7Cu) + 0x04040404u) & 0x80808080u;
+    else t = ((w & 0x7F807F80u) + 0x00800080u) & 0x80008000u;
+    return t;
+}
+template <int ST>
+__device__ __forceinline__ uint32_t cleared(uint32_t w, uint32_t t) {
+    return ST == kBf16 ? w & ~((t >> 15) * 0xFFFFu) : w & ~((t >> 7) * 0xFFu);
+}
+
+// One value of the cache as fp32.
+template <int ST>
+__device__ __forceinline__ float value_at(const uint8_t* p, int d) {
+    if constexpr (ST == kBf16) return as_f32((uint32_t)reinterpret_cast<const uint16_t*>(p)[d] << 16);
+    else return as_f32(decode2<ST>(p[d], false) << 16);
+}
+
+// 16 values of a cache row: 16 bytes of codes or 32 of bf16
+template <int ST>
+struct Unit {
+    uint4 w[kElemBytes<ST>];
+    __device__ __forceinline__ void load(const uint8_t* p) {
+#pragma unroll
+        for (int i = 0; i < kElemBytes<ST>; ++i) w[i] = reinterpret_cast<const uint4*>(p)[i];
+    }
+    __device__ __forceinline__ void clear() {
+#pragma unroll
+        for (int i = 0; i < kElemBytes<ST>; ++i) w[i] = make_uint4(0, 0, 0, 0);
+    }
+    // 1 if anything is not finite; clears these values
+    __device__ __forceinline__ bool clean() {
+        uint32_t any = 0;
+#pragma unroll
+        for (int i = 0; i < kElemBytes<ST>; ++i)
+            any |= not_finite<ST>(w[i].x) | not_finite<ST>(w[i].y) | not_finite<ST>(w[i].z) | not_finite<ST>(w[i].w);
+        if (any) {
+#pragma unroll
+            for (int i = 0; i < kElemBytes<ST>; ++i) {
+                w[i].x = cleared<ST>(w[i].x, not_finite<ST>(w[i].x));
+                w[i].y = cleared<ST>(w[i].y, not_finite<ST>(w[i].y));
+                w[i].z = cleared<ST>(w[i].z, not_finite<ST>(w[i].z));
+                w[i].w = cleared<ST>(w[i].w, not_finite<ST>(w[i].w));
+            }
+        }
+        return any != 0;
+    }
+    // as bf16 into LDS (32 bytes)
+    __device__ __forceinline__ void put(uint8_t* to) const {
+        uint4 a, b;
+        if constexpr (ST == kBf16) {
+            a = w[0];
+            b = w[1];
+        } else {
+            a = make_uint4(decode2<ST>(w[0].x, false), decode2<ST>(w[0].x, true), decode2<ST>(w[0].y, false),
+                           decode2<ST>(w[0].y, true));
+            b = make_uint4(decode2<ST>(w[0].z, false), decode2<ST>(w[0].z, true), decode2<ST>(w[0].w, false),
+                           decode2<ST>(w[0].w, true));
+        }
+        reinterpret_cast<uint4*>(to)[0] = a;
+        reinterpret_cast<uint4*>(to)[1] = b;
+    }
+};
+
+typedef short s4 __attribute__((ext_vector_type(4)));
+__device__ __forceinline__ s4 read_tr(const uint8_t* p) {
+    return __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) s4*)(uintptr_t)p);
+}
+
+template <int KST, int VST, int DP>
+__global__ __launch_bounds__(kThreads, DP <= 128 ? 2 : 1) void k_extend(const ExtendParams a) {
+    constexpr int KM = DP / 16;                     // matrix steps over the channels of K
+    constexpr int DT = DP / 32;                     // 32-channel tiles of the output
+    constexpr int UR = DP / 16;                     // units of a row
+    constexpr int UT = kStep * UR / kThreads;       // units a thread stages
+    using L = Lds<DP>;
+    extern __shared__ __align__(16) uint8_t smem[];
+    L& lds = *reinterpret_cast<L*>(smem);
+
+    const KvView& kv = a.kv;
+    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+    const int c = lane & 31, g = lane >> 5;
+    const int h = blockIdx.x % kv.heads;
+    // the sequence whose slots hold this tile; later (longer) tiles first
+    const int64_t slot = (int64_t)gridDim.x / kv.heads - 1 - blockIdx.x / kv.heads;
+    int b = 0;
+    for (int hi = kv.batch; hi - b > 1;) {
+        const int mid = (b + hi) >> 1;
+        if (first_slot(a, mid) <= slot) b = mid; else hi = mid;
+    }
+    int64_t q_first;
+    int n;
+    queries_of(a, b, &q_first, &n);
+    const int64_t row0 = (slot - first_slot(a, b)) * kRows, rows = (int64_t)n * a.group;
+    if (row0 < 0 || row0 >= rows) return;
+
+    const int len = seq_len(kv, b), base = len - n;
+    const int G = a.group, D = kv.head_dim;
+    const int r_last = (int)min(row0 + kRows, rows) - 1;
+    const int p_first = base + (int)row0 / G, p_last = base + r_last / G;
+    const Steps<kStep> steps(p_first, p_last, a.window, a.sinks);
+
+    // this lane's row
+    const int r = (int)row0 + wave * 32 + c;
+    const bool live = r < rows;
+    const int tok = r / G, hq = h * G + (r - tok * G);
+    const int pos = live ? base + tok : -1;
+    b8 qf[KM];
+    {
+        const uint16_t* qr = a.q + (q_first + tok) * a.ldq + (int64_t)hq * D;
+#pragma unroll
+        for (int s = 0; s < KM; ++s) {
+            uint4 t = make_uint4(0, 0, 0, 0);
+            if (live && s * 16 < D) t = *reinterpret_cast<const uint4*>(qr + s * 16 + g * 8);
+            qf[s] = __builtin_bit_cast(b8, t);
+        }
+    }
+    f16v o[DT];
+#pragma unroll
+    for (int i = 0; i < DT; ++i) o[i] = f16v{0};
+    float m = kLowest, l = 0.0f;
+
+    const int64_t k_row = (int64_t)kv.heads * D * kElemBytes<KST>, v_row = (int64_t)kv.heads * D * kElemBytes<VST>;
+    const uint8_t* kb = static_cast<const uint8_t*>(kv.k) + (int64_t)h * D * kElemBytes<KST>;
+    const uint8_t* vb = static_cast<const uint8_t*>(kv.v) + (int64_t)h * D * kElemBytes<VST>;
+    const int32_t* table = kv.table + b * kv.table_ld;
+    const bool k_tok = KST != kBf16 && !kv.per_head, v_tok = VST != kBf16 && !kv.per_head;
+    const float k_head = (KST == kBf16 || k_tok ? 1.0f : kv.k_scale[h]) * a.scale_log2;
+    const float v_head = VST == kBf16 || v_tok ? 1.0f : kv.v_scale[h];
+
+    Unit<KST> ku[UT];
+    Unit<VST> vu[UT];
+    float sc = 0.0f;
+    auto entry_of = [&](int i) -> int {         // threads 0..63: the page of a step's token
+        if (tid >= kStep || i >= steps.count) return -1;
+        const int j = steps.token(i) + tid;
+        return j <= p_last ? table[j >> kv.page_shift] : -1;
+    };
+    auto put_row = [&](int i, int entry) {
+        if (tid < kStep) lds.row[i % 3][tid] = entry >= 0 ? row_of_entry(kv, entry, steps.token(i) + tid) : -1;
+    };
+    auto load = [&](int i) {                    // a step's K, V and scales into registers
+        const int* rows_i = lds.row[i % 3];
+#pragma unroll
+        for (int u = 0; u < UT; ++u) {
+            const int t = (tid + u * kThreads) / UR, e = ((tid + u * kThreads) % UR) * 16;
+            const int row = rows_i[t];
+            ku[u].clear();
+            vu[u].clear();
+            if (row >= 0 && e < D) {
+                ku[u].load(kb + row * k_row + e * kElemBytes<KST>);
+                vu[u].load(vb + row * v_row + e * kElemBytes<VST>);
+            }
+        }
+        if (tid < 2 * kStep) {
+            const bool key = tid < kStep;
+            sc = key ? k_head : v_head;
+            if (key ? k_tok : v_tok) {
+                const int row = rows_i[tid & (kStep - 1)];
+                const float s = row >= 0 ? (key ? kv.k_scale : kv.v_scale)[(int64_t)row * kv.heads + h] : 0.0f;
+                sc *= s;
+            }
+        }
+    };
+    auto put = [&](int i) {                     // the registers into a step's LDS buffer
+        typename L::Buf& buf = lds.buf[i & 1];
+#pragma unroll
+        for (int u = 0; u < UT; ++u) {
+            const int t = (tid + u * kThreads) / UR, e = (tid + u * kThreads) % UR;
+            if (vu[u].clean()) atomicOr(reinterpret_cast<unsigned long long*>(&lds.bad[i % 3]), 1ull << t);
+            ku[u].put(buf.k + t * L::kK + e * 32);
+            vu[u].put(buf.v + t * L::kV + e * 32);
+        }
+        if (tid < 2 * kStep) (tid < kStep ? buf.ks : buf.vs)[tid & (kStep - 1)] = sc;
+    };
+
+    if (steps.count > 0) {
+        if (tid < 3) lds.bad[tid] = 0;
+        put_row(0, entry_of(0));
+        put_row(1, entry_of(1));
+        __syncthreads();
+        load(0);
+        put(0);
+        __syncthreads();
+    }
+    for (int i = 0; i < steps.count; ++i) {
+        const bool more = i + 1 < steps.count;
+        if (more) load(i + 1);
+        const int entry = entry_of(i + 2);
+        const typename L::Buf& buf = lds.buf[i & 1];
+        const int j0 = steps.token(i);
+
+        f16v x[2];
+#pragma unroll
+        for (int t = 0; t < 2; ++t) {
+            x[t] = f16v{0};
+#pragma unroll
+            for (int s = 0; s < KM; ++s) {
+                if (DP > 64 && s * 16 >= D) break;
+                const b8 kf = *reinterpret_cast<const b8*>(buf.k + (t * 32 + c) * L::kK + s * 32 + g * 16);
+                x[t] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(kf, qf[s], x[t], 0, 0, 0);
+            }
+        }
+#pragma unroll
+        for (int t = 0; t < 2; ++t)
+#pragma unroll
+            for (int u = 0; u < 4; ++u) {
+                const f4 ks = *reinterpret_cast<const f4*>(&buf.ks[t * 32 + u * 8 + g * 4]);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) x[t][u * 4 + e] *= ks[e];
+            }
+        const int* rows_i = lds.row[i % 3];
+        const bool edge = j0 + kStep - 1 > p_first ||
+                          (a.window > 0 && j0 <= p_last - a.window && j0 + kStep - 1 >= a.sinks);
+        if (edge || !__all(rows_i[lane] >= 0)) {
+#pragma unroll
+            for (int t = 0; t < 2; ++t)
+#pragma unroll
+                for (int u = 0; u < 4; ++u) {
+                    const int at = t * 32 + u * 8 + g * 4;
+                    const int4 rr = *reinterpret_cast<const int4*>(&rows_i[at]);
+                    const int ra[4] = {rr.x, rr.y, rr.z, rr.w};
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        if (ra[e] < 0 || !sees(j0 + at + e, pos, a.window, a.sinks)) x[t][u * 4 + e] = -INFINITY;
+                }
+        }
+        float mx = kLowest;
+#pragma unroll
+        for (int t = 0; t < 2; ++t)
+#pragma unroll
+            for (int e = 0; e < 16; ++e) mx = fmaxf(mx, x[t][e]);
+        if (__any(mx > m + kSlack)) {
+            const float mn = fmaxf(m, max_xor32(mx));
+            const float f = __builtin_amdgcn_exp2f(m - mn);
+            m = mn;
+            l *= f;
+#pragma unroll
+            for (int d = 0; d < DT; ++d) o[d] *= f;
+        }
+        b8 pf[4];
+        const uint64_t bad = lds.bad[i % 3];
+#pragma unroll
+        for (int t = 0; t < 2; ++t) {
+#pragma unroll
+            for (int u = 0; u < 4; ++u) {
+                const f4 vs = *reinterpret_cast<const f4*>(&buf.vs[t * 32 + u * 8 + g * 4]);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const float w = __builtin_amdgcn_exp2f(x[t][u * 4 + e] - m);
+                    l += w;
+                    // a scale of a row that is not there, or not seen, multiplies nothing
+                    x[t][u * 4 + e] = x[t][u * 4 + e] == -INFINITY ? 0.0f : w * vs[e];
+                }
+            }
+#pragma unroll
+            for (int u = 0; u < 2; ++u) {
+                u4 w;
+#pragma unroll
+                for (int e = 0; e < 4; ++e) w[e] = pack2(x[t][u * 8 + 2 * e], x[t][u * 8 + 2 * e + 1]);
+                pf[t * 2 + u] = __builtin_bit_cast(b8, w);
+            }
+        }
+        if (bad) {                              // values of V taken out of the tile
+            for (uint64_t left = bad; left; left &= left - 1) {
+                const int t = __builtin_ctzll(left), reg = (t >> 5) * 16 + ((t & 31) >> 3) * 4 + (t & 3);
+                float w = 0.0f;
+#pragma unroll
+                for (int e = 0; e < 32; ++e) w = e == reg ? x[e >> 4][e & 15] : w;
+                w = __shfl(w, c + 32 * ((t >> 2) & 1), 64);
+                if (sees(j0 + t, pos, a.window, a.sinks)) {
+                    const uint8_t* vr = vb + rows_i[t] * v_row;
+#pragma unroll
+                    for (int d = 0; d < DT; ++d)
+#pragma unroll
+                        for (int e = 0; e < 16; ++e) {
+                            const int ch = d * 32 + (e >> 2) * 8 + g * 4 + (e & 3);
+                            if (ch < D) {
+                                const float v = value_at<VST>(vr, ch);
+                                if (!__builtin_isfinite(v)) o[d][e] += w * v;
+                            }
+                        }
+                }
+            }
+        }
+#pragma unroll
+        for (int d = 0; d < DT; ++d) {
+            if (DP > 64 && d * 32 >= D) break;
+#pragma unroll
+            for (int t = 0; t < 4; ++t) {
+                // lane i of 16 points at row i / 4, channels 4 (i % 4).. of a
+                // 4 x 16 block and receives its column i
+                const uint8_t* p = buf.v + (t * 16 + g * 4 + ((lane & 15) >> 2)) * L::kV +
+                                   (d * 32 + ((lane >> 4) & 1) * 16 + (lane & 3) * 4) * 2;
+                const s4 lo = read_tr(p), hi = read_tr(p + 8 * L::kV);
+                typedef short s8 __attribute__((ext_vector_type(8)));
+                const s8 w = __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
+                o[d] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(b8, w), pf[t], o[d], 0, 0, 0);
+            }
+        }
+        if (more) put(i + 1);
+        put_row(i + 2, entry);
+        if (tid == 0) lds.bad[(i + 2) % 3] = 0;
+        __syncthreads();
+    }
+
+    l = sum_xor32(l);
+    if (!live) return;
+    const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+    uint16_t* to = a.out + (q_first + tok) * a.ldo + (int64_t)hq * D;
+#pragma unroll
+    for (int d = 0; d < DT; ++d)
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+            const int ch = d * 32 + u * 8 + g * 4;
+            if (ch < D)
+                *reinterpret_cast<uint2*>(to + ch) =
+                    make_uint2(pack2(o[d][u * 4] * inv, o[d][u * 4 + 1] * inv),
+                               pack2(o[d][u * 4 + 2] * inv, o[d][u * 4 + 3] * inv));
+        }
+    if (g == 0 && a.lse)
+        a.lse[(q_first + tok) * a.q_heads + hq] = l == 0.0f ? -INFINITY : (m + __builtin_amdgcn_logf(l)) * kLn2;
+}
+
+// Weights: a wave holds 32 tokens' K as the A operand and takes the rows 32
+// at a time as columns.
+template <int KST, int DP>
+__global__ __launch_bounds__(kThreads) void k_weights(const ExtendParams a) {
+    constexpr int KM = DP / 16;
+    constexpr int KC = DP * kElemBytes<KST> / 32;       // 16-byte pieces of K a lane holds
+    const KvView& kv = a.kv;
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    const int c = lane & 31, g = lane >> 5;
+    const int h = blockIdx.x % kv.heads, b = blockIdx.y;
+    const int len = seq_len(kv, b);
+    const int j0 = (int)(blockIdx.x / kv.heads) * kRows + wave * 32;
+    if (j0 >= len) return;
+    int64_t q_first;
+    int n;
+    queries_of(a, b, &q_first, &n);
+    const int G = a.group, D = kv.head_dim, base = len - n;
+
+    const int j = j0 + c;
+    int row = -1;
+    if (j < len) {
+        const int entry = kv.table[b * kv.table_ld + (j >> kv.page_shift)];
+        row = entry >= 0 ? row_of_entry(kv, entry, j) : -1;
+    }
+    if (!__any(row >= 0)) return;
+    uint4 kr[KC];
+#pragma unroll
+    for (int i = 0; i < KC; ++i) {
+        const int e = (i * 32 + g * 16) / kElemBytes<KST>;
+        kr[i] = make_uint4(0, 0, 0, 0);
+        if (row >= 0 && e < D)
+            kr[i] = *reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(kv.k) +
+                                                    ((int64_t)row * kv.heads + h) * D * kElemBytes<KST> + i * 32 +
+                                                    g * 16);
+    }
+    float sc = a.scale_log2;
+    if (KST != kBf16) sc *= kv.per_head ? kv.k_scale[h] : row >= 0 ? kv.k_scale[(int64_t)row * kv.heads + h] : 0.0f;
+    b8 kf[KM];
+#pragma unroll
+    for (int s = 0; s < KM; ++s) {
+        uint4 w;
+        if constexpr (KST == kBf16) {
+            w = kr[s];
+        } else {
+            const uint4 t = kr[s >> 1];
+            const uint32_t w0 = (s & 1) ? t.z : t.x, w1 = (s & 1) ? t.w : t.y;
+            w = make_uint4(decode2<KST>(w0, false), decode2<KST>(w0, true), decode2<KST>(w1, false),
+                           decode2<KST>(w1, true));
+        }
+        kf[s] = __builtin_bit_cast(b8, w);
+    }
+    // of the accumulator's token rows: the factor, and whether it is there
+    float ks[16];
+    uint32_t there = 0;
+#pragma unroll
+    for (int e = 0; e < 16; ++e) {
+        const int t = (e >> 2) * 8 + g * 4 + (e & 3);
+        ks[e] = __shfl(sc, t, 64);
+        there |= (__shfl(row, t, 64) >= 0 ? 1u : 0u) << e;
+    }
+    // rows (token of the call, head in the group) that see any of these tokens
+    int i_lo = j0 - base, i_hi = n;
+    if (a.window > 0 && j0 >= a.sinks) i_hi = min(i_hi, j0 + 31 + a.window - base);
+    i_lo = i_lo < 0 ? 0 : i_lo;
+    float w[16];
+#pragma unroll
+    for (int e = 0; e < 16; ++e) w[e] = 0.0f;
+    const int r_end = i_hi * G;
+    for (int r0 = i_lo * G; r0 < r_end; r0 += 32) {
+        const int r = r0 + c;
+        const bool live = r < r_end;
+        const int tok = r / G, hq = h * G + (r - tok * G);
+        const uint16_t* qr = a.q + (q_first + tok) * a.ldq + (int64_t)hq * D;
+        f16v x = f16v{0};
+#pragma unroll
+        for (int s = 0; s < KM; ++s) {
+            const int e = KST == kBf16 ? s * 16 + g * 8 : (s >> 1) * 32 + g * 16 + (s & 1) * 8;
+            uint4 t = make_uint4(0, 0, 0, 0);
+            if (live && e < D) t = *reinterpret_cast<const uint4*>(qr + e);
+            x = __builtin_amdgcn_mfma_f32_32x32x16_bf16(kf[s], __builtin_bit_cast(b8, t), x, 0, 0, 0);
+        }
+        const float lse = live ? a.lse[(q_first + tok) * a.q_heads + hq] * kLog2e : -INFINITY;
+        const int pos = lse == -INFINITY ? -1 : base + tok;     // a row that sees nothing gives nothing
+#pragma unroll
+        for (int e = 0; e < 16; ++e) {
+            const int t = j0 + (e >> 2) * 8 + g * 4 + (e & 3);
+            const float p = __builtin_amdgcn_exp2f(x[e] * ks[e] - lse);
+            w[e] += sees(t, pos, a.window, a.sinks) ? p : 0.0f;
+        }
+    }
+    float* to = a.weights + ((int64_t)b * kv.heads + h) * a.ldw;
+#pragma unroll
+    for (int e = 0; e < 16; ++e) {
+#pragma unroll
+        for (int off = 16; off >= 1; off >>= 1) w[e] += __shfl_xor(w[e], off, 64);
+        const int t = j0 + (e >> 2) * 8 + g * 4 + (e & 3);
+        if (c == 0 && t < len && (there >> e & 1)) to[t] += w[e];
+    }
+}
+
+template <int KST, int VST, int DP>
+hipError_t run_extend(const ExtendParams& p, hipStream_t stream) {
+    static_assert(sizeof(Lds<DP>) <= 160 * 1024, "LDS");
+    constexpr int bytes = sizeof(Lds<DP>);
+    hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(&k_extend<KST, VST, DP>),
+                                       hipFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    if (e != hipSuccess) return e;
+    int64_t tiles;
+    if (p.q_offsets == nullptr) tiles = p.kv.batch * ((p.total_q / p.kv.batch * p.group + kRows - 1) / kRows);
+    else tiles = p.total_q * p.group / kRows + p.kv.batch;
+    hipLaunchKernelGGL((k_extend<KST, VST, DP>), dim3((unsigned)(tiles * p.kv.heads)), dim3(kThreads), bytes, stream,
+                       p);
+    return hipGetLastError();
+}
+
+template <int KST, int VST>
+hipError_t extend_dim(const ExtendParams& p, hipStream_t stream) {
+    if (p.kv.head_dim <= 64) return run_extend<KST, VST, 64>(p, stream);
+    if (p.kv.head_dim <= 128) return run_extend<KST, VST, 128>(p, stream);
+    return run_extend<KST, VST, 256>(p, stream);
+}
+
+template <int KST>
+hipError_t extend_v(const ExtendParams& p, hipStream_t stream) {
+    switch (p.kv.v_st) {
+    case FP8_KV_E4M3: return extend_dim<KST, kE4M3>(p, stream);
+    case FP8_KV_E5M2: return extend_dim<KST, kE5M2>(p, stream);
+    default: return extend_dim<KST, kBf16>(p, stream);
+    }
+}
+
+template <int KST>
+hipError_t weights_dim(const ExtendParams& p, hipStream_t stream) {
+    const unsigned tiles = (unsigned)((p.kv.max_len + kRows - 1) / kRows);
+    const dim3 grid(tiles * p.kv.heads, (unsigned)p.kv.batch), block(kThreads);
+    if (p.kv.head_dim <= 64) hipLaunchKernelGGL((k_weights<KST, 64>), grid, block, 0, stream, p);
+    else if (p.kv.head_dim <= 128) hipLaunchKernelGGL((k_weights<KST, 128>), grid, block, 0, stream, p);
+    else hipLaunchKernelGGL((k_weights<KST, 256>), grid, block, 0, stream, p);
+    return hipGetLastError();
+}
+
+ExtendParams params_of(const AttnArgs& a) {
+    ExtendParams p;
+    p.kv = a.kv; p.q = a.q; p.ldq = a.ldq; p.total_q = a.total_q; p.q_heads = a.q_heads;
+    p.group = a.q_heads / a.kv.heads; p.q_offsets = a.q_offsets; p.scale_log2 = a.scale * kLog2e;
+    p.window = a.window; p.sinks = a.sinks; p.out = a.out; p.ldo = a.ldo; p.lse = a.lse;
+    p.weights = a.weights; p.ldw = a.ldw;
+    return p;
+}
+
+}  // namespace
+
+hipError_t launch_extend(const AttnArgs& a) {
+    const ExtendParams p = params_of(a);
+    switch (a.kv.k_st) {
+    case FP8_KV_E4M3: return extend_v<kE4M3>(p, a.stream);
+    case FP8_KV_E5M2: return extend_v<kE5M2>(p, a.stream);
+    default: return extend_v<kBf16>(p, a.stream);
+    }
+}
+
+hipError_t launch_attention_weights(const AttnArgs& a) {
+    if (a.kv.max_len == 0) return hipSuccess;
+    const ExtendParams p = params_of(a);
+    switch (a.kv.k_st) {
+    case FP8_KV_E4M3: return weights_dim<kE4M3>(p, a.stream);
+    case FP8_KV_E5M2: return weights_dim<kE5M2>(p, a.stream);
+    default: return weights_dim<kBf16>(p, a.stream);
+    }
+}
+
+}  // namespace fp8mi

@@ -103,6 +103,56 @@ struct KvLoadArgs {
     hipStream_t stream = nullptr;
 };
 
+// A layer's K and V caches as the attention and eviction kernels see them
+// (fp8_kv_pair, checked).
+struct KvView {
+    void* k = nullptr;
+    void* v = nullptr;
+    float* k_scale = nullptr;    // null: bf16 storage
+    float* v_scale = nullptr;
+    int k_st = 0, v_st = 0;      // fp8_kv_storage
+    bool per_head = false;       // FP8_KV_PER_HEAD
+    int heads = 0, head_dim = 0;
+    int64_t capacity = 0;        // < 2^31
+    const int32_t* table = nullptr;
+    int64_t table_ld = 0;
+    int page_shift = 0;
+    const int32_t* lens = nullptr;
+    int batch = 0;
+    int64_t max_len = 0;         // < 2^31, <= pages * page size
+};
+
+struct AttnArgs {
+    KvView kv;
+    const uint16_t* q = nullptr;
+    int64_t ldq = 0, total_q = 0;
+    int q_heads = 0;
+    const int32_t* q_offsets = nullptr;   // null: total_q / batch queries a sequence
+    float scale = 0.0f;
+    int window = 0, sinks = 0;            // window 0: none; < max_len otherwise
+    uint16_t* out = nullptr;
+    int64_t ldo = 0;
+    float* lse = nullptr;
+    float* weights = nullptr;
+    int64_t ldw = 0;
+    uint8_t* workspace = nullptr;
+    hipStream_t stream = nullptr;
+};
+
+struct EvictArgs {
+    KvView kv;
+    const float* weights = nullptr;      // [batch, heads, ldw]
+    int64_t ldw = 0;
+    float* weights_out = nullptr;        // [batch, heads, ldwo]; weights itself: in place
+    int64_t ldwo = 0;
+    int budget = 0, sinks = 0, recent = 0;
+    const int32_t* dst_table = nullptr;  // null: in place
+    int64_t dst_ld = 0;
+    int32_t* kept = nullptr;             // [batch, heads, budget]
+    int32_t* new_lens = nullptr;         // [batch]
+    hipStream_t stream = nullptr;
+};
+
 hipError_t launch_quantize(const QuantArgs& a);
 hipError_t launch_quantize_multi(const MultiQuantArgs& a);
 // Address on the current device of the workspace fp8_quantize_noalloc uses
@@ -110,6 +160,13 @@ hipError_t launch_quantize_multi(const MultiQuantArgs& a);
 hipError_t static_workspace(uint32_t** out);
 hipError_t launch_kv_store(const KvStoreArgs& a);
 hipError_t launch_kv_load(const KvLoadArgs& a);
+// One query per sequence; the workspace's bytes follow the same rules as the
+// launch's splits.
+int64_t decode_workspace(const AttnArgs& a);
+hipError_t launch_decode(const AttnArgs& a);
+hipError_t launch_extend(const AttnArgs& a);
+hipError_t launch_attention_weights(const AttnArgs& a);   // after one of them: reads a.lse
+hipError_t launch_evict(const EvictArgs& a);
 hipError_t launch_history_init(fp8_amax_history* h, int32_t len, hipStream_t stream);
 hipError_t launch_history_set_guard(fp8_amax_history* h, float threshold, hipStream_t stream);
 hipError_t launch_scaled_gemm(const GemmArgs& a);

@@ -384,6 +384,108 @@ fp8_status fp8_kv_load(const void* cache, fp8_kv_storage storage, fp8_kv_scaling
                        const int64_t* slots, int64_t n_tokens, fp8_out_dtype out_dtype, void* out,
                        int64_t ld_out, void* stream);
 
+/* A layer's K and V caches with the pages of a batch of sequences (a host-side
+ * descriptor; its pointers are device pointers).  Storage, layout and scales
+ * as above; both caches share capacity, heads, head_dim and scaling.
+ *   page_table: int32 [batch x page_ld] (page_ld >= max_len / page_size,
+ *     rounded up): token j of sequence b lives in cache row
+ *     page_table[b*page_ld + j/page_size] * page_size + j % page_size, the
+ *     slot fp8_kv_store stored it at.  A row outside [0, capacity) is a token
+ *     that is not there: no query sees it.
+ *   lens: int32 [batch], cached tokens per sequence, read on the device and
+ *     clamped to [0, max_len].
+ * Requirements (else FP8_ERR_UNSUPPORTED_SHAPE / FP8_ERR_MISALIGNED):
+ * page_size a power of two <= 2^20; head_dim % 16 == 0, 16 <= head_dim <= 256;
+ * capacity and max_len < 2^31; batch <= 65535; caches 16-byte aligned. */
+typedef struct fp8_kv_pair {
+    void* k;
+    void* v;
+    float* k_scale_inv;      /* ignored for FP8_KV_BF16 storage */
+    float* v_scale_inv;
+    int64_t capacity;
+    const int32_t* page_table;
+    int64_t page_ld;
+    const int32_t* lens;
+    int64_t max_len;
+    int32_t k_storage;       /* fp8_kv_storage */
+    int32_t v_storage;
+    int32_t scaling;         /* fp8_kv_scaling */
+    int32_t heads;
+    int32_t head_dim;
+    int32_t page_size;
+    int32_t batch;
+    int32_t reserved;        /* 0 */
+} fp8_kv_pair;
+
+/* Attention over the cache ([DeepL] 3.1: K's precision drives the attention
+ * scores, V's the mixed output), reading the codes in place.  Sequence b has
+ * n_b new tokens (stored in the cache before the call), the last n_b of its
+ * len_b; new token i is at position p = len_b - n_b + i.  Query head x uses
+ * KV head x / (q_heads / heads).  With K_j, V_j the dequantized vectors:
+ *   s_j = scale * (q . K_j) for the tokens j that position p sees: j <= p and
+ *         (window == 0 or j > p - window or j < sinks);
+ *   lse = log(sum_j exp(s_j)),   out = sum_j exp(s_j - lse) * V_j.
+ * A row that sees nothing (or whose scores are all -inf) gives out 0, lse
+ * -inf.  What a token that a row does not see holds, NaN and Inf included,
+ * has no part in that row.
+ * q: bf16 [total_q x (q_heads*head_dim)], leading dimension ldq; out: bf16,
+ * the same shape, ldo (both multiples of 8, 16-byte aligned).  q_heads a
+ * multiple of heads, total_q * q_heads < 2^31.
+ * q_offsets: NULL = every sequence has total_q / batch new tokens (total_q a
+ * multiple of batch); else DEVICE int32 [batch + 1], non-decreasing, within
+ * [0, total_q]: sequence b's queries are rows q_offsets[b]..q_offsets[b+1]-1
+ * (clamped on the device; decreasing offsets leave the overlapping rows
+ * unspecified, never an out-of-range access).  Rows in no sequence are not
+ * written.
+ * lse: fp32 [total_q x q_heads], or NULL.
+ * weights: NULL, or fp32 [batch x heads x ldw] (ldw >= max_len) to which the
+ * call ADDS what every cached token receives, summed over the sequence's
+ * queries and the query heads of the KV head: weights[b,h,j] += sum exp(s_j -
+ * lse).  Needs lse.  Entries of tokens that are not there are left alone.
+ * workspace: fp8_kv_attention_workspace() bytes, 16-byte aligned, as the
+ * other workspaces (no initialization; not shared by calls that can run at
+ * the same time, captured graphs included); NULL is fine when that is 0.
+ * Sums are in fp32 and in a fixed order: results are bit-reproducible run to
+ * run; they may differ in the last bits between splits (batch sizes, max_len).
+ * Scores, softmax and sums are in fp32; the weights enter the product with V
+ * as bf16 pairs (one new token per sequence) or as bf16 (else). */
+fp8_status fp8_kv_attention(const fp8_kv_pair* cache, const void* q, int64_t ldq, int64_t total_q, int32_t q_heads,
+                            const int32_t* q_offsets, float scale, int32_t window, int32_t sinks, void* out,
+                            int64_t ldo, float* lse, float* weights, int64_t ldw, void* workspace,
+                            int64_t workspace_bytes, void* stream);
+
+/* Bytes of workspace fp8_kv_attention needs for these arguments (ragged:
+ * q_offsets is not NULL), from sizes alone (no pointer is read); -1 if it
+ * would reject them (see fp8_last_error). */
+int64_t fp8_kv_attention_workspace(const fp8_kv_pair* cache, int64_t total_q, int32_t q_heads, int32_t ragged,
+                                   int32_t window, int32_t sinks);
+
+/* Eviction by accumulated attention weight: a sequence of n = len_b > budget
+ * tokens keeps, for every KV head by itself, its first `sinks` tokens, its
+ * last `recent`, and of those between the budget - sinks - recent with the
+ * largest weights[b,h,j] (the lower position among equals; NaN is largest).
+ * Their vectors and per-(token, head) scales of K and V move, in their order,
+ * to positions 0..budget-1 of the sequence, and so do their weights; the
+ * weights behind are set to 0.  A sequence of n <= budget keeps everything.
+ * weights: fp32 [batch x heads x ldw], ldw >= max_len.
+ * weights_out: NULL = in place (entries budget..n-1 become 0); else fp32
+ *   [batch x heads x ldwo], ldwo >= budget, of which every head's first
+ *   `budget` entries are written, weights itself is then only read.
+ * dst_page_table: NULL = in place; else int32 [batch x dst_page_ld] pages of
+ *   the same caches (dst_page_ld * page_size >= budget) that hold no page of
+ *   page_table: the kept tokens of every sequence, shorter ones included, are
+ *   copied there and the old pages stay as they are.  Tokens whose source or
+ *   destination row is outside the cache are left out.
+ * Sequences (of one call) must not share pages that are written.
+ * kept: int32 [batch x heads x budget], the positions kept (increasing), -1
+ *   behind the last of a shorter sequence.  new_lens: int32 [batch],
+ *   min(len_b, budget); lens itself is not changed (a model's layers share
+ *   it).
+ * 0 <= sinks, 0 <= recent, sinks + recent <= budget, budget >= 1. */
+fp8_status fp8_kv_evict(const fp8_kv_pair* cache, float* weights, int64_t ldw, int32_t budget, int32_t sinks,
+                        int32_t recent, const int32_t* dst_page_table, int64_t dst_page_ld, float* weights_out,
+                        int64_t ldwo, int32_t* kept, int32_t* new_lens, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -1,0 +1,422 @@
+"""fp8_kv_attention on the GPU against a float64 reference: one and several
+new tokens per sequence, every storage and scaling, head dimensions and group
+sizes, page sizes, lengths from 0, windows and sinks, absent pages, rows that
+see nothing, values that are not finite in places that are not seen,
+accumulated weights, captured graphs and other streams.  Everything no
+sequence holds is NaN in these caches, so a read of it shows."""
+from __future__ import annotations
+
+import numpy as np
+import pytest
+import torch
+
+from tests import attention_ref as ref
+from tests.gpu_util import say
+
+pytestmark = pytest.mark.gpu
+
+fp8 = pytest.importorskip("fp8_precision_quantization_amd")
+
+
+@pytest.fixture(autouse=True)
+def _need_gpu(gpu):
+    yield
+
+
+def _run(cache, n, q_heads, window=0, sinks=0, ragged=None, weights=None, scale=None, seed=1, **more):
+    q = ref.queries(cache, n, q_heads, seed)
+    args = cache.device()
+    if ragged is None:
+        ragged = len(set(n)) > 1
+    if ragged:
+        args["q_offsets"] = torch.tensor(np.concatenate([[0], np.cumsum(n)]), dtype=torch.int32).cuda()
+    args.update(more)
+    say("kv_attention", dict(lens=cache.lens[:6], n=list(n)[:6], heads=cache.heads, q_heads=q_heads, dim=cache.dim,
+                             page=cache.page, k=cache.k_storage, v=cache.v_storage, scaling=cache.scaling,
+                             window=window, sinks=sinks, ragged=ragged, weights=weights is not None))
+    out, lse = fp8.kv_attention(q.cuda(), window=window, sinks=sinks, weights=weights, scale=scale, return_lse=True,
+                                **args)
+    torch.cuda.synchronize()
+    return q, out, lse
+
+
+def _check(cache, n, q_heads, window=0, sinks=0, p_bits=8, **more):
+    q, out, lse = _run(cache, n, q_heads, window, sinks, **more)
+    ref.check_attention(cache, q, n, out, lse, window, sinks, more.get("scale"), p_bits)
+    return q, out, lse
+
+
+STORAGES = [("e4m3", "e4m3", "token_head"), ("e4m3", "e4m3", "head"), ("e5m2", "e5m2", "token_head"),
+            ("e5m2", "e4m3", "head"), ("bf16", "bf16", "token_head"), ("bf16", "e4m3", "token_head"),
+            ("e5m2", "bf16", "token_head"), ("e4m3", "e5m2", "token_head"), ("bf16", "e5m2", "head")]
+
+
+@pytest.mark.parametrize("dim", [64, 128, 256])
+@pytest.mark.parametrize("storage", STORAGES, ids=lambda s: "-".join(s))
+def test_decode_storages(storage, dim):
+    k, v, scaling = storage
+    lens = [1, 31, 32, 33, 127, 300, 700]
+    c = ref.Cache(lens, 2, dim, 16, k, v, scaling, seed=dim)
+    _check(c, [1] * len(lens), 8, p_bits=15)
+
+
+@pytest.mark.parametrize("dim", [16, 32, 48, 80, 96, 112, 144, 192, 208, 240])
+@pytest.mark.parametrize("storage", [("e4m3", "e4m3"), ("bf16", "bf16"), ("e4m3", "bf16")], ids="-".join)
+def test_decode_odd_dims(storage, dim):
+    c = ref.Cache([5, 64, 211], 3, dim, 8, *storage, seed=dim)
+    _check(c, [1, 1, 1], 6, p_bits=15)
+
+
+@pytest.mark.parametrize("group", [1, 3, 5, 7, 8, 15, 16, 17, 32, 33, 71])
+def test_decode_groups(group):
+    c = ref.Cache([1, 90, 259], 2, 64, 16, seed=group)
+    _check(c, [1, 1, 1], 2 * group, p_bits=15)
+
+
+@pytest.mark.parametrize("page", [1, 2, 4, 16, 64, 256, 4096])
+def test_decode_pages(page):
+    c = ref.Cache([3, 65, 300, 513], 2, 64, page, seed=page)
+    _check(c, [1] * 4, 4, p_bits=15)
+
+
+@pytest.mark.parametrize("lens", [[2000], [5000, 1, 0, 37, 2048], [4096] * 3, [9000, 8999]])
+def test_decode_long(lens):
+    """Several splits joined; sequences shorter than a split and empty ones among them."""
+    c = ref.Cache(lens, 2, 64, 16, seed=len(lens))
+    _check(c, [1] * len(lens), 4, p_bits=15)
+
+
+WINDOWS = [(1, 0), (1, 4), (16, 0), (31, 1), (33, 4), (64, 64), (100, 5), (1000, 40), (256, 300), (4000, 4)]
+
+
+@pytest.mark.parametrize("window, sinks", WINDOWS)
+def test_decode_windows(window, sinks):
+    c = ref.Cache([1, 4, 40, 150, 1200, 3000], 2, 64, 16, seed=window + sinks)
+    _check(c, [1] * 6, 4, window, sinks, p_bits=15)
+
+
+def test_decode_nothing_to_see():
+    """Empty sequences and sequences whose pages are all absent give zeros and -inf."""
+    c = ref.Cache([0, 16, 40, 0], 2, 64, 16, seed=3, absent=[(1, 0)])
+    q, out, lse = _check(c, [1] * 4, 4, p_bits=15)
+    for b in (0, 1, 3):
+        assert (out[b] == 0).all() and torch.isneginf(lse[b]).all()
+
+
+@pytest.mark.parametrize("n", [[1] * 3, [5] * 3, [1, 40, 17]])
+def test_absent_pages(n):
+    c = ref.Cache([100, 260, 333], 2, 128, 16, seed=4, absent=[(0, 1), (1, 0), (1, 7), (2, 20), (2, 3)])
+    _check(c, n, 8)
+    _check(c, n, 8, 50, 20)
+
+
+def test_empty_capacity():
+    """A cache without rows: nothing is there."""
+    args = dict(k_cache=torch.empty((0, 2, 64), dtype=torch.uint8, device="cuda"),
+                v_cache=torch.empty((0, 2, 64), dtype=torch.uint8, device="cuda"),
+                k_scale_inv=torch.empty((0, 2), device="cuda"), v_scale_inv=torch.empty((0, 2), device="cuda"),
+                page_table=torch.zeros((2, 4), dtype=torch.int32, device="cuda"),
+                lens=torch.tensor([3, 40], dtype=torch.int32, device="cuda"), page_size=16)
+    for n in (2, 6):
+        q = torch.randn(n, 4, 64, device="cuda").bfloat16()
+        say("empty cache", n)
+        out, lse = fp8.kv_attention(q, return_lse=True, **args)
+        torch.cuda.synchronize()
+        assert (out == 0).all() and torch.isneginf(lse).all()
+
+
+@pytest.mark.parametrize("dim", [64, 128, 256])
+@pytest.mark.parametrize("storage", STORAGES, ids=lambda s: "-".join(s))
+def test_extend_storages(storage, dim):
+    k, v, scaling = storage
+    n = [1, 3, 64, 130]
+    c = ref.Cache([1, 70, 64, 333], 2, dim, 16, k, v, scaling, seed=dim)
+    _check(c, n, 6)
+
+
+@pytest.mark.parametrize("dim", [16, 48, 80, 96, 112, 160, 192, 240])
+@pytest.mark.parametrize("storage", [("e4m3", "e4m3"), ("bf16", "bf16")], ids="-".join)
+def test_extend_odd_dims(storage, dim):
+    c = ref.Cache([20, 150], 2, dim, 8, *storage, seed=dim)
+    _check(c, [7, 33], 4)
+
+
+@pytest.mark.parametrize("group", [1, 2, 3, 5, 7, 8, 16, 33, 130])
+def test_extend_groups(group):
+    c = ref.Cache([30, 200], 2, 64, 16, seed=group)
+    _check(c, [3, 50], 2 * group)
+
+
+@pytest.mark.parametrize("n, length", [(1, 1), (2, 2), (33, 33), (128, 128), (129, 500), (300, 301), (512, 1100)])
+def test_extend_uniform(n, length):
+    """Every sequence the same number of queries (no q_offsets)."""
+    c = ref.Cache([length, max(n, length - 1)], 2, 64, 32, seed=n)
+    _check(c, [n, n], 4)
+
+
+@pytest.mark.parametrize("window, sinks", WINDOWS)
+def test_extend_windows(window, sinks):
+    c = ref.Cache([1, 40, 150, 900], 2, 64, 16, seed=window + sinks)
+    _check(c, [1, 7, 150, 300], 4, window, sinks)
+
+
+def test_extend_more_queries_than_tokens():
+    """Queries at positions before the first token see nothing."""
+    c = ref.Cache([5, 0, 100], 2, 64, 16, seed=9)
+    q, out, lse = _check(c, [9, 4, 120], 4)
+    assert (out[:4] == 0).all() and torch.isneginf(lse[:4]).all()
+
+
+def test_extend_empty_sequences_and_rows_outside():
+    """Sequences without queries; rows before the first offset and behind the last stay as they were."""
+    c = ref.Cache([60, 33, 200, 10], 2, 64, 16, seed=10)
+    n = [4, 0, 90, 0]
+    q = ref.queries(c, [5] + n + [6], 4)
+    off = torch.tensor([5, 9, 9, 99, 99], dtype=torch.int32).cuda()
+    out = torch.full((105, 4, 64), 7.0, dtype=torch.bfloat16, device="cuda")
+    lse = torch.full((105, 4), 7.0, device="cuda")
+    say("ragged with outside rows")
+    fp8.kv_attention(q.cuda(), q_offsets=off, out=out, lse=lse, **c.device())
+    torch.cuda.synchronize()
+    assert (out[:5] == 7).all() and (out[99:] == 7).all() and (lse[:5] == 7).all() and (lse[99:] == 7).all()
+    ref.check_attention(c, q[5:99], n, out[5:99], lse[5:99])
+
+
+def test_extend_bad_offsets_stay_in_bounds():
+    """Offsets outside [0, total_q] are clamped: every write stays in out."""
+    c = ref.Cache([60, 33], 2, 64, 16, seed=11)
+    q = ref.queries(c, [20], 4)
+    big = torch.full((24, 4, 64), 7.0, dtype=torch.bfloat16, device="cuda")
+    for off in ([-5, 10, 900], [0, 25, 20], [20, 3, 9]):
+        say("offsets", off)
+        fp8.kv_attention(q.cuda(), q_offsets=torch.tensor(off, dtype=torch.int32).cuda(), out=big[2:22], **c.device())
+        torch.cuda.synchronize()
+        assert (big[:2] == 7).all() and (big[22:] == 7).all()
+
+
+def test_strided_queries_and_outputs():
+    """q as a slice of a packed projection, out with a row pitch."""
+    c = ref.Cache([40, 90], 2, 64, 16, seed=12)
+    for n in (1, 9):
+        q = ref.queries(c, [n, n], 4)
+        wide = torch.full((2 * n, 10, 64), float("nan"), dtype=torch.bfloat16, device="cuda")
+        wide[:, 3:7] = q.cuda()
+        out = torch.full((2 * n, 6, 64), 5.0, dtype=torch.bfloat16, device="cuda")
+        say("strided", n)
+        fp8.kv_attention(wide[:, 3:7], out=out[:, 1:5], **c.device())
+        torch.cuda.synchronize()
+        assert (out[:, 0] == 5).all() and (out[:, 5] == 5).all()
+        ref.check_attention(c, q, [n, n], out[:, 1:5], None)
+
+
+@pytest.mark.parametrize("k_st, v_st", [("e4m3", "e4m3"), ("e5m2", "e5m2"), ("bf16", "bf16")])
+@pytest.mark.parametrize("n", [1, 6, 40])
+def test_values_not_finite_where_not_seen(k_st, v_st, n):
+    """NaN and Inf in tokens a row does not see (future ones, those outside
+    the window) have no part in it; rows that see them get them."""
+    L, W, S = 200, 50, 3
+    c = ref.Cache([L], 2, 64, 16, k_st, v_st, seed=n)
+    clean = [c.v64[0].copy()]
+    bad = {"e4m3": [0x7F, 0xFF], "e5m2": [0x7C, 0xFE], "bf16": [float("inf"), float("nan")]}
+    # token 5: outside every window, no sink; token L - 1: the last query's own;
+    # token L - n: the first query's, leaves no window
+    for t, x in ((5, 0), (L - 1, 1), (L - n, 0)):
+        row = c.rows[0][t]
+        c.v[row, 0, 7] = bad[v_st][x]
+        if t == 5:
+            c.k[row, 1, :] = bad[k_st][1]
+    q, out, lse = _run(c, [n], 4, W, S)
+    c.v64 = clean
+    want = ref.attention(c, q, [n], W, S)[0]
+    o = out.double().cpu().numpy()
+    assert np.isfinite(lse.cpu().numpy()).all()
+    sees = {"last": np.arange(n) == n - 1, "first": np.ones(n, bool)}
+    hit = sees["first"] | sees["last"]                 # every row sees token L - n
+    touched = np.zeros(o.shape, bool)
+    touched[hit, :2, 7] = True
+    assert np.isfinite(o[~touched]).all()
+    assert not np.isfinite(o[touched]).any()
+    assert np.abs(o - want)[~touched].max() < 0.05 * np.abs(want).max()
+    if n > 1 and v_st != "e4m3":                       # Inf at the first token only: rows before the last hold Inf
+        assert np.isinf(o[:n - 1, :2, 7]).all()
+
+
+@pytest.mark.parametrize("n", [1, 5])
+def test_values_not_finite_where_seen(n):
+    """A NaN key gives NaN to the rows that see it and to no others."""
+    c = ref.Cache([70, 70], 2, 64, 16, seed=2)
+    c.k[c.rows[1][20], 1, 3] = 0x7F
+    q, out, lse = _run(c, [n, n], 4)
+    o = out.double().cpu().numpy()
+    assert np.isfinite(o[:n]).all() and np.isfinite(o[n:, :2]).all()
+    assert np.isnan(o[n:, 2:]).all() and np.isnan(lse.cpu().numpy()[n:, 2:]).all()
+
+
+@pytest.mark.parametrize("n", [1, 4])
+def test_large_and_equal_scores(n):
+    """Scores of several hundred (the running maximum moves a lot) and all equal ones."""
+    c = ref.Cache([513, 40], 2, 64, 16, seed=5)
+    q, out, lse = _run(c, [n, n], 4, scale=4.0)
+    ref.check_attention(c, q, [n, n], out, lse, scale=4.0)
+    q, out, lse = _run(c, [n, n], 4, scale=0.0)
+    ref.check_attention(c, q, [n, n], out, lse, scale=0.0)
+    q, out, lse = _run(c, [n, n], 4, scale=-1.0)
+    ref.check_attention(c, q, [n, n], out, lse, scale=-1.0)
+
+
+def _check_weights(cache, n, w0, got, want, delta, acc):
+    H = cache.heads
+    for b, w in enumerate(want):
+        L = cache.lens[b]
+        g = got[b].double().cpu().numpy()
+        start = w0[b].double().cpu().numpy()
+        dmax = float(delta.max()) if delta.size else 0.0
+        bound = (2 * dmax + acc + 2.0 ** -20) * (np.abs(w) + 1e-6 * n[b]) + 2.0 ** -23 * (np.abs(start[:, :L]) + w)
+        err = np.abs(g[:, :L] - start[:, :L] - w)
+        assert (err <= bound).all(), (b, err.max(), float((err / bound).max()))
+        assert np.array_equal(g[:, L:], start[:, L:])
+    assert H == got.shape[1]
+
+
+@pytest.mark.parametrize("dim", [64, 96, 128, 256])
+@pytest.mark.parametrize("k_st", ["e4m3", "e5m2", "bf16"])
+@pytest.mark.parametrize("n, window, sinks", [([1, 1, 1, 1], 0, 0), ([1, 1, 1, 1], 60, 4), ([1, 33, 200, 2], 0, 0),
+                                              ([4, 4, 4, 4], 100, 40), ([1, 33, 200, 2], 30, 2)])
+def test_weights(dim, k_st, n, window, sinks):
+    c = ref.Cache([1, 150, 400, 0], 2, dim, 16, k_st, "e4m3", seed=dim, absent=[(1, 2)])
+    w0 = torch.rand(4, 2, c.max_len + 3, generator=torch.Generator().manual_seed(5)).cuda()
+    w = w0.clone()
+    q, out, lse = _run(c, n, 6, window, sinks, weights=w)
+    want, delta, acc = ref.check_attention(c, q, n, out, lse, window, sinks)
+    _check_weights(c, n, w0, w, want, delta, acc)
+
+
+def test_weights_sum_to_the_rows():
+    """Every query head gives one in all."""
+    c = ref.Cache([300, 77], 4, 128, 16, seed=8)
+    w = torch.zeros(2, 4, c.max_len, device="cuda")
+    _run(c, [1, 1], 16, weights=w)
+    assert np.allclose(w.sum(2).cpu().numpy(), 4.0, atol=1e-4)
+    _run(c, [5, 40], 16, weights=w)
+    assert np.allclose(w.sum(2).cpu().numpy(), 4.0 + 4 * np.array([[5], [40]]), atol=1e-3)
+
+
+def test_reproducible_and_batch_independent():
+    """The same call gives the same bits; what a sequence's neighbours hold does not matter."""
+    lens = [700, 3, 2500, 41]
+    c = ref.Cache(lens, 2, 128, 16, seed=6)
+    for n in ([1] * 4, [3, 2, 70, 1]):
+        _, a, la = _run(c, n, 8)
+        _, b, lb = _run(c, n, 8)
+        assert torch.equal(a, b) and torch.equal(la, lb)
+
+
+@pytest.mark.parametrize("n", [1, 7])
+def test_captured_and_replayed(n):
+    """A graph with its own workspace, replayed between eager calls, on new queries and lengths."""
+    c = ref.Cache([1500, 90], 2, 64, 16, seed=7)
+    args = c.device()
+    q0 = ref.queries(c, [n, n], 8).cuda()
+    q = q0.clone()
+    w = torch.zeros(2, 2, c.max_len, device="cuda")
+    out = torch.empty_like(q)
+    lse = torch.empty(2 * n, 8, device="cuda")
+    ws = torch.empty(1 << 22, dtype=torch.uint8, device="cuda")
+    call = lambda o, l, ww: fp8.kv_attention(q, out=o, lse=l, weights=ww, workspace=ws, **args)  # noqa: E731
+    call(out, lse, w)
+    torch.cuda.synchronize()
+    w.zero_()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        call(out, lse, w)
+    for step in range(4):
+        q.copy_(ref.queries(c, [n, n], 8, seed=20 + step).cuda())
+        args["lens"].copy_(torch.tensor([1500 - 300 * step, 90 - 7 * step], dtype=torch.int32))
+        w.zero_()
+        say("replay", step)
+        graph.replay()
+        torch.cuda.synchronize()
+        got = out.clone(), lse.clone(), w.clone()
+        ww = torch.zeros_like(w)
+        eager = torch.empty_like(out), torch.empty_like(lse)
+        call(*eager, ww)
+        torch.cuda.synchronize()
+        assert torch.equal(got[0], eager[0]) and torch.equal(got[1], eager[1]) and torch.equal(got[2], ww)
+
+
+def test_two_streams_at_once():
+    c = ref.Cache([3000] * 4, 2, 128, 16, seed=8)
+    args = c.device()
+    qs = [ref.queries(c, [1] * 4, 8, seed=s).cuda() for s in (1, 2)]
+    want = [fp8.kv_attention(q, **args) for q in qs]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in qs]
+    got = [[], []]
+    for _ in range(5):
+        for i, s in enumerate(streams):
+            with torch.cuda.stream(s):
+                got[i].append(fp8.kv_attention(qs[i], **args))
+    torch.cuda.synchronize()
+    for i in range(2):
+        for o in got[i]:
+            assert torch.equal(o, want[i])
+
+
+def test_cache_past_2_31_elements():
+    """Offsets past 32 bits: a cache of more than 2^32 bytes, sequences at its end."""
+    heads, dim, page = 8, 128, 16
+    capacity = (1 << 32) // (heads * dim) + 4096
+    k = torch.zeros((capacity, heads, dim), dtype=torch.uint8, device="cuda")
+    v = torch.zeros_like(k)
+    ks = torch.ones((capacity, heads), device="cuda")
+    small = ref.Cache([200, 90], heads, dim, page, seed=9)
+    first = capacity - small.capacity
+    first -= first % page
+    k[first:first + small.capacity] = small.k.cuda()
+    v[first:first + small.capacity] = small.v.cuda()
+    ks[first:first + small.capacity] = small.ks.cuda()
+    vs = torch.ones_like(ks)
+    vs[first:first + small.capacity] = small.vs.cuda()
+    table = torch.from_numpy(small.table + first // page).cuda()
+    lens = torch.tensor(small.lens, dtype=torch.int32).cuda()
+    for n in ([1, 1], [9, 30]):
+        q = ref.queries(small, n, 16)
+        off = torch.tensor([0, n[0], sum(n)], dtype=torch.int32).cuda() if n[0] > 1 else None
+        w = torch.zeros(2, heads, small.max_len, device="cuda")
+        say("long cache", n)
+        out, lse = fp8.kv_attention(q.cuda(), k, v, table, lens, page, ks, vs, q_offsets=off, weights=w,
+                                    return_lse=True)
+        torch.cuda.synchronize()
+        ref.check_attention(small, q, n, out, lse)
+
+
+def test_refusals():
+    c = ref.Cache([40, 20], 2, 64, 16, seed=1)
+    args = c.device()
+    q = ref.queries(c, [1, 1], 4).cuda()
+
+    def refused(exc, match, qq=q, **change):
+        with pytest.raises(exc, match=match):
+            fp8.kv_attention(qq, **{**args, **change})
+
+    refused(TypeError, "bfloat16", q.float())
+    refused(ValueError, r"\[n, heads, 64\]", q[:, :, :32].contiguous())
+    refused(fp8.Fp8Error, "multiple of heads", q[:, :3])
+    refused(ValueError, "packed heads", q.transpose(0, 1).contiguous().transpose(0, 1))
+    refused(ValueError, "page_table", page_table=args["page_table"].long())
+    refused(TypeError, "lens", lens=args["lens"].long())
+    refused(ValueError, "lens", lens=args["lens"][:1])
+    refused(fp8.Fp8Error, "power of two", page_size=12)
+    refused(ValueError, "max_len", max_len=1000)
+    refused(fp8.Fp8Error, "window", window=-1)
+    refused(fp8.Fp8Error, "multiple of batch", torch.cat([q, q[:1]]))
+    refused(TypeError, "q_offsets", q_offsets=torch.tensor([0, 1, 2]).cuda())
+    refused(ValueError, "weights", weights=torch.zeros(2, 2, 5).cuda())
+    refused(ValueError, "weights", weights=torch.zeros(2, 4, 60).cuda()[:, ::2, :].transpose(1, 2))
+    refused(ValueError, "v_cache", v_storage="bf16")
+    refused(fp8.Fp8Error, "scale_inv is NULL", k_scale_inv=None)
+    refused(fp8.Fp8Error, "finite", scale=float("nan"))
+    refused(fp8.Fp8Error, "16-byte aligned", q.new_zeros(4 * 128 + 1)[1:].view(2, 4, 64))
+    long = ref.Cache([5000, 20], 2, 64, 16, seed=1)
+    with pytest.raises(fp8.Fp8Error, match="workspace_bytes"):
+        fp8.kv_attention(q, workspace=torch.empty(64, dtype=torch.uint8, device="cuda"), **long.device())
