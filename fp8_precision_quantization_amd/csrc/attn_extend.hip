@@ -20,10 +20,11 @@
 // LDS rows are padded (K by 16 bytes, V by 32) so that the 16-byte reads of
 // 8 K rows, and the transposing reads of 4 V rows, fall into different banks.
 //
-// Values that are not finite in V: a product with weight 0 would turn a token
-// that one row does not see into NaN for that row.  Staging takes such values
-// out of the tile and notes the token; the block then adds them by hand to
-// the rows that do see it.
+// Values of V that are not finite (and tokens whose V scale is not): a product
+// with weight 0 would turn a token that one row does not see into NaN for that
+// row.  Staging puts 0 in their place and marks the step; a block that met one
+// goes over its marked steps once more at the end and adds these values, row
+// by row, to the rows that see them.
 //
 // k_weights.  weights[b, h, j] += sum over the rows of 2^(x_ij - lse_i): a
 // block owns 128 tokens of a (sequence, KV head) with their K in registers
@@ -42,11 +43,13 @@ constexpr int kStep = 64;        // cached tokens of one step
 constexpr int kWaves = 4;
 constexpr int kThreads = 64 * kWaves;
 constexpr int kRows = 32 * kWaves;
+constexpr int kMarks = 1024;
 
 struct ExtendParams {
     KvView kv;
     const uint16_t* q;
-    int64_t ldq, total_q;
+    int64_t ldq;
+    int total_q, each;           // each: queries of every sequence without q_offsets
     int q_heads, group;
     const int32_t* q_offsets;
     float scale_log2;
@@ -59,31 +62,23 @@ struct ExtendParams {
 };
 
 // Queries of sequence b: the first and their number, inside [0, total_q].
-__device__ __forceinline__ void queries_of(const ExtendParams& a, int b, int64_t* first, int* n) {
+__device__ __forceinline__ void queries_of(const ExtendParams& a, int b, int* first, int* n) {
     if (a.q_offsets == nullptr) {
-        const int64_t each = a.total_q / a.kv.batch;
-        *first = b * each;
-        *n = (int)each;
+        *first = b * a.each;
+        *n = a.each;
     } else {
-        int64_t lo = a.q_offsets[b], hi = a.q_offsets[b + 1];
-        lo = lo < 0 ? 0 : lo > a.total_q ? a.total_q : lo;
-        hi = hi < lo ? lo : hi > a.total_q ? a.total_q : hi;
+        const int lo = min(max(a.q_offsets[b], 0), a.total_q), hi = min(max(a.q_offsets[b + 1], lo), a.total_q);
         *first = lo;
-        *n = (int)(hi - lo);
+        *n = hi - lo;
     }
 }
 
 // Slot of the first row tile of sequence b when a sequence's tiles start at
 // floor(first row / kRows) + b: increasing in b, and no two sequences share a
 // slot, without a prefix sum over the sequences.
-__device__ __forceinline__ int64_t first_slot(const ExtendParams& a, int b) {
-    if (a.q_offsets == nullptr) {
-        const int64_t each = a.total_q / a.kv.batch;
-        return b * ((each * a.group + kRows - 1) / kRows);
-    }
-    int64_t lo = a.q_offsets[b];
-    lo = lo < 0 ? 0 : lo > a.total_q ? a.total_q : lo;
-    return lo * a.group / kRows + b;
+__device__ __forceinline__ int first_slot(const ExtendParams& a, int b) {
+    if (a.q_offsets == nullptr) return b * ((a.each * a.group + kRows - 1) / kRows);
+    return min(max(a.q_offsets[b], 0), a.total_q) * a.group / kRows + b;
 }
 
 template <int DP>
@@ -97,7 +92,7 @@ struct Lds {
     };
     Buf buf[2];
     alignas(16) int row[3][kStep];
-    uint64_t bad[3];
+    uint32_t bad[kMarks / 32];      // step i marks bit i % kMarks
 };
 
 // Words of w that hold a value that is not finite, and the same words with
@@ -188,32 +183,31 @@ __global__ __launch_bounds__(kThreads, DP <= 128 ? 2 : 1) void k_extend(const Ex
     const int c = lane & 31, g = lane >> 5;
     const int h = blockIdx.x % kv.heads;
     // the sequence whose slots hold this tile; later (longer) tiles first
-    const int64_t slot = (int64_t)gridDim.x / kv.heads - 1 - blockIdx.x / kv.heads;
+    const int slot = (int)(gridDim.x / kv.heads - 1 - blockIdx.x / kv.heads);
     int b = 0;
     for (int hi = kv.batch; hi - b > 1;) {
         const int mid = (b + hi) >> 1;
         if (first_slot(a, mid) <= slot) b = mid; else hi = mid;
     }
-    int64_t q_first;
-    int n;
+    int q_first, n;
     queries_of(a, b, &q_first, &n);
-    const int64_t row0 = (slot - first_slot(a, b)) * kRows, rows = (int64_t)n * a.group;
+    const int row0 = (slot - first_slot(a, b)) * kRows, rows = n * a.group;
     if (row0 < 0 || row0 >= rows) return;
 
     const int len = seq_len(kv, b), base = len - n;
     const int G = a.group, D = kv.head_dim;
-    const int r_last = (int)min(row0 + kRows, rows) - 1;
-    const int p_first = base + (int)row0 / G, p_last = base + r_last / G;
+    const int r_last = min(row0 + kRows, rows) - 1;
+    const int p_first = base + row0 / G, p_last = base + r_last / G;
     const Steps<kStep> steps(p_first, p_last, a.window, a.sinks);
 
     // this lane's row
-    const int r = (int)row0 + wave * 32 + c;
+    const int r = row0 + wave * 32 + c;
     const bool live = r < rows;
     const int tok = r / G, hq = h * G + (r - tok * G);
     const int pos = live ? base + tok : -1;
     b8 qf[KM];
     {
-        const uint16_t* qr = a.q + (q_first + tok) * a.ldq + (int64_t)hq * D;
+        const uint16_t* qr = a.q + (int64_t)(q_first + tok) * a.ldq + (int64_t)hq * D;
 #pragma unroll
         for (int s = 0; s < KM; ++s) {
             uint4 t = make_uint4(0, 0, 0, 0);
@@ -268,20 +262,25 @@ __global__ __launch_bounds__(kThreads, DP <= 128 ? 2 : 1) void k_extend(const Ex
             }
         }
     };
+    auto mark = [&](int i) { atomicOr(&lds.bad[i % kMarks / 32], 1u << (i % 32)); };
     auto put = [&](int i) {                     // the registers into a step's LDS buffer
         typename L::Buf& buf = lds.buf[i & 1];
 #pragma unroll
         for (int u = 0; u < UT; ++u) {
             const int t = (tid + u * kThreads) / UR, e = (tid + u * kThreads) % UR;
-            if (vu[u].clean()) atomicOr(reinterpret_cast<unsigned long long*>(&lds.bad[i % 3]), 1ull << t);
+            if (vu[u].clean()) mark(i);
             ku[u].put(buf.k + t * L::kK + e * 32);
             vu[u].put(buf.v + t * L::kV + e * 32);
+        }
+        if (tid >= kStep && tid < 2 * kStep && !__builtin_isfinite(sc)) {
+            sc = 0.0f;
+            mark(i);
         }
         if (tid < 2 * kStep) (tid < kStep ? buf.ks : buf.vs)[tid & (kStep - 1)] = sc;
     };
 
     if (steps.count > 0) {
-        if (tid < 3) lds.bad[tid] = 0;
+        if (tid < kMarks / 32) lds.bad[tid] = 0;
         put_row(0, entry_of(0));
         put_row(1, entry_of(1));
         __syncthreads();
@@ -302,7 +301,6 @@ __global__ __launch_bounds__(kThreads, DP <= 128 ? 2 : 1) void k_extend(const Ex
             x[t] = f16v{0};
 #pragma unroll
             for (int s = 0; s < KM; ++s) {
-                if (DP > 64 && s * 16 >= D) break;
                 const b8 kf = *reinterpret_cast<const b8*>(buf.k + (t * 32 + c) * L::kK + s * 32 + g * 16);
                 x[t] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(kf, qf[s], x[t], 0, 0, 0);
             }
@@ -344,10 +342,8 @@ __global__ __launch_bounds__(kThreads, DP <= 128 ? 2 : 1) void k_extend(const Ex
 #pragma unroll
             for (int d = 0; d < DT; ++d) o[d] *= f;
         }
-        b8 pf[4];
-        const uint64_t bad = lds.bad[i % 3];
 #pragma unroll
-        for (int t = 0; t < 2; ++t) {
+        for (int t = 0; t < 2; ++t)
 #pragma unroll
             for (int u = 0; u < 4; ++u) {
                 const f4 vs = *reinterpret_cast<const f4*>(&buf.vs[t * 32 + u * 8 + g * 4]);
@@ -355,43 +351,20 @@ __global__ __launch_bounds__(kThreads, DP <= 128 ? 2 : 1) void k_extend(const Ex
                 for (int e = 0; e < 4; ++e) {
                     const float w = __builtin_amdgcn_exp2f(x[t][u * 4 + e] - m);
                     l += w;
-                    // a scale of a row that is not there, or not seen, multiplies nothing
-                    x[t][u * 4 + e] = x[t][u * 4 + e] == -INFINITY ? 0.0f : w * vs[e];
+                    x[t][u * 4 + e] = w * vs[e];
                 }
             }
+        b8 pf[4];
 #pragma unroll
-            for (int u = 0; u < 2; ++u) {
-                u4 w;
+        for (int t = 0; t < 4; ++t) {
+            u4 w;
 #pragma unroll
-                for (int e = 0; e < 4; ++e) w[e] = pack2(x[t][u * 8 + 2 * e], x[t][u * 8 + 2 * e + 1]);
-                pf[t * 2 + u] = __builtin_bit_cast(b8, w);
-            }
-        }
-        if (bad) {                              // values of V taken out of the tile
-            for (uint64_t left = bad; left; left &= left - 1) {
-                const int t = __builtin_ctzll(left), reg = (t >> 5) * 16 + ((t & 31) >> 3) * 4 + (t & 3);
-                float w = 0.0f;
-#pragma unroll
-                for (int e = 0; e < 32; ++e) w = e == reg ? x[e >> 4][e & 15] : w;
-                w = __shfl(w, c + 32 * ((t >> 2) & 1), 64);
-                if (sees(j0 + t, pos, a.window, a.sinks)) {
-                    const uint8_t* vr = vb + rows_i[t] * v_row;
-#pragma unroll
-                    for (int d = 0; d < DT; ++d)
-#pragma unroll
-                        for (int e = 0; e < 16; ++e) {
-                            const int ch = d * 32 + (e >> 2) * 8 + g * 4 + (e & 3);
-                            if (ch < D) {
-                                const float v = value_at<VST>(vr, ch);
-                                if (!__builtin_isfinite(v)) o[d][e] += w * v;
-                            }
-                        }
-                }
-            }
+            for (int e = 0; e < 4; ++e)
+                w[e] = pack2(x[t >> 1][(t & 1) * 8 + 2 * e], x[t >> 1][(t & 1) * 8 + 2 * e + 1]);
+            pf[t] = __builtin_bit_cast(b8, w);
         }
 #pragma unroll
         for (int d = 0; d < DT; ++d) {
-            if (DP > 64 && d * 32 >= D) break;
 #pragma unroll
             for (int t = 0; t < 4; ++t) {
                 // lane i of 16 points at row i / 4, channels 4 (i % 4).. of a
@@ -406,14 +379,48 @@ __global__ __launch_bounds__(kThreads, DP <= 128 ? 2 : 1) void k_extend(const Ex
         }
         if (more) put(i + 1);
         put_row(i + 2, entry);
-        if (tid == 0) lds.bad[(i + 2) % 3] = 0;
         __syncthreads();
     }
 
     l = sum_xor32(l);
+    uint32_t met = 0;
+    if (steps.count > 0 && lane < kMarks / 32) met = lds.bad[lane];
+    if (__any(met != 0)) {
+        for (int i = 0; i < steps.count; ++i) {
+            if (!(lds.bad[i % kMarks / 32] >> (i % 32) & 1)) continue;
+            for (int j = steps.token(i); j < steps.token(i) + kStep && j <= p_last; ++j) {
+                const int row = row_of_entry(kv, table[j >> kv.page_shift], j);
+                if (row < 0) continue;
+                const uint8_t* vr = vb + row * v_row;
+                const float s = v_tok ? kv.v_scale[(int64_t)row * kv.heads + h] : v_head;
+                bool odd = !__builtin_isfinite(s);
+                for (int d = lane; d < D; d += 64) odd = odd || !__builtin_isfinite(value_at<VST>(vr, d));
+                if (!__any(odd)) continue;
+                // the token's score for this lane's row
+                const uint8_t* kr = kb + row * k_row;
+                const uint16_t* qr = a.q + (int64_t)(q_first + tok) * a.ldq + (int64_t)hq * D;
+                float x = 0.0f;
+                if (live)
+                    for (int d = 0; d < D; ++d) x += value_at<KST>(kr, d) * as_f32((uint32_t)qr[d] << 16);
+                x *= k_head * (k_tok ? kv.k_scale[(int64_t)row * kv.heads + h] : 1.0f);
+                const float w = __builtin_amdgcn_exp2f(x - m);
+                if (!sees(j, pos, a.window, a.sinks)) continue;
+#pragma unroll
+                for (int d = 0; d < DT; ++d)
+#pragma unroll
+                    for (int e = 0; e < 16; ++e) {
+                        const int ch = d * 32 + (e >> 2) * 8 + g * 4 + (e & 3);
+                        if (ch < D) {
+                            const float v = value_at<VST>(vr, ch);
+                            if (!__builtin_isfinite(v) || !__builtin_isfinite(s)) o[d][e] += w * (v * s);
+                        }
+                    }
+            }
+        }
+    }
     if (!live) return;
     const float inv = l == 0.0f ? 0.0f : 1.0f / l;
-    uint16_t* to = a.out + (q_first + tok) * a.ldo + (int64_t)hq * D;
+    uint16_t* to = a.out + (int64_t)(q_first + tok) * a.ldo + (int64_t)hq * D;
 #pragma unroll
     for (int d = 0; d < DT; ++d)
 #pragma unroll
@@ -425,7 +432,7 @@ __global__ __launch_bounds__(kThreads, DP <= 128 ? 2 : 1) void k_extend(const Ex
                                pack2(o[d][u * 4 + 2] * inv, o[d][u * 4 + 3] * inv));
         }
     if (g == 0 && a.lse)
-        a.lse[(q_first + tok) * a.q_heads + hq] = l == 0.0f ? -INFINITY : (m + __builtin_amdgcn_logf(l)) * kLn2;
+        a.lse[(int64_t)(q_first + tok) * a.q_heads + hq] = l == 0.0f ? -INFINITY : (m + __builtin_amdgcn_logf(l)) * kLn2;
 }
 
 // Weights: a wave holds 32 tokens' K as the A operand and takes the rows 32
@@ -441,8 +448,7 @@ __global__ __launch_bounds__(kThreads) void k_weights(const ExtendParams a) {
     const int len = seq_len(kv, b);
     const int j0 = (int)(blockIdx.x / kv.heads) * kRows + wave * 32;
     if (j0 >= len) return;
-    int64_t q_first;
-    int n;
+    int q_first, n;
     queries_of(a, b, &q_first, &n);
     const int G = a.group, D = kv.head_dim, base = len - n;
 
@@ -500,7 +506,7 @@ __global__ __launch_bounds__(kThreads) void k_weights(const ExtendParams a) {
         const int r = r0 + c;
         const bool live = r < r_end;
         const int tok = r / G, hq = h * G + (r - tok * G);
-        const uint16_t* qr = a.q + (q_first + tok) * a.ldq + (int64_t)hq * D;
+        const uint16_t* qr = a.q + (int64_t)(q_first + tok) * a.ldq + (int64_t)hq * D;
         f16v x = f16v{0};
 #pragma unroll
         for (int s = 0; s < KM; ++s) {
@@ -509,7 +515,7 @@ __global__ __launch_bounds__(kThreads) void k_weights(const ExtendParams a) {
             if (live && e < D) t = *reinterpret_cast<const uint4*>(qr + e);
             x = __builtin_amdgcn_mfma_f32_32x32x16_bf16(kf[s], __builtin_bit_cast(b8, t), x, 0, 0, 0);
         }
-        const float lse = live ? a.lse[(q_first + tok) * a.q_heads + hq] * kLog2e : -INFINITY;
+        const float lse = live ? a.lse[(int64_t)(q_first + tok) * a.q_heads + hq] * kLog2e : -INFINITY;
         const int pos = lse == -INFINITY ? -1 : base + tok;     // a row that sees nothing gives nothing
 #pragma unroll
         for (int e = 0; e < 16; ++e) {
@@ -535,9 +541,9 @@ hipError_t run_extend(const ExtendParams& p, hipStream_t stream) {
     hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(&k_extend<KST, VST, DP>),
                                        hipFuncAttributeMaxDynamicSharedMemorySize, bytes);
     if (e != hipSuccess) return e;
-    int64_t tiles;
-    if (p.q_offsets == nullptr) tiles = p.kv.batch * ((p.total_q / p.kv.batch * p.group + kRows - 1) / kRows);
-    else tiles = p.total_q * p.group / kRows + p.kv.batch;
+    // total_q * q_heads < 2^31: a tile count is far inside int
+    const int tiles = p.q_offsets == nullptr ? p.kv.batch * ((p.each * p.group + kRows - 1) / kRows)
+                                             : p.total_q * p.group / kRows + p.kv.batch;
     hipLaunchKernelGGL((k_extend<KST, VST, DP>), dim3((unsigned)(tiles * p.kv.heads)), dim3(kThreads), bytes, stream,
                        p);
     return hipGetLastError();
@@ -571,7 +577,7 @@ hipError_t weights_dim(const ExtendParams& p, hipStream_t stream) {
 
 ExtendParams params_of(const AttnArgs& a) {
     ExtendParams p;
-    p.kv = a.kv; p.q = a.q; p.ldq = a.ldq; p.total_q = a.total_q; p.q_heads = a.q_heads;
+    p.kv = a.kv; p.q = a.q; p.ldq = a.ldq; p.total_q = (int)a.total_q; p.each = (int)(a.total_q / a.kv.batch); p.q_heads = a.q_heads;
     p.group = a.q_heads / a.kv.heads; p.q_offsets = a.q_offsets; p.scale_log2 = a.scale * kLog2e;
     p.window = a.window; p.sinks = a.sinks; p.out = a.out; p.ldo = a.ldo; p.lse = a.lse;
     p.weights = a.weights; p.ldw = a.ldw;

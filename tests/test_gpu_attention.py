@@ -420,3 +420,25 @@ def test_refusals():
     long = ref.Cache([5000, 20], 2, 64, 16, seed=1)
     with pytest.raises(fp8.Fp8Error, match="workspace_bytes"):
         fp8.kv_attention(q, workspace=torch.empty(64, dtype=torch.uint8, device="cuda"), **long.device())
+
+
+@pytest.mark.parametrize("n", [1, 6, 40])
+def test_scales_not_finite_where_not_seen(n):
+    """A NaN or Inf V (or K) scale of a token outside the window has no part
+    in the rows that do not see it; rows that see a NaN scale are NaN."""
+    L, W, S = 200, 50, 3
+    c = ref.Cache([L], 2, 64, 16, seed=n)
+    clean = [c.v64[0].copy()]
+    c.vs[c.rows[0][9], 0] = float("nan")
+    c.ks[c.rows[0][10], 0] = float("inf")
+    c.vs[c.rows[0][L - 1], 1] = float("inf")           # seen by the last query alone
+    q, out, lse = _run(c, [n], 4, W, S)
+    o = out.double().cpu().numpy()
+    c.v64 = clean
+    want = ref.attention(c, q, [n], W, S)[0]
+    assert np.isfinite(lse.cpu().numpy()).all()
+    assert np.isfinite(o[:, :2]).all() and np.isfinite(o[:n - 1]).all()
+    assert not np.isfinite(o[n - 1, 2:]).any()
+    touched = np.zeros(o.shape, bool)
+    touched[n - 1, 2:] = True
+    assert np.abs(o - want)[~touched].max() < 0.05 * np.abs(want).max()
