@@ -17,8 +17,8 @@
 // rounded once to bf16 (relative error 2^-8 at most, each token its own, so
 // the sum's is smaller than the output's own bf16 rounding).
 //
-// LDS rows are padded (K by 16 bytes, V by 32) so that the 16-byte reads of
-// 8 K rows, and the transposing reads of 4 V rows, fall into different banks.
+// LDS rows are padded (K by 16 bytes, V by 64) so that the 16-byte reads of
+// 16 K rows, and the transposing reads of 4 V rows, fall into different banks.
 //
 // Values of V that are not finite (and tokens whose V scale is not): a product
 // with weight 0 would turn a token that one row does not see into NaN for that
@@ -83,7 +83,7 @@ __device__ __forceinline__ int first_slot(const ExtendParams& a, int b) {
 
 template <int DP>
 struct Lds {
-    static constexpr int kK = DP * 2 + 16, kV = DP * 2 + 32;     // bytes of a padded row
+    static constexpr int kK = DP * 2 + 16, kV = DP * 2 + 64;     // bytes of a padded row
     struct Buf {
         alignas(16) uint8_t k[kStep * kK];
         alignas(16) uint8_t v[kStep * kV];
@@ -214,6 +214,9 @@ __global__ __launch_bounds__(kThreads, DP <= 128 ? 2 : 1) void k_extend(const Ex
             if (live && s * 16 < D) t = *reinterpret_cast<const uint4*>(qr + s * 16 + g * 8);
             qf[s] = __builtin_bit_cast(b8, t);
         }
+        // arrived before the loop, which then waits for no load of its own step
+#pragma unroll
+        for (int s = 0; s < KM; ++s) asm volatile("" : "+v"(qf[s]));
     }
     f16v o[DT];
 #pragma unroll
@@ -295,14 +298,30 @@ __global__ __launch_bounds__(kThreads, DP <= 128 ? 2 : 1) void k_extend(const Ex
         const typename L::Buf& buf = lds.buf[i & 1];
         const int j0 = steps.token(i);
 
+        // Both products run their LDS reads two matrix steps ahead; the
+        // scheduling barriers keep the compiler from packing reads and
+        // products back together when registers are short.
+        const int* rows_i = lds.row[i % 3];
+        const bool there = rows_i[lane] >= 0;
         f16v x[2];
+        x[0] = f16v{0};
+        x[1] = f16v{0};
+        {
+            b8 kf[3][2];
+            auto read_k = [&](int s) {
 #pragma unroll
-        for (int t = 0; t < 2; ++t) {
-            x[t] = f16v{0};
+                for (int t = 0; t < 2; ++t)
+                    kf[s % 3][t] = *reinterpret_cast<const b8*>(buf.k + (t * 32 + c) * L::kK + s * 32 + g * 16);
+            };
+            read_k(0);
+            read_k(1);
 #pragma unroll
             for (int s = 0; s < KM; ++s) {
-                const b8 kf = *reinterpret_cast<const b8*>(buf.k + (t * 32 + c) * L::kK + s * 32 + g * 16);
-                x[t] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(kf, qf[s], x[t], 0, 0, 0);
+                if (s + 2 < KM) read_k(s + 2);
+                __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+                for (int t = 0; t < 2; ++t)
+                    x[t] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(kf[s % 3][t], qf[s], x[t], 0, 0, 0);
             }
         }
 #pragma unroll
@@ -311,12 +330,11 @@ __global__ __launch_bounds__(kThreads, DP <= 128 ? 2 : 1) void k_extend(const Ex
             for (int u = 0; u < 4; ++u) {
                 const f4 ks = *reinterpret_cast<const f4*>(&buf.ks[t * 32 + u * 8 + g * 4]);
 #pragma unroll
-                for (int e = 0; e < 4; ++e) x[t][u * 4 + e] *= ks[e];
+                for (int e = 0; e < 4; ++e) x[t][u * 4 + e] *= KST == kBf16 ? a.scale_log2 : ks[e];
             }
-        const int* rows_i = lds.row[i % 3];
         const bool edge = j0 + kStep - 1 > p_first ||
                           (a.window > 0 && j0 <= p_last - a.window && j0 + kStep - 1 >= a.sinks);
-        if (edge || !__all(rows_i[lane] >= 0)) {
+        if (edge || !__all(there)) {
 #pragma unroll
             for (int t = 0; t < 2; ++t)
 #pragma unroll
@@ -363,18 +381,32 @@ __global__ __launch_bounds__(kThreads, DP <= 128 ? 2 : 1) void k_extend(const Ex
                 w[e] = pack2(x[t >> 1][(t & 1) * 8 + 2 * e], x[t >> 1][(t & 1) * 8 + 2 * e + 1]);
             pf[t] = __builtin_bit_cast(b8, w);
         }
+        {
+            // V^T of matrix step n: tokens of group n % 4, channels of the
+            // tiles 2 (n / 4) and 2 (n / 4) + 1.  Lane i of 16 points at row
+            // i / 4, channels 4 (i % 4).. of a 4 x 16 block and receives its
+            // column i.
+            b8 vf[3][2];
+            const uint8_t* vp = buf.v + (g * 4 + ((lane & 15) >> 2)) * L::kV + (((lane >> 4) & 1) * 16 + (lane & 3) * 4) * 2;
+            auto read_v = [&](int n) {
 #pragma unroll
-        for (int d = 0; d < DT; ++d) {
+                for (int d = 0; d < 2; ++d) {
+                    const uint8_t* p = vp + (n & 3) * 16 * L::kV + ((n >> 2) * 2 + d) * 64;
+                    const s4 lo = read_tr(p), hi = read_tr(p + 8 * L::kV);
+                    vf[n % 3][d] = __builtin_bit_cast(b8, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
+                }
+            };
+            read_v(0);
+            read_v(1);
 #pragma unroll
-            for (int t = 0; t < 4; ++t) {
-                // lane i of 16 points at row i / 4, channels 4 (i % 4).. of a
-                // 4 x 16 block and receives its column i
-                const uint8_t* p = buf.v + (t * 16 + g * 4 + ((lane & 15) >> 2)) * L::kV +
-                                   (d * 32 + ((lane >> 4) & 1) * 16 + (lane & 3) * 4) * 2;
-                const s4 lo = read_tr(p), hi = read_tr(p + 8 * L::kV);
-                typedef short s8 __attribute__((ext_vector_type(8)));
-                const s8 w = __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
-                o[d] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(b8, w), pf[t], o[d], 0, 0, 0);
+            for (int n = 0; n < 2 * DT; ++n) {
+                if (n + 2 < 2 * DT) read_v(n + 2);
+                __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+                for (int d = 0; d < 2; ++d) {
+                    f16v& to = o[(n >> 2) * 2 + d];
+                    to = __builtin_amdgcn_mfma_f32_32x32x16_bf16(vf[n % 3][d], pf[n & 3], to, 0, 0, 0);
+                }
             }
         }
         if (more) put(i + 1);
