@@ -146,8 +146,8 @@ struct Unit {
         }
         return any != 0;
     }
-    // as bf16 into LDS (32 bytes)
-    __device__ __forceinline__ void put(uint8_t* to) const {
+    // as bf16 into LDS: two pieces of 16 bytes, `apart` bytes from each other
+    __device__ __forceinline__ void put(uint8_t* to, int apart) const {
         uint4 a, b;
         if constexpr (ST == kBf16) {
             a = w[0];
@@ -158,10 +158,18 @@ struct Unit {
             b = make_uint4(decode2<ST>(w[0].z, false), decode2<ST>(w[0].z, true), decode2<ST>(w[0].w, false),
                            decode2<ST>(w[0].w, true));
         }
-        reinterpret_cast<uint4*>(to)[0] = a;
-        reinterpret_cast<uint4*>(to)[1] = b;
+        *reinterpret_cast<uint4*>(to) = a;
+        *reinterpret_cast<uint4*>(to + apart) = b;
     }
 };
+
+// First channel of piece p (8 channels) of an LDS row: the even pieces of the
+// row come first, then the odd ones, so that the lanes that stage a row write
+// 16 bytes next to each other.  Q and the output follow the same order.
+template <int DP>
+__device__ __forceinline__ constexpr int channel_of(int p) {
+    return p < DP / 16 ? p * 16 : (p - DP / 16) * 16 + 8;
+}
 
 typedef short s4 __attribute__((ext_vector_type(4)));
 __device__ __forceinline__ s4 read_tr(const uint8_t* p) {
@@ -211,7 +219,8 @@ __global__ __launch_bounds__(kThreads, DP <= 128 ? 2 : 1) void k_extend(const Ex
 #pragma unroll
         for (int s = 0; s < KM; ++s) {
             uint4 t = make_uint4(0, 0, 0, 0);
-            if (live && s * 16 < D) t = *reinterpret_cast<const uint4*>(qr + s * 16 + g * 8);
+            const int e = channel_of<DP>(2 * s) + g * (channel_of<DP>(2 * s + 1) - channel_of<DP>(2 * s));
+            if (live && e < D) t = *reinterpret_cast<const uint4*>(qr + e);
             qf[s] = __builtin_bit_cast(b8, t);
         }
         // arrived before the loop, which then waits for no load of its own step
@@ -221,7 +230,7 @@ __global__ __launch_bounds__(kThreads, DP <= 128 ? 2 : 1) void k_extend(const Ex
     f16v o[DT];
 #pragma unroll
     for (int i = 0; i < DT; ++i) o[i] = f16v{0};
-    float m = kLowest, l = 0.0f;
+    float m = 0.0f, l = 0.0f, limit = kLowest;      // limit: where the row's reference moves
 
     const int64_t k_row = (int64_t)kv.heads * D * kElemBytes<KST>, v_row = (int64_t)kv.heads * D * kElemBytes<VST>;
     const uint8_t* kb = static_cast<const uint8_t*>(kv.k) + (int64_t)h * D * kElemBytes<KST>;
@@ -272,8 +281,8 @@ __global__ __launch_bounds__(kThreads, DP <= 128 ? 2 : 1) void k_extend(const Ex
         for (int u = 0; u < UT; ++u) {
             const int t = (tid + u * kThreads) / UR, e = (tid + u * kThreads) % UR;
             if (vu[u].clean()) mark(i);
-            ku[u].put(buf.k + t * L::kK + e * 32);
-            vu[u].put(buf.v + t * L::kV + e * 32);
+            ku[u].put(buf.k + t * L::kK + e * 16, UR * 16);
+            vu[u].put(buf.v + t * L::kV + e * 16, UR * 16);
         }
         if (tid >= kStep && tid < 2 * kStep && !__builtin_isfinite(sc)) {
             sc = 0.0f;
@@ -324,13 +333,15 @@ __global__ __launch_bounds__(kThreads, DP <= 128 ? 2 : 1) void k_extend(const Ex
                     x[t] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(kf[s % 3][t], qf[s], x[t], 0, 0, 0);
             }
         }
+        // scores against the row's reference m (0 until the row has seen a token)
 #pragma unroll
         for (int t = 0; t < 2; ++t)
 #pragma unroll
             for (int u = 0; u < 4; ++u) {
-                const f4 ks = *reinterpret_cast<const f4*>(&buf.ks[t * 32 + u * 8 + g * 4]);
+                f4 ks = f4{a.scale_log2, a.scale_log2, a.scale_log2, a.scale_log2};
+                if (KST != kBf16) ks = *reinterpret_cast<const f4*>(&buf.ks[t * 32 + u * 8 + g * 4]);
 #pragma unroll
-                for (int e = 0; e < 4; ++e) x[t][u * 4 + e] *= KST == kBf16 ? a.scale_log2 : ks[e];
+                for (int e = 0; e < 4; ++e) x[t][u * 4 + e] = __builtin_fmaf(x[t][u * 4 + e], ks[e], -m);
             }
         const bool edge = j0 + kStep - 1 > p_first ||
                           (a.window > 0 && j0 <= p_last - a.window && j0 + kStep - 1 >= a.sinks);
@@ -347,31 +358,45 @@ __global__ __launch_bounds__(kThreads, DP <= 128 ? 2 : 1) void k_extend(const Ex
                         if (ra[e] < 0 || !sees(j0 + at + e, pos, a.window, a.sinks)) x[t][u * 4 + e] = -INFINITY;
                 }
         }
-        float mx = kLowest;
+        float mx = -INFINITY;
 #pragma unroll
         for (int t = 0; t < 2; ++t)
 #pragma unroll
             for (int e = 0; e < 16; ++e) mx = fmaxf(mx, x[t][e]);
-        if (__any(mx > m + kSlack)) {
-            const float mn = fmaxf(m, max_xor32(mx));
-            const float f = __builtin_amdgcn_exp2f(m - mn);
-            m = mn;
+        if (__any(mx > limit)) {
+            mx = max_xor32(mx);
+            const float up = mx > limit ? mx : 0.0f;
+            const float f = limit == kLowest ? 1.0f : __builtin_amdgcn_exp2f(-up);  // before the first: o, l are 0
+            limit = mx > limit ? kSlack : limit;
+            m += up;
             l *= f;
 #pragma unroll
-            for (int d = 0; d < DT; ++d) o[d] *= f;
+            for (int t = 0; t < 2; ++t)
+#pragma unroll
+                for (int e = 0; e < 16; ++e) x[t][e] -= up;
+            if (i > 0) {
+#pragma unroll
+                for (int d = 0; d < DT; ++d)
+#pragma unroll
+                    for (int e = 0; e < 16; ++e) o[d][e] = o[d][e] * f;
+            }
         }
+        float part[4] = {0, 0, 0, 0};
 #pragma unroll
         for (int t = 0; t < 2; ++t)
 #pragma unroll
             for (int u = 0; u < 4; ++u) {
-                const f4 vs = *reinterpret_cast<const f4*>(&buf.vs[t * 32 + u * 8 + g * 4]);
+                f4 vs = f4{1, 1, 1, 1};
+                if (VST != kBf16) vs = *reinterpret_cast<const f4*>(&buf.vs[t * 32 + u * 8 + g * 4]);
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
-                    const float w = __builtin_amdgcn_exp2f(x[t][u * 4 + e] - m);
-                    l += w;
-                    x[t][u * 4 + e] = w * vs[e];
+                    const float w = __builtin_amdgcn_exp2f(x[t][u * 4 + e]);
+                    part[e] += w;
+                    x[t][u * 4 + e] = VST == kBf16 ? w : w * vs[e];
                 }
             }
+        l += (part[0] + part[1]) + (part[2] + part[3]);
+        asm volatile("" : "+v"(l));             // here, so that no weight has to stay for it
         b8 pf[4];
 #pragma unroll
         for (int t = 0; t < 4; ++t) {
@@ -441,7 +466,7 @@ __global__ __launch_bounds__(kThreads, DP <= 128 ? 2 : 1) void k_extend(const Ex
                 for (int d = 0; d < DT; ++d)
 #pragma unroll
                     for (int e = 0; e < 16; ++e) {
-                        const int ch = d * 32 + (e >> 2) * 8 + g * 4 + (e & 3);
+                        const int ch = channel_of<DP>(d * 4 + (e >> 2)) + g * 4 + (e & 3);
                         if (ch < D) {
                             const float v = value_at<VST>(vr, ch);
                             if (!__builtin_isfinite(v) || !__builtin_isfinite(s)) o[d][e] += w * (v * s);
@@ -457,7 +482,7 @@ __global__ __launch_bounds__(kThreads, DP <= 128 ? 2 : 1) void k_extend(const Ex
     for (int d = 0; d < DT; ++d)
 #pragma unroll
         for (int u = 0; u < 4; ++u) {
-            const int ch = d * 32 + u * 8 + g * 4;
+            const int ch = channel_of<DP>(d * 4 + u) + g * 4;
             if (ch < D)
                 *reinterpret_cast<uint2*>(to + ch) =
                     make_uint2(pack2(o[d][u * 4] * inv, o[d][u * 4 + 1] * inv),
