@@ -243,6 +243,11 @@ __global__ __launch_bounds__(kThreads, DP <= 128 ? 2 : 1) void k_extend(const Ex
     Unit<KST> ku[UT];
     Unit<VST> vu[UT];
     float sc = 0.0f;
+#pragma unroll
+    for (int u = 0; u < UT; ++u) {              // channels past head_dim stay 0
+        ku[u].clear();
+        vu[u].clear();
+    }
     auto entry_of = [&](int i) -> int {         // threads 0..63: the page of a step's token
         if (tid >= kStep || i >= steps.count) return -1;
         const int j = steps.token(i) + tid;
@@ -256,10 +261,10 @@ __global__ __launch_bounds__(kThreads, DP <= 128 ? 2 : 1) void k_extend(const Ex
 #pragma unroll
         for (int u = 0; u < UT; ++u) {
             const int t = (tid + u * kThreads) / UR, e = ((tid + u * kThreads) % UR) * 16;
-            const int row = rows_i[t];
-            ku[u].clear();
-            vu[u].clear();
-            if (row >= 0 && e < D) {
+            // a token that is not there: any row (its score is masked, its
+            // weight 0, and staging keeps values finite)
+            const int64_t row = max(rows_i[t], 0);
+            if (D == DP || e < D) {
                 ku[u].load(kb + row * k_row + e * kElemBytes<KST>);
                 vu[u].load(vb + row * v_row + e * kElemBytes<VST>);
             }
@@ -280,7 +285,7 @@ __global__ __launch_bounds__(kThreads, DP <= 128 ? 2 : 1) void k_extend(const Ex
 #pragma unroll
         for (int u = 0; u < UT; ++u) {
             const int t = (tid + u * kThreads) / UR, e = (tid + u * kThreads) % UR;
-            if (vu[u].clean()) mark(i);
+            if (vu[u].clean() && lds.row[i % 3][t] >= 0) mark(i);
             ku[u].put(buf.k + t * L::kK + e * 16, UR * 16);
             vu[u].put(buf.v + t * L::kV + e * 16, UR * 16);
         }
@@ -346,6 +351,7 @@ __global__ __launch_bounds__(kThreads, DP <= 128 ? 2 : 1) void k_extend(const Ex
         const bool edge = j0 + kStep - 1 > p_first ||
                           (a.window > 0 && j0 <= p_last - a.window && j0 + kStep - 1 >= a.sinks);
         if (edge || !__all(there)) {
+            const int lo = a.window > 0 ? pos - a.window + 1 : 0;
 #pragma unroll
             for (int t = 0; t < 2; ++t)
 #pragma unroll
@@ -354,8 +360,11 @@ __global__ __launch_bounds__(kThreads, DP <= 128 ? 2 : 1) void k_extend(const Ex
                     const int4 rr = *reinterpret_cast<const int4*>(&rows_i[at]);
                     const int ra[4] = {rr.x, rr.y, rr.z, rr.w};
 #pragma unroll
-                    for (int e = 0; e < 4; ++e)
-                        if (ra[e] < 0 || !sees(j0 + at + e, pos, a.window, a.sinks)) x[t][u * 4 + e] = -INFINITY;
+                    for (int e = 0; e < 4; ++e) {
+                        const int j = j0 + at + e;
+                        const bool seen = (ra[e] >= 0) & (j <= pos) & ((j >= lo) | (j < a.sinks));
+                        x[t][u * 4 + e] = seen ? x[t][u * 4 + e] : -INFINITY;
+                    }
                 }
         }
         float mx = -INFINITY;
