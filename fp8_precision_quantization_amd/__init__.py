@@ -13,6 +13,8 @@ call raises if the library is missing or the device is not gfx950.
 from __future__ import annotations
 
 import ctypes
+import functools
+import struct
 from dataclasses import dataclass
 from typing import Optional
 
@@ -43,8 +45,14 @@ def _gran(g) -> int:
     return int(g)
 
 
+# the handle of a device's current stream, without a Stream object around it
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
 def _stream(device: torch.device) -> int:
-    return torch.cuda.current_stream(device).cuda_stream
+    if _raw_stream is None or device.index is None:
+        return torch.cuda.current_stream(device).cuda_stream
+    return _raw_stream(device.index)
 
 
 def _ptr(t: Optional[torch.Tensor]):
@@ -548,17 +556,22 @@ def kv_load(cache: torch.Tensor, scale_inv: Optional[torch.Tensor], n: Optional[
 
 
 # ---------------------------------------- attention over the cache, eviction --
+_PAIR = struct.Struct("PPPPqPqPqiiiiiiii")     # fp8_kv_pair (_lib.Fp8KvPair) as the bytes a call passes
+
+
 def _kv_pair(k_cache, v_cache, page_table, lens, page_size, k_scale_inv, v_scale_inv, k_storage, v_storage, scaling,
              max_len):
-    """The fp8_kv_pair of a layer's K and V caches and a batch's pages; raises
-    before any launch if a buffer is not what the library would read."""
-    if k_cache.dim() != 3 or not k_cache.is_cuda:
+    """The fp8_kv_pair (as bytes) of a layer's K and V caches and a batch's
+    pages, and the sizes in it: (pair, heads, head_dim, batch, max_len).
+    Raises before any launch if a buffer is not what the library would read."""
+    shape = k_cache.shape
+    if len(shape) != 3 or not k_cache.is_cuda:
         raise ValueError("k_cache must be a [capacity, heads, head_dim] device tensor")
-    capacity, heads, head_dim = k_cache.shape
+    capacity, heads, head_dim = shape
     dev = k_cache.device
-    if v_cache.shape != k_cache.shape:
+    if v_cache.shape != shape:
         raise ValueError("k_cache and v_cache must have one shape, got %s and %s"
-                         % (tuple(k_cache.shape), tuple(v_cache.shape)))
+                         % (tuple(shape), tuple(v_cache.shape)))
     for cache, st, name in ((k_cache, k_storage, "k_cache"), (v_cache, v_storage, "v_cache")):
         want = torch.bfloat16 if st == "bf16" else torch.uint8
         if cache.dtype != want or not cache.is_contiguous() or cache.device != dev:
@@ -566,20 +579,30 @@ def _kv_pair(k_cache, v_cache, page_table, lens, page_size, k_scale_inv, v_scale
     if page_table.dim() != 2 or page_table.dtype != torch.int32 or page_table.device != dev:
         raise ValueError("page_table must be an int32 [batch, pages] tensor on %s" % dev)
     batch, pages = page_table.shape
-    if pages > 1 and page_table.stride(1) != 1:
+    page_ld, last = page_table.stride()
+    if pages > 1 and last != 1:
         raise ValueError("page_table must have a contiguous last dimension")
-    page_ld = page_table.stride(0) if batch > 1 else pages
-    if page_ld < pages:
+    if batch <= 1:
+        page_ld = pages
+    elif page_ld < pages:
         raise ValueError("page_table must not overlap itself")
     if max_len is None:
         max_len = pages * page_size
     elif max_len > pages * page_size:
         raise ValueError("max_len=%d needs more than the %d pages of page_table" % (max_len, pages))
-    return _lib.Fp8KvPair(
-        k_cache.data_ptr(), v_cache.data_ptr(), _kv_scales(k_scale_inv, k_storage, scaling, capacity, heads, dev),
-        _kv_scales(v_scale_inv, v_storage, scaling, capacity, heads, dev), capacity, page_table.data_ptr(), page_ld,
-        _buf(lens, batch, torch.int32, dev, "lens"), max_len, KV_STORAGE[k_storage], KV_STORAGE[v_storage],
+    pair = _PAIR.pack(
+        k_cache.data_ptr(), v_cache.data_ptr(), _kv_scales(k_scale_inv, k_storage, scaling, capacity, heads, dev) or 0,
+        _kv_scales(v_scale_inv, v_storage, scaling, capacity, heads, dev) or 0, capacity, page_table.data_ptr(),
+        page_ld, _buf(lens, batch, torch.int32, dev, "lens"), max_len, KV_STORAGE[k_storage], KV_STORAGE[v_storage],
         KV_SCALING[scaling], heads, head_dim, page_size, batch, 0)
+    return pair, heads, head_dim, batch, max_len
+
+
+@functools.lru_cache(maxsize=1024)
+def _attention_workspace(heads, head_dim, page_size, batch, max_len, total_q, q_heads, window, sinks) -> int:
+    """fp8_kv_attention_workspace of these sizes (it reads nothing else)."""
+    pair = _PAIR.pack(0, 0, 0, 0, 1, 0, max_len, 0, max_len, 0, 0, 0, heads, head_dim, page_size, batch, 0)
+    return _lib.lib().fp8_kv_attention_workspace(pair, total_q, q_heads, 0, window, sinks)
 
 
 def _kv_weights(weights, batch: int, heads: int, least: int, device, name: str) -> int:
@@ -614,21 +637,12 @@ def _heads_matrix(x, head_dim: int, name: str):
     return n, heads, x.stride(0) if n > 1 else heads * head_dim
 
 
-class _on_device:
-    """Launch on a tensor's device whatever the current one is."""
-
-    def __init__(self, device):
-        self.index, self.back = device.index, None
-
-    def __enter__(self):
-        current = torch.cuda.current_device()
-        if self.index is not None and self.index != current:
-            self.back = current
-            torch.cuda.set_device(self.index)
-
-    def __exit__(self, *_):
-        if self.back is not None:
-            torch.cuda.set_device(self.back)
+def _call_on(device, func, *args):
+    """func(*args, stream) on the device's current stream, whatever the current device is."""
+    if device.index == torch.cuda.current_device():
+        return func(*args, _stream(device))
+    with torch.cuda.device(device):
+        return func(*args, _stream(device))
 
 
 def kv_attention(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor, page_table: torch.Tensor,
@@ -664,17 +678,17 @@ def kv_attention(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor, 
     given) also the fp32 log-sum-exp of the scores [total_q, q_heads]."""
     if v_storage is None:
         v_storage = k_storage
-    pair = _kv_pair(k_cache, v_cache, page_table, lens, page_size, k_scale_inv, v_scale_inv, k_storage, v_storage,
-                    scaling, max_len)
+    pair, heads, head_dim, batch, max_len = _kv_pair(k_cache, v_cache, page_table, lens, page_size, k_scale_inv,
+                                                     v_scale_inv, k_storage, v_storage, scaling, max_len)
     dev = k_cache.device
     _same_device(q, dev, "q")
-    n, q_heads, ldq = _heads_matrix(q, pair.head_dim, "q")
+    n, q_heads, ldq = _heads_matrix(q, head_dim, "q")
     if out is None:
-        out = torch.empty((n, q_heads, pair.head_dim), dtype=torch.bfloat16, device=dev)
-        ldo = q_heads * pair.head_dim
+        out = torch.empty((n, q_heads, head_dim), dtype=torch.bfloat16, device=dev)
+        ldo = q_heads * head_dim
     else:
         _same_device(out, dev, "out")
-        n2, h2, ldo = _heads_matrix(out, pair.head_dim, "out")
+        n2, h2, ldo = _heads_matrix(out, head_dim, "out")
         if (n2, h2) != (n, q_heads):
             raise ValueError("out must have shape %s, got %s" % (tuple(q.shape), tuple(out.shape)))
     want_lse = return_lse or lse is not None
@@ -684,26 +698,22 @@ def kv_attention(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor, 
         lse = torch.empty((n, q_heads), dtype=torch.float32, device=dev)
     offsets = None
     if q_offsets is not None:
-        offsets = _buf(q_offsets, pair.batch + 1, torch.int32, dev, "q_offsets")
+        offsets = _buf(q_offsets, batch + 1, torch.int32, dev, "q_offsets")
     ldw = 0
     if weights is not None:
-        ldw = _kv_weights(weights, pair.batch, pair.heads, pair.max_len, dev, "weights")
-    L = _lib.lib()
+        ldw = _kv_weights(weights, batch, heads, max_len, dev, "weights")
     ws_bytes = 0
-    if q_offsets is None and n == pair.batch:
-        ws_bytes = L.fp8_kv_attention_workspace(ctypes.byref(pair), n, q_heads, 0, window, sinks)
     if workspace is not None:
         if not isinstance(workspace, torch.Tensor) or workspace.device != dev or not workspace.is_contiguous():
             raise ValueError("workspace must be a contiguous tensor on %s" % dev)
         ws_bytes = workspace.numel() * workspace.element_size()
-    elif ws_bytes > 0:
-        workspace = torch.empty(ws_bytes, dtype=torch.uint8, device=dev)
-    if scale is None:
-        scale = pair.head_dim ** -0.5
-    with _on_device(dev):
-        st = L.fp8_kv_attention(
-            ctypes.byref(pair), q.data_ptr(), ldq, n, q_heads, offsets, scale, window, sinks, out.data_ptr(), ldo,
-            _ptr(lse), _ptr(weights), ldw, _ptr(workspace), ws_bytes, _stream(dev))
+    elif offsets is None and n == batch:
+        ws_bytes = _attention_workspace(heads, head_dim, page_size, batch, max_len, n, q_heads, window, sinks)
+        if ws_bytes > 0:
+            workspace = torch.empty(ws_bytes, dtype=torch.uint8, device=dev)
+    st = _call_on(dev, _lib.lib().fp8_kv_attention, pair, q.data_ptr(), ldq, n, q_heads, offsets,
+                  head_dim ** -0.5 if scale is None else scale, window, sinks, out.data_ptr(), ldo, _ptr(lse),
+                  _ptr(weights), ldw, _ptr(workspace), ws_bytes)
     _lib.check(st, "fp8_kv_attention")
     return (out, lse) if want_lse else out
 
@@ -728,36 +738,33 @@ def kv_evict(k_cache: torch.Tensor, v_cache: torch.Tensor, weights: torch.Tensor
     every layer of a model evicts with the same one."""
     if v_storage is None:
         v_storage = k_storage
-    pair = _kv_pair(k_cache, v_cache, page_table, lens, page_size, k_scale_inv, v_scale_inv, k_storage, v_storage,
-                    scaling, max_len)
+    pair, heads, _, batch, max_len = _kv_pair(k_cache, v_cache, page_table, lens, page_size, k_scale_inv, v_scale_inv,
+                                              k_storage, v_storage, scaling, max_len)
     dev = k_cache.device
     if budget < 1:
         raise ValueError("budget must be >= 1, got %d" % budget)
-    ldw = _kv_weights(weights, pair.batch, pair.heads, pair.max_len, dev, "weights")
+    ldw = _kv_weights(weights, batch, heads, max_len, dev, "weights")
     ldwo = 0
     if weights_out is not None:
-        ldwo = _kv_weights(weights_out, pair.batch, pair.heads, budget, dev, "weights_out")
+        ldwo = _kv_weights(weights_out, batch, heads, budget, dev, "weights_out")
     dst, dst_ld = None, 0
     if dst_page_table is not None:
         if (dst_page_table.dim() != 2 or dst_page_table.dtype != torch.int32 or dst_page_table.device != dev
-                or dst_page_table.shape[0] != pair.batch
+                or dst_page_table.shape[0] != batch
                 or (dst_page_table.shape[1] > 1 and dst_page_table.stride(1) != 1)):
             raise ValueError("dst_page_table must be an int32 [%d, pages] tensor on %s with a contiguous last "
-                             "dimension" % (pair.batch, dev))
+                             "dimension" % (batch, dev))
         if dst_page_table.shape[1] * page_size < budget:
             raise ValueError("dst_page_table holds fewer than budget=%d tokens" % budget)
         dst = dst_page_table.data_ptr()
-        dst_ld = dst_page_table.stride(0) if pair.batch > 1 else dst_page_table.shape[1]
+        dst_ld = dst_page_table.stride(0) if batch > 1 else dst_page_table.shape[1]
     if kept is None:
-        kept = torch.empty((pair.batch, pair.heads, budget), dtype=torch.int32, device=dev)
-    _buf(kept, pair.batch * pair.heads * budget, torch.int32, dev, "kept")
+        kept = torch.empty((batch, heads, budget), dtype=torch.int32, device=dev)
     if new_lens is None:
-        new_lens = torch.empty(pair.batch, dtype=torch.int32, device=dev)
-    _buf(new_lens, pair.batch, torch.int32, dev, "new_lens")
-    with _on_device(dev):
-        st = _lib.lib().fp8_kv_evict(
-            ctypes.byref(pair), weights.data_ptr(), ldw, budget, sinks, recent, dst, dst_ld, _ptr(weights_out),
-            ldwo, kept.data_ptr(), new_lens.data_ptr(), _stream(dev))
+        new_lens = torch.empty(batch, dtype=torch.int32, device=dev)
+    st = _call_on(dev, _lib.lib().fp8_kv_evict, pair, weights.data_ptr(), ldw, budget, sinks, recent, dst, dst_ld,
+                  _ptr(weights_out), ldwo, _buf(kept, batch * heads * budget, torch.int32, dev, "kept"),
+                  _buf(new_lens, batch, torch.int32, dev, "new_lens"))
     _lib.check(st, "fp8_kv_evict")
     return kept, new_lens
 

@@ -591,6 +591,8 @@ static fp8_status attention_args(const fp8_kv_pair* cache, bool sizes, int64_t t
                     (long long)total_q, (int)cache->batch);
     if (window < 0 || sinks < 0)
         return fail(FP8_ERR_INVALID_ARG, "window=%d and sinks=%d must be >= 0", (int)window, (int)sinks);
+    if (cache->batch * cache->max_len >= (int64_t(1) << 35))
+        return fail(FP8_ERR_UNSUPPORTED_SHAPE, "batch * max_len must be < 2^35");
     a->total_q = total_q; a->q_heads = q_heads;
     if (cache->capacity == 0) a->kv.max_len = 0;    // a cache without rows holds no token
     // a window that reaches every token is none; sinks past the end are all

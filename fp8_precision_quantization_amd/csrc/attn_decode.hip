@@ -46,17 +46,73 @@ struct DecodeParams {
     int q_heads, group, col_tiles;
     float scale_log2;
     int window, sinks;
-    int chunk, splits;           // steps of a split, splits of the longest sequence
+    int shares, least;           // waves that share the batch's steps, per KV head and column tile
     uint16_t* out;
     int64_t ldo;
     float* lse;
-    float2* part_ml;             // [batch, q_heads, splits]
-    float* part_o;               // [batch, q_heads, splits, head_dim]
+    float2* part_ml;             // [shares + batch, q_heads]
+    float* part_o;               // [shares + batch, q_heads, head_dim]
 };
 
-__device__ __forceinline__ int splits_of(const DecodeParams& a, int len) {
-    const Steps<kStep> st(len - 1, len - 1, a.window, a.sinks);
-    return (st.count + a.chunk - 1) / a.chunk;
+// How a batch's steps are shared out.  The sequences' steps lie one after the
+// other (a sequence without any counts as one, for its zeros); share i takes
+// `chunk` of them from i * chunk, across sequence borders, so workers have
+// equal work whatever the lengths.  The piece of sequence b in share i has
+// slot i + b of the partial results: each next piece starts a new share or a
+// new sequence, so slots are distinct.
+struct Work {
+    int total = 0, chunk = 0;
+    int b = 0, len = 0, before = 0;      // a sequence, its tokens and the steps before it
+};
+
+__device__ __forceinline__ int steps_of(const DecodeParams& a, int len) {
+    const int n = Steps<kStep>(len - 1, len - 1, a.window, a.sinks).count;
+    return n < 1 ? 1 : n;
+}
+
+__device__ __forceinline__ int wave_scan(int v, int lane) {
+#pragma unroll
+    for (int off = 1; off < 64; off <<= 1) {
+        const int t = __shfl_up(v, off, 64);
+        if (lane >= off) v += t;
+    }
+    return v;
+}
+
+// The total and the chunk, then the sequence that step `at` of the whole (or,
+// with seq >= 0, the sequence `seq`) lies in.  Every wave computes it for
+// itself, 64 sequences at a time.
+__device__ __forceinline__ Work work_of(const DecodeParams& a, int share, int seq, int lane) {
+    Work w;
+    const int B = a.kv.batch;
+    int sum = 0, mine = 0, len = 0;      // of the last 64 sequences looked at
+    auto look = [&](int b0) {
+        len = b0 + lane < B ? seq_len(a.kv, b0 + lane) : 0;
+        mine = b0 + lane < B ? steps_of(a, len) : 0;
+        sum = wave_scan(mine, lane);
+    };
+    for (int b0 = 0; b0 < B; b0 += 64) {
+        look(b0);
+        w.total += __builtin_amdgcn_readlane(sum, 63);
+    }
+    const int even = (w.total + a.shares - 1) / a.shares, mean = (w.total + B - 1) / B;
+    const int least = mean < a.least ? mean : a.least;     // a share's fewest steps, unless sequences are shorter
+    w.chunk = even < least ? least : even;
+    const int at = share * w.chunk;
+    for (int b0 = 0; b0 < B; b0 += 64) {
+        if (B > 64) look(b0);
+        const uint64_t in = seq >= 0 ? (seq < b0 + 64 ? 1ull << (seq & 63) : 0)
+                                     : __ballot(w.before + sum > at && mine > 0);
+        if (in) {
+            const int l = __builtin_ctzll(in);
+            w.b = b0 + l;
+            w.len = __builtin_amdgcn_readlane(len, l);
+            w.before += __builtin_amdgcn_readlane(sum, l) - __builtin_amdgcn_readlane(mine, l);
+            return w;
+        }
+        w.before += __builtin_amdgcn_readlane(sum, 63);
+    }
+    return w;
 }
 
 // VD values of one token (one lane's channels) as raw words
@@ -83,35 +139,45 @@ __device__ __forceinline__ Raw<W> load_raw(const uint8_t* p) {
     return r;
 }
 
+// One step's loads: K pieces, V words, the scale of this lane's token (K's in
+// lanes 0-31, V's in 32-63), which of the lane's 8 tokens are not seen.
+template <int KC, int VW>
+struct Loads {
+    uint4 k[2][KC];
+    Raw<VW> v[8];
+    float scale;
+    uint32_t hide;
+    uint64_t there;
+};
+
 template <int KST, int VST, int DP, int NT>
-__global__ __launch_bounds__(64 * kWaves) void k_decode(const DecodeParams a) {
+__global__ __launch_bounds__(64 * kWaves, DP <= 128 && NT == 1 ? 2 : 1) void k_decode(const DecodeParams a) {
     constexpr int VD = DP / 16;                         // channels of V a lane holds
     constexpr int KC = DP * kElemBytes<KST> / 64;       // 16-byte pieces of K a lane holds per token
     constexpr int KM = DP / 32;                         // matrix steps over the channels
     constexpr int VW = VD * kElemBytes<VST> / 4;        // words of V a lane holds per token
-    constexpr int kOPad = DP + 4;
-    __shared__ int s_row[kWaves][kStep];
-    __shared__ float s_scale[kWaves][2 * kStep];
-    __shared__ float s_ml[kWaves][2][16 * NT];
-    __shared__ float s_o[16 * NT][kOPad];
+    // a step is loaded while the one before is computed on, where registers allow
+    constexpr bool kAhead = NT * (8 * KC + 8 * VW) <= 64;
+    __shared__ __align__(16) int s_row[kWaves][kStep];
+    __shared__ __align__(16) float s_scale[kWaves][2 * kStep];
 
     const KvView& kv = a.kv;
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int c = lane & 15, g = lane >> 4;
-    // All KV heads of a run of tokens on one XCD (their scales share lines).
+    // A worker is one wave.  The KV heads of a share are neighbours, in one
+    // block and on one XCD: their scales and page entries share cache lines.
     const int units = kv.heads * a.col_tiles;
-    const int xcd = blockIdx.x & 7, k = blockIdx.x >> 3;
-    const int hc = k % units, run = (k / units) * 8 + xcd;
-    if (run >= kv.batch * a.splits) return;
+    const int worker = (blockIdx.x >> 3) * kWaves + wave;
+    const int hc = worker % units, share = (worker / units) * 8 + (blockIdx.x & 7);
+    if (share >= a.shares) return;
     const int h = hc % kv.heads, ct = hc / kv.heads;
-    const int b = run / a.splits, split = run % a.splits;
-
-    const int len = seq_len(kv, b);
+    const Work work = work_of(a, share, -1, lane);
+    const int share_end = min(work.total, (share + 1) * work.chunk);
+    for (int at = share * work.chunk, b = work.b, len = work.len, before = work.before; at < share_end;) {
     const int pos = len - 1;
     const Steps<kStep> steps(pos, pos, a.window, a.sinks);
-    const int nsplit = (steps.count + a.chunk - 1) / a.chunk;
-    if (split >= nsplit && split > 0) return;
-    const int s_end = min(steps.count, (split + 1) * a.chunk);
+    const int seq_steps = steps.count < 1 ? 1 : steps.count;
+    const int s_begin = at - before, s_end = min(steps.count, share_end - before);
 
     const int D = kv.head_dim;
     const int head0 = ct * 16 * NT;                     // first query head of this block within the group
@@ -148,51 +214,73 @@ __global__ __launch_bounds__(64 * kWaves) void k_decode(const DecodeParams a) {
     const bool k_per_token = KST != kBf16 && !kv.per_head, v_per_token = VST != kBf16 && !kv.per_head;
 
     const int half = lane & 31;
-    // the page of this lane's token of a step, -1 where the query does not see it
+    // This lane's page entry of a step; a step or token past the end reads a
+    // valid entry, which row_of drops.
     auto entry_of = [&](int st) -> int {
-        if (st >= s_end) return -1;
-        const int j = steps.token(st) + half;
-        return sees(j, pos, a.window, a.sinks) ? table[j >> kv.page_shift] : -1;
+        const int j = min(steps.token(min(st, s_end - 1)) + half, pos);
+        return table[j >> kv.page_shift];
     };
-    int entry = entry_of(split * a.chunk + wave);
-    for (int st = split * a.chunk + wave; st < s_end; st += kWaves) {
+    auto row_of = [&](int st, int entry) -> int {
         const int j = steps.token(st) + half;
-        const int row = entry >= 0 ? row_of_entry(kv, entry, j) : -1;
-        entry = entry_of(st + kWaves);
-        const uint64_t there = __ballot(row >= 0);
-        if (there == 0) continue;
-        const bool whole = there == ~0ull;
+        return st < s_end && sees(j, pos, a.window, a.sinks) ? row_of_entry(kv, entry, j) : -1;
+    };
+    // A step's loads.  None of them is conditional, so a wait for one step's
+    // does not wait for the next one's: a token that is not seen reads row 0.
+    auto load = [&](Loads<KC, VW>& s, int row) {
+        s.there = __ballot(row >= 0);
         wave_sync();
         s_row[wave][half] = row;
         wave_sync();
-        float sc = lane < 32 ? k_head : v_head;
-        if (lane < 32 ? k_per_token : v_per_token) {
-            sc = 0.0f;
-            if (row >= 0) sc = (lane < 32 ? kv.k_scale : kv.v_scale)[(int64_t)row * kv.heads + h];
-            if (lane < 32) sc *= a.scale_log2;
-        }
-        uint4 kr[2][KC];
-        int vrow[8];
-        Raw<VW> vr[8];
+        const bool key = lane < 32, per_token = key ? k_per_token : v_per_token;
+        const float* sp = per_token ? (key ? kv.k_scale : kv.v_scale) : reinterpret_cast<const float*>(table);
+        s.scale = sp[per_token ? (int64_t)max(row, 0) * kv.heads + h : 0];
+        s.scale = !per_token ? (key ? k_head : v_head) : row < 0 ? 0.0f : key ? s.scale * a.scale_log2 : s.scale;
 #pragma unroll
         for (int t = 0; t < 2; ++t) {
             const uint8_t* p = kb + max(s_row[wave][16 * t + c], 0) * k_row;
 #pragma unroll
             for (int i = 0; i < KC; ++i) {
                 const int e = (i * 64 + g * 16) / kElemBytes<KST>;
-                kr[t][i] = make_uint4(0, 0, 0, 0);
-                if (e < D) kr[t][i] = *reinterpret_cast<const uint4*>(p + i * 64 + g * 16);
+                s.k[t][i] = *reinterpret_cast<const uint4*>(p + (e < D ? i * 64 + g * 16 : 0));
             }
         }
+        s.hide = 0;
 #pragma unroll
         for (int t = 0; t < 2; ++t) {
             const int4 r = *reinterpret_cast<const int4*>(&s_row[wave][16 * t + 4 * g]);
-            vrow[4 * t] = r.x; vrow[4 * t + 1] = r.y; vrow[4 * t + 2] = r.z; vrow[4 * t + 3] = r.w;
-        }
+            const int ra[4] = {r.x, r.y, r.z, r.w};
 #pragma unroll
-        for (int i = 0; i < 8; ++i) vr[i] = load_raw<VW>(vb + max(vrow[i], 0) * v_row);
-        s_scale[wave][lane] = sc;
+            for (int i = 0; i < 4; ++i) {
+                s.hide |= (ra[i] < 0 ? 1u : 0u) << (4 * t + i);
+                s.v[4 * t + i] = load_raw<VW>(vb + max(ra[i], 0) * v_row);
+            }
+        }
+    };
+    if (s_begin < s_end) {
+    Loads<KC, VW> cur, next;
+    int entry = entry_of(s_begin);
+    const int row = row_of(s_begin, entry);
+    entry = entry_of(s_begin + 1);
+    load(cur, row);
+    for (int st = s_begin; st < s_end; ++st, cur = next) {
+        const int row = row_of(st + 1, entry);
+        entry = entry_of(st + 2);
+        if (kAhead) load(next, row);
+        if (cur.there == 0) {
+            if (!kAhead) load(next, row);
+            continue;
+        }
+        const bool whole = cur.there == ~0ull;
         wave_sync();
+        s_scale[wave][lane] = cur.scale;
+        wave_sync();
+        if (D < DP) {            // pieces past head_dim
+#pragma unroll
+            for (int t = 0; t < 2; ++t)
+#pragma unroll
+                for (int i = 0; i < KC; ++i)
+                    if ((i * 64 + g * 16) / kElemBytes<KST> >= D) cur.k[t][i] = make_uint4(0, 0, 0, 0);
+        }
 
         // scores of the step: x[nt][4t + i] of token 16t + 4g + i
         float x[NT][8];
@@ -205,9 +293,9 @@ __global__ __launch_bounds__(64 * kWaves) void k_decode(const DecodeParams a) {
             for (int e = 0; e < KM; ++e) {
                 uint4 w;
                 if constexpr (KST == kBf16) {
-                    w = kr[t][e];
+                    w = cur.k[t][e];
                 } else {
-                    const uint4 r = kr[t][e >> 1];
+                    const uint4 r = cur.k[t][e >> 1];
                     const uint32_t w0 = (e & 1) ? r.z : r.x, w1 = (e & 1) ? r.w : r.y;
                     w = make_uint4(decode2<KST>(w0, false), decode2<KST>(w0, true), decode2<KST>(w1, false),
                                    decode2<KST>(w1, true));
@@ -228,12 +316,11 @@ __global__ __launch_bounds__(64 * kWaves) void k_decode(const DecodeParams a) {
             // vector (which may hold anything, NaN included)
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
-                if (vrow[i] < 0) {
+                const bool hidden = cur.hide >> i & 1;
 #pragma unroll
-                    for (int nt = 0; nt < NT; ++nt) x[nt][i] = -INFINITY;
+                for (int nt = 0; nt < NT; ++nt) x[nt][i] = hidden ? -INFINITY : x[nt][i];
 #pragma unroll
-                    for (int w = 0; w < VW; ++w) vr[i].w[w] = 0;
-                }
+                for (int w = 0; w < VW; ++w) cur.v[i].w[w] = hidden ? 0 : cur.v[i].w[w];
             }
         }
         // weights, as the B operand of the second product
@@ -263,7 +350,7 @@ __global__ __launch_bounds__(64 * kWaves) void k_decode(const DecodeParams a) {
             for (int i = 0; i < 8; ++i) {
                 p[i] = __builtin_amdgcn_exp2f(x[nt][i] - m[nt]);
                 l[nt] += p[i];
-                p[i] = vrow[i] < 0 ? 0.0f : p[i] * vs[i];
+                p[i] *= vs[i];      // a scale that is not seen is 0
             }
             u4 hi, lo;
 #pragma unroll
@@ -289,7 +376,7 @@ __global__ __launch_bounds__(64 * kWaves) void k_decode(const DecodeParams a) {
                 u4 f0, f1;
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
-                    const uint32_t x0 = vr[2 * i].w[w], x1 = vr[2 * i + 1].w[w];
+                    const uint32_t x0 = cur.v[2 * i].w[w], x1 = cur.v[2 * i + 1].w[w];
                     f0[i] = __builtin_amdgcn_perm(x1, x0, 0x05040100u);
                     f1[i] = __builtin_amdgcn_perm(x1, x0, 0x07060302u);
                 }
@@ -299,7 +386,7 @@ __global__ __launch_bounds__(64 * kWaves) void k_decode(const DecodeParams a) {
                 u4 f[4];
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
-                    const uint32_t x0 = vr[2 * i].w[w], x1 = vr[2 * i + 1].w[w];
+                    const uint32_t x0 = cur.v[2 * i].w[w], x1 = cur.v[2 * i + 1].w[w];
                     const uint32_t p0 = __builtin_amdgcn_perm(x1, x0, 0x05010400u);
                     const uint32_t p1 = __builtin_amdgcn_perm(x1, x0, 0x07030602u);
                     f[0][i] = decode2<VST>(p0, false);
@@ -311,98 +398,74 @@ __global__ __launch_bounds__(64 * kWaves) void k_decode(const DecodeParams a) {
                 for (int e = 0; e < 4; ++e) add(4 * w + e, f[e]);
             }
         }
+        if (!kAhead) load(next, row);
+    }
     }
 
-    // the block's waves, joined in their order
+    const bool alone = s_begin == 0 && share_end - before >= seq_steps;      // the sequence's only piece
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
-        l[nt] = sum_xor16(sum_xor32(l[nt]));
+        const int col = head0 + nt * 16 + c, hq = h * a.group + col;
+        const float sum = sum_xor16(sum_xor32(l[nt]));
+        if (col >= a.group) continue;
+        const float f = !alone ? 1.0f : sum == 0.0f ? 0.0f : 1.0f / sum;
+        const int64_t part = (int64_t)(share + b) * a.q_heads + hq;
         if (g == 0) {
-            s_ml[wave][0][nt * 16 + c] = m[nt];
-            s_ml[wave][1][nt * 16 + c] = l[nt];
+            if (!alone) a.part_ml[part] = make_float2(m[nt], sum);
+            else if (a.lse)
+                a.lse[(int64_t)b * a.q_heads + hq] = sum == 0.0f ? -INFINITY : (m[nt] + __builtin_amdgcn_logf(sum)) * kLn2;
         }
-    }
-    __syncthreads();
-    float mt[NT], lt[NT];
 #pragma unroll
-    for (int nt = 0; nt < NT; ++nt) {
-        mt[nt] = kLowest; lt[nt] = 0.0f;
+        for (int i = 0; i < 4; ++i) {
+            const int d0 = VD * (4 * g + i);
+            if (d0 >= D) continue;
 #pragma unroll
-        for (int w = 0; w < kWaves; ++w) mt[nt] = fmaxf(mt[nt], s_ml[w][0][nt * 16 + c]);
-#pragma unroll
-        for (int w = 0; w < kWaves; ++w)
-            lt[nt] += s_ml[w][1][nt * 16 + c] * __builtin_amdgcn_exp2f(s_ml[w][0][nt * 16 + c] - mt[nt]);
-    }
-    for (int w = 0; w < kWaves; ++w) {
-        if (wave == w) {
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt) {
-                const float f = __builtin_amdgcn_exp2f(m[nt] - mt[nt]);
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-#pragma unroll
-                    for (int d = 0; d < VD; d += 4) {
-                        f4* to = reinterpret_cast<f4*>(&s_o[nt * 16 + c][VD * (4 * g + i) + d]);
-                        f4 v = f4{o[nt][d][i] * f, o[nt][d + 1][i] * f, o[nt][d + 2][i] * f, o[nt][d + 3][i] * f};
-                        *to = w == 0 ? v : *to + v;
-                    }
-                }
+            for (int d = 0; d < VD; d += 4) {
+                const f4 v = f4{o[nt][d][i], o[nt][d + 1][i], o[nt][d + 2][i], o[nt][d + 3][i]} * f;
+                if (alone)
+                    *reinterpret_cast<uint2*>(a.out + b * a.ldo + (int64_t)hq * D + d0 + d) =
+                        make_uint2(pack2(v[0], v[1]), pack2(v[2], v[3]));
+                else
+                    *reinterpret_cast<f4*>(a.part_o + part * D + d0 + d) = v;
             }
         }
-        __syncthreads();
     }
-    // every wave holds mt, lt of column c: publish them for the writers below
-    if (wave == 0 && g == 0) {
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
-            s_ml[0][0][nt * 16 + c] = mt[nt];
-            s_ml[0][1][nt * 16 + c] = lt[nt];
-        }
-    }
-    __syncthreads();
-    const int cols = min(16 * NT, a.group - head0);
-    const int quads = D >> 2;
-    for (int i = threadIdx.x; i < cols * quads; i += 64 * kWaves) {
-        const int col = i / quads, d = (i - col * quads) * 4;
-        const int hq = h * a.group + head0 + col;
-        const float mm = s_ml[0][0][col], ll = s_ml[0][1][col];
-        const f4 v = *reinterpret_cast<const f4*>(&s_o[col][d]);
-        if (nsplit <= 1) {
-            const float r = ll == 0.0f ? 0.0f : 1.0f / ll;
-            *reinterpret_cast<uint2*>(a.out + b * a.ldo + (int64_t)hq * D + d) =
-                make_uint2(pack2(v[0] * r, v[1] * r), pack2(v[2] * r, v[3] * r));
-            if (d == 0 && a.lse)
-                a.lse[(int64_t)b * a.q_heads + hq] = ll == 0.0f ? -INFINITY : (mm + __builtin_amdgcn_logf(ll)) * kLn2;
-        } else {
-            const int64_t part = ((int64_t)b * a.q_heads + hq) * a.splits + split;
-            *reinterpret_cast<f4*>(a.part_o + part * D + d) = v;
-            if (d == 0) a.part_ml[part] = make_float2(mm, ll);
-        }
+    before += seq_steps;
+    at = before;
+    if (at < share_end) len = seq_len(kv, ++b);
     }
 }
 
-// One block per (query head, sequence): joins the splits in their order.
-// Threads take 4 channels each, several splits side by side.
+// One block per (query head, sequence): joins the pieces of a sequence that
+// several shares hold, in their order.  Threads take 4 channels each, several
+// pieces side by side.
 constexpr int kJoinThreads = 256;
 
 __global__ __launch_bounds__(kJoinThreads) void k_decode_join(const DecodeParams a) {
     __shared__ f4 s_acc[kJoinThreads];
     const int hq = blockIdx.x, b = blockIdx.y;
-    const int n = splits_of(a, seq_len(a.kv, b));
+    const Work w = work_of(a, 0, b, threadIdx.x & 63);
+    const int i0 = w.before / w.chunk, n = (w.before + steps_of(a, w.len) - 1) / w.chunk - i0 + 1;
     if (n <= 1) return;
     const int D = a.kv.head_dim, quads = D >> 2;
-    const int64_t part = ((int64_t)b * a.q_heads + hq) * a.splits;
+    const int64_t part = (int64_t)(i0 + b) * a.q_heads + hq, next = a.q_heads;
     const float2* ml = a.part_ml + part;
+    const int lane = threadIdx.x & 63;
     float m = kLowest, l = 0.0f;
-    for (int s = 0; s < n; ++s) m = fmaxf(m, ml[s].x);
-    for (int s = 0; s < n; ++s) l += ml[s].y * __builtin_amdgcn_exp2f(ml[s].x - m);
-    const int lanes = kJoinThreads / quads;             // splits side by side (4 or more)
+    for (int s = lane; s < n; s += 64) m = fmaxf(m, ml[s * next].x);
+#pragma unroll
+    for (int off = 1; off < 64; off <<= 1) m = fmaxf(m, __shfl_xor(m, off, 64));
+    for (int s = lane; s < n; s += 64) l += ml[s * next].y * __builtin_amdgcn_exp2f(ml[s * next].x - m);
+#pragma unroll
+    for (int off = 1; off < 64; off <<= 1) l += __shfl_xor(l, off, 64);
+    const int lanes = kJoinThreads / quads;             // pieces side by side (4 or more)
     const int side = threadIdx.x / quads, d = (threadIdx.x - side * quads) * 4;
     f4 acc = {0, 0, 0, 0};
     if (side < lanes) {
+#pragma unroll 4
         for (int s = side; s < n; s += lanes) {
-            const float f = __builtin_amdgcn_exp2f(ml[s].x - m);
-            acc += *reinterpret_cast<const f4*>(a.part_o + (part + s) * D + d) * f;
+            const float f = __builtin_amdgcn_exp2f(ml[s * next].x - m);
+            acc += *reinterpret_cast<const f4*>(a.part_o + (part + s * next) * D + d) * f;
         }
     }
     s_acc[threadIdx.x] = acc;
@@ -416,43 +479,45 @@ __global__ __launch_bounds__(kJoinThreads) void k_decode_join(const DecodeParams
         a.lse[(int64_t)b * a.q_heads + hq] = l == 0.0f ? -INFINITY : (m + __builtin_amdgcn_logf(l)) * kLn2;
 }
 
-// How a launch is split: steps of a split and splits of the longest sequence.
+// How a launch is shared out: waves per KV head and column tile.
 struct Plan {
-    int col_tiles, wide, chunk, splits;
+    int col_tiles, wide, shares, least;
+    bool joined;                 // a sequence may lie in several shares
     int64_t blocks;
 };
 
 Plan plan_of(const AttnArgs& a) {
     Plan p;
     const int group = a.q_heads / a.kv.heads;
-    p.wide = group > 16 ? 2 : 1;
+    p.wide = group > 16 && a.kv.head_dim <= 128 ? 2 : 1;    // column tiles of a wave (256 channels: registers for one)
     p.col_tiles = (group + 16 * p.wide - 1) / (16 * p.wide);
-    int64_t steps = (a.kv.max_len + kStep - 1) / kStep;
+    int64_t steps = (a.kv.max_len + kStep - 1) / kStep;     // of the longest sequence
     if (a.window > 0) {
         const int64_t seen = (a.window + kStep - 1) / kStep + 1 + (a.sinks + kStep - 1) / kStep;
         steps = seen < steps ? seen : steps;
     }
     if (steps < 1) steps = 1;
-    const int64_t units = (int64_t)a.kv.batch * a.kv.heads * p.col_tiles;
-    // enough blocks to fill the CUs several times over, and at least two
-    // steps for each wave of a block
-    int64_t chunk = (steps * units + 1023) / 1024;
-    const int64_t least = 2 * kWaves;
-    chunk = chunk < least ? least : chunk;
-    chunk = chunk < steps ? chunk : steps;
-    p.chunk = (int)chunk;
-    p.splits = (int)((steps + chunk - 1) / chunk);
-    p.blocks = (((int64_t)a.kv.batch * p.splits + 7) / 8) * 8 * a.kv.heads * p.col_tiles;
+    const int64_t units = (int64_t)a.kv.heads * p.col_tiles, most = steps * a.kv.batch;
+    const int64_t target = 2048;
+    p.least = 4;
+    int64_t shares = (target + units - 1) / units;
+    shares = shares < most ? shares : most;
+    p.shares = (int)(shares < 1 ? 1 : shares);
+    p.joined = steps > 1;
+    p.blocks = ((p.shares + 7) / 8 * units + kWaves - 1) / kWaves * 8;
     return p;
 }
 
 template <int KST, int VST, int DP>
 hipError_t launch_wide(const DecodeParams& p, const Plan& plan, hipStream_t stream) {
     const dim3 grid((unsigned)plan.blocks), block(64 * kWaves);
-    if (plan.wide == 1)
-        hipLaunchKernelGGL((k_decode<KST, VST, DP, 1>), grid, block, 0, stream, p);
-    else
-        hipLaunchKernelGGL((k_decode<KST, VST, DP, 2>), grid, block, 0, stream, p);
+    if constexpr (DP <= 128) {
+        if (plan.wide == 2) {
+            hipLaunchKernelGGL((k_decode<KST, VST, DP, 2>), grid, block, 0, stream, p);
+            return hipGetLastError();
+        }
+    }
+    hipLaunchKernelGGL((k_decode<KST, VST, DP, 1>), grid, block, 0, stream, p);
     return hipGetLastError();
 }
 
@@ -476,8 +541,8 @@ hipError_t launch_v(const DecodeParams& p, const Plan& plan, hipStream_t stream)
 
 int64_t decode_workspace(const AttnArgs& a) {
     const Plan p = plan_of(a);
-    if (p.splits <= 1) return 0;
-    const int64_t parts = (int64_t)a.kv.batch * a.q_heads * p.splits;
+    if (!p.joined) return 0;
+    const int64_t parts = (int64_t)(p.shares + a.kv.batch) * a.q_heads;
     return ((parts * 8 + 15) / 16) * 16 + parts * a.kv.head_dim * 4;
 }
 
@@ -486,8 +551,8 @@ hipError_t launch_decode(const AttnArgs& a) {
     DecodeParams p;
     p.kv = a.kv; p.q = a.q; p.ldq = a.ldq; p.q_heads = a.q_heads; p.group = a.q_heads / a.kv.heads;
     p.col_tiles = plan.col_tiles; p.scale_log2 = a.scale * kLog2e; p.window = a.window; p.sinks = a.sinks;
-    p.chunk = plan.chunk; p.splits = plan.splits; p.out = a.out; p.ldo = a.ldo; p.lse = a.lse;
-    const int64_t parts = (int64_t)a.kv.batch * a.q_heads * plan.splits;
+    p.shares = plan.shares; p.least = plan.least; p.out = a.out; p.ldo = a.ldo; p.lse = a.lse;
+    const int64_t parts = (int64_t)(plan.shares + a.kv.batch) * a.q_heads;
     p.part_ml = reinterpret_cast<float2*>(a.workspace);
     p.part_o = reinterpret_cast<float*>(a.workspace + ((parts * 8 + 15) / 16) * 16);
     hipError_t e;
@@ -496,7 +561,7 @@ hipError_t launch_decode(const AttnArgs& a) {
     case FP8_KV_E5M2: e = launch_v<kE5M2>(p, plan, a.stream); break;
     default: e = launch_v<kBf16>(p, plan, a.stream); break;
     }
-    if (e != hipSuccess || plan.splits <= 1) return e;
+    if (e != hipSuccess || !plan.joined) return e;
     hipLaunchKernelGGL(k_decode_join, dim3((unsigned)a.q_heads, (unsigned)a.kv.batch), dim3(kJoinThreads), 0, a.stream,
                        p);
     return hipGetLastError();

@@ -396,7 +396,8 @@ fp8_status fp8_kv_load(const void* cache, fp8_kv_storage storage, fp8_kv_scaling
  *     clamped to [0, max_len].
  * Requirements (else FP8_ERR_UNSUPPORTED_SHAPE / FP8_ERR_MISALIGNED):
  * page_size a power of two <= 2^20; head_dim % 16 == 0, 16 <= head_dim <= 256;
- * capacity and max_len < 2^31; batch <= 65535; caches 16-byte aligned. */
+ * capacity and max_len < 2^31; batch <= 65535, and batch * max_len < 2^35 for
+ * the attention; caches 16-byte aligned. */
 typedef struct fp8_kv_pair {
     void* k;
     void* v;
