@@ -599,10 +599,12 @@ def _kv_pair(k_cache, v_cache, page_table, lens, page_size, k_scale_inv, v_scale
 
 
 @functools.lru_cache(maxsize=1024)
-def _attention_workspace(heads, head_dim, page_size, batch, max_len, total_q, q_heads, window, sinks) -> int:
+def _attention_workspace(k_storage, heads, head_dim, page_size, batch, max_len, total_q, q_heads, window, sinks,
+                         weighted) -> int:
     """fp8_kv_attention_workspace of these sizes (it reads nothing else)."""
-    pair = _PAIR.pack(0, 0, 0, 0, 1, 0, max_len, 0, max_len, 0, 0, 0, heads, head_dim, page_size, batch, 0)
-    return _lib.lib().fp8_kv_attention_workspace(pair, total_q, q_heads, 0, window, sinks)
+    pair = _PAIR.pack(0, 0, 0, 0, 1, 0, max_len, 0, max_len, KV_STORAGE[k_storage], 0, 0, heads, head_dim, page_size,
+                      batch, 0)
+    return _lib.lib().fp8_kv_attention_workspace(pair, total_q, q_heads, 0, window, sinks, weighted)
 
 
 def _kv_weights(weights, batch: int, heads: int, least: int, device, name: str) -> int:
@@ -708,7 +710,8 @@ def kv_attention(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor, 
             raise ValueError("workspace must be a contiguous tensor on %s" % dev)
         ws_bytes = workspace.numel() * workspace.element_size()
     elif offsets is None and n == batch:
-        ws_bytes = _attention_workspace(heads, head_dim, page_size, batch, max_len, n, q_heads, window, sinks)
+        ws_bytes = _attention_workspace(k_storage, heads, head_dim, page_size, batch, max_len, n, q_heads, window,
+                                        sinks, weights is not None)
         if ws_bytes > 0:
             workspace = torch.empty(ws_bytes, dtype=torch.uint8, device=dev)
     st = _call_on(dev, _lib.lib().fp8_kv_attention, pair, q.data_ptr(), ldq, n, q_heads, offsets,

@@ -82,7 +82,7 @@ SIGNATURES = {
     "fp8_kv_load": (_INT, [_P, _INT, _INT, _P, _I64, _I32, _I32, _P, _I64, _INT, _P, _I64, _P]),
     "fp8_kv_attention": (_INT, [_P, _P, _I64, _I64, _I32, _P, ctypes.c_float, _I32, _I32, _P, _I64, _P, _P, _I64,
                                 _P, _I64, _P]),
-    "fp8_kv_attention_workspace": (_I64, [_P, _I64, _I32, _I32, _I32, _I32]),
+    "fp8_kv_attention_workspace": (_I64, [_P, _I64, _I32, _I32, _I32, _I32, _I32]),
     "fp8_kv_evict": (_INT, [_P, _P, _I64, _I32, _I32, _I32, _P, _I64, _P, _I64, _P, _P, _P]),
 }
 

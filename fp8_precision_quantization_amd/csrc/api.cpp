@@ -576,7 +576,7 @@ static fp8_status check_kv_pair(const fp8_kv_pair* c, bool sizes, fp8mi::KvView*
 }
 
 static fp8_status attention_args(const fp8_kv_pair* cache, bool sizes, int64_t total_q, int32_t q_heads, bool ragged,
-                                 int32_t window, int32_t sinks, fp8mi::AttnArgs* a) {
+                                 int32_t window, int32_t sinks, bool weighted, fp8mi::AttnArgs* a) {
     fp8_status st = check_kv_pair(cache, sizes, &a->kv);
     if (st != FP8_OK) return st;
     if (total_q < 0) return fail(FP8_ERR_INVALID_ARG, "negative size total_q=%lld", (long long)total_q);
@@ -593,7 +593,7 @@ static fp8_status attention_args(const fp8_kv_pair* cache, bool sizes, int64_t t
         return fail(FP8_ERR_INVALID_ARG, "window=%d and sinks=%d must be >= 0", (int)window, (int)sinks);
     if (cache->batch * cache->max_len >= (int64_t(1) << 35))
         return fail(FP8_ERR_UNSUPPORTED_SHAPE, "batch * max_len must be < 2^35");
-    a->total_q = total_q; a->q_heads = q_heads;
+    a->total_q = total_q; a->q_heads = q_heads; a->weighted = weighted;
     if (cache->capacity == 0) a->kv.max_len = 0;    // a cache without rows holds no token
     // a window that reaches every token is none; sinks past the end are all
     a->window = window >= cache->max_len ? 0 : window;
@@ -604,9 +604,10 @@ static fp8_status attention_args(const fp8_kv_pair* cache, bool sizes, int64_t t
 static bool one_each(const fp8mi::AttnArgs& a, bool ragged) { return !ragged && a.total_q == a.kv.batch; }
 
 int64_t fp8_kv_attention_workspace(const fp8_kv_pair* cache, int64_t total_q, int32_t q_heads, int32_t ragged,
-                                   int32_t window, int32_t sinks) {
+                                   int32_t window, int32_t sinks, int32_t weighted) {
     fp8mi::AttnArgs a;
-    if (attention_args(cache, true, total_q, q_heads, ragged != 0, window, sinks, &a) != FP8_OK) return -1;
+    if (attention_args(cache, true, total_q, q_heads, ragged != 0, window, sinks, weighted != 0, &a) != FP8_OK)
+        return -1;
     ok();
     return total_q > 0 && one_each(a, ragged != 0) ? fp8mi::decode_workspace(a) : 0;
 }
@@ -617,7 +618,7 @@ fp8_status fp8_kv_attention(const fp8_kv_pair* cache, const void* q, int64_t ldq
                             int64_t workspace_bytes, void* stream) {
     fp8mi::AttnArgs a;
     const bool ragged = q_offsets != nullptr;
-    fp8_status st = attention_args(cache, false, total_q, q_heads, ragged, window, sinks, &a);
+    fp8_status st = attention_args(cache, false, total_q, q_heads, ragged, window, sinks, weights != nullptr, &a);
     if (st != FP8_OK) return st;
     const int64_t width = (int64_t)q_heads * cache->head_dim;
     if (ldq < width || ldo < width)
@@ -654,9 +655,7 @@ fp8_status fp8_kv_attention(const fp8_kv_pair* cache, const void* q, int64_t ldq
     a.q = static_cast<const uint16_t*>(q); a.ldq = ldq; a.q_offsets = q_offsets; a.scale = scale;
     a.out = static_cast<uint16_t*>(out); a.ldo = ldo; a.lse = lse; a.weights = weights; a.ldw = ldw;
     a.workspace = static_cast<uint8_t*>(workspace); a.stream = (hipStream_t)stream;
-    st = launch_result(decode ? fp8mi::launch_decode(a) : fp8mi::launch_extend(a), "fp8_kv_attention");
-    if (st != FP8_OK || weights == nullptr) return st;
-    return launch_result(fp8mi::launch_attention_weights(a), "fp8_kv_attention (weights)");
+    return launch_result(decode ? fp8mi::launch_decode(a) : fp8mi::launch_extend(a), "fp8_kv_attention");
 }
 
 fp8_status fp8_kv_evict(const fp8_kv_pair* cache, float* weights, int64_t ldw, int32_t budget, int32_t sinks,

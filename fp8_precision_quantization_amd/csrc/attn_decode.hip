@@ -52,6 +52,10 @@ struct DecodeParams {
     float* lse;
     float2* part_ml;             // [shares + batch, q_heads]
     float* part_o;               // [shares + batch, q_heads, head_dim]
+    float* scores;               // null, or [batch, q_heads, span]: x_j of every token of every step
+    int64_t span;
+    float* weights;
+    int64_t ldw;
 };
 
 // How a batch's steps are shared out.  The sequences' steps lie one after the
@@ -267,6 +271,9 @@ __global__ __launch_bounds__(64 * kWaves, DP <= 128 && NT == 1 ? 2 : 1) void k_d
         entry = entry_of(st + 2);
         if (kAhead) load(next, row);
         if (cur.there == 0) {
+            if (a.scores && lane < kStep)
+                for (int col = head0; col < min(head0 + 16 * NT, a.group); ++col)
+                    a.scores[((int64_t)b * a.q_heads + h * a.group + col) * a.span + st * kStep + lane] = -INFINITY;
             if (!kAhead) load(next, row);
             continue;
         }
@@ -321,6 +328,17 @@ __global__ __launch_bounds__(64 * kWaves, DP <= 128 && NT == 1 ? 2 : 1) void k_d
                 for (int nt = 0; nt < NT; ++nt) x[nt][i] = hidden ? -INFINITY : x[nt][i];
 #pragma unroll
                 for (int w = 0; w < VW; ++w) cur.v[i].w[w] = hidden ? 0 : cur.v[i].w[w];
+            }
+        }
+        if (a.scores) {
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) {
+                const int col = head0 + nt * 16 + c;
+                if (col < a.group) {
+                    float* to = a.scores + ((int64_t)b * a.q_heads + h * a.group + col) * a.span + st * kStep + 4 * g;
+                    *reinterpret_cast<f4*>(to) = f4{x[nt][0], x[nt][1], x[nt][2], x[nt][3]};
+                    *reinterpret_cast<f4*>(to + 16) = f4{x[nt][4], x[nt][5], x[nt][6], x[nt][7]};
+                }
             }
         }
         // weights, as the B operand of the second product
@@ -436,11 +454,48 @@ __global__ __launch_bounds__(64 * kWaves, DP <= 128 && NT == 1 ? 2 : 1) void k_d
     }
 }
 
+// The maximum and sum of a query head's row over its sequence's n pieces,
+// 64 at a time; every lane returns them.
+__device__ __forceinline__ float2 join_ml(const float2* ml, int64_t next, int n, int lane) {
+    float m = kLowest, l = 0.0f;
+    for (int s = lane; s < n; s += 64) m = fmaxf(m, ml[s * next].x);
+#pragma unroll
+    for (int off = 1; off < 64; off <<= 1) m = fmaxf(m, __shfl_xor(m, off, 64));
+    for (int s = lane; s < n; s += 64) l += ml[s * next].y * __builtin_amdgcn_exp2f(ml[s * next].x - m);
+#pragma unroll
+    for (int off = 1; off < 64; off <<= 1) l += __shfl_xor(l, off, 64);
+    return make_float2(m, l);
+}
+
+constexpr int kJoinThreads = 256;
+
+// weights[b, h, j] += sum over the group of 2^(x_j - lse), one thread a token.
+__global__ __launch_bounds__(kJoinThreads) void k_decode_weights(const DecodeParams a) {
+    const int h = blockIdx.x % a.kv.heads, tile = blockIdx.x / a.kv.heads, b = blockIdx.y;
+    const int at = tile * kJoinThreads + threadIdx.x, lane = threadIdx.x & 63;
+    const int pos = seq_len(a.kv, b) - 1;
+    const Steps<kStep> steps(pos, pos, a.window, a.sinks);
+    if (tile * kJoinThreads >= steps.count * kStep) return;
+    const int j = steps.token(at / kStep) + at % kStep;
+    const bool seen = at < steps.count * kStep && sees(j, pos, a.window, a.sinks);
+    const int64_t hq0 = (int64_t)b * a.q_heads + h * a.group;
+    float w = 0.0f;
+    for (int g0 = 0; g0 < a.group; g0 += 64) {
+        const int gn = min(64, a.group - g0);
+        const float z = lane < gn ? a.lse[hq0 + g0 + lane] * kLog2e : 0.0f;
+#pragma unroll 4
+        for (int g = 0; g < gn; ++g) {
+            const float lse = as_f32(__builtin_amdgcn_readlane(__builtin_bit_cast(int, z), g));
+            const float x = seen ? a.scores[(hq0 + g0 + g) * a.span + at] : -INFINITY;
+            w += x == -INFINITY ? 0.0f : __builtin_amdgcn_exp2f(x - lse);
+        }
+    }
+    if (seen) a.weights[((int64_t)b * a.kv.heads + h) * a.ldw + j] += w;
+}
+
 // One block per (query head, sequence): joins the pieces of a sequence that
 // several shares hold, in their order.  Threads take 4 channels each, several
 // pieces side by side.
-constexpr int kJoinThreads = 256;
-
 __global__ __launch_bounds__(kJoinThreads) void k_decode_join(const DecodeParams a) {
     __shared__ f4 s_acc[kJoinThreads];
     const int hq = blockIdx.x, b = blockIdx.y;
@@ -450,14 +505,8 @@ __global__ __launch_bounds__(kJoinThreads) void k_decode_join(const DecodeParams
     const int D = a.kv.head_dim, quads = D >> 2;
     const int64_t part = (int64_t)(i0 + b) * a.q_heads + hq, next = a.q_heads;
     const float2* ml = a.part_ml + part;
-    const int lane = threadIdx.x & 63;
-    float m = kLowest, l = 0.0f;
-    for (int s = lane; s < n; s += 64) m = fmaxf(m, ml[s * next].x);
-#pragma unroll
-    for (int off = 1; off < 64; off <<= 1) m = fmaxf(m, __shfl_xor(m, off, 64));
-    for (int s = lane; s < n; s += 64) l += ml[s * next].y * __builtin_amdgcn_exp2f(ml[s * next].x - m);
-#pragma unroll
-    for (int off = 1; off < 64; off <<= 1) l += __shfl_xor(l, off, 64);
+    const float2 all = join_ml(ml, next, n, threadIdx.x & 63);
+    const float m = all.x, l = all.y;
     const int lanes = kJoinThreads / quads;             // pieces side by side (4 or more)
     const int side = threadIdx.x / quads, d = (threadIdx.x - side * quads) * 4;
     f4 acc = {0, 0, 0, 0};
@@ -483,7 +532,8 @@ __global__ __launch_bounds__(kJoinThreads) void k_decode_join(const DecodeParams
 struct Plan {
     int col_tiles, wide, shares, least;
     bool joined;                 // a sequence may lie in several shares
-    int64_t blocks;
+    bool scores;                 // the weights come from stored scores
+    int64_t blocks, span;        // span: tokens of the longest sequence's steps
 };
 
 Plan plan_of(const AttnArgs& a) {
@@ -504,6 +554,10 @@ Plan plan_of(const AttnArgs& a) {
     shares = shares < most ? shares : most;
     p.shares = (int)(shares < 1 ? 1 : shares);
     p.joined = steps > 1;
+    p.span = steps * kStep;
+    // a token's scores written and read again against its key read again
+    const int key = a.kv.head_dim * (a.kv.k_st == FP8_KV_BF16 ? 2 : 1);
+    p.scores = a.weighted && group * 8 <= key;
     p.blocks = ((p.shares + 7) / 8 * units + kWaves - 1) / kWaves * 8;
     return p;
 }
@@ -539,11 +593,20 @@ hipError_t launch_v(const DecodeParams& p, const Plan& plan, hipStream_t stream)
 
 }  // namespace
 
+// Bytes of the parts of the workspace: (m, l) and o of the pieces, scores.
+struct Parts {
+    int64_t ml = 0, o = 0, scores = 0;
+    Parts(const AttnArgs& a, const Plan& p) {
+        const int64_t pieces = p.joined ? (int64_t)(p.shares + a.kv.batch) * a.q_heads : 0;
+        ml = (pieces * 8 + 15) / 16 * 16;
+        o = pieces * a.kv.head_dim * 4;
+        scores = p.scores ? (int64_t)a.kv.batch * a.q_heads * p.span * 4 : 0;
+    }
+};
+
 int64_t decode_workspace(const AttnArgs& a) {
-    const Plan p = plan_of(a);
-    if (!p.joined) return 0;
-    const int64_t parts = (int64_t)(p.shares + a.kv.batch) * a.q_heads;
-    return ((parts * 8 + 15) / 16) * 16 + parts * a.kv.head_dim * 4;
+    const Parts parts(a, plan_of(a));
+    return parts.ml + parts.o + parts.scores;
 }
 
 hipError_t launch_decode(const AttnArgs& a) {
@@ -552,18 +615,28 @@ hipError_t launch_decode(const AttnArgs& a) {
     p.kv = a.kv; p.q = a.q; p.ldq = a.ldq; p.q_heads = a.q_heads; p.group = a.q_heads / a.kv.heads;
     p.col_tiles = plan.col_tiles; p.scale_log2 = a.scale * kLog2e; p.window = a.window; p.sinks = a.sinks;
     p.shares = plan.shares; p.least = plan.least; p.out = a.out; p.ldo = a.ldo; p.lse = a.lse;
-    const int64_t parts = (int64_t)(plan.shares + a.kv.batch) * a.q_heads;
+    const Parts parts(a, plan);
     p.part_ml = reinterpret_cast<float2*>(a.workspace);
-    p.part_o = reinterpret_cast<float*>(a.workspace + ((parts * 8 + 15) / 16) * 16);
+    p.part_o = reinterpret_cast<float*>(a.workspace + parts.ml);
+    p.scores = plan.scores ? reinterpret_cast<float*>(a.workspace + parts.ml + parts.o) : nullptr;
+    p.span = plan.span; p.weights = a.weights; p.ldw = a.ldw;
     hipError_t e;
     switch (a.kv.k_st) {
     case FP8_KV_E4M3: e = launch_v<kE4M3>(p, plan, a.stream); break;
     case FP8_KV_E5M2: e = launch_v<kE5M2>(p, plan, a.stream); break;
     default: e = launch_v<kBf16>(p, plan, a.stream); break;
     }
-    if (e != hipSuccess || !plan.joined) return e;
-    hipLaunchKernelGGL(k_decode_join, dim3((unsigned)a.q_heads, (unsigned)a.kv.batch), dim3(kJoinThreads), 0, a.stream,
-                       p);
+    if (e != hipSuccess) return e;
+    if (plan.joined) {
+        hipLaunchKernelGGL(k_decode_join, dim3((unsigned)a.q_heads, (unsigned)a.kv.batch), dim3(kJoinThreads), 0,
+                           a.stream, p);
+        e = hipGetLastError();
+    }
+    if (e != hipSuccess || !a.weighted) return e;
+    if (!plan.scores) return launch_attention_weights(a);
+    const unsigned tiles = (unsigned)((plan.span + kJoinThreads - 1) / kJoinThreads);
+    hipLaunchKernelGGL(k_decode_weights, dim3(tiles * (unsigned)a.kv.heads, (unsigned)a.kv.batch), dim3(kJoinThreads),
+                       0, a.stream, p);
     return hipGetLastError();
 }
 

@@ -654,11 +654,13 @@ ExtendParams params_of(const AttnArgs& a) {
 
 hipError_t launch_extend(const AttnArgs& a) {
     const ExtendParams p = params_of(a);
+    hipError_t e;
     switch (a.kv.k_st) {
-    case FP8_KV_E4M3: return extend_v<kE4M3>(p, a.stream);
-    case FP8_KV_E5M2: return extend_v<kE5M2>(p, a.stream);
-    default: return extend_v<kBf16>(p, a.stream);
+    case FP8_KV_E4M3: e = extend_v<kE4M3>(p, a.stream); break;
+    case FP8_KV_E5M2: e = extend_v<kE5M2>(p, a.stream); break;
+    default: e = extend_v<kBf16>(p, a.stream); break;
     }
+    return e != hipSuccess || !a.weighted ? e : launch_attention_weights(a);
 }
 
 hipError_t launch_attention_weights(const AttnArgs& a) {

@@ -133,6 +133,7 @@ struct AttnArgs {
     uint16_t* out = nullptr;
     int64_t ldo = 0;
     float* lse = nullptr;
+    bool weighted = false;                // weights are asked for (known before their address)
     float* weights = nullptr;
     int64_t ldw = 0;
     uint8_t* workspace = nullptr;
@@ -163,9 +164,9 @@ hipError_t launch_kv_load(const KvLoadArgs& a);
 // One query per sequence; the workspace's bytes follow the same rules as the
 // launch's splits.
 int64_t decode_workspace(const AttnArgs& a);
-hipError_t launch_decode(const AttnArgs& a);
-hipError_t launch_extend(const AttnArgs& a);
-hipError_t launch_attention_weights(const AttnArgs& a);   // after one of them: reads a.lse
+hipError_t launch_decode(const AttnArgs& a);              // weights included
+hipError_t launch_extend(const AttnArgs& a);              // weights included
+hipError_t launch_attention_weights(const AttnArgs& a);   // the weights alone, from the keys and a.lse
 hipError_t launch_evict(const EvictArgs& a);
 hipError_t launch_history_init(fp8_amax_history* h, int32_t len, hipStream_t stream);
 hipError_t launch_history_set_guard(fp8_amax_history* h, float threshold, hipStream_t stream);

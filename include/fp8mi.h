@@ -456,10 +456,11 @@ fp8_status fp8_kv_attention(const fp8_kv_pair* cache, const void* q, int64_t ldq
                             int64_t workspace_bytes, void* stream);
 
 /* Bytes of workspace fp8_kv_attention needs for these arguments (ragged:
- * q_offsets is not NULL), from sizes alone (no pointer is read); -1 if it
- * would reject them (see fp8_last_error). */
+ * q_offsets is not NULL; weighted: weights is not NULL), from the sizes,
+ * storage and scaling alone (no pointer is read); -1 if it would reject them
+ * (see fp8_last_error). */
 int64_t fp8_kv_attention_workspace(const fp8_kv_pair* cache, int64_t total_q, int32_t q_heads, int32_t ragged,
-                                   int32_t window, int32_t sinks);
+                                   int32_t window, int32_t sinks, int32_t weighted);
 
 /* Eviction by accumulated attention weight: a sequence of n = len_b > budget
  * tokens keeps, for every KV head by itself, its first `sinks` tokens, its

@@ -84,8 +84,8 @@ def test_attention(change, status, word):
 def test_attention_workspace():
     lib = L.lib()
 
-    def size(p, total=2, q_heads=32, ragged=0, window=0, sinks=0):
-        return lib.fp8_kv_attention_workspace(ctypes.byref(p), total, q_heads, ragged, window, sinks)
+    def size(p, total=2, q_heads=32, ragged=0, window=0, sinks=0, weighted=0):
+        return lib.fp8_kv_attention_workspace(ctypes.byref(p), total, q_heads, ragged, window, sinks, weighted)
 
     long = pair(max_len=65536, page_ld=4096)
     need = size(long)
@@ -95,13 +95,17 @@ def test_attention_workspace():
     check(attention(long, ws=FAKE + 8), M, "workspace")
     assert size(pair(max_len=32, page_ld=2)) == 0        # one split
     assert size(long, window=16) < need
+    weighted = size(long, weighted=1)                   # the scores too
+    assert weighted >= need + 2 * 32 * 65536 * 4
+    check(attention(long, wsb=weighted - 1, weights=FAKE, ldw=65536), I, "workspace_bytes")
+    assert size(long, q_heads=256, weighted=1) == size(long, q_heads=256)       # keys read again instead
     assert size(pair(batch=0), total=0) == 0
     # sizes alone: no pointer is needed
     assert size(pair(k=None, v=None, k_scale_inv=None, v_scale_inv=None, lens=None, page_table=None, max_len=65536,
                      page_ld=4096)) == need
     assert size(long, total=3) == -1 and "multiple of batch" in lib.fp8_last_error().decode()
     assert size(pair(page_size=3)) == -1
-    assert lib.fp8_kv_attention_workspace(None, 2, 32, 0, 0, 0) == -1
+    assert lib.fp8_kv_attention_workspace(None, 2, 32, 0, 0, 0, 0) == -1
 
 
 @pytest.mark.parametrize("change, status, word", [
