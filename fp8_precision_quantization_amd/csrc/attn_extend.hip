@@ -501,30 +501,75 @@ __global__ __launch_bounds__(kThreads, DP <= 128 ? 2 : 1) void k_extend(const Ex
         a.lse[(int64_t)(q_first + tok) * a.q_heads + hq] = l == 0.0f ? -INFINITY : (m + __builtin_amdgcn_logf(l)) * kLn2;
 }
 
-// Weights: a wave holds 32 tokens' K as the A operand and takes the rows 32
-// at a time as columns.
+// Weights: a wave holds 32 tokens' K as the A operand; a step's queries go
+// through LDS (read from memory row by row, as columns of the product they
+// would be 64 separate lines a load) and are shared by the block's four waves.
 template <int KST, int DP>
 __global__ __launch_bounds__(kThreads) void k_weights(const ExtendParams a) {
     constexpr int KM = DP / 16;
     constexpr int KC = DP * kElemBytes<KST> / 32;       // 16-byte pieces of K a lane holds
+    constexpr int R = DP <= 128 ? 64 : 32;              // rows of a step
+    constexpr int PR = DP / 8, PT = R * PR / kThreads;  // 16-byte pieces of a row, of a thread
+    constexpr int kQ = DP * 2 + 16;                     // bytes of a padded row
+    __shared__ __align__(16) uint8_t s_q[2][R * kQ];
+    __shared__ float s_lse[2][R];
+    __shared__ int s_pos[2][R];
     const KvView& kv = a.kv;
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int c = lane & 31, g = lane >> 5;
     const int h = blockIdx.x % kv.heads, b = blockIdx.y;
     const int len = seq_len(kv, b);
-    const int j0 = (int)(blockIdx.x / kv.heads) * kRows + wave * 32;
-    if (j0 >= len) return;
+    const int block0 = (int)(blockIdx.x / kv.heads) * kRows, j0 = block0 + wave * 32;
+    if (block0 >= len) return;
     int q_first, n;
     queries_of(a, b, &q_first, &n);
     const int G = a.group, D = kv.head_dim, base = len - n;
 
+    // rows (token of the call, head in the group) that see any of the block's tokens
+    int i_lo = block0 - base, i_hi = n;
+    if (a.window > 0 && block0 >= a.sinks) i_hi = min(i_hi, block0 + kRows - 1 + a.window - base);
+    i_lo = i_lo < 0 ? 0 : i_lo;
+    if (i_lo >= i_hi) return;
+    const int r_first = i_lo * G, r_end = i_hi * G;
+
+    // Q of a step into registers and from there into LDS; a row past the end
+    // reads the last one and has an infinite lse: it gives nothing.
+    uint4 qu[PT];
+    float lse = 0.0f;
+    int pos = 0;
+#pragma unroll
+    for (int u = 0; u < PT; ++u) qu[u] = make_uint4(0, 0, 0, 0);
+    auto load = [&](int r0) {
+#pragma unroll
+        for (int u = 0; u < PT; ++u) {
+            const int p = tid + u * kThreads, e = (p % PR) * 8;
+            const int r = min(r0 + p / PR, r_end - 1), tok = r / G, hq = h * G + (r - tok * G);
+            if (D == DP || e < D)
+                qu[u] = *reinterpret_cast<const uint4*>(a.q + (int64_t)(q_first + tok) * a.ldq + (int64_t)hq * D + e);
+        }
+        if (tid < R) {
+            const int r = min(r0 + tid, r_end - 1), tok = r / G, hq = h * G + (r - tok * G);
+            lse = a.lse[(int64_t)(q_first + tok) * a.q_heads + hq];
+            lse = r0 + tid >= r_end || lse == -INFINITY ? INFINITY : lse * kLog2e;
+            pos = base + tok;
+        }
+    };
+    auto put = [&](int i) {
+#pragma unroll
+        for (int u = 0; u < PT; ++u) {
+            const int p = tid + u * kThreads;
+            *reinterpret_cast<uint4*>(&s_q[i & 1][p / PR * kQ + p % PR * 16]) = qu[u];
+        }
+        if (tid < R) {
+            s_lse[i & 1][tid] = lse;
+            s_pos[i & 1][tid] = pos;
+        }
+    };
+    load(r_first);
+
     const int j = j0 + c;
     int row = -1;
-    if (j < len) {
-        const int entry = kv.table[b * kv.table_ld + (j >> kv.page_shift)];
-        row = entry >= 0 ? row_of_entry(kv, entry, j) : -1;
-    }
-    if (!__any(row >= 0)) return;
+    if (j < len) row = row_of_entry(kv, kv.table[b * kv.table_ld + (j >> kv.page_shift)], j);
     uint4 kr[KC];
 #pragma unroll
     for (int i = 0; i < KC; ++i) {
@@ -560,35 +605,39 @@ __global__ __launch_bounds__(kThreads) void k_weights(const ExtendParams a) {
         ks[e] = __shfl(sc, t, 64);
         there |= (__shfl(row, t, 64) >= 0 ? 1u : 0u) << e;
     }
-    // rows (token of the call, head in the group) that see any of these tokens
-    int i_lo = j0 - base, i_hi = n;
-    if (a.window > 0 && j0 >= a.sinks) i_hi = min(i_hi, j0 + 31 + a.window - base);
-    i_lo = i_lo < 0 ? 0 : i_lo;
     float w[16];
 #pragma unroll
     for (int e = 0; e < 16; ++e) w[e] = 0.0f;
-    const int r_end = i_hi * G;
-    for (int r0 = i_lo * G; r0 < r_end; r0 += 32) {
-        const int r = r0 + c;
-        const bool live = r < r_end;
-        const int tok = r / G, hq = h * G + (r - tok * G);
-        const uint16_t* qr = a.q + (int64_t)(q_first + tok) * a.ldq + (int64_t)hq * D;
-        f16v x = f16v{0};
+    put(0);
+    __syncthreads();
+    for (int i = 0, r0 = r_first; r0 < r_end; ++i, r0 += R) {
+        if (r0 + R < r_end) load(r0 + R);
 #pragma unroll
-        for (int s = 0; s < KM; ++s) {
-            const int e = KST == kBf16 ? s * 16 + g * 8 : (s >> 1) * 32 + g * 16 + (s & 1) * 8;
-            uint4 t = make_uint4(0, 0, 0, 0);
-            if (live && e < D) t = *reinterpret_cast<const uint4*>(qr + e);
-            x = __builtin_amdgcn_mfma_f32_32x32x16_bf16(kf[s], __builtin_bit_cast(b8, t), x, 0, 0, 0);
-        }
-        const float lse = live ? a.lse[(int64_t)(q_first + tok) * a.q_heads + hq] * kLog2e : -INFINITY;
-        const int pos = lse == -INFINITY ? -1 : base + tok;     // a row that sees nothing gives nothing
+        for (int half = 0; half < R / 32; ++half) {
+            const uint8_t* q = &s_q[i & 1][(half * 32 + c) * kQ];
+            f16v x = f16v{0};
 #pragma unroll
-        for (int e = 0; e < 16; ++e) {
-            const int t = j0 + (e >> 2) * 8 + g * 4 + (e & 3);
-            const float p = __builtin_amdgcn_exp2f(x[e] * ks[e] - lse);
-            w[e] += sees(t, pos, a.window, a.sinks) ? p : 0.0f;
+            for (int s = 0; s < KM; ++s) {
+                const int e = KST == kBf16 ? s * 16 + g * 8 : (s >> 1) * 32 + g * 16 + (s & 1) * 8;
+                const b8 qf = *reinterpret_cast<const b8*>(q + e * 2);
+                x = __builtin_amdgcn_mfma_f32_32x32x16_bf16(kf[s], qf, x, 0, 0, 0);
+            }
+            const float z = s_lse[i & 1][half * 32 + c];
+            const int p = s_pos[i & 1][half * 32 + c], lo = a.window > 0 ? p - a.window + 1 : 0;
+            if (__all(j0 + 31 <= p && (j0 >= lo || j0 + 31 < a.sinks))) {
+#pragma unroll
+                for (int e = 0; e < 16; ++e) w[e] += __builtin_amdgcn_exp2f(__builtin_fmaf(x[e], ks[e], -z));
+            } else {
+#pragma unroll
+                for (int e = 0; e < 16; ++e) {
+                    const int t = j0 + (e >> 2) * 8 + g * 4 + (e & 3);
+                    const bool seen = (t <= p) & ((t >= lo) | (t < a.sinks));
+                    w[e] += seen ? __builtin_amdgcn_exp2f(__builtin_fmaf(x[e], ks[e], -z)) : 0.0f;
+                }
+            }
         }
+        if (r0 + R < r_end) put(i + 1);
+        __syncthreads();
     }
     float* to = a.weights + ((int64_t)b * kv.heads + h) * a.ldw;
 #pragma unroll

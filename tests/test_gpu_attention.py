@@ -442,3 +442,15 @@ def test_scales_not_finite_where_not_seen(n):
     touched = np.zeros(o.shape, bool)
     touched[n - 1, 2:] = True
     assert np.abs(o - want)[~touched].max() < 0.05 * np.abs(want).max()
+
+
+@pytest.mark.parametrize("n", [[1, 1], [3, 90]])
+@pytest.mark.parametrize("group", [1, 5, 16, 33, 70])
+def test_weights_groups(group, n):
+    """Small and large groups (weights from stored scores, and from the keys read again)."""
+    c = ref.Cache([210, 135], 2, 64, 16, seed=group)
+    w0 = torch.rand(2, 2, c.max_len, generator=torch.Generator().manual_seed(5)).cuda()
+    w = w0.clone()
+    q, out, lse = _run(c, n, 2 * group, 70, 5, weights=w)
+    want, delta, acc = ref.check_attention(c, q, n, out, lse, 70, 5)
+    _check_weights(c, [x * group for x in n], w0, w, want, delta, acc)
