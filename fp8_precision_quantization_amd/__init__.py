@@ -599,12 +599,12 @@ def _kv_pair(k_cache, v_cache, page_table, lens, page_size, k_scale_inv, v_scale
 
 
 @functools.lru_cache(maxsize=1024)
-def _attention_workspace(k_storage, heads, head_dim, page_size, batch, max_len, total_q, q_heads, window, sinks,
-                         weighted) -> int:
+def _attention_workspace(k_storage, heads, head_dim, page_size, batch, max_len, total_q, q_heads, ragged, window,
+                         sinks, weighted) -> int:
     """fp8_kv_attention_workspace of these sizes (it reads nothing else)."""
     pair = _PAIR.pack(0, 0, 0, 0, 1, 0, max_len, 0, max_len, KV_STORAGE[k_storage], 0, 0, heads, head_dim, page_size,
                       batch, 0)
-    return _lib.lib().fp8_kv_attention_workspace(pair, total_q, q_heads, 0, window, sinks, weighted)
+    return _lib.lib().fp8_kv_attention_workspace(pair, total_q, q_heads, ragged, window, sinks, weighted)
 
 
 def _kv_weights(weights, batch: int, heads: int, least: int, device, name: str) -> int:
@@ -709,9 +709,9 @@ def kv_attention(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor, 
         if not isinstance(workspace, torch.Tensor) or workspace.device != dev or not workspace.is_contiguous():
             raise ValueError("workspace must be a contiguous tensor on %s" % dev)
         ws_bytes = workspace.numel() * workspace.element_size()
-    elif offsets is None and n == batch:
-        ws_bytes = _attention_workspace(k_storage, heads, head_dim, page_size, batch, max_len, n, q_heads, window,
-                                        sinks, weights is not None)
+    else:
+        ws_bytes = _attention_workspace(k_storage, heads, head_dim, page_size, batch, max_len, n, q_heads,
+                                        offsets is not None, window, sinks, weights is not None)
         if ws_bytes > 0:
             workspace = torch.empty(ws_bytes, dtype=torch.uint8, device=dev)
     st = _call_on(dev, _lib.lib().fp8_kv_attention, pair, q.data_ptr(), ldq, n, q_heads, offsets,

@@ -603,13 +603,18 @@ static fp8_status attention_args(const fp8_kv_pair* cache, bool sizes, int64_t t
 
 static bool one_each(const fp8mi::AttnArgs& a, bool ragged) { return !ragged && a.total_q == a.kv.batch; }
 
+static int64_t attention_bytes(const fp8mi::AttnArgs& a, bool ragged) {
+    if (a.total_q == 0) return 0;
+    return one_each(a, ragged) ? fp8mi::decode_workspace(a) : fp8mi::extend_workspace(a, ragged);
+}
+
 int64_t fp8_kv_attention_workspace(const fp8_kv_pair* cache, int64_t total_q, int32_t q_heads, int32_t ragged,
                                    int32_t window, int32_t sinks, int32_t weighted) {
     fp8mi::AttnArgs a;
     if (attention_args(cache, true, total_q, q_heads, ragged != 0, window, sinks, weighted != 0, &a) != FP8_OK)
         return -1;
     ok();
-    return total_q > 0 && one_each(a, ragged != 0) ? fp8mi::decode_workspace(a) : 0;
+    return attention_bytes(a, ragged != 0);
 }
 
 fp8_status fp8_kv_attention(const fp8_kv_pair* cache, const void* q, int64_t ldq, int64_t total_q, int32_t q_heads,
@@ -638,8 +643,7 @@ fp8_status fp8_kv_attention(const fp8_kv_pair* cache, const void* q, int64_t ldq
     if (weights != nullptr && ldw < cache->max_len)
         return fail(FP8_ERR_INVALID_ARG, "ldw=%lld must be >= max_len=%lld", (long long)ldw,
                     (long long)cache->max_len);
-    const bool decode = one_each(a, ragged);
-    const int64_t need = total_q > 0 && decode ? fp8mi::decode_workspace(a) : 0;
+    const int64_t need = attention_bytes(a, ragged);
     if (need > 0) {
         if (workspace == nullptr)
             return fail(FP8_ERR_INVALID_ARG, "workspace is NULL (this call needs %lld bytes)", (long long)need);
@@ -655,7 +659,7 @@ fp8_status fp8_kv_attention(const fp8_kv_pair* cache, const void* q, int64_t ldq
     a.q = static_cast<const uint16_t*>(q); a.ldq = ldq; a.q_offsets = q_offsets; a.scale = scale;
     a.out = static_cast<uint16_t*>(out); a.ldo = ldo; a.lse = lse; a.weights = weights; a.ldw = ldw;
     a.workspace = static_cast<uint8_t*>(workspace); a.stream = (hipStream_t)stream;
-    return launch_result(decode ? fp8mi::launch_decode(a) : fp8mi::launch_extend(a), "fp8_kv_attention");
+    return launch_result(one_each(a, ragged) ? fp8mi::launch_decode(a) : fp8mi::launch_extend(a), "fp8_kv_attention");
 }
 
 fp8_status fp8_kv_evict(const fp8_kv_pair* cache, float* weights, int64_t ldw, int32_t budget, int32_t sinks,

@@ -59,6 +59,9 @@ struct ExtendParams {
     float* lse;
     float* weights;
     int64_t ldw;
+    int splits;                  // blocks that may share a row tile's steps
+    float2* part_ml;             // [total_q * q_heads, splits]
+    float* part_o;               // [total_q * q_heads, splits, head_dim]
 };
 
 // Queries of sequence b: the first and their number, inside [0, total_q].
@@ -79,6 +82,38 @@ __device__ __forceinline__ void queries_of(const ExtendParams& a, int b, int* fi
 __device__ __forceinline__ int first_slot(const ExtendParams& a, int b) {
     if (a.q_offsets == nullptr) return b * ((a.each * a.group + kRows - 1) / kRows);
     return min(max(a.q_offsets[b], 0), a.total_q) * a.group / kRows + b;
+}
+
+// The row tile of a slot: its sequence, rows [row0, row0 + kRows) of that
+// sequence's rows, the positions of its first and last token.
+struct Tile {
+    int b = 0, q_first, rows, row0, base, p_first, p_last;
+    __device__ __forceinline__ Tile(const ExtendParams& a, int slot) {
+        // first_slot increases: halve down to 64 sequences, then one look
+        int hi = a.kv.batch;
+        while (hi - b > 64) {
+            const int mid = (b + hi) >> 1;
+            if (first_slot(a, mid) <= slot) b = mid; else hi = mid;
+        }
+        const int lane = threadIdx.x & 63;
+        const uint64_t at = __ballot(b + lane < hi && first_slot(a, min(b + lane, hi - 1)) <= slot);
+        if (at) b += 63 - __builtin_clzll(at);
+        int n;
+        queries_of(a, b, &q_first, &n);
+        row0 = (slot - first_slot(a, b)) * kRows;
+        rows = n * a.group;
+        base = seq_len(a.kv, b) - n;
+        p_first = base + row0 / a.group;
+        p_last = base + (min(row0 + kRows, rows) - 1) / a.group;
+    }
+    __device__ __forceinline__ bool any() const { return row0 >= 0 && row0 < rows; }
+};
+
+// Steps of one block of a row tile: an even part, and no fewer than kLeast.
+constexpr int kLeast = 4;
+__device__ __forceinline__ int chunk_of(const ExtendParams& a, int steps) {
+    const int even = (steps + a.splits - 1) / a.splits;
+    return even < kLeast ? kLeast : even;
 }
 
 template <int DP>
@@ -189,24 +224,16 @@ __global__ __launch_bounds__(kThreads, DP <= 128 ? 2 : 1) void k_extend(const Ex
     const KvView& kv = a.kv;
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
     const int c = lane & 31, g = lane >> 5;
-    const int h = blockIdx.x % kv.heads;
-    // the sequence whose slots hold this tile; later (longer) tiles first
-    const int slot = (int)(gridDim.x / kv.heads - 1 - blockIdx.x / kv.heads);
-    int b = 0;
-    for (int hi = kv.batch; hi - b > 1;) {
-        const int mid = (b + hi) >> 1;
-        if (first_slot(a, mid) <= slot) b = mid; else hi = mid;
-    }
-    int q_first, n;
-    queries_of(a, b, &q_first, &n);
-    const int row0 = (slot - first_slot(a, b)) * kRows, rows = n * a.group;
-    if (row0 < 0 || row0 >= rows) return;
-
-    const int len = seq_len(kv, b), base = len - n;
+    const int h = blockIdx.x % kv.heads, split = blockIdx.x / kv.heads % a.splits;
+    // later (longer) tiles first
+    const Tile tile(a, (int)(gridDim.x / kv.heads / a.splits - 1 - blockIdx.x / kv.heads / a.splits));
+    if (!tile.any()) return;
+    const int b = tile.b, q_first = tile.q_first, rows = tile.rows, row0 = tile.row0, base = tile.base;
+    const int p_first = tile.p_first, p_last = tile.p_last;
     const int G = a.group, D = kv.head_dim;
-    const int r_last = min(row0 + kRows, rows) - 1;
-    const int p_first = base + row0 / G, p_last = base + r_last / G;
     const Steps<kStep> steps(p_first, p_last, a.window, a.sinks);
+    const int chunk = chunk_of(a, steps.count), s_begin = split * chunk, s_end = min(s_begin + chunk, steps.count);
+    if (s_begin >= steps.count && split > 0) return;
 
     // this lane's row
     const int r = row0 + wave * 32 + c;
@@ -249,7 +276,7 @@ __global__ __launch_bounds__(kThreads, DP <= 128 ? 2 : 1) void k_extend(const Ex
         vu[u].clear();
     }
     auto entry_of = [&](int i) -> int {         // threads 0..63: the page of a step's token
-        if (tid >= kStep || i >= steps.count) return -1;
+        if (tid >= kStep || i >= s_end) return -1;
         const int j = steps.token(i) + tid;
         return j <= p_last ? table[j >> kv.page_shift] : -1;
     };
@@ -296,17 +323,17 @@ __global__ __launch_bounds__(kThreads, DP <= 128 ? 2 : 1) void k_extend(const Ex
         if (tid < 2 * kStep) (tid < kStep ? buf.ks : buf.vs)[tid & (kStep - 1)] = sc;
     };
 
-    if (steps.count > 0) {
+    if (s_begin < s_end) {
         if (tid < kMarks / 32) lds.bad[tid] = 0;
-        put_row(0, entry_of(0));
-        put_row(1, entry_of(1));
+        put_row(s_begin, entry_of(s_begin));
+        put_row(s_begin + 1, entry_of(s_begin + 1));
         __syncthreads();
-        load(0);
-        put(0);
+        load(s_begin);
+        put(s_begin);
         __syncthreads();
     }
-    for (int i = 0; i < steps.count; ++i) {
-        const bool more = i + 1 < steps.count;
+    for (int i = s_begin; i < s_end; ++i) {
+        const bool more = i + 1 < s_end;
         if (more) load(i + 1);
         const int entry = entry_of(i + 2);
         const typename L::Buf& buf = lds.buf[i & 1];
@@ -383,7 +410,7 @@ __global__ __launch_bounds__(kThreads, DP <= 128 ? 2 : 1) void k_extend(const Ex
             for (int t = 0; t < 2; ++t)
 #pragma unroll
                 for (int e = 0; e < 16; ++e) x[t][e] -= up;
-            if (i > 0) {
+            if (i > s_begin) {
 #pragma unroll
                 for (int d = 0; d < DT; ++d)
 #pragma unroll
@@ -450,9 +477,9 @@ __global__ __launch_bounds__(kThreads, DP <= 128 ? 2 : 1) void k_extend(const Ex
 
     l = sum_xor32(l);
     uint32_t met = 0;
-    if (steps.count > 0 && lane < kMarks / 32) met = lds.bad[lane];
+    if (s_begin < s_end && lane < kMarks / 32) met = lds.bad[lane];
     if (__any(met != 0)) {
-        for (int i = 0; i < steps.count; ++i) {
+        for (int i = s_begin; i < s_end; ++i) {
             if (!(lds.bad[i % kMarks / 32] >> (i % 32) & 1)) continue;
             for (int j = steps.token(i); j < steps.token(i) + kStep && j <= p_last; ++j) {
                 const int row = row_of_entry(kv, table[j >> kv.page_shift], j);
@@ -485,6 +512,21 @@ __global__ __launch_bounds__(kThreads, DP <= 128 ? 2 : 1) void k_extend(const Ex
         }
     }
     if (!live) return;
+    const int64_t row = (int64_t)(q_first + tok) * a.q_heads + hq;
+    if (chunk < steps.count) {                  // one of several blocks of this tile
+        if (g == 0) a.part_ml[row * a.splits + split] = make_float2(limit == kLowest ? kLowest : m, l);
+        float* to = a.part_o + (row * a.splits + split) * D;
+#pragma unroll
+        for (int d = 0; d < DT; ++d)
+#pragma unroll
+            for (int u = 0; u < 4; ++u) {
+                const int ch = channel_of<DP>(d * 4 + u) + g * 4;
+                if (ch < D)
+                    *reinterpret_cast<f4*>(to + ch) =
+                        f4{o[d][u * 4], o[d][u * 4 + 1], o[d][u * 4 + 2], o[d][u * 4 + 3]};
+            }
+        return;
+    }
     const float inv = l == 0.0f ? 0.0f : 1.0f / l;
     uint16_t* to = a.out + (int64_t)(q_first + tok) * a.ldo + (int64_t)hq * D;
 #pragma unroll
@@ -497,8 +539,42 @@ __global__ __launch_bounds__(kThreads, DP <= 128 ? 2 : 1) void k_extend(const Ex
                     make_uint2(pack2(o[d][u * 4] * inv, o[d][u * 4 + 1] * inv),
                                pack2(o[d][u * 4 + 2] * inv, o[d][u * 4 + 3] * inv));
         }
-    if (g == 0 && a.lse)
-        a.lse[(int64_t)(q_first + tok) * a.q_heads + hq] = l == 0.0f ? -INFINITY : (m + __builtin_amdgcn_logf(l)) * kLn2;
+    if (g == 0 && a.lse) a.lse[row] = l == 0.0f ? -INFINITY : (m + __builtin_amdgcn_logf(l)) * kLn2;
+}
+
+// Joins the blocks of a row tile in their order; threads take 4 channels of a
+// row each.
+constexpr int kJoinRows = 16;
+
+__global__ __launch_bounds__(kThreads) void k_extend_join(const ExtendParams a) {
+    const int h = blockIdx.x % a.kv.heads;
+    const Tile tile(a, blockIdx.x / a.kv.heads);
+    if (!tile.any()) return;
+    const Steps<kStep> steps(tile.p_first, tile.p_last, a.window, a.sinks);
+    const int chunk = chunk_of(a, steps.count);
+    if (chunk >= steps.count) return;
+    const int n = (steps.count + chunk - 1) / chunk;
+    const int D = a.kv.head_dim, quads = D >> 2;
+    const int r0 = tile.row0 + blockIdx.y * kJoinRows, rn = min(r0 + kJoinRows, tile.rows) - r0;
+    for (int i = threadIdx.x; i < rn * quads; i += kThreads) {
+        const int r = r0 + i / quads, d = i % quads * 4;
+        const int tok = tile.q_first + r / a.group, hq = h * a.group + r % a.group;
+        const int64_t row = (int64_t)tok * a.q_heads + hq;
+        const float2* ml = a.part_ml + row * a.splits;
+        float m = kLowest, l = 0.0f;
+        for (int s = 0; s < n; ++s) m = fmaxf(m, ml[s].x);
+        f4 acc = {0, 0, 0, 0};
+#pragma unroll 4
+        for (int s = 0; s < n; ++s) {
+            const float f = __builtin_amdgcn_exp2f(ml[s].x - m);
+            l += ml[s].y * f;
+            acc += *reinterpret_cast<const f4*>(a.part_o + (row * a.splits + s) * D + d) * f;
+        }
+        const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+        *reinterpret_cast<uint2*>(a.out + (int64_t)tok * a.ldo + (int64_t)hq * D + d) =
+            make_uint2(pack2(acc[0] * inv, acc[1] * inv), pack2(acc[2] * inv, acc[3] * inv));
+        if (d == 0 && a.lse) a.lse[row] = l == 0.0f ? -INFINITY : (m + __builtin_amdgcn_logf(l)) * kLn2;
+    }
 }
 
 // Weights: a wave holds 32 tokens' K as the A operand; a step's queries go
@@ -649,6 +725,12 @@ __global__ __launch_bounds__(kThreads) void k_weights(const ExtendParams a) {
     }
 }
 
+// total_q * q_heads < 2^31: a tile count is far inside int
+int tiles_of(const ExtendParams& p) {
+    return p.q_offsets == nullptr ? p.kv.batch * ((p.each * p.group + kRows - 1) / kRows)
+                                  : p.total_q * p.group / kRows + p.kv.batch;
+}
+
 template <int KST, int VST, int DP>
 hipError_t run_extend(const ExtendParams& p, hipStream_t stream) {
     static_assert(sizeof(Lds<DP>) <= 160 * 1024, "LDS");
@@ -656,10 +738,12 @@ hipError_t run_extend(const ExtendParams& p, hipStream_t stream) {
     hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(&k_extend<KST, VST, DP>),
                                        hipFuncAttributeMaxDynamicSharedMemorySize, bytes);
     if (e != hipSuccess) return e;
-    // total_q * q_heads < 2^31: a tile count is far inside int
-    const int tiles = p.q_offsets == nullptr ? p.kv.batch * ((p.each * p.group + kRows - 1) / kRows)
-                                             : p.total_q * p.group / kRows + p.kv.batch;
-    hipLaunchKernelGGL((k_extend<KST, VST, DP>), dim3((unsigned)(tiles * p.kv.heads)), dim3(kThreads), bytes, stream,
+    const int tiles = tiles_of(p);
+    hipLaunchKernelGGL((k_extend<KST, VST, DP>), dim3((unsigned)(tiles * p.kv.heads * p.splits)), dim3(kThreads), bytes,
+                       stream, p);
+    e = hipGetLastError();
+    if (e != hipSuccess || p.splits == 1) return e;
+    hipLaunchKernelGGL(k_extend_join, dim3((unsigned)(tiles * p.kv.heads), kRows / kJoinRows), dim3(kThreads), 0, stream,
                        p);
     return hipGetLastError();
 }
@@ -696,13 +780,44 @@ ExtendParams params_of(const AttnArgs& a) {
     p.group = a.q_heads / a.kv.heads; p.q_offsets = a.q_offsets; p.scale_log2 = a.scale * kLog2e;
     p.window = a.window; p.sinks = a.sinks; p.out = a.out; p.ldo = a.ldo; p.lse = a.lse;
     p.weights = a.weights; p.ldw = a.ldw;
+    p.splits = 1; p.part_ml = nullptr; p.part_o = nullptr;
     return p;
+}
+
+// Blocks that share a row tile's steps: 1 where the tiles alone are two rounds
+// of blocks, else as many as make up these (1024 blocks measured 68 us against
+// 73 for 512 and 103 unsplit, 12 sequences of up to 77 queries and 3001
+// tokens), of at least 2 * kLeast steps in the longest sequence.
+int splits_of(const AttnArgs& a, bool ragged) {
+    const int64_t group = a.q_heads / a.kv.heads, each = a.total_q / a.kv.batch;
+    const int64_t tiles = ragged ? a.total_q * group / kRows + a.kv.batch
+                                 : a.kv.batch * ((each * group + kRows - 1) / kRows);
+    const int64_t blocks = tiles * a.kv.heads;
+    int64_t steps = (a.kv.max_len + kStep - 1) / kStep;
+    if (a.window > 0) {
+        // a tile's tokens, their window and the sinks
+        const int64_t span = kRows / group + 1 + a.window, seen = (span + kStep - 1) / kStep + 1 + (a.sinks + kStep - 1) / kStep;
+        steps = seen < steps ? seen : steps;
+    }
+    int64_t s = 1024 / blocks;
+    const int64_t most = steps / (2 * kLeast);
+    s = s < most ? s : most;
+    return (int)(s < 1 ? 1 : s);
 }
 
 }  // namespace
 
+int64_t extend_workspace(const AttnArgs& a, bool ragged) {
+    const int64_t s = splits_of(a, ragged), rows = a.total_q * a.q_heads;
+    return s == 1 ? 0 : (rows * s * 8 + 15) / 16 * 16 + rows * s * a.kv.head_dim * 4;
+}
+
 hipError_t launch_extend(const AttnArgs& a) {
-    const ExtendParams p = params_of(a);
+    ExtendParams p = params_of(a);
+    p.splits = splits_of(a, a.q_offsets != nullptr);
+    const int64_t rows = a.total_q * a.q_heads;
+    p.part_ml = reinterpret_cast<float2*>(a.workspace);
+    p.part_o = reinterpret_cast<float*>(a.workspace + (rows * p.splits * 8 + 15) / 16 * 16);
     hipError_t e;
     switch (a.kv.k_st) {
     case FP8_KV_E4M3: e = extend_v<kE4M3>(p, a.stream); break;

@@ -161,9 +161,10 @@ hipError_t launch_quantize_multi(const MultiQuantArgs& a);
 hipError_t static_workspace(uint32_t** out);
 hipError_t launch_kv_store(const KvStoreArgs& a);
 hipError_t launch_kv_load(const KvLoadArgs& a);
-// One query per sequence; the workspace's bytes follow the same rules as the
-// launch's splits.
+// One query per sequence (decode) or several; the workspace's bytes follow the
+// same rules as the launch's splits.
 int64_t decode_workspace(const AttnArgs& a);
+int64_t extend_workspace(const AttnArgs& a, bool ragged);
 hipError_t launch_decode(const AttnArgs& a);              // weights included
 hipError_t launch_extend(const AttnArgs& a);              // weights included
 hipError_t launch_attention_weights(const AttnArgs& a);   // the weights alone, from the keys and a.lse
