@@ -126,7 +126,7 @@ struct Lds {
         alignas(16) float vs[kStep];
     };
     Buf buf[2];
-    alignas(16) int row[3][kStep];
+    alignas(16) int row[4][kStep];
     uint32_t bad[kMarks / 32];      // step i marks bit i % kMarks
 };
 
@@ -281,10 +281,10 @@ __global__ __launch_bounds__(kThreads, DP <= 128 ? 2 : 1) void k_extend(const Ex
         return j <= p_last ? table[j >> kv.page_shift] : -1;
     };
     auto put_row = [&](int i, int entry) {
-        if (tid < kStep) lds.row[i % 3][tid] = entry >= 0 ? row_of_entry(kv, entry, steps.token(i) + tid) : -1;
+        if (tid < kStep) lds.row[i & 3][tid] = entry >= 0 ? row_of_entry(kv, entry, steps.token(i) + tid) : -1;
     };
     auto load = [&](int i) {                    // a step's K, V and scales into registers
-        const int* rows_i = lds.row[i % 3];
+        const int* rows_i = lds.row[i & 3];
 #pragma unroll
         for (int u = 0; u < UT; ++u) {
             const int t = (tid + u * kThreads) / UR, e = ((tid + u * kThreads) % UR) * 16;
@@ -312,7 +312,7 @@ __global__ __launch_bounds__(kThreads, DP <= 128 ? 2 : 1) void k_extend(const Ex
 #pragma unroll
         for (int u = 0; u < UT; ++u) {
             const int t = (tid + u * kThreads) / UR, e = (tid + u * kThreads) % UR;
-            if (vu[u].clean() && lds.row[i % 3][t] >= 0) mark(i);
+            if (vu[u].clean() && lds.row[i & 3][t] >= 0) mark(i);
             ku[u].put(buf.k + t * L::kK + e * 16, UR * 16);
             vu[u].put(buf.v + t * L::kV + e * 16, UR * 16);
         }
@@ -323,64 +323,65 @@ __global__ __launch_bounds__(kThreads, DP <= 128 ? 2 : 1) void k_extend(const Ex
         if (tid < 2 * kStep) (tid < kStep ? buf.ks : buf.vs)[tid & (kStep - 1)] = sc;
     };
 
+    // Rows are known three steps ahead, K and V are in registers one step ahead
+    // and in LDS the step before they are needed.
+    int entry = 0;
     if (s_begin < s_end) {
         if (tid < kMarks / 32) lds.bad[tid] = 0;
         put_row(s_begin, entry_of(s_begin));
         put_row(s_begin + 1, entry_of(s_begin + 1));
+        put_row(s_begin + 2, entry_of(s_begin + 2));
+        entry = entry_of(s_begin + 3);
         __syncthreads();
         load(s_begin);
         put(s_begin);
+        if (s_begin + 1 < s_end) load(s_begin + 1);
         __syncthreads();
     }
     for (int i = s_begin; i < s_end; ++i) {
-        const bool more = i + 1 < s_end;
-        if (more) load(i + 1);
-        const int entry = entry_of(i + 2);
         const typename L::Buf& buf = lds.buf[i & 1];
+        const int* rows_i = lds.row[i & 3];
         const int j0 = steps.token(i);
-
-        // Both products run their LDS reads two matrix steps ahead; the
-        // scheduling barriers keep the compiler from packing reads and
-        // products back together when registers are short.
-        const int* rows_i = lds.row[i % 3];
         const bool there = rows_i[lane] >= 0;
+
+        // The step in halves of 32 tokens, so that matrix products of one run
+        // beside the exponentials of the other:
+        //   S0 = K0 Q | S1 = K1 Q with P0 = 2^S0 | O += V0 P0 with P1 = 2^S1 | O += V1 P1
+        // LDS reads run a few products ahead; the scheduling barriers keep
+        // this order.
+        b8 kf[4];
+        auto read_k = [&](int n) {
+            kf[n & 3] = *reinterpret_cast<const b8*>(buf.k + (n / KM * 32 + c) * L::kK + n % KM * 32 + g * 16);
+        };
+        read_k(0);
+        read_k(1);
+        read_k(2);
+        if (i + 1 < s_end) put(i + 1);
+        if (i + 2 < s_end) load(i + 2);
+        put_row(i + 3, entry);
+        entry = entry_of(i + 4);
+
+        const bool edge = j0 + kStep - 1 > p_first ||
+                          (a.window > 0 && j0 <= p_last - a.window && j0 + kStep - 1 >= a.sinks);
+        const bool masked = edge || !__all(there);
         f16v x[2];
-        x[0] = f16v{0};
-        x[1] = f16v{0};
-        {
-            b8 kf[3][2];
-            auto read_k = [&](int s) {
-#pragma unroll
-                for (int t = 0; t < 2; ++t)
-                    kf[s % 3][t] = *reinterpret_cast<const b8*>(buf.k + (t * 32 + c) * L::kK + s * 32 + g * 16);
-            };
-            read_k(0);
-            read_k(1);
-#pragma unroll
-            for (int s = 0; s < KM; ++s) {
-                if (s + 2 < KM) read_k(s + 2);
-                __builtin_amdgcn_sched_barrier(0);
-#pragma unroll
-                for (int t = 0; t < 2; ++t)
-                    x[t] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(kf[s % 3][t], qf[s], x[t], 0, 0, 0);
-            }
-        }
-        // scores against the row's reference m (0 until the row has seen a token)
-#pragma unroll
-        for (int t = 0; t < 2; ++t)
+        uint32_t pw[16];            // the weights as bf16 pairs, 4 words a B operand
+        float part[2] = {0, 0};
+        f4 vs[4];
+        // scores of half t against the row's reference m (0 until the row has
+        // seen a token), masked; the reference moves if one passes the limit
+        auto scores = [&](int t) {
 #pragma unroll
             for (int u = 0; u < 4; ++u) {
                 f4 ks = f4{a.scale_log2, a.scale_log2, a.scale_log2, a.scale_log2};
                 if (KST != kBf16) ks = *reinterpret_cast<const f4*>(&buf.ks[t * 32 + u * 8 + g * 4]);
+                vs[u] = f4{1, 1, 1, 1};
+                if (VST != kBf16) vs[u] = *reinterpret_cast<const f4*>(&buf.vs[t * 32 + u * 8 + g * 4]);
 #pragma unroll
                 for (int e = 0; e < 4; ++e) x[t][u * 4 + e] = __builtin_fmaf(x[t][u * 4 + e], ks[e], -m);
             }
-        const bool edge = j0 + kStep - 1 > p_first ||
-                          (a.window > 0 && j0 <= p_last - a.window && j0 + kStep - 1 >= a.sinks);
-        if (edge || !__all(there)) {
-            const int lo = a.window > 0 ? pos - a.window + 1 : 0;
-#pragma unroll
-            for (int t = 0; t < 2; ++t)
+            if (masked) {
+                const int lo = a.window > 0 ? pos - a.window + 1 : 0;
 #pragma unroll
                 for (int u = 0; u < 4; ++u) {
                     const int at = t * 32 + u * 8 + g * 4;
@@ -393,85 +394,91 @@ __global__ __launch_bounds__(kThreads, DP <= 128 ? 2 : 1) void k_extend(const Ex
                         x[t][u * 4 + e] = seen ? x[t][u * 4 + e] : -INFINITY;
                     }
                 }
-        }
-        float mx = -INFINITY;
-#pragma unroll
-        for (int t = 0; t < 2; ++t)
+            }
+            float mx = -INFINITY;
 #pragma unroll
             for (int e = 0; e < 16; ++e) mx = fmaxf(mx, x[t][e]);
-        if (__any(mx > limit)) {
-            mx = max_xor32(mx);
-            const float up = mx > limit ? mx : 0.0f;
-            const float f = limit == kLowest ? 1.0f : __builtin_amdgcn_exp2f(-up);  // before the first: o, l are 0
-            limit = mx > limit ? kSlack : limit;
-            m += up;
-            l *= f;
-#pragma unroll
-            for (int t = 0; t < 2; ++t)
+            if (__any(mx > limit)) {
+                // m moves by whole powers of two, so everything that depends
+                // on it, the first half's bf16 weights included, scales exactly
+                mx = max_xor32(mx);
+                const float up = mx > limit ? __builtin_ceilf(mx) : 0.0f;
+                const float f = limit == kLowest ? 1.0f : __builtin_amdgcn_exp2f(-up);  // before the first: o, l are 0
+                limit = mx > limit ? kSlack : limit;
+                m += up;
+                l *= f;
 #pragma unroll
                 for (int e = 0; e < 16; ++e) x[t][e] -= up;
-            if (i > s_begin) {
+                if (t == 1) {
+                    part[0] *= f;
+                    part[1] *= f;
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) pw[e] = pack2(as_f32(pw[e] << 16) * f, as_f32(pw[e] & 0xFFFF0000u) * f);
+                }
 #pragma unroll
                 for (int d = 0; d < DT; ++d)
 #pragma unroll
                     for (int e = 0; e < 16; ++e) o[d][e] = o[d][e] * f;
             }
-        }
-        float part[4] = {0, 0, 0, 0};
+        };
+        // part n of `parts` of half t's weights; the bf16 pairs as they fill
+        auto weights = [&](int t, int n, int parts) {
 #pragma unroll
-        for (int t = 0; t < 2; ++t)
-#pragma unroll
-            for (int u = 0; u < 4; ++u) {
-                f4 vs = f4{1, 1, 1, 1};
-                if (VST != kBf16) vs = *reinterpret_cast<const f4*>(&buf.vs[t * 32 + u * 8 + g * 4]);
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    const float w = __builtin_amdgcn_exp2f(x[t][u * 4 + e]);
-                    part[e] += w;
-                    x[t][u * 4 + e] = VST == kBf16 ? w : w * vs[e];
+            for (int e = n * 16 / parts; e < (n + 1) * 16 / parts; ++e) {
+                const float w = __builtin_amdgcn_exp2f(x[t][e]);
+                part[e & 1] += w;
+                x[t][e] = VST == kBf16 ? w : w * vs[e >> 2][e & 3];
+                if (e & 1) {
+                    uint32_t& q = pw[t * 8 + (e >> 1)];
+                    q = pack2(x[t][e - 1], x[t][e]);
+                    // here, beside the products, and not where they are used
+                    asm volatile("" : "+v"(q), "+v"(part[0]), "+v"(part[1]));
                 }
             }
-        l += (part[0] + part[1]) + (part[2] + part[3]);
-        asm volatile("" : "+v"(l));             // here, so that no weight has to stay for it
-        b8 pf[4];
+        };
+        x[0] = f16v{0};
+        x[1] = f16v{0};
 #pragma unroll
-        for (int t = 0; t < 4; ++t) {
-            u4 w;
-#pragma unroll
-            for (int e = 0; e < 4; ++e)
-                w[e] = pack2(x[t >> 1][(t & 1) * 8 + 2 * e], x[t >> 1][(t & 1) * 8 + 2 * e + 1]);
-            pf[t] = __builtin_bit_cast(b8, w);
+        for (int n = 0; n < KM; ++n) {
+            read_k(n + 3);
+            x[0] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(kf[n & 3], qf[n], x[0], 0, 0, 0);
+            __builtin_amdgcn_sched_barrier(0);
         }
-        {
-            // V^T of matrix step n: tokens of group n % 4, channels of the
-            // tiles 2 (n / 4) and 2 (n / 4) + 1.  Lane i of 16 points at row
-            // i / 4, channels 4 (i % 4).. of a 4 x 16 block and receives its
-            // column i.
-            b8 vf[3][2];
-            const uint8_t* vp = buf.v + (g * 4 + ((lane & 15) >> 2)) * L::kV + (((lane >> 4) & 1) * 16 + (lane & 3) * 4) * 2;
-            auto read_v = [&](int n) {
+        scores(0);
+        __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-                for (int d = 0; d < 2; ++d) {
-                    const uint8_t* p = vp + (n & 3) * 16 * L::kV + ((n >> 2) * 2 + d) * 64;
-                    const s4 lo = read_tr(p), hi = read_tr(p + 8 * L::kV);
-                    vf[n % 3][d] = __builtin_bit_cast(b8, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
-                }
-            };
-            read_v(0);
-            read_v(1);
-#pragma unroll
-            for (int n = 0; n < 2 * DT; ++n) {
-                if (n + 2 < 2 * DT) read_v(n + 2);
-                __builtin_amdgcn_sched_barrier(0);
-#pragma unroll
-                for (int d = 0; d < 2; ++d) {
-                    f16v& to = o[(n >> 2) * 2 + d];
-                    to = __builtin_amdgcn_mfma_f32_32x32x16_bf16(vf[n % 3][d], pf[n & 3], to, 0, 0, 0);
-                }
-            }
+        for (int n = KM; n < 2 * KM; ++n) {
+            if (n + 3 < 2 * KM) read_k(n + 3);
+            x[1] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(kf[n & 3], qf[n - KM], x[1], 0, 0, 0);
+            weights(0, n - KM, KM);
+            __builtin_amdgcn_sched_barrier(0);
         }
-        if (more) put(i + 1);
-        put_row(i + 2, entry);
+        // V^T of product n: tokens of group n / DT, channels of tile n % DT.
+        // Lane i of 16 points at row i / 4, channels 4 (i % 4).. of a 4 x 16
+        // block and receives its column i.
+        b8 vf[4];
+        const uint8_t* vp = buf.v + (g * 4 + ((lane & 15) >> 2)) * L::kV + (((lane >> 4) & 1) * 16 + (lane & 3) * 4) * 2;
+        auto read_v = [&](int n) {
+            const uint8_t* p = vp + n / DT * 16 * L::kV + n % DT * 64;
+            const s4 lo = read_tr(p), hi = read_tr(p + 8 * L::kV);
+            vf[n & 3] = __builtin_bit_cast(b8, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
+        };
+        read_v(0);
+        read_v(1);
+        read_v(2);
+        scores(1);
+        __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+        for (int n = 0; n < 4 * DT; ++n) {
+            if (n + 3 < 4 * DT) read_v(n + 3);
+            const u4 pf = u4{pw[n / DT * 4], pw[n / DT * 4 + 1], pw[n / DT * 4 + 2], pw[n / DT * 4 + 3]};
+            o[n % DT] =
+                __builtin_amdgcn_mfma_f32_32x32x16_bf16(vf[n & 3], __builtin_bit_cast(b8, pf), o[n % DT], 0, 0, 0);
+            if (n < 2 * DT) weights(1, n, 2 * DT);
+            __builtin_amdgcn_sched_barrier(0);
+        }
+        l += part[0] + part[1];
+        asm volatile("" : "+v"(l));
         __syncthreads();
     }
 
