@@ -76,11 +76,10 @@ __device__ __forceinline__ void queries_of(const ExtendParams& a, int b, int* fi
     }
 }
 
-// Slot of the first row tile of sequence b when a sequence's tiles start at
-// floor(first row / kRows) + b: increasing in b, and no two sequences share a
-// slot, without a prefix sum over the sequences.
+// With q_offsets: slot of the first row tile of sequence b.  A sequence's
+// tiles start at floor(first row / kRows) + b: increasing in b, and no two
+// sequences share a slot, without a prefix sum over the sequences.
 __device__ __forceinline__ int first_slot(const ExtendParams& a, int b) {
-    if (a.q_offsets == nullptr) return b * ((a.each * a.group + kRows - 1) / kRows);
     return min(max(a.q_offsets[b], 0), a.total_q) * a.group / kRows + b;
 }
 
@@ -89,18 +88,25 @@ __device__ __forceinline__ int first_slot(const ExtendParams& a, int b) {
 struct Tile {
     int b = 0, q_first, rows, row0, base, p_first, p_last;
     __device__ __forceinline__ Tile(const ExtendParams& a, int slot) {
-        // first_slot increases: halve down to 64 sequences, then one look
-        int hi = a.kv.batch;
-        while (hi - b > 64) {
-            const int mid = (b + hi) >> 1;
-            if (first_slot(a, mid) <= slot) b = mid; else hi = mid;
+        if (a.q_offsets == nullptr) {
+            // tile by tile over the sequences: taken from the last slot on, the
+            // longest tiles of all of them come first
+            b = slot % a.kv.batch;
+            row0 = slot / a.kv.batch * kRows;
+        } else {
+            // first_slot increases: halve down to 64 sequences, then one look
+            int hi = a.kv.batch;
+            while (hi - b > 64) {
+                const int mid = (b + hi) >> 1;
+                if (first_slot(a, mid) <= slot) b = mid; else hi = mid;
+            }
+            const int lane = threadIdx.x & 63;
+            const uint64_t at = __ballot(b + lane < hi && first_slot(a, min(b + lane, hi - 1)) <= slot);
+            if (at) b += 63 - __builtin_clzll(at);
+            row0 = (slot - first_slot(a, b)) * kRows;
         }
-        const int lane = threadIdx.x & 63;
-        const uint64_t at = __ballot(b + lane < hi && first_slot(a, min(b + lane, hi - 1)) <= slot);
-        if (at) b += 63 - __builtin_clzll(at);
         int n;
         queries_of(a, b, &q_first, &n);
-        row0 = (slot - first_slot(a, b)) * kRows;
         rows = n * a.group;
         base = seq_len(a.kv, b) - n;
         p_first = base + row0 / a.group;
@@ -250,9 +256,6 @@ __global__ __launch_bounds__(kThreads, DP <= 128 ? 2 : 1) void k_extend(const Ex
             if (live && e < D) t = *reinterpret_cast<const uint4*>(qr + e);
             qf[s] = __builtin_bit_cast(b8, t);
         }
-        // arrived before the loop, which then waits for no load of its own step
-#pragma unroll
-        for (int s = 0; s < KM; ++s) asm volatile("" : "+v"(qf[s]));
     }
     f16v o[DT];
 #pragma unroll
@@ -264,63 +267,65 @@ __global__ __launch_bounds__(kThreads, DP <= 128 ? 2 : 1) void k_extend(const Ex
     const uint8_t* vb = static_cast<const uint8_t*>(kv.v) + (int64_t)h * D * kElemBytes<VST>;
     const int32_t* table = kv.table + b * kv.table_ld;
     const bool k_tok = KST != kBf16 && !kv.per_head, v_tok = VST != kBf16 && !kv.per_head;
-    const float k_head = (KST == kBf16 || k_tok ? 1.0f : kv.k_scale[h]) * a.scale_log2;
+    float scale_log2 = a.scale_log2;
+    asm volatile("" : "+s"(scale_log2));      // a register: selects below must not pick an argument's address
+    const float k_head = (KST == kBf16 || k_tok ? 1.0f : kv.k_scale[h]) * scale_log2;
     const float v_head = VST == kBf16 || v_tok ? 1.0f : kv.v_scale[h];
 
+    // Staging.  No load is conditional, so that a wait for one counts the later
+    // ones: tokens that are not there (their score is masked, their weight 0)
+    // read row 0, steps past the end the last token.
     Unit<KST> ku[UT];
     Unit<VST> vu[UT];
     float sc = 0.0f;
-#pragma unroll
-    for (int u = 0; u < UT; ++u) {              // channels past head_dim stay 0
-        ku[u].clear();
-        vu[u].clear();
-    }
-    auto entry_of = [&](int i) -> int {         // threads 0..63: the page of a step's token
-        if (tid >= kStep || i >= s_end) return -1;
-        const int j = steps.token(i) + tid;
-        return j <= p_last ? table[j >> kv.page_shift] : -1;
+    // the scale a thread stages: K's of token tid, or V's of token tid - kStep
+    const bool key = (tid & kStep) == 0, per_token = key ? k_tok : v_tok;
+    const float* const k_scales = k_tok ? kv.k_scale : reinterpret_cast<const float*>(table);
+    const float* const v_scales = v_tok ? kv.v_scale : reinterpret_cast<const float*>(table);
+    const float* const scales = key ? k_scales : v_scales;
+    const float scale_of_head = key ? k_head : v_head, scale_by = key ? scale_log2 : 1.0f;
+    auto entry_of = [&](int i) -> int {         // the page of token tid % kStep of a step
+        const int j = steps.token(min(i, s_end - 1)) + (tid & (kStep - 1));
+        return table[min(j, p_last) >> kv.page_shift];
     };
     auto put_row = [&](int i, int entry) {
-        if (tid < kStep) lds.row[i & 3][tid] = entry >= 0 ? row_of_entry(kv, entry, steps.token(i) + tid) : -1;
+        const int j = steps.token(i) + tid;
+        if (tid < kStep) lds.row[i & 3][tid] = i < s_end && j <= p_last ? row_of_entry(kv, entry, j) : -1;
     };
     auto load = [&](int i) {                    // a step's K, V and scales into registers
         const int* rows_i = lds.row[i & 3];
+        const int64_t srow = max(rows_i[tid & (kStep - 1)], 0);
+        sc = scales[per_token ? srow * kv.heads + h : 0];
 #pragma unroll
         for (int u = 0; u < UT; ++u) {
             const int t = (tid + u * kThreads) / UR, e = ((tid + u * kThreads) % UR) * 16;
-            // a token that is not there: any row (its score is masked, its
-            // weight 0, and staging keeps values finite)
             const int64_t row = max(rows_i[t], 0);
-            if (D == DP || e < D) {
-                ku[u].load(kb + row * k_row + e * kElemBytes<KST>);
-                vu[u].load(vb + row * v_row + e * kElemBytes<VST>);
-            }
-        }
-        if (tid < 2 * kStep) {
-            const bool key = tid < kStep;
-            sc = key ? k_head : v_head;
-            if (key ? k_tok : v_tok) {
-                const int row = rows_i[tid & (kStep - 1)];
-                const float s = row >= 0 ? (key ? kv.k_scale : kv.v_scale)[(int64_t)row * kv.heads + h] : 0.0f;
-                sc *= s;
-            }
+            const int d = D == DP || e < D ? e : 0;
+            ku[u].load(kb + row * k_row + d * kElemBytes<KST>);
+            vu[u].load(vb + row * v_row + d * kElemBytes<VST>);
         }
     };
     auto mark = [&](int i) { atomicOr(&lds.bad[i % kMarks / 32], 1u << (i % 32)); };
-    auto put = [&](int i) {                     // the registers into a step's LDS buffer
+    auto put = [&](int i, int part) {           // K or V of one unit into a step's LDS buffer, the scales with the first
         typename L::Buf& buf = lds.buf[i & 1];
-#pragma unroll
-        for (int u = 0; u < UT; ++u) {
-            const int t = (tid + u * kThreads) / UR, e = (tid + u * kThreads) % UR;
+        const int u = part >> 1, t = (tid + u * kThreads) / UR, e = (tid + u * kThreads) % UR;
+        if (part & 1) {
+            if (D < DP && e * 16 >= D) vu[u].clear();
             if (vu[u].clean() && lds.row[i & 3][t] >= 0) mark(i);
-            ku[u].put(buf.k + t * L::kK + e * 16, UR * 16);
             vu[u].put(buf.v + t * L::kV + e * 16, UR * 16);
+        } else {
+            if (D < DP && e * 16 >= D) ku[u].clear();
+            ku[u].put(buf.k + t * L::kK + e * 16, UR * 16);
         }
-        if (tid >= kStep && tid < 2 * kStep && !__builtin_isfinite(sc)) {
-            sc = 0.0f;
-            mark(i);
+        if (part == 0 && tid < 2 * kStep) {
+            const bool there = lds.row[i & 3][tid & (kStep - 1)] >= 0;
+            float s = per_token ? sc * scale_by : scale_of_head;
+            if (per_token && (!there || (!key && !__builtin_isfinite(s)))) {
+                if (there) mark(i);
+                s = 0.0f;
+            }
+            (key ? buf.ks : buf.vs)[tid & (kStep - 1)] = s;
         }
-        if (tid < 2 * kStep) (tid < kStep ? buf.ks : buf.vs)[tid & (kStep - 1)] = sc;
     };
 
     // Rows are known three steps ahead, K and V are in registers one step ahead
@@ -328,14 +333,19 @@ __global__ __launch_bounds__(kThreads, DP <= 128 ? 2 : 1) void k_extend(const Ex
     int entry = 0;
     if (s_begin < s_end) {
         if (tid < kMarks / 32) lds.bad[tid] = 0;
-        put_row(s_begin, entry_of(s_begin));
-        put_row(s_begin + 1, entry_of(s_begin + 1));
-        put_row(s_begin + 2, entry_of(s_begin + 2));
+        const int e0 = entry_of(s_begin), e1 = entry_of(s_begin + 1), e2 = entry_of(s_begin + 2);
         entry = entry_of(s_begin + 3);
+        put_row(s_begin, e0);
+        put_row(s_begin + 1, e1);
+        put_row(s_begin + 2, e2);
         __syncthreads();
         load(s_begin);
-        put(s_begin);
-        if (s_begin + 1 < s_end) load(s_begin + 1);
+#pragma unroll
+        for (int n = 0; n < 2 * UT; ++n) put(s_begin, n);
+        load(s_begin + 1);
+        // Q has arrived before the loop, which then waits for no load of its own step
+#pragma unroll
+        for (int s = 0; s < KM; ++s) asm volatile("" : "+v"(qf[s]));
         __syncthreads();
     }
     for (int i = s_begin; i < s_end; ++i) {
@@ -346,7 +356,8 @@ __global__ __launch_bounds__(kThreads, DP <= 128 ? 2 : 1) void k_extend(const Ex
 
         // The step in halves of 32 tokens, so that matrix products of one run
         // beside the exponentials of the other:
-        //   S0 = K0 Q | S1 = K1 Q with P0 = 2^S0 | O += V0 P0 with P1 = 2^S1 | O += V1 P1
+        //   S0 = K0 Q | S1 = K1 Q with P0 = 2^S0 | O += V0 P0 with P1 = 2^S1 |
+        //   O += V1 P1 with the next step's K and V into LDS
         // LDS reads run a few products ahead; the scheduling barriers keep
         // this order.
         b8 kf[4];
@@ -356,10 +367,6 @@ __global__ __launch_bounds__(kThreads, DP <= 128 ? 2 : 1) void k_extend(const Ex
         read_k(0);
         read_k(1);
         read_k(2);
-        if (i + 1 < s_end) put(i + 1);
-        if (i + 2 < s_end) load(i + 2);
-        put_row(i + 3, entry);
-        entry = entry_of(i + 4);
 
         const bool edge = j0 + kStep - 1 > p_first ||
                           (a.window > 0 && j0 <= p_last - a.window && j0 + kStep - 1 >= a.sinks);
@@ -373,7 +380,7 @@ __global__ __launch_bounds__(kThreads, DP <= 128 ? 2 : 1) void k_extend(const Ex
         auto scores = [&](int t) {
 #pragma unroll
             for (int u = 0; u < 4; ++u) {
-                f4 ks = f4{a.scale_log2, a.scale_log2, a.scale_log2, a.scale_log2};
+                f4 ks = f4{scale_log2, scale_log2, scale_log2, scale_log2};
                 if (KST != kBf16) ks = *reinterpret_cast<const f4*>(&buf.ks[t * 32 + u * 8 + g * 4]);
                 vs[u] = f4{1, 1, 1, 1};
                 if (VST != kBf16) vs[u] = *reinterpret_cast<const f4*>(&buf.vs[t * 32 + u * 8 + g * 4]);
@@ -475,8 +482,12 @@ __global__ __launch_bounds__(kThreads, DP <= 128 ? 2 : 1) void k_extend(const Ex
             o[n % DT] =
                 __builtin_amdgcn_mfma_f32_32x32x16_bf16(vf[n & 3], __builtin_bit_cast(b8, pf), o[n % DT], 0, 0, 0);
             if (n < 2 * DT) weights(1, n, 2 * DT);
+            else if ((n - 2 * DT) % (DT / UT) == 0) put(i + 1, (n - 2 * DT) / (DT / UT));
             __builtin_amdgcn_sched_barrier(0);
         }
+        put_row(i + 3, entry);
+        entry = entry_of(i + 4);
+        load(i + 2);
         l += part[0] + part[1];
         asm volatile("" : "+v"(l));
         __syncthreads();
