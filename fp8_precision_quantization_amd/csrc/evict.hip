@@ -4,12 +4,12 @@
 // budget - sinks - recent with the largest weights (the lower position among
 // equals), and its kept tokens move together in their order.
 //
-// k_evict_select: one block per (KV head, sequence).  A radix select finds
-// the k-th largest weight in three histogram passes over 11, 11 and 10 bits
-// of an order-preserving key (2048 bins: softmax weights crowd few exponents,
-// so coarse bins would serialize the counters), then one pass counts and one
-// writes the kept positions in order, each wave on a run of its own with
-// ballots.  The weights are re-read from the L2 in every pass.
+// Selection: one block per (KV head, sequence).  A radix select finds the
+// k-th largest weight in three histogram passes over 11, 11 and 10 bits of an
+// order-preserving key (2048 bins: softmax weights crowd few exponents, so
+// coarse bins would serialize the counters); then ballots count, and place,
+// the kept positions in order.  Up to 32768 tokens the keys stay in registers
+// and each weight is read once.
 //
 // k_evict_move: kept[r] >= r and increasing, so rows can move in place if a
 // block takes them in order, reads a tile before it writes it, and no other
@@ -24,7 +24,6 @@
 namespace fp8mi {
 namespace {
 
-using attn::row_of_entry;
 using attn::seq_len;
 
 constexpr int kSelThreads = 1024;
@@ -41,12 +40,16 @@ __device__ __forceinline__ uint32_t key_of(float w) {
     return (u >> 31) ? ~u : u | 0x80000000u;
 }
 
-__global__ __launch_bounds__(kSelThreads) void k_evict_select(const EvictArgs a) {
-    __shared__ uint32_t hist[kBins];
-    __shared__ uint32_t wave_tot[kSelWaves];
-    __shared__ uint32_t found[2];           // bin, and how many above it
-    __shared__ uint32_t n_gt[kSelWaves], n_eq[kSelWaves];
-    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+// What one block of a selection chooses from, and the outputs that need no
+// choice: false if nothing is left to choose.
+struct Choice {
+    const float* w;
+    int32_t* kept;
+    int lo, hi;                 // positions chosen among
+    int k;                      // how many of them stay
+};
+
+__device__ __forceinline__ bool begin_choice(const EvictArgs& a, int tid, Choice* c) {
     const int h = blockIdx.x, b = blockIdx.y;
     const int n = seq_len(a.kv, b);
     const int64_t bh = (int64_t)b * a.kv.heads + h;
@@ -54,56 +57,170 @@ __global__ __launch_bounds__(kSelThreads) void k_evict_select(const EvictArgs a)
     if (h == 0 && tid == 0) a.new_lens[b] = min(n, a.budget);
     if (n <= a.budget) {
         for (int r = tid; r < a.budget; r += kSelThreads) kept[r] = r < n ? r : -1;
-        return;
+        return false;
     }
-    const int lo = a.sinks, hi = n - a.recent;          // the tokens chosen among
-    const int k = a.budget - a.sinks - a.recent;
+    *c = Choice{a.weights + bh * a.ldw, kept + a.sinks, a.sinks, n - a.recent, a.budget - a.sinks - a.recent};
     for (int r = tid; r < a.sinks; r += kSelThreads) kept[r] = r;
-    for (int r = tid; r < a.recent; r += kSelThreads) kept[a.sinks + k + r] = hi + r;
-    if (k == 0) return;
-    const float* w = a.weights + bh * a.ldw;
+    for (int r = tid; r < a.recent; r += kSelThreads) kept[a.sinks + c->k + r] = c->hi + r;
+    return c->k > 0;
+}
 
-    uint32_t key = 0, need = (uint32_t)k;               // bits of the k-th largest found so far
-    int low = 32;                                       // lowest bit of them
-#pragma unroll 1
-    for (int pass = 0; pass < 3; ++pass) {
-        const int width = pass < 2 ? 11 : 10;
-        const int next = low - width;
-        for (int i = tid; i < kBins; i += kSelThreads) hist[i] = 0;
-        __syncthreads();
-#pragma unroll 4
-        for (int j = lo + tid; j < hi; j += kSelThreads) {
-            const uint32_t u = key_of(w[j]);
-            if (pass == 0 || (u >> low) == (key >> low)) atomicAdd(&hist[(u >> next) & ((1u << width) - 1)], 1u);
-        }
-        __syncthreads();
-        // keys above bin 2t + 1, by a scan from the top bin down
-        const int b1 = kBins - 1 - 2 * tid, b0 = b1 - 1;
-        const uint32_t h1 = hist[b1], h0 = hist[b0];
-        uint32_t sum = h1 + h0;
+struct SelLds {
+    uint32_t hist[kBins];
+    uint32_t wave_tot[kSelWaves];
+    uint32_t found[2];          // bin, and how many keys lie above it
+};
+
+// One radix pass: with the histogram of the keys that match `key` above bit
+// `low` in place, extends `key` by the bin that holds the need-th largest.
+__device__ __forceinline__ void find_bin(SelLds& s, int tid, int next, uint32_t* key, uint32_t* need) {
+    const int lane = tid & 63, wave = tid >> 6;
+    // keys above bin 2t + 1, by a scan from the top bin down
+    const int b1 = kBins - 1 - 2 * tid, b0 = b1 - 1;
+    const uint32_t h1 = s.hist[b1], h0 = s.hist[b0];
+    uint32_t sum = h1 + h0;
 #pragma unroll
-        for (int off = 1; off < 64; off <<= 1) {
-            const uint32_t t = __shfl_up(sum, off, 64);
-            if (lane >= off) sum += t;
+    for (int off = 1; off < 64; off <<= 1) {
+        const uint32_t t = __shfl_up(sum, off, 64);
+        if (lane >= off) sum += t;
+    }
+    if (lane == 63) s.wave_tot[wave] = sum;
+    __syncthreads();
+    uint32_t tot = lane < kSelWaves ? s.wave_tot[lane] : 0;
+#pragma unroll
+    for (int off = 1; off < kSelWaves; off <<= 1) {
+        const uint32_t t = __shfl_up(tot, off, 64);
+        if (lane >= off) tot += t;
+    }
+    const uint32_t above = sum - h1 - h0 + (wave ? __shfl(tot, wave - 1, 64) : 0);
+    if (above < *need && *need <= above + h1) { s.found[0] = b1; s.found[1] = above; }
+    if (above + h1 < *need && *need <= above + h1 + h0) { s.found[0] = b0; s.found[1] = above + h1; }
+    __syncthreads();
+    *key |= s.found[0] << next;
+    *need -= s.found[1];
+}
+
+constexpr int kPasses = 3;
+__device__ __forceinline__ int low_bit(int pass) { return pass == 0 ? 21 : pass == 1 ? 10 : 0; }
+
+// The keys stay in registers, KPT a thread: key i of thread t is position
+// lo + i * 1024 + t.  For up to KPT * 1024 tokens; each weight is read once.
+template <int KPT>
+__global__ __launch_bounds__(kSelThreads) void k_evict_select_regs(const EvictArgs a) {
+    __shared__ SelLds s;
+    __shared__ uint32_t n_gt[KPT * kSelWaves], n_eq[KPT * kSelWaves];   // per 64 positions; then their prefix sums
+    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+    Choice c;
+    if (!begin_choice(a, tid, &c)) return;
+    uint32_t u[KPT];
+    uint32_t live = 0;
+    const int size = c.hi - c.lo;
+#pragma unroll
+    for (int i = 0; i < KPT; ++i) {                     // all loads before the first use
+        if (i * kSelThreads >= size) break;
+        u[i] = __float_as_uint(c.w[min(c.lo + i * kSelThreads + tid, c.hi - 1)]);
+    }
+#pragma unroll
+    for (int i = 0; i < KPT; ++i) {
+        if (i * kSelThreads >= size) break;
+        u[i] = key_of(__uint_as_float(u[i]));
+        live |= (i * kSelThreads + tid < size ? 1u : 0u) << i;
+    }
+    uint32_t key = 0, need = (uint32_t)c.k;
+#pragma unroll
+    for (int pass = 0; pass < kPasses; ++pass) {
+        const int next = low_bit(pass), low = pass == 0 ? 32 : low_bit(pass - 1);
+        for (int i = tid; i < kBins; i += kSelThreads) s.hist[i] = 0;
+        __syncthreads();
+#pragma unroll
+        for (int i = 0; i < KPT; ++i) {
+            if (i * kSelThreads >= size) break;
+            if ((live >> i & 1) && (pass == 0 || (u[i] >> (low & 31)) == (key >> (low & 31))))
+                atomicAdd(&s.hist[(u[i] >> next) & ((1u << (low - next)) - 1)], 1u);
         }
-        if (lane == 63) wave_tot[wave] = sum;
         __syncthreads();
-        uint32_t above = sum - h1 - h0;
-        for (int i = 0; i < wave; ++i) above += wave_tot[i];
-        if (above < need && need <= above + h1) { found[0] = b1; found[1] = above; }
-        if (above + h1 < need && need <= above + h1 + h0) { found[0] = b0; found[1] = above + h1; }
-        __syncthreads();
-        key |= found[0] << next;
-        need -= found[1];
-        low = next;
+        find_bin(s, tid, next, &key, &need);
     }
     // keep every key above `key`, and the first `need` equal to it
-    const int run = ((hi - lo + kSelThreads - 1) / kSelThreads) * 64;
-    const int r0 = lo + wave * run, r1 = min(hi, r0 + run);
+#pragma unroll
+    for (int i = 0; i < KPT; ++i) {
+        if (i * kSelThreads >= size) break;
+        const bool in = live >> i & 1;
+        const uint64_t mg = __ballot(in && u[i] > key), me = __ballot(in && u[i] == key);
+        if (lane == 0) {
+            n_gt[i * kSelWaves + wave] = __popcll(mg);
+            n_eq[i * kSelWaves + wave] = __popcll(me);
+        }
+    }
+    __syncthreads();
+    // exclusive prefix sums over the runs of 64, by wave 0 and wave 1, each
+    // lane over consecutive ones
+    if (wave < 2) {
+        constexpr int E = KPT * kSelWaves / 64;
+        uint32_t* v = (wave == 0 ? n_gt : n_eq) + lane * E;
+        const int end = (size + 63) / 64 - lane * E;            // runs that were counted
+        uint32_t own[E], sum = 0;
+#pragma unroll
+        for (int i = 0; i < E; ++i) {
+            own[i] = i < end ? v[i] : 0;
+            sum += own[i];
+        }
+        uint32_t at = sum;
+#pragma unroll
+        for (int off = 1; off < 64; off <<= 1) {
+            const uint32_t t = __shfl_up(at, off, 64);
+            if (lane >= off) at += t;
+        }
+        at -= sum;
+#pragma unroll
+        for (int i = 0; i < E; ++i) {
+            v[i] = at;
+            at += own[i];
+        }
+    }
+    __syncthreads();
+    const uint64_t below = (1ull << lane) - 1;
+#pragma unroll
+    for (int i = 0; i < KPT; ++i) {
+        if (i * kSelThreads >= size) break;
+        const bool in = live >> i & 1;
+        const uint64_t mg = __ballot(in && u[i] > key), me = __ballot(in && u[i] == key);
+        const uint32_t g = n_gt[i * kSelWaves + wave] + __popcll(mg & below);
+        const uint32_t e = n_eq[i * kSelWaves + wave] + __popcll(me & below);
+        if (in && (u[i] > key || (u[i] == key && e < need)))
+            c.kept[g + min(e, need)] = c.lo + i * kSelThreads + tid;
+    }
+}
+
+// Any number of tokens: the weights are read again (from the L2) in every
+// pass, and each wave writes out a run of its own.
+__global__ __launch_bounds__(kSelThreads) void k_evict_select(const EvictArgs a) {
+    __shared__ SelLds s;
+    __shared__ uint32_t n_gt[kSelWaves], n_eq[kSelWaves];
+    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+    Choice c;
+    if (!begin_choice(a, tid, &c)) return;
+    uint32_t key = 0, need = (uint32_t)c.k;
+#pragma unroll 1
+    for (int pass = 0; pass < kPasses; ++pass) {
+        const int next = low_bit(pass), low = pass == 0 ? 32 : low_bit(pass - 1);
+        for (int i = tid; i < kBins; i += kSelThreads) s.hist[i] = 0;
+        __syncthreads();
+#pragma unroll 8
+        for (int j = c.lo + tid; j < c.hi; j += kSelThreads) {
+            const uint32_t u = key_of(c.w[j]);
+            if (pass == 0 || (u >> (low & 31)) == (key >> (low & 31)))
+                atomicAdd(&s.hist[(u >> next) & ((1u << (low - next)) - 1)], 1u);
+        }
+        __syncthreads();
+        find_bin(s, tid, next, &key, &need);
+    }
+    const int run = ((c.hi - c.lo + kSelThreads - 1) / kSelThreads) * 64;
+    const int r0 = c.lo + wave * run, r1 = min(c.hi, r0 + run);
     uint32_t gt = 0, eq = 0;
-#pragma unroll 4
+#pragma unroll 8
     for (int j = r0 + lane; j < r0 + run; j += 64) {
-        const uint32_t u = j < r1 ? key_of(w[j]) : 0;
+        const uint32_t u = j < r1 ? key_of(c.w[j]) : 0;
         gt += __popcll(__ballot(j < r1 && u > key));
         eq += __popcll(__ballot(j < r1 && u == key));
     }
@@ -112,104 +229,137 @@ __global__ __launch_bounds__(kSelThreads) void k_evict_select(const EvictArgs a)
     gt = 0; eq = 0;
     for (int i = 0; i < wave; ++i) { gt += n_gt[i]; eq += n_eq[i]; }
     const uint64_t below = (1ull << lane) - 1;
+#pragma unroll 8
     for (int j = r0 + lane; j < r0 + run; j += 64) {
-        const uint32_t u = j < r1 ? key_of(w[j]) : 0;
+        const uint32_t u = j < r1 ? key_of(c.w[j]) : 0;
         const uint64_t mg = __ballot(j < r1 && u > key), me = __ballot(j < r1 && u == key);
         const uint32_t g = gt + __popcll(mg & below), e = eq + __popcll(me & below);
-        if (j < r1 && (u > key || (u == key && e < need))) kept[a.sinks + g + min(e, need)] = j;
+        if (j < r1 && (u > key || (u == key && e < need))) c.kept[g + min(e, need)] = j;
         gt += __popcll(mg);
         eq += __popcll(me);
     }
 }
 
-// Moves rows [0, m) of one array, `per` pieces of type T a row: piece q of
-// row r from src(kept[r], q) to dst(r, q); a null address is left out.
-template <typename T, typename Src, typename Dst>
-__device__ __forceinline__ void move_rows(const int32_t* kept, int m, int per, bool in_place, int first, int step,
-                                          Src src, Dst dst) {
-    const int rows = kMoveThreads * kPieces / per;      // of a tile
-    const int tiles = (m + rows - 1) / rows;
-    for (int tile = first; tile < tiles; tile += step) {
-        const int r0 = tile * rows, rn = min(m - r0, rows);
-        if (in_place && kept[r0 + rn - 1] == r0 + rn - 1) continue;     // nothing before it was dropped
+// Where a block's rows come from and go to.
+struct Route {
+    const int32_t* kept;
+    const int32_t* from;        // page tables of the sequence
+    const int32_t* to;
+    int shift, capacity;
+    int m;                      // rows kept
+    bool in_place;
+    int first, step;            // tiles of this block
+    __device__ __forceinline__ int row(const int32_t* table, int j) const {
+        const int64_t r = ((int64_t)table[j >> shift] << shift) + (j & ((1 << shift) - 1));
+        return r >= 0 && r < capacity ? (int)r : -1;
+    }
+    __device__ __forceinline__ int src(int j) const { return row(from, j); }
+    __device__ __forceinline__ int dst(int r) const { return row(to, r); }
+};
+
+// Moves rows of one array of a head: `per` pieces of type T a row, rows
+// `pitch` pieces apart.  A thread's pieces are the same part of rows a pass
+// apart, kPieces of them in flight.
+template <typename T>
+__device__ __forceinline__ void move_rows(const Route& w, T* data, int64_t pitch, int per) {
+    const int pass = kMoveThreads / per, tile_rows = pass * kPieces;
+    const int rr = threadIdx.x / per, q = threadIdx.x - rr * per;
+    T* const base = data + q;
+    for (int r0 = w.first * tile_rows; r0 < w.m; r0 += w.step * tile_rows) {
+        const int last = min(r0 + tile_rows, w.m) - 1;
+        if (w.in_place && w.kept[last] == last) continue;       // nothing before it was dropped
+        // loads in three rounds, none of them conditional: positions, pages, rows
+        int j[kPieces], to[kPieces];
         T v[kPieces];
-        T* to[kPieces];
+#pragma unroll
+        for (int i = 0; i < kPieces; ++i) j[i] = w.kept[min(r0 + i * pass + rr, w.m - 1)];
 #pragma unroll
         for (int i = 0; i < kPieces; ++i) {
-            const int p = threadIdx.x + i * kMoveThreads, r = p / per, q = p - r * per;
-            to[i] = nullptr;
-            if (r < rn) {
-                const T* from = src(kept[r0 + r], q);
-                if (from) {
-                    to[i] = dst(r0 + r, q);
-                    v[i] = *from;
-                }
-            }
+            const int r = r0 + i * pass + rr;
+            j[i] = w.src(j[i]);
+            to[i] = w.dst(min(r, w.m - 1));
+            if (j[i] < 0 || r >= w.m || rr >= pass) to[i] = -1;
         }
+#pragma unroll
+        for (int i = 0; i < kPieces; ++i) v[i] = base[max(j[i], 0) * pitch];
         // every read of the tile has arrived before any of it is written;
         // what is written is read by no later tile
-        if (in_place) {
+        if (w.in_place) {
             __builtin_amdgcn_s_waitcnt(0);
             __syncthreads();
         }
 #pragma unroll
         for (int i = 0; i < kPieces; ++i)
-            if (to[i]) *to[i] = v[i];
+            if (to[i] >= 0) base[to[i] * pitch] = v[i];
     }
 }
 
 __global__ __launch_bounds__(kMoveThreads) void k_evict_move(const EvictArgs a, int parts) {
     const KvView& kv = a.kv;
     const int part = blockIdx.x % parts, h = blockIdx.x / parts, b = blockIdx.y;
-    const int first = blockIdx.z, step = gridDim.z;
     const int n = seq_len(kv, b), m = min(n, a.budget);
     const int64_t bh = (int64_t)b * kv.heads + h;
-    const int32_t* kept = a.kept + bh * a.budget;
-    const bool weights_in_place = a.weights == a.weights_out;
-    const bool in_place = part == 4 ? weights_in_place : a.dst_table == nullptr;
-    if (in_place && (n <= a.budget || first > 0)) return;
-
-    auto src_row = [&](int j) { return row_of_entry(kv, kv.table[b * kv.table_ld + (j >> kv.page_shift)], j); };
-    auto dst_row = [&](int r) {
-        const int32_t* t = in_place ? kv.table + b * kv.table_ld : a.dst_table + b * a.dst_ld;
-        return row_of_entry(kv, t[r >> kv.page_shift], r);
-    };
-    const int stp = in_place ? 1 : step;
-    if (part < 2) {
-        uint4* data = static_cast<uint4*>(part == 0 ? kv.k : kv.v);
-        const int per = kv.head_dim * ((part == 0 ? kv.k_st : kv.v_st) == FP8_KV_BF16 ? 2 : 1) / 16;
-        auto at = [&](int row, int q) -> uint4* {
-            return row < 0 ? nullptr : data + ((int64_t)row * kv.heads + h) * per + q;
-        };
-        move_rows<uint4>(kept, m, per, in_place, first, stp, [&](int j, int q) { return at(src_row(j), q); },
-                         [&](int r, int q) { return at(dst_row(r), q); });
-    } else if (part < 4) {
-        float* sc = part == 2 ? kv.k_scale : kv.v_scale;
-        if (sc == nullptr || kv.per_head) return;
-        auto at = [&](int row) -> float* { return row < 0 ? nullptr : sc + (int64_t)row * kv.heads + h; };
-        move_rows<float>(kept, m, 1, in_place, first, stp, [&](int j, int) { return at(src_row(j)); },
-                         [&](int r, int) { return at(dst_row(r)); });
-    } else {
-        const float* from = a.weights + bh * a.ldw;
-        float* to = a.weights_out + bh * a.ldwo;
-        move_rows<float>(kept, m, 1, in_place, first, stp, [&](int j, int) { return from + j; },
-                         [&](int r, int) { return to + r; });
+    const bool in_place = part == 4 ? a.weights == a.weights_out : a.dst_table == nullptr;
+    if (in_place && (n <= a.budget || blockIdx.z > 0)) return;
+    if (part < 4 && (kv.capacity == 0 || m == 0)) return;
+    const int32_t* from = kv.table + b * kv.table_ld;
+    const Route w = {a.kept + bh * a.budget, from, in_place || part == 4 ? from : a.dst_table + b * a.dst_ld,
+                     kv.page_shift, (int)kv.capacity, m, in_place, (int)blockIdx.z, in_place ? 1 : (int)gridDim.z};
+    const int kper = kv.head_dim * (kv.k_st == FP8_KV_BF16 ? 2 : 1) / 16;
+    const int vper = kv.head_dim * (kv.v_st == FP8_KV_BF16 ? 2 : 1) / 16;
+    switch (part) {
+    case 0: move_rows(w, static_cast<attn::u4*>(kv.k) + (int64_t)h * kper, (int64_t)kv.heads * kper, kper); break;
+    case 1: move_rows(w, static_cast<attn::u4*>(kv.v) + (int64_t)h * vper, (int64_t)kv.heads * vper, vper); break;
+    case 2:
+        if (kv.k_scale && !kv.per_head) move_rows(w, kv.k_scale + h, (int64_t)kv.heads, 1);
+        break;
+    case 3:
+        if (kv.v_scale && !kv.per_head) move_rows(w, kv.v_scale + h, (int64_t)kv.heads, 1);
+        break;
+    default: {
+        const float* src = a.weights + bh * a.ldw;
+        float* dst = a.weights_out + bh * a.ldwo;
+        constexpr int rows = kMoveThreads * kPieces;
+        for (int r0 = w.first * rows; r0 < m; r0 += w.step * rows) {
+            float v[kPieces];
+#pragma unroll
+            for (int i = 0; i < kPieces; ++i) {
+                const int r = r0 + i * kMoveThreads + threadIdx.x;
+                v[i] = r < m ? src[w.kept[r]] : 0.0f;
+            }
+            if (in_place) {
+                __builtin_amdgcn_s_waitcnt(0);
+                __syncthreads();
+            }
+#pragma unroll
+            for (int i = 0; i < kPieces; ++i) {
+                const int r = r0 + i * kMoveThreads + threadIdx.x;
+                if (r < m) dst[r] = v[i];
+            }
+        }
         // nothing has been received behind the kept tokens
         const int end = in_place ? n : a.budget;
-        for (int r = m + first * kMoveThreads + threadIdx.x; r < end; r += stp * kMoveThreads) to[r] = 0.0f;
+        for (int r = m + w.first * kMoveThreads + threadIdx.x; r < end; r += w.step * kMoveThreads) dst[r] = 0.0f;
+    }
     }
 }
 
 }  // namespace
 
 hipError_t launch_evict(const EvictArgs& a) {
-    const dim3 grid((unsigned)a.kv.heads, (unsigned)a.kv.batch);
-    hipLaunchKernelGGL(k_evict_select, grid, dim3(kSelThreads), 0, a.stream, a);
+    const dim3 grid((unsigned)a.kv.heads, (unsigned)a.kv.batch), threads(kSelThreads);
+    if (a.kv.max_len <= 8 * kSelThreads)
+        hipLaunchKernelGGL(k_evict_select_regs<8>, grid, threads, 0, a.stream, a);
+    else if (a.kv.max_len <= 32 * kSelThreads)
+        hipLaunchKernelGGL(k_evict_select_regs<32>, grid, threads, 0, a.stream, a);
+    else
+        hipLaunchKernelGGL(k_evict_select, grid, threads, 0, a.stream, a);
     hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
     constexpr int parts = 5;
-    const int64_t widest = a.kv.head_dim / 8;           // 16-byte pieces of a bf16 row
-    const int64_t tiles = (a.budget * widest + kMoveThreads * kPieces - 1) / (kMoveThreads * kPieces);
+    const bool wide = a.kv.k_st == FP8_KV_BF16 || a.kv.v_st == FP8_KV_BF16;
+    const int64_t widest = a.kv.head_dim * (wide ? 2 : 1) / 16;         // 16-byte pieces of a row
+    const int64_t rows = kMoveThreads / widest * kPieces, tiles = (a.budget + rows - 1) / rows;
     const bool in_place = a.dst_table == nullptr && a.weights == a.weights_out;
     const dim3 move((unsigned)(parts * a.kv.heads), (unsigned)a.kv.batch,
                     in_place ? 1u : (unsigned)(tiles < 1 ? 1 : tiles > 64 ? 64 : tiles));
