@@ -88,27 +88,36 @@ __device__ __forceinline__ int first_slot(const ExtendParams& a, int b) {
 struct Tile {
     int b = 0, q_first, rows, row0, base, p_first, p_last;
     __device__ __forceinline__ Tile(const ExtendParams& a, int slot) {
+        int n, len;
         if (a.q_offsets == nullptr) {
             // tile by tile over the sequences: taken from the last slot on, the
             // longest tiles of all of them come first
             b = slot % a.kv.batch;
             row0 = slot / a.kv.batch * kRows;
+            queries_of(a, b, &q_first, &n);
+            len = seq_len(a.kv, b);
         } else {
-            // first_slot increases: halve down to 64 sequences, then one look
+            // first_slot increases: halve down to 64 sequences, then one look,
+            // at everything of them that is needed
             int hi = a.kv.batch;
             while (hi - b > 64) {
                 const int mid = (b + hi) >> 1;
                 if (first_slot(a, mid) <= slot) b = mid; else hi = mid;
             }
-            const int lane = threadIdx.x & 63;
-            const uint64_t at = __ballot(b + lane < hi && first_slot(a, min(b + lane, hi - 1)) <= slot);
-            if (at) b += 63 - __builtin_clzll(at);
-            row0 = (slot - first_slot(a, b)) * kRows;
+            const int mine = min(b + (int)(threadIdx.x & 63), hi - 1);
+            int first, count;
+            queries_of(a, mine, &first, &count);
+            const int tokens = seq_len(a.kv, mine), start = first * a.group / kRows + mine;
+            const uint64_t at = __ballot(start <= slot);
+            const int l = min(at ? 63 - __builtin_clzll(at) : 0, hi - 1 - b);
+            q_first = __builtin_amdgcn_readlane(first, l);
+            n = __builtin_amdgcn_readlane(count, l);
+            len = __builtin_amdgcn_readlane(tokens, l);
+            row0 = (slot - __builtin_amdgcn_readlane(start, l)) * kRows;
+            b += l;
         }
-        int n;
-        queries_of(a, b, &q_first, &n);
         rows = n * a.group;
-        base = seq_len(a.kv, b) - n;
+        base = len - n;
         p_first = base + row0 / a.group;
         p_last = base + (min(row0 + kRows, rows) - 1) / a.group;
     }
