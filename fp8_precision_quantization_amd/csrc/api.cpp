@@ -540,8 +540,8 @@ static fp8_status check_kv_pair(const fp8_kv_pair* c, bool sizes, fp8mi::KvView*
     if (c->batch < 0 || c->max_len < 0)
         return fail(FP8_ERR_INVALID_ARG, "negative size batch=%d max_len=%lld", (int)c->batch, (long long)c->max_len);
     if (c->batch > 65535) return fail(FP8_ERR_UNSUPPORTED_SHAPE, "batch=%d must be <= 65535", (int)c->batch);
-    if (c->max_len >= (int64_t(1) << 31) || c->capacity >= (int64_t(1) << 31))
-        return fail(FP8_ERR_UNSUPPORTED_SHAPE, "max_len and capacity must be < 2^31");
+    if (c->max_len >= (int64_t(1) << 30) || c->capacity >= (int64_t(1) << 31))
+        return fail(FP8_ERR_UNSUPPORTED_SHAPE, "max_len must be < 2^30 and capacity < 2^31");
     const int32_t ps = c->page_size;
     if (ps < 1 || ps > (1 << 20) || (ps & (ps - 1)) != 0)
         return fail(FP8_ERR_UNSUPPORTED_SHAPE, "page_size=%d must be a power of two <= 2^20", (int)ps);
@@ -583,8 +583,13 @@ static fp8_status attention_args(const fp8_kv_pair* cache, bool sizes, int64_t t
     if (q_heads < 1 || q_heads % cache->heads != 0)
         return fail(FP8_ERR_INVALID_ARG, "q_heads=%d must be a multiple of heads=%d", (int)q_heads,
                     (int)cache->heads);
-    if (total_q >= (int64_t(1) << 31) / q_heads || q_heads > 65535)
-        return fail(FP8_ERR_UNSUPPORTED_SHAPE, "total_q * q_heads must be < 2^31 and q_heads <= 65535");
+    if (total_q >= (int64_t(1) << 30) || total_q >= (int64_t(1) << 31) / q_heads || q_heads > 65535)
+        return fail(FP8_ERR_UNSUPPORTED_SHAPE,
+                    "total_q must be < 2^30, total_q * q_heads < 2^31 and q_heads <= 65535");
+    // blocks of the launches
+    if ((int64_t)cache->batch * cache->heads >= (int64_t(1) << 30) ||
+        (cache->max_len / 128 + 1) * cache->heads >= (int64_t(1) << 31))
+        return fail(FP8_ERR_UNSUPPORTED_SHAPE, "batch * heads must be < 2^30 and max_len / 128 * heads < 2^31");
     if (total_q > 0 && cache->batch == 0) return fail(FP8_ERR_INVALID_ARG, "total_q=%lld with batch=0", (long long)total_q);
     if (!ragged && cache->batch > 0 && total_q % cache->batch != 0)
         return fail(FP8_ERR_INVALID_ARG, "total_q=%lld must be a multiple of batch=%d without q_offsets",

@@ -396,8 +396,9 @@ fp8_status fp8_kv_load(const void* cache, fp8_kv_storage storage, fp8_kv_scaling
  *     clamped to [0, max_len].
  * Requirements (else FP8_ERR_UNSUPPORTED_SHAPE / FP8_ERR_MISALIGNED):
  * page_size a power of two <= 2^20; head_dim % 16 == 0, 16 <= head_dim <= 256;
- * capacity and max_len < 2^31; batch <= 65535, and batch * max_len < 2^35 for
- * the attention; caches 16-byte aligned. */
+ * capacity < 2^31, max_len < 2^30; heads and batch <= 65535; for the attention
+ * also batch * max_len < 2^35, batch * heads < 2^30 and max_len / 128 * heads
+ * < 2^31; caches 16-byte aligned. */
 typedef struct fp8_kv_pair {
     void* k;
     void* v;
@@ -430,8 +431,9 @@ typedef struct fp8_kv_pair {
  * -inf.  What a token that a row does not see holds, NaN and Inf included,
  * has no part in that row.
  * q: bf16 [total_q x (q_heads*head_dim)], leading dimension ldq; out: bf16,
- * the same shape, ldo (both multiples of 8, 16-byte aligned).  q_heads a
- * multiple of heads, total_q * q_heads < 2^31.
+ * the same shape, ldo (both multiples of 8, 16-byte aligned); out must not
+ * overlap anything the call reads.  q_heads a multiple of heads and <= 65535,
+ * total_q < 2^30, total_q * q_heads < 2^31.
  * q_offsets: NULL = every sequence has total_q / batch new tokens (total_q a
  * multiple of batch); else DEVICE int32 [batch + 1], non-decreasing, within
  * [0, total_q]: sequence b's queries are rows q_offsets[b]..q_offsets[b+1]-1

@@ -52,7 +52,7 @@ PAIRS = [
     (dict(k_storage=3), I, "storage"), (dict(scaling=2), I, "scaling"), (dict(reserved=1), I, "reserved"),
     (dict(head_dim=8), U, "head_dim"), (dict(head_dim=120), U, "head_dim"), (dict(head_dim=272), U, "head_dim"),
     (dict(heads=0), I, "heads"), (dict(batch=-1), I, "batch"), (dict(batch=65536), U, "batch"),
-    (dict(max_len=-1), I, "max_len"), (dict(max_len=1 << 31), U, "max_len"), (dict(capacity=1 << 31), U, "capacity"),
+    (dict(max_len=-1), I, "max_len"), (dict(max_len=1 << 30), U, "max_len"), (dict(capacity=1 << 31), U, "capacity"),
     (dict(capacity=-1), I, "capacity"),
     (dict(page_size=0), U, "page_size"), (dict(page_size=24), U, "page_size"), (dict(page_size=1 << 21), U, "page_size"),
     (dict(page_ld=15), I, "page_ld"), (dict(lens=None), I, "lens"), (dict(page_table=None), I, "page_table"),
@@ -71,7 +71,7 @@ def test_pair(change, status, word):
     (dict(out=FAKE + 2), M, "16-byte"), (dict(ldq=4088), I, "ldq"), (dict(ldo=4095), I, "ldo"),
     (dict(ldq=4100), M, "ldq"), (dict(ldo=4097), M, "ldo"), (dict(total_q=-1), I, "total_q"),
     (dict(total_q=3), I, "multiple of batch"), (dict(q_heads=0), I, "q_heads"), (dict(q_heads=12), I, "q_heads"),
-    (dict(total_q=1 << 28), U, "total_q"), (dict(window=-1), I, "window"), (dict(sinks=-2), I, "sinks"),
+    (dict(total_q=1 << 28), U, "total_q"), (dict(total_q=1 << 30, q_heads=8), U, "total_q"), (dict(window=-1), I, "window"), (dict(sinks=-2), I, "sinks"),
     (dict(scale=float("inf")), I, "scale"), (dict(scale=float("nan")), I, "scale"),
     (dict(q_offsets=FAKE + 2), M, "q_offsets"), (dict(lse=FAKE + 2), M, "lse"),
     (dict(weights=FAKE, ldw=256, lse=None), I, "lse"), (dict(weights=FAKE, ldw=255), I, "ldw"),
@@ -128,3 +128,11 @@ def test_null_descriptor():
 
 def test_descriptor_size_matches_the_header():
     assert ctypes.sizeof(L.Fp8KvPair) == 104
+
+
+def test_attention_limits_of_sizes():
+    check(attention(pair(batch=65535, heads=32768, max_len=16), total_q=0, q_heads=32768, ldq=1 << 23, ldo=1 << 23), U,
+          "batch * heads")
+    check(attention(pair(batch=64, max_len=1 << 29, page_ld=1 << 25), total_q=64), U, "batch * max_len")
+    check(attention(pair(batch=2, max_len=1 << 29, page_ld=1 << 25, heads=1024), total_q=2, q_heads=1024, ldq=1 << 18,
+                    ldo=1 << 18), U, "max_len / 128")

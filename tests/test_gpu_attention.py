@@ -454,3 +454,76 @@ def test_weights_groups(group, n):
     q, out, lse = _run(c, n, 2 * group, 70, 5, weights=w)
     want, delta, acc = ref.check_attention(c, q, n, out, lse, 70, 5)
     _check_weights(c, [x * group for x in n], w0, w, want, delta, acc)
+
+
+@pytest.mark.parametrize("window, sinks", [(0, 0), (500, 70)])
+def test_extend_long_split(window, sinks):
+    """Few queries over long caches: row tiles shared among blocks and joined, weights from the joined lse."""
+    n = [5, 70, 1, 0]
+    c = ref.Cache([3000, 2100, 900, 1500], 2, 64, 16, seed=21, absent=[(0, 30), (1, 2)])
+    w0 = torch.rand(4, 2, c.max_len, generator=torch.Generator().manual_seed(5)).cuda()
+    w = w0.clone()
+    q, out, lse = _run(c, n, 6, window, sinks, weights=w)
+    want, delta, acc = ref.check_attention(c, q, n, out, lse, window, sinks)
+    _check_weights(c, n, w0, w, want, delta, acc)
+
+
+def test_extend_long_split_not_finite():
+    """Values that are not finite in one block's steps reach the joined rows that see them, and only those."""
+    L, n, W = 4000, 6, 300
+    c = ref.Cache([L, L], 2, 128, 16, seed=22)
+    clean = [v.copy() for v in c.v64]
+    c.v[c.rows[0][100], 0, 3] = 0x7F            # outside every window
+    c.v[c.rows[1][L - 200], 1, 9] = 0x7F        # inside all of them
+    q, out, lse = _run(c, [n, n], 4, W, 2)
+    o = out.double().cpu().numpy()
+    c.v64 = clean
+    want = ref.attention(c, q, [n, n], W, 2)[0]
+    bad = np.zeros(o.shape, bool)
+    bad[n:, 2:, 9] = True
+    assert np.isnan(o[bad]).all() and np.isfinite(o[~bad]).all()
+    assert np.abs(o - want)[~bad].max() < 0.05 * np.abs(want).max()
+    q, out, lse = _run(c, [n, n], 4)            # no window: the first sequence sees its own too
+    o = out.double().cpu().numpy()
+    bad[:n, :2, 3] = True
+    assert np.isnan(o[bad]).all() and np.isfinite(o[~bad]).all()
+
+
+@pytest.mark.parametrize("n", [1, 2, None])
+def test_many_sequences(n):
+    """More sequences than a wave has lanes, empty ones among them."""
+    rng = np.random.default_rng(3)
+    B = 150
+    lens = [int(x) for x in rng.integers(0, 300, B)]
+    each = [n] * B if n else [int(x) for x in rng.integers(0, 9, B)]
+    c = ref.Cache(lens, 1, 32, 16, seed=23)
+    _check(c, each, 2, ragged=n is None)
+
+
+def test_no_sequences_and_no_queries():
+    c = ref.Cache([40, 20], 2, 64, 16, seed=1)
+    args = c.device()
+    empty = torch.empty(0, 4, 64, dtype=torch.bfloat16, device="cuda")
+    out, lse = fp8.kv_attention(empty, return_lse=True, **args)
+    assert out.shape == (0, 4, 64) and lse.shape == (0, 4)
+    out = fp8.kv_attention(empty, q_offsets=torch.zeros(3, dtype=torch.int32, device="cuda"), **args)
+    assert out.shape == (0, 4, 64)
+    args.update(page_table=args["page_table"][:0], lens=args["lens"][:0])
+    assert fp8.kv_attention(empty, **args).shape == (0, 4, 64)
+    torch.cuda.synchronize()
+
+
+def test_max_len_and_lens_beyond_it():
+    """max_len bounds what is read: longer lens are clamped to it."""
+    c = ref.Cache([200, 100], 2, 64, 16, seed=24)
+    args = c.device()
+    short = ref.Cache([200, 100], 2, 64, 16, seed=24)
+    short.lens = [128, 100]
+    short.k64 = [x[:m] for x, m in zip(c.k64, short.lens)]
+    short.v64 = [x[:m] for x, m in zip(c.v64, short.lens)]
+    short.there = [x[:m] for x, m in zip(c.there, short.lens)]
+    for n in (1, 5):
+        q = ref.queries(c, [n, n], 4)
+        out, lse = fp8.kv_attention(q.cuda(), max_len=128, return_lse=True, **args)
+        torch.cuda.synchronize()
+        ref.check_attention(short, q, [n, n], out, lse)

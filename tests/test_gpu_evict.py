@@ -250,3 +250,38 @@ def test_refusals():
     refused(fp8.Fp8Error, "is page_table", dst_page_table=args["page_table"])
     refused(ValueError, "kept", kept=torch.empty(2, 2, 8, dtype=torch.int32, device="cuda"))
     refused(fp8.Fp8Error, "new_lens is lens", new_lens=args["lens"])
+
+
+def test_nothing_to_do():
+    """No sequences; empty sequences; a budget longer than any sequence."""
+    c = ref.Cache([40, 0], 2, 64, 16, seed=1)
+    args = c.device()
+    w = _weights(2, 2, c.max_len, 1).cuda()
+    keep = args["k_cache"].clone(), w.clone()
+    kept, lens = fp8.kv_evict(weights=w, budget=1000, sinks=4, recent=16, **args)
+    torch.cuda.synchronize()
+    assert lens.tolist() == [40, 0] and torch.equal(kept[0, 0, :40].cpu(), torch.arange(40, dtype=torch.int32))
+    assert (kept[0, :, 40:] == -1).all() and (kept[1] == -1).all()
+    assert torch.equal(keep[0], args["k_cache"]) and torch.equal(keep[1], w)
+    args.update(page_table=args["page_table"][:0], lens=args["lens"][:0])
+    kept, lens = fp8.kv_evict(weights=w[:0], budget=8, **args)
+    assert kept.shape == (0, 2, 8) and lens.shape == (0,)
+
+
+def test_absent_pages_are_left_out():
+    """Tokens whose source or destination row is outside the cache do not move; the others do."""
+    c = ref.Cache([64], 1, 32, 16, seed=7, absent=[(0, 1)])
+    args = c.device()
+    before = args["k_cache"].clone()
+    w = torch.arange(64, 0, -1, dtype=torch.float32).view(1, 1, 64).cuda()
+    w[0, 0, 20] = 0.5                       # position 20, in the absent page, is dropped with 63
+    kept, lens = fp8.kv_evict(weights=w, budget=62, **args)
+    torch.cuda.synchronize()
+    want = [j for j in range(63) if j != 20]
+    assert kept[0, 0].tolist() == want and lens.tolist() == [62]
+    t = c.table[0].astype(np.int64)
+    for r, j in enumerate(want):
+        if r // 16 == 1 or j // 16 == 1:
+            continue
+        dst, src = t[r // 16] * 16 + r % 16, t[j // 16] * 16 + j % 16
+        assert torch.equal(args["k_cache"][dst], before[src])
