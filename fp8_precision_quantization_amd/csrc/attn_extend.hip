@@ -607,16 +607,26 @@ __global__ __launch_bounds__(kThreads) void k_extend_join(const ExtendParams a) 
 // Weights: a wave holds 32 tokens' K as the A operand; a step's queries go
 // through LDS (read from memory row by row, as columns of the product they
 // would be 64 separate lines a load) and are shared by the block's four waves.
+template <int DP>
+struct WeightsLds {
+    static constexpr int kR = DP <= 128 ? 128 : 64;     // rows of a step
+    static constexpr int kQ = DP * 2 + 16;              // bytes of a padded row
+    alignas(16) uint8_t q[2][kR * kQ];
+    float lse[2][kR];
+    int pos[2][kR];
+};
+
 template <int KST, int DP>
-__global__ __launch_bounds__(kThreads) void k_weights(const ExtendParams a) {
+__global__ __launch_bounds__(kThreads, DP <= 128 ? 2 : 1) void k_weights(const ExtendParams a) {
     constexpr int KM = DP / 16;
     constexpr int KC = DP * kElemBytes<KST> / 32;       // 16-byte pieces of K a lane holds
-    constexpr int R = DP <= 128 ? 64 : 32;              // rows of a step
+    constexpr int R = WeightsLds<DP>::kR, kQ = WeightsLds<DP>::kQ;
     constexpr int PR = DP / 8, PT = R * PR / kThreads;  // 16-byte pieces of a row, of a thread
-    constexpr int kQ = DP * 2 + 16;                     // bytes of a padded row
-    __shared__ __align__(16) uint8_t s_q[2][R * kQ];
-    __shared__ float s_lse[2][R];
-    __shared__ int s_pos[2][R];
+    extern __shared__ __align__(16) uint8_t smem[];
+    WeightsLds<DP>& lds = *reinterpret_cast<WeightsLds<DP>*>(smem);
+    auto& s_q = lds.q;
+    auto& s_lse = lds.lse;
+    auto& s_pos = lds.pos;
     const KvView& kv = a.kv;
     const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int c = lane & 31, g = lane >> 5;
@@ -715,28 +725,59 @@ __global__ __launch_bounds__(kThreads) void k_weights(const ExtendParams a) {
     __syncthreads();
     for (int i = 0, r0 = r_first; r0 < r_end; ++i, r0 += R) {
         if (r0 + R < r_end) load(r0 + R);
+        // 32 rows at a time: the products of the next ones beside the
+        // exponentials of the last
+        f16v x[2];
+        b8 qf[4];
+        auto read_q = [&](int n) {              // operand n % KM of rows 32 (n / KM)..
+            const int s = n % KM, e = KST == kBf16 ? s * 16 + g * 8 : (s >> 1) * 32 + g * 16 + (s & 1) * 8;
+            qf[n & 3] = *reinterpret_cast<const b8*>(&s_q[i & 1][(n / KM * 32 + c) * kQ + e * 2]);
+        };
+        constexpr int H = R / 32;
+        read_q(0);
+        read_q(1);
+        read_q(2);
+        float z = 0.0f;
+        int p = 0, lo = 0;
+        bool whole = false;
 #pragma unroll
-        for (int half = 0; half < R / 32; ++half) {
-            const uint8_t* q = &s_q[i & 1][(half * 32 + c) * kQ];
-            f16v x = f16v{0};
+        for (int half = 0; half <= H; ++half) {
+            // exponentials of rows half - 1, products of rows half
+            if (half > 0) {
+                z = s_lse[i & 1][(half - 1) * 32 + c];
+                p = s_pos[i & 1][(half - 1) * 32 + c];
+                lo = a.window > 0 ? p - a.window + 1 : 0;
+                whole = __all(j0 + 31 <= p && (j0 >= lo || j0 + 31 < a.sinks));
+                if (!whole) {
+#pragma unroll
+                    for (int e = 0; e < 16; ++e) {
+                        const int t = j0 + (e >> 2) * 8 + g * 4 + (e & 3);
+                        const bool seen = (t <= p) & ((t >= lo) | (t < a.sinks));
+                        x[(half - 1) & 1][e] = seen ? x[(half - 1) & 1][e] * ks[e] : -INFINITY;
+                    }
+                } else {
+#pragma unroll
+                    for (int e = 0; e < 16; ++e) x[(half - 1) & 1][e] *= ks[e];
+                }
+                // what is not seen, and rows that give nothing (z infinite), weigh 0
+            }
+            if (half < H) x[half & 1] = f16v{0};
+            __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
             for (int s = 0; s < KM; ++s) {
-                const int e = KST == kBf16 ? s * 16 + g * 8 : (s >> 1) * 32 + g * 16 + (s & 1) * 8;
-                const b8 qf = *reinterpret_cast<const b8*>(q + e * 2);
-                x = __builtin_amdgcn_mfma_f32_32x32x16_bf16(kf[s], qf, x, 0, 0, 0);
-            }
-            const float z = s_lse[i & 1][half * 32 + c];
-            const int p = s_pos[i & 1][half * 32 + c], lo = a.window > 0 ? p - a.window + 1 : 0;
-            if (__all(j0 + 31 <= p && (j0 >= lo || j0 + 31 < a.sinks))) {
-#pragma unroll
-                for (int e = 0; e < 16; ++e) w[e] += __builtin_amdgcn_exp2f(__builtin_fmaf(x[e], ks[e], -z));
-            } else {
-#pragma unroll
-                for (int e = 0; e < 16; ++e) {
-                    const int t = j0 + (e >> 2) * 8 + g * 4 + (e & 3);
-                    const bool seen = (t <= p) & ((t >= lo) | (t < a.sinks));
-                    w[e] += seen ? __builtin_amdgcn_exp2f(__builtin_fmaf(x[e], ks[e], -z)) : 0.0f;
+                const int n = half * KM + s;
+                if (half < H) {
+                    if (n + 3 < H * KM) read_q(n + 3);
+                    x[half & 1] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(kf[s], qf[n & 3], x[half & 1], 0, 0, 0);
                 }
+                if (half > 0) {
+#pragma unroll
+                    for (int e = s * 16 / KM; e < (s + 1) * 16 / KM; ++e) {
+                        w[e] += __builtin_amdgcn_exp2f(x[(half - 1) & 1][e] - z);
+                        asm volatile("" : "+v"(w[e]));
+                    }
+                }
+                __builtin_amdgcn_sched_barrier(0);
             }
         }
         if (r0 + R < r_end) put(i + 1);
@@ -791,14 +832,24 @@ hipError_t extend_v(const ExtendParams& p, hipStream_t stream) {
     }
 }
 
+template <int KST, int DP>
+hipError_t run_weights(const ExtendParams& p, dim3 grid, hipStream_t stream) {
+    constexpr int bytes = sizeof(WeightsLds<DP>);
+    static_assert(bytes <= 160 * 1024, "LDS");
+    const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(&k_weights<KST, DP>),
+                                             hipFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    if (e != hipSuccess) return e;
+    hipLaunchKernelGGL((k_weights<KST, DP>), grid, dim3(kThreads), bytes, stream, p);
+    return hipGetLastError();
+}
+
 template <int KST>
 hipError_t weights_dim(const ExtendParams& p, hipStream_t stream) {
     const unsigned tiles = (unsigned)((p.kv.max_len + kRows - 1) / kRows);
-    const dim3 grid(tiles * p.kv.heads, (unsigned)p.kv.batch), block(kThreads);
-    if (p.kv.head_dim <= 64) hipLaunchKernelGGL((k_weights<KST, 64>), grid, block, 0, stream, p);
-    else if (p.kv.head_dim <= 128) hipLaunchKernelGGL((k_weights<KST, 128>), grid, block, 0, stream, p);
-    else hipLaunchKernelGGL((k_weights<KST, 256>), grid, block, 0, stream, p);
-    return hipGetLastError();
+    const dim3 grid(tiles * p.kv.heads, (unsigned)p.kv.batch);
+    if (p.kv.head_dim <= 64) return run_weights<KST, 64>(p, grid, stream);
+    if (p.kv.head_dim <= 128) return run_weights<KST, 128>(p, grid, stream);
+    return run_weights<KST, 256>(p, grid, stream);
 }
 
 ExtendParams params_of(const AttnArgs& a) {
