@@ -27,6 +27,13 @@
 // P is held as bf16 head plus bf16 remainder (two matrix products), so that
 // the weights keep 16 significant bits; the kernel waits for memory, not for
 // the matrix cores, and the second product costs nothing that shows.
+//
+// Bound by HBM: 2 * group operations a code byte.  Measured on one MI355X, 8
+// KV heads of 128, group 4: 8 sequences of 65536 tokens (E5M2, scale per
+// head) 196 us = 5.5 TB/s, a device copy's rate here being 5.2; 64 ragged
+// sequences up to 4096 (E4M3, scale per (token, head), pages of 16) 68 us =
+// 4.1 TB/s, of which the join is 8.  One sequence of 517 tokens takes 15 us:
+// lens -> page entry -> scales, K and V are dependent reads, then the join.
 #include <hip/hip_runtime.h>
 
 #include "attention.hpp"
@@ -38,6 +45,7 @@ using namespace attn;
 
 constexpr int kStep = 32;       // tokens of one wave step
 constexpr int kWaves = 4;
+constexpr int kMaxScored = 64;  // query heads of a KV head up to which scores are stored for the weights
 
 struct DecodeParams {
     KvView kv;
@@ -480,15 +488,12 @@ __global__ __launch_bounds__(kJoinThreads) void k_decode_weights(const DecodePar
     const bool seen = at < steps.count * kStep && sees(j, pos, a.window, a.sinks);
     const int64_t hq0 = (int64_t)b * a.q_heads + h * a.group;
     float w = 0.0f;
-    for (int g0 = 0; g0 < a.group; g0 += 64) {
-        const int gn = min(64, a.group - g0);
-        const float z = lane < gn ? a.lse[hq0 + g0 + lane] * kLog2e : 0.0f;
+    const float z = lane < a.group ? a.lse[hq0 + lane] * kLog2e : 0.0f;     // at most kMaxScored heads
 #pragma unroll 4
-        for (int g = 0; g < gn; ++g) {
-            const float lse = as_f32(__builtin_amdgcn_readlane(__builtin_bit_cast(int, z), g));
-            const float x = seen ? a.scores[(hq0 + g0 + g) * a.span + at] : -INFINITY;
-            w += x == -INFINITY ? 0.0f : __builtin_amdgcn_exp2f(x - lse);
-        }
+    for (int g = 0; g < a.group; ++g) {
+        const float lse = as_f32(__builtin_amdgcn_readlane(__builtin_bit_cast(int, z), g));
+        const float x = seen ? a.scores[(hq0 + g) * a.span + at] : -INFINITY;
+        w += x == -INFINITY ? 0.0f : __builtin_amdgcn_exp2f(x - lse);
     }
     if (seen) a.weights[((int64_t)b * a.kv.heads + h) * a.ldw + j] += w;
 }
@@ -548,16 +553,22 @@ Plan plan_of(const AttnArgs& a) {
     }
     if (steps < 1) steps = 1;
     const int64_t units = (int64_t)a.kv.heads * p.col_tiles, most = steps * a.kv.batch;
+    // 2048 waves are two per SIMD, all resident at once, so equal shares end
+    // together; 1.5 to 6 times as many (more loads in flight, but more partial
+    // results and a second round) took 3-40 % longer over batches of 1 to 64.
     const int64_t target = 2048;
-    p.least = 4;
+    p.least = 4;                 // steps worth a share's prologue and its row in the join
     int64_t shares = (target + units - 1) / units;
     shares = shares < most ? shares : most;
     p.shares = (int)(shares < 1 ? 1 : shares);
     p.joined = steps > 1;
     p.span = steps * kStep;
-    // a token's scores written and read again against its key read again
-    const int key = a.kv.head_dim * (a.kv.k_st == FP8_KV_BF16 ? 2 : 1);
-    p.scores = a.weighted && group * 8 <= key;
+    // Weights from stored scores, or from the keys read again by k_weights,
+    // which takes 32 rows of queries at a time however few there are.  16
+    // sequences up to 8192, whole calls in us, stored / read again: 8 KV heads
+    // of 128 in E4M3, group 4 56 / 142, group 32 110 / 180; 2 KV heads, group
+    // 64 77 / 84 (bf16 79 / 82, 256 channels 102 / 130), group 128 117 / 105.
+    p.scores = a.weighted && group <= kMaxScored;
     p.blocks = ((p.shares + 7) / 8 * units + kWaves - 1) / kWaves * 8;
     return p;
 }

@@ -4,12 +4,19 @@
 // budget - sinks - recent with the largest weights (the lower position among
 // equals), and its kept tokens move together in their order.
 //
+// Measured on one MI355X, 8 KV heads of 128 in E4M3, pages of 16: 16 sequences
+// cut from 16384 to 4096 tokens 98 us (selection 21, move 70-76, which reads
+// and writes 289 MB: 4 TB/s where a copy reaches 5.2); one sequence from 1100
+// to 1024 18 us, two dependent launches of 7 and 5 us.
+//
 // Selection: one block per (KV head, sequence).  A radix select finds the
 // k-th largest weight in three histogram passes over 11, 11 and 10 bits of an
 // order-preserving key (2048 bins: softmax weights crowd few exponents, so
 // coarse bins would serialize the counters); then ballots count, and place,
 // the kept positions in order.  Up to 32768 tokens the keys stay in registers
-// and each weight is read once.
+// and each weight is read once (whole calls of 16 sequences: from 16384 tokens
+// 98 us against 106 with the weights read again in every pass, from 8000 51
+// against 56, and 53 with registers for 32768).
 //
 // k_evict_move: kept[r] >= r and increasing, so rows can move in place if a
 // block takes them in order, reads a tile before it writes it, and no other

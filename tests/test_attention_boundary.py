@@ -98,7 +98,7 @@ def test_attention_workspace():
     weighted = size(long, weighted=1)                   # the scores too
     assert weighted >= need + 2 * 32 * 65536 * 4
     check(attention(long, wsb=weighted - 1, weights=FAKE, ldw=65536), I, "workspace_bytes")
-    assert size(long, q_heads=256, weighted=1) == size(long, q_heads=256)       # keys read again instead
+    assert size(long, q_heads=1024, weighted=1) == size(long, q_heads=1024)       # keys read again instead
     assert size(pair(batch=0), total=0) == 0
     # sizes alone: no pointer is needed
     assert size(pair(k=None, v=None, k_scale_inv=None, v_scale_inv=None, lens=None, page_table=None, max_len=65536,
