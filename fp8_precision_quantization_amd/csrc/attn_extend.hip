@@ -663,33 +663,50 @@ __global__ __launch_bounds__(kThreads, DP <= 128 ? 2 : 1) void k_weights(const E
     const int r_first = i_lo * G, r_end = i_hi * G;
 
     // Q of a step into registers and from there into LDS; a row past the end
-    // reads the last one and has an infinite lse: it gives nothing.
+    // reads one of the last token's and has an infinite lse: it gives nothing.
+    // (token, head) of a thread's rows advance without divisions: pieces u and
+    // u + 1 are kThreads / PR rows apart, steps R rows.
+    struct RowAt {
+        int tok, head;
+        __device__ __forceinline__ void advance(int tokens, int heads, int group) {
+            tok += tokens;
+            head += heads;
+            const bool over = head >= group;
+            tok += over ? 1 : 0;
+            head -= over ? group : 0;
+        }
+    };
+    constexpr int kApart = kThreads / PR;
+    const int piece_tok = kApart / G, piece_head = kApart - piece_tok * G;
+    const int step_tok = R / G, step_head = R - step_tok * G;
+    const int first_of = tid / PR, e_of = tid % PR * 8;     // row in the step, first channel
+    RowAt q_at = {i_lo + first_of / G, first_of % G}, lse_at = {i_lo + tid % R / G, tid % R % G};
+    const bool in_dim = D == DP || e_of < D;
+    const uint32_t keep = in_dim ? ~0u : 0u;
+    const uint16_t* q_base = a.q + (int64_t)q_first * a.ldq + (int64_t)h * G * D + (in_dim ? e_of : 0);
+    const float* lse_base = a.lse + (int64_t)q_first * a.q_heads + h * G;
     uint4 qu[PT];
-    float lse = 0.0f;
-    int pos = 0;
-#pragma unroll
-    for (int u = 0; u < PT; ++u) qu[u] = make_uint4(0, 0, 0, 0);
+    float lse;
+    int pos;
     auto load = [&](int r0) {
+        RowAt at = q_at;
 #pragma unroll
         for (int u = 0; u < PT; ++u) {
-            const int p = tid + u * kThreads, e = (p % PR) * 8;
-            const int r = min(r0 + p / PR, r_end - 1), tok = r / G, hq = h * G + (r - tok * G);
-            if (D == DP || e < D)
-                qu[u] = *reinterpret_cast<const uint4*>(a.q + (int64_t)(q_first + tok) * a.ldq + (int64_t)hq * D + e);
+            qu[u] = *reinterpret_cast<const uint4*>(q_base + min(at.tok, i_hi - 1) * a.ldq + at.head * D);
+            at.advance(piece_tok, piece_head, G);
         }
-        if (tid < R) {
-            const int r = min(r0 + tid, r_end - 1), tok = r / G, hq = h * G + (r - tok * G);
-            lse = a.lse[(int64_t)(q_first + tok) * a.q_heads + hq];
-            lse = r0 + tid >= r_end || lse == -INFINITY ? INFINITY : lse * kLog2e;
-            pos = base + tok;
-        }
+        q_at.advance(step_tok, step_head, G);
+        const int tok = min(lse_at.tok, i_hi - 1);
+        lse = lse_base[(int64_t)tok * a.q_heads + lse_at.head];
+        lse = r0 + tid % R >= r_end || lse == -INFINITY ? INFINITY : lse * kLog2e;
+        pos = base + tok;
+        lse_at.advance(step_tok, step_head, G);
     };
     auto put = [&](int i) {
 #pragma unroll
-        for (int u = 0; u < PT; ++u) {
-            const int p = tid + u * kThreads;
-            *reinterpret_cast<uint4*>(&s_q[i & 1][p / PR * kQ + p % PR * 16]) = qu[u];
-        }
+        for (int u = 0; u < PT; ++u)
+            *reinterpret_cast<uint4*>(&s_q[i & 1][(first_of + u * kApart) * kQ + e_of * 2]) =
+                make_uint4(qu[u].x & keep, qu[u].y & keep, qu[u].z & keep, qu[u].w & keep);
         if (tid < R) {
             s_lse[i & 1][tid] = lse;
             s_pos[i & 1][tid] = pos;
@@ -754,29 +771,29 @@ __global__ __launch_bounds__(kThreads, DP <= 128 ? 2 : 1) void k_weights(const E
         read_q(0);
         read_q(1);
         read_q(2);
-        float z = 0.0f;
-        int p = 0, lo = 0;
-        bool whole = false;
+        float z[2];
+        int p[2];
 #pragma unroll
         for (int half = 0; half <= H; ++half) {
             // exponentials of rows half - 1, products of rows half
+            if (half < H) {
+                z[half & 1] = s_lse[i & 1][half * 32 + c];
+                p[half & 1] = s_pos[i & 1][half * 32 + c];
+            }
             if (half > 0) {
-                z = s_lse[i & 1][(half - 1) * 32 + c];
-                p = s_pos[i & 1][(half - 1) * 32 + c];
-                lo = a.window > 0 ? p - a.window + 1 : 0;
-                whole = __all(j0 + 31 <= p && (j0 >= lo || j0 + 31 < a.sinks));
-                if (!whole) {
+                // what is not seen, and rows that give nothing (z infinite), weigh 0
+                const int o = (half - 1) & 1;
+                const int lo = a.window > 0 ? p[o] - a.window + 1 : 0;
+#pragma unroll
+                for (int e = 0; e < 16; ++e) x[o][e] = x[o][e] * ks[e] - z[o];
+                if (!__all(j0 + 31 <= p[o] && (j0 >= lo || j0 + 31 < a.sinks))) {
 #pragma unroll
                     for (int e = 0; e < 16; ++e) {
                         const int t = j0 + (e >> 2) * 8 + g * 4 + (e & 3);
-                        const bool seen = (t <= p) & ((t >= lo) | (t < a.sinks));
-                        x[(half - 1) & 1][e] = seen ? x[(half - 1) & 1][e] * ks[e] : -INFINITY;
+                        const bool seen = (t <= p[o]) & ((t >= lo) | (t < a.sinks));
+                        x[o][e] = seen ? x[o][e] : -INFINITY;
                     }
-                } else {
-#pragma unroll
-                    for (int e = 0; e < 16; ++e) x[(half - 1) & 1][e] *= ks[e];
                 }
-                // what is not seen, and rows that give nothing (z infinite), weigh 0
             }
             if (half < H) x[half & 1] = f16v{0};
             __builtin_amdgcn_sched_barrier(0);
@@ -790,7 +807,7 @@ __global__ __launch_bounds__(kThreads, DP <= 128 ? 2 : 1) void k_weights(const E
                 if (half > 0) {
 #pragma unroll
                     for (int e = s * 16 / KM; e < (s + 1) * 16 / KM; ++e) {
-                        w[e] += __builtin_amdgcn_exp2f(x[(half - 1) & 1][e] - z);
+                        w[e] += __builtin_amdgcn_exp2f(x[(half - 1) & 1][e]);
                         asm volatile("" : "+v"(w[e]));
                     }
                 }
