@@ -31,8 +31,8 @@
 // Bound by HBM: 2 * group operations a code byte.  Measured on one MI355X, 8
 // KV heads of 128, group 4: 8 sequences of 65536 tokens (E5M2, scale per
 // head) 196 us = 5.5 TB/s, a device copy's rate here being 5.2; 64 ragged
-// sequences up to 4096 (E4M3, scale per (token, head), pages of 16) 68 us =
-// 4.1 TB/s, of which the join is 8.  One sequence of 517 tokens takes 15 us:
+// sequences up to 4096 (E4M3, scale per (token, head), pages of 16) 66 us =
+// 4.2 TB/s, of which the join is 5.  One sequence of 517 tokens takes 15 us:
 // lens -> page entry -> scales, K and V are dependent reads, then the join.
 #include <hip/hip_runtime.h>
 
@@ -64,6 +64,7 @@ struct DecodeParams {
     int64_t span;
     float* weights;
     int64_t ldw;
+    int join_waves;              // waves of the join that share a query head: 1 or kJoinWaves
 };
 
 // How a batch's steps are shared out.  The sequences' steps lie one after the
@@ -476,6 +477,7 @@ __device__ __forceinline__ float2 join_ml(const float2* ml, int64_t next, int n,
 }
 
 constexpr int kJoinThreads = 256;
+constexpr int kJoinWaves = kJoinThreads / 64;
 
 // weights[b, h, j] += sum over the group of 2^(x_j - lse), one thread a token.
 __global__ __launch_bounds__(kJoinThreads) void k_decode_weights(const DecodeParams a) {
@@ -498,34 +500,53 @@ __global__ __launch_bounds__(kJoinThreads) void k_decode_weights(const DecodePar
     if (seen) a.weights[((int64_t)b * a.kv.heads + h) * a.ldw + j] += w;
 }
 
-// One block per (query head, sequence): joins the pieces of a sequence that
-// several shares hold, in their order.  Threads take 4 channels each, several
-// pieces side by side.
+// Joins the pieces of a sequence that several shares hold, in their order: a
+// query head takes `a.join_waves` waves of a block, a thread 4 channels, and
+// what a wave has lanes for goes on to further pieces side by side.
 __global__ __launch_bounds__(kJoinThreads) void k_decode_join(const DecodeParams a) {
     __shared__ f4 s_acc[kJoinThreads];
-    const int hq = blockIdx.x, b = blockIdx.y;
-    const Work w = work_of(a, 0, b, threadIdx.x & 63);
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), b = blockIdx.y;
+    const int W = a.join_waves, part_of = wave % W;
+    const int hq = blockIdx.x * (kJoinWaves / W) + wave / W;
+    const Work w = work_of(a, 0, b, lane);
     const int i0 = w.before / w.chunk, n = (w.before + steps_of(a, w.len) - 1) / w.chunk - i0 + 1;
-    if (n <= 1) return;
+    if (n <= 1 || hq >= a.q_heads) return;              // the same for all W waves
     const int D = a.kv.head_dim, quads = D >> 2;
     const int64_t part = (int64_t)(i0 + b) * a.q_heads + hq, next = a.q_heads;
     const float2* ml = a.part_ml + part;
-    const float2 all = join_ml(ml, next, n, threadIdx.x & 63);
+    const int sides = 64 / quads, side = lane / quads, d = (lane - side * quads) * 4;
+    const int s0 = part_of * sides + side, apart = W * sides;
+    const bool on = side < sides;
+    // the first pieces are read beside the maxima and sums
+    constexpr int kFirst = 4;
+    f4 o[kFirst];
+    float piece_m[kFirst];
+#pragma unroll
+    for (int i = 0; i < kFirst; ++i) {
+        const int64_t s = min(s0 + i * apart, n - 1) * next;
+        o[i] = *reinterpret_cast<const f4*>(a.part_o + (part + s) * D + d);
+        piece_m[i] = ml[s].x;
+    }
+    const float2 all = join_ml(ml, next, n, lane);
     const float m = all.x, l = all.y;
-    const int lanes = kJoinThreads / quads;             // pieces side by side (4 or more)
-    const int side = threadIdx.x / quads, d = (threadIdx.x - side * quads) * 4;
     f4 acc = {0, 0, 0, 0};
-    if (side < lanes) {
+    if (on) {
+#pragma unroll
+        for (int i = 0; i < kFirst; ++i)
+            if (s0 + i * apart < n) acc += o[i] * __builtin_amdgcn_exp2f(piece_m[i] - m);
 #pragma unroll 4
-        for (int s = side; s < n; s += lanes) {
+        for (int s = s0 + kFirst * apart; s < n; s += apart) {
             const float f = __builtin_amdgcn_exp2f(ml[s * next].x - m);
             acc += *reinterpret_cast<const f4*>(a.part_o + (part + s * next) * D + d) * f;
         }
     }
     s_acc[threadIdx.x] = acc;
-    __syncthreads();
-    if (side != 0) return;
-    for (int s = 1; s < lanes; ++s) acc += s_acc[s * quads + threadIdx.x];
+    if (W == 1) wave_sync();
+    else __syncthreads();
+    if (side != 0 || part_of != 0) return;
+    const f4* mine = s_acc + (threadIdx.x - lane);
+    for (int v = 0; v < W; ++v)
+        for (int s = v == 0 ? 1 : 0; s < sides; ++s) acc += mine[v * 64 + s * quads + lane];
     const float r = l == 0.0f ? 0.0f : 1.0f / l;
     *reinterpret_cast<uint2*>(a.out + b * a.ldo + (int64_t)hq * D + d) =
         make_uint2(pack2(acc[0] * r, acc[1] * r), pack2(acc[2] * r, acc[3] * r));
@@ -631,6 +652,9 @@ hipError_t launch_decode(const AttnArgs& a) {
     p.part_o = reinterpret_cast<float*>(a.workspace + parts.ml);
     p.scores = plan.scores ? reinterpret_cast<float*>(a.workspace + parts.ml + parts.o) : nullptr;
     p.span = plan.span; p.weights = a.weights; p.ldw = a.ldw;
+    // Few pieces a sequence: a wave each is enough, in a quarter of the blocks
+    // (64 sequences of 5 pieces 5.0 us against 8.2; 16 of 17 pieces 6.2 against 5.6).
+    p.join_waves = plan.shares / a.kv.batch > 8 ? kJoinWaves : 1;
     hipError_t e;
     switch (a.kv.k_st) {
     case FP8_KV_E4M3: e = launch_v<kE4M3>(p, plan, a.stream); break;
@@ -639,8 +663,9 @@ hipError_t launch_decode(const AttnArgs& a) {
     }
     if (e != hipSuccess) return e;
     if (plan.joined) {
-        hipLaunchKernelGGL(k_decode_join, dim3((unsigned)a.q_heads, (unsigned)a.kv.batch), dim3(kJoinThreads), 0,
-                           a.stream, p);
+        const unsigned heads = (unsigned)(kJoinWaves / p.join_waves);
+        hipLaunchKernelGGL(k_decode_join, dim3(((unsigned)a.q_heads + heads - 1) / heads, (unsigned)a.kv.batch),
+                           dim3(kJoinThreads), 0, a.stream, p);
         e = hipGetLastError();
     }
     if (e != hipSuccess || !a.weighted) return e;
