@@ -46,6 +46,8 @@
 // over 4096 cached take 95 us.
 #include <hip/hip_runtime.h>
 
+#include <algorithm>
+
 #include "attention.hpp"
 
 namespace fp8mi {
@@ -73,7 +75,7 @@ struct ExtendParams {
     float* lse;
     float* weights;
     int64_t ldw;
-    int splits;                  // blocks that may share a row tile's steps
+    int splits, least;           // blocks that may share a row tile's steps, the fewest of one
     float2* part_ml;             // [total_q * q_heads, splits]
     float* part_o;               // [total_q * q_heads, splits, head_dim]
 };
@@ -138,11 +140,10 @@ struct Tile {
     __device__ __forceinline__ bool any() const { return row0 >= 0 && row0 < rows; }
 };
 
-// Steps of one block of a row tile: an even part, and no fewer than kLeast.
-constexpr int kLeast = 4;
+// Steps of one block of a row tile: an even part, and no fewer than a.least.
 __device__ __forceinline__ int chunk_of(const ExtendParams& a, int steps) {
     const int even = (steps + a.splits - 1) / a.splits;
-    return even < kLeast ? kLeast : even;
+    return even < a.least ? a.least : even;
 }
 
 template <int DP>
@@ -892,15 +893,21 @@ ExtendParams params_of(const AttnArgs& a) {
     p.group = a.q_heads / a.kv.heads; p.q_offsets = a.q_offsets; p.scale_log2 = a.scale * kLog2e;
     p.window = a.window; p.sinks = a.sinks; p.out = a.out; p.ldo = a.ldo; p.lse = a.lse;
     p.weights = a.weights; p.ldw = a.ldw;
-    p.splits = 1; p.part_ml = nullptr; p.part_o = nullptr;
+    p.splits = 1; p.least = 1; p.part_ml = nullptr; p.part_o = nullptr;
     return p;
 }
 
-// Blocks that share a row tile's steps: 1 where the tiles alone are two rounds
-// of blocks, else as many as make up these (1024 blocks measured 68 us against
-// 73 for 512 and 103 unsplit, 12 sequences of up to 77 queries and 3001
-// tokens), of at least 2 * kLeast steps in the longest sequence.
-int splits_of(const AttnArgs& a, bool ragged) {
+// Blocks that share a row tile's steps.  As many as make up one resident round
+// of 512, of 2 steps or more (one sequence, 32 queries, 8 KV heads: over 1024
+// tokens 17 us against 26 with pieces of 8 steps); in a ragged batch two rounds
+// where pieces keep 8 steps, since its tiles differ in length (12 sequences, up
+// to 77 queries and 3001 tokens: 66 us, one round 73, unsplit 103; of equal
+// lengths, 2 x 64 queries over 60000 tokens: 219 us, one round 190).  The join
+// reads all pieces one after the other, which bounds their number (one
+// sequence, 32 queries: over 4096 tokens 24 pieces 23 us and 32 29, over 100000
+// 24 pieces 142 and 32 119).  A tile of up to 8 steps stays whole: the join
+// costs what it saves.
+int splits_of(const AttnArgs& a, bool ragged, int* least) {
     const int64_t group = a.q_heads / a.kv.heads, each = a.total_q / a.kv.batch;
     const int64_t tiles = ragged ? a.total_q * group / kRows + a.kv.batch
                                  : a.kv.batch * ((each * group + kRows - 1) / kRows);
@@ -911,22 +918,27 @@ int splits_of(const AttnArgs& a, bool ragged) {
         const int64_t span = kRows / group + 1 + a.window, seen = (span + kStep - 1) / kStep + 1 + (a.sinks + kStep - 1) / kStep;
         steps = seen < steps ? seen : steps;
     }
-    int64_t s = 1024 / blocks;
-    const int64_t most = steps / (2 * kLeast);
-    s = s < most ? s : most;
-    return (int)(s < 1 ? 1 : s);
+    *least = 4;
+    if (steps <= 8 || blocks < 1) return 1;
+    const int64_t one = std::min(512 / blocks, steps / 2), two = ragged ? std::min(1024 / blocks, steps / 8) : 0;
+    const int64_t s = std::clamp<int64_t>(std::max(one, two), 1, steps <= 128 ? 24 : 32);
+    // shorter tiles of a ragged batch take fewer blocks, not shorter pieces
+    // (16 sequences up to 60 queries and 1500 tokens: 47 us, from 2 steps on 52)
+    *least = (int)std::clamp<int64_t>(steps / s, 2, 4);
+    return (int)s;
 }
 
 }  // namespace
 
 int64_t extend_workspace(const AttnArgs& a, bool ragged) {
-    const int64_t s = splits_of(a, ragged), rows = a.total_q * a.q_heads;
+    int least;
+    const int64_t s = splits_of(a, ragged, &least), rows = a.total_q * a.q_heads;
     return s == 1 ? 0 : (rows * s * 8 + 15) / 16 * 16 + rows * s * a.kv.head_dim * 4;
 }
 
 hipError_t launch_extend(const AttnArgs& a) {
     ExtendParams p = params_of(a);
-    p.splits = splits_of(a, a.q_offsets != nullptr);
+    p.splits = splits_of(a, a.q_offsets != nullptr, &p.least);
     const int64_t rows = a.total_q * a.q_heads;
     p.part_ml = reinterpret_cast<float2*>(a.workspace);
     p.part_o = reinterpret_cast<float*>(a.workspace + (rows * p.splits * 8 + 15) / 16 * 16);
