@@ -42,8 +42,9 @@
 // k_weights.  weights[b, h, j] += sum over the rows of 2^(x_ij - lse_i): a
 // block owns 128 tokens of a (sequence, KV head) with their K in registers
 // and walks the rows that see them, so every weight has one writer and the
-// sums have a fixed order.  Bound by the exponentials: 3 x 512 new tokens
-// over 4096 cached take 95 us.
+// sums have a fixed order.  Bound by the vector units (an fma, an exponential
+// and an addition a score) and by uneven blocks: 3 sequences of up to 512 new
+// tokens over up to 4096 cached take 77 us.
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
@@ -624,7 +625,7 @@ __global__ __launch_bounds__(kThreads) void k_extend_join(const ExtendParams a) 
 // would be 64 separate lines a load: 168 us where LDS took 102) and are shared
 // by the block's four waves, 128 rows at a time so that 32 rows' products
 // stand beside the exponentials of the 32 before (101 -> 95 us against 64 rows
-// one after the other).
+// one after the other; rows that advance without divisions 95 -> 78).
 template <int DP>
 struct WeightsLds {
     static constexpr int kR = DP <= 128 ? 128 : 64;     // rows of a step

@@ -5,9 +5,10 @@
 // equals), and its kept tokens move together in their order.
 //
 // Measured on one MI355X, 8 KV heads of 128 in E4M3, pages of 16: 16 sequences
-// cut from 16384 to 4096 tokens 98 us (selection 21, move 70-76, which reads
-// and writes 289 MB: 4 TB/s where a copy reaches 5.2); one sequence from 1100
-// to 1024 18 us, two dependent launches of 7 and 5 us.
+// cut from 16384 to 4096 tokens into other pages 96-98 us (selection 21, move
+// 70-76, which reads and writes 280 MB in rows of 128 bytes: 4 TB/s where a
+// copy reaches 5.2), in place 107 us; one sequence from 1100 to 1024 15-20 us,
+// two dependent launches of 7 and 5 us.
 //
 // Selection: one block per (KV head, sequence).  A radix select finds the
 // k-th largest weight in three histogram passes over 11, 11 and 10 bits of an
@@ -256,25 +257,24 @@ struct Route {
     int m;                      // rows kept
     bool in_place;
     int first, step;            // tiles of this block
-    __device__ __forceinline__ int row(const int32_t* table, int j) const {
-        const int64_t r = ((int64_t)table[j >> shift] << shift) + (j & ((1 << shift) - 1));
+    // cache row of token j, whose page is `entry`; -1 where there is none
+    __device__ __forceinline__ int row(int entry, int j) const {
+        const int64_t r = ((int64_t)entry << shift) + (j & ((1 << shift) - 1));
         return r >= 0 && r < capacity ? (int)r : -1;
     }
-    __device__ __forceinline__ int src(int j) const { return row(from, j); }
-    __device__ __forceinline__ int dst(int r) const { return row(to, r); }
+    __device__ __forceinline__ int src(int j) const { return row(from[j >> shift], j); }
+    __device__ __forceinline__ int dst(int r) const { return row(to[r >> shift], r); }
 };
 
-// Moves rows of one array of a head: `per` pieces of type T a row, rows
+// Copies rows of one array of a head into other pages: `per` pieces of type T a row, rows
 // `pitch` pieces apart.  A thread's pieces are the same part of rows a pass
 // apart, kPieces of them in flight.
 template <typename T>
-__device__ __forceinline__ void move_rows(const Route& w, T* data, int64_t pitch, int per) {
+__device__ __forceinline__ void copy_rows(const Route& w, T* data, int64_t pitch, int per) {
     const int pass = kMoveThreads / per, tile_rows = pass * kPieces;
     const int rr = threadIdx.x / per, q = threadIdx.x - rr * per;
     T* const base = data + q;
     for (int r0 = w.first * tile_rows; r0 < w.m; r0 += w.step * tile_rows) {
-        const int last = min(r0 + tile_rows, w.m) - 1;
-        if (w.in_place && w.kept[last] == last) continue;       // nothing before it was dropped
         // loads in three rounds, none of them conditional: positions, pages, rows
         int j[kPieces], to[kPieces];
         T v[kPieces];
@@ -289,24 +289,101 @@ __device__ __forceinline__ void move_rows(const Route& w, T* data, int64_t pitch
         }
 #pragma unroll
         for (int i = 0; i < kPieces; ++i) v[i] = base[max(j[i], 0) * pitch];
-        // every read of the tile has arrived before any of it is written;
-        // what is written is read by no later tile
-        if (w.in_place) {
-            __builtin_amdgcn_s_waitcnt(0);
-            __syncthreads();
-        }
 #pragma unroll
         for (int i = 0; i < kPieces; ++i)
             if (to[i] >= 0) base[to[i] * pitch] = v[i];
     }
 }
 
+// The same in place, by one block: tile after tile, each through four stages,
+// one a round, so that every round issues the loads of three tiles at once:
+// positions, page entries, pieces, and the stores.  2 sequences from 60000 to
+// 30000 tokens 304 us against 361 with one tile at a time (4 from 16384 to
+// 12000: 121 against 141); where a block has one tile, above, the registers of
+// the stages cost more than they bring (99 against 112).
+template <typename T>
+__device__ __forceinline__ void move_in_place(const Route& w, T* data, int64_t pitch, int per) {
+    const int pass = kMoveThreads / per, tile_rows = pass * kPieces;
+    const int rr = threadIdx.x / per, q = threadIdx.x - rr * per;
+    T* const base = data + q;
+    int r0 = 0;
+    for (; r0 < w.m; r0 += tile_rows) {         // nothing before these was dropped
+        const int last = min(r0 + tile_rows, w.m) - 1;
+        if (w.kept[last] != last) break;
+    }
+    if (r0 >= w.m) return;
+    // No load is conditional: past the end they repeat the last row, and what
+    // they bring is not stored.
+    int kept[kPieces];
+    int at[kPieces], entry[kPieces], to_entry[kPieces];
+    T x[kPieces], y[kPieces];
+    int x_to[kPieces], y_to[kPieces];
+    auto row_of = [&](int i, int tile) { return tile + i * pass + rr; };
+    auto positions = [&](int tile) {
+#pragma unroll
+        for (int i = 0; i < kPieces; ++i) kept[i] = w.kept[min(row_of(i, tile), w.m - 1)];
+    };
+    auto entries = [&](int tile) {
+#pragma unroll
+        for (int i = 0; i < kPieces; ++i) {
+            at[i] = kept[i];
+            entry[i] = w.from[at[i] >> w.shift];
+            to_entry[i] = w.to[min(row_of(i, tile), w.m - 1) >> w.shift];
+        }
+    };
+    auto pieces = [&](int tile, T* v, int* to) {
+#pragma unroll
+        for (int i = 0; i < kPieces; ++i) {
+            const int r = row_of(i, tile), src = w.row(entry[i], at[i]);
+            to[i] = src < 0 || r >= w.m || rr >= pass ? -1 : w.row(to_entry[i], r);
+            v[i] = base[max(src, 0) * pitch];
+        }
+    };
+    // Every read of the tile has arrived before any of it is written.  What is
+    // written is read by no later tile, so their reads may be on the way.
+    auto store = [&](T* v, const int* to) {
+#pragma unroll
+        for (int i = 0; i < kPieces; ++i) asm volatile("" : "+v"(v[i]));
+        __syncthreads();
+#pragma unroll
+        for (int i = 0; i < kPieces; ++i)
+            if (to[i] >= 0) base[to[i] * pitch] = v[i];
+    };
+    positions(r0);
+    entries(r0);
+    positions(r0 + tile_rows);
+    pieces(r0, x, x_to);
+    entries(r0 + tile_rows);
+    positions(r0 + 2 * tile_rows);
+    for (;;) {
+        pieces(r0 + tile_rows, y, y_to);
+        entries(r0 + 2 * tile_rows);
+        positions(r0 + 3 * tile_rows);
+        store(x, x_to);
+        r0 += tile_rows;
+        if (r0 >= w.m) break;
+        pieces(r0 + tile_rows, x, x_to);
+        entries(r0 + 2 * tile_rows);
+        positions(r0 + 3 * tile_rows);
+        store(y, y_to);
+        r0 += tile_rows;
+        if (r0 >= w.m) break;
+    }
+}
+
+template <bool IN_PLACE, typename T>
+__device__ __forceinline__ void move_rows(const Route& w, T* data, int64_t pitch, int per) {
+    if constexpr (IN_PLACE) move_in_place(w, data, pitch, per);
+    else copy_rows(w, data, pitch, per);
+}
+
+template <bool IN_PLACE>
 __global__ __launch_bounds__(kMoveThreads) void k_evict_move(const EvictArgs a, int parts) {
     const KvView& kv = a.kv;
     const int part = blockIdx.x % parts, h = blockIdx.x / parts, b = blockIdx.y;
     const int n = seq_len(kv, b), m = min(n, a.budget);
     const int64_t bh = (int64_t)b * kv.heads + h;
-    const bool in_place = part == 4 ? a.weights == a.weights_out : a.dst_table == nullptr;
+    const bool in_place = part == 4 ? a.weights == a.weights_out : IN_PLACE;
     if (in_place && (n <= a.budget || blockIdx.z > 0)) return;
     if (part < 4 && (kv.capacity == 0 || m == 0)) return;
     const int32_t* from = kv.table + b * kv.table_ld;
@@ -315,13 +392,13 @@ __global__ __launch_bounds__(kMoveThreads) void k_evict_move(const EvictArgs a, 
     const int kper = kv.head_dim * (kv.k_st == FP8_KV_BF16 ? 2 : 1) / 16;
     const int vper = kv.head_dim * (kv.v_st == FP8_KV_BF16 ? 2 : 1) / 16;
     switch (part) {
-    case 0: move_rows(w, static_cast<attn::u4*>(kv.k) + (int64_t)h * kper, (int64_t)kv.heads * kper, kper); break;
-    case 1: move_rows(w, static_cast<attn::u4*>(kv.v) + (int64_t)h * vper, (int64_t)kv.heads * vper, vper); break;
+    case 0: move_rows<IN_PLACE>(w, static_cast<attn::u4*>(kv.k) + (int64_t)h * kper, (int64_t)kv.heads * kper, kper); break;
+    case 1: move_rows<IN_PLACE>(w, static_cast<attn::u4*>(kv.v) + (int64_t)h * vper, (int64_t)kv.heads * vper, vper); break;
     case 2:
-        if (kv.k_scale && !kv.per_head) move_rows(w, kv.k_scale + h, (int64_t)kv.heads, 1);
+        if (kv.k_scale && !kv.per_head) move_rows<IN_PLACE>(w, kv.k_scale + h, (int64_t)kv.heads, 1);
         break;
     case 3:
-        if (kv.v_scale && !kv.per_head) move_rows(w, kv.v_scale + h, (int64_t)kv.heads, 1);
+        if (kv.v_scale && !kv.per_head) move_rows<IN_PLACE>(w, kv.v_scale + h, (int64_t)kv.heads, 1);
         break;
     default: {
         const float* src = a.weights + bh * a.ldw;
@@ -367,10 +444,12 @@ hipError_t launch_evict(const EvictArgs& a) {
     const bool wide = a.kv.k_st == FP8_KV_BF16 || a.kv.v_st == FP8_KV_BF16;
     const int64_t widest = a.kv.head_dim * (wide ? 2 : 1) / 16;         // 16-byte pieces of a row
     const int64_t rows = kMoveThreads / widest * kPieces, tiles = (a.budget + rows - 1) / rows;
-    const bool in_place = a.dst_table == nullptr && a.weights == a.weights_out;
     const dim3 move((unsigned)(parts * a.kv.heads), (unsigned)a.kv.batch,
-                    in_place ? 1u : (unsigned)(tiles < 1 ? 1 : tiles > 64 ? 64 : tiles));
-    hipLaunchKernelGGL(k_evict_move, move, dim3(kMoveThreads), 0, a.stream, a, parts);
+                    a.dst_table == nullptr ? 1u : (unsigned)(tiles < 1 ? 1 : tiles > 64 ? 64 : tiles));
+    if (a.dst_table == nullptr)
+        hipLaunchKernelGGL(k_evict_move<true>, move, dim3(kMoveThreads), 0, a.stream, a, parts);
+    else
+        hipLaunchKernelGGL(k_evict_move<false>, move, dim3(kMoveThreads), 0, a.stream, a, parts);
     return hipGetLastError();
 }
 

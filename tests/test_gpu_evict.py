@@ -116,6 +116,16 @@ def test_storages(k_st, v_st, scaling, dim, in_place):
     _check(c, _weights(4, 2, c.max_len, dim), budget, 4, 50, in_place, out_of_place_weights=not in_place, dst=dst)
 
 
+@pytest.mark.parametrize("dim, storage, lens, budget", [
+    (256, "bf16", [2500, 1900], 1500), (256, "bf16", [1300, 1000], 900), (128, "e4m3", [3300, 2200], 2100),
+    (16, "e4m3", [9500, 4097], 8300)])
+@pytest.mark.parametrize("kind", ["heavy", "ties"])
+def test_in_place_many_tiles(dim, storage, lens, budget, kind):
+    """Even and odd numbers of tiles of vectors, and of scales, one after the other."""
+    c = ref.Cache(lens, 2, dim, 16, storage, storage, seed=dim)
+    _check(c, _weights(2, 2, c.max_len, budget, kind), budget, 4, 100)
+
+
 @pytest.mark.parametrize("page", [1, 4, 64, 1024])
 @pytest.mark.parametrize("in_place", [True, False])
 def test_pages(page, in_place):
