@@ -733,7 +733,8 @@ def kv_evict(k_cache: torch.Tensor, v_cache: torch.Tensor, weights: torch.Tensor
     max_len] (the lower position among equals), moved together in their order.
     Without dst_page_table the cache, its scales and the weights are changed in
     place; with it (int32 [batch, pages] other pages of the same caches) the
-    kept tokens are copied there.  weights_out [batch, heads, >= budget]: the
+    kept tokens are copied there.  Sequences of one call must not share pages
+    that are written: with shared prefixes, evict into other pages.  weights_out [batch, heads, >= budget]: the
     kept tokens' weights go there instead of into weights.
 
     Returns (kept, new_lens): int32 [batch, heads, budget] positions kept, -1
