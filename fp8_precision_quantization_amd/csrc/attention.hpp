@@ -50,6 +50,21 @@ __device__ __forceinline__ uint32_t decode2(uint32_t w, bool high) {
     return __builtin_bit_cast(uint32_t, r);
 }
 
+// Words of w that hold a value that is not finite, and the same words with
+// these values cleared.
+template <int ST>
+__device__ __forceinline__ uint32_t not_finite(uint32_t w) {
+    uint32_t t;     // the top bit of every element that is not finite
+    if constexpr (ST == kE4M3) t = ((w & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u;
+    else if constexpr (ST == kE5M2) t = ((w & 0x7C7C7C7Cu) + 0x04040404u) & 0x80808080u;
+    else t = ((w & 0x7F807F80u) + 0x00800080u) & 0x80008000u;
+    return t;
+}
+template <int ST>
+__device__ __forceinline__ uint32_t cleared(uint32_t w, uint32_t t) {
+    return ST == kBf16 ? w & ~((t >> 15) * 0xFFFFu) : w & ~((t >> 7) * 0xFFu);
+}
+
 // Two fp32 -> two bf16 (round to nearest even), low half first.
 __device__ __forceinline__ uint32_t pack2(float a, float b) {
     const f2 v = {a, b};

@@ -161,21 +161,6 @@ struct Lds {
     uint32_t bad[kMarks / 32];      // step i marks bit i % kMarks
 };
 
-// Words of w that hold a value that is not finite, and the same words with
-// these values cleared.
-template <int ST>
-__device__ __forceinline__ uint32_t not_finite(uint32_t w) {
-    uint32_t t;     // the top bit of every element that is not finite
-    if constexpr (ST == kE4M3) t = ((w & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u;
-    else if constexpr (ST == kE5M2) t = ((w & 0x7C7C7C7Cu) + 0x04040404u) & 0x80808080u;
-    else t = ((w & 0x7F807F80u) + 0x00800080u) & 0x80008000u;
-    return t;
-}
-template <int ST>
-__device__ __forceinline__ uint32_t cleared(uint32_t w, uint32_t t) {
-    return ST == kBf16 ? w & ~((t >> 15) * 0xFFFFu) : w & ~((t >> 7) * 0xFFu);
-}
-
 // One value of the cache as fp32.
 template <int ST>
 __device__ __forceinline__ float value_at(const uint8_t* p, int d) {
