@@ -676,6 +676,11 @@ def kv_attention(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor, 
     tensor for callers that may not allocate (fp8_kv_attention_workspace
     bytes).
 
+    Scores, softmax and sums are in fp32.  The weights of one new token per
+    sequence enter the product with V with 16 significant bits, those of
+    several rounded once to bf16 (up to 2^-8 of sum p |v|, beside the output's
+    own rounding).
+
     Returns out [total_q, q_heads, head_dim] bf16, with return_lse (or lse
     given) also the fp32 log-sum-exp of the scores [total_q, q_heads]."""
     if v_storage is None:

@@ -16,8 +16,13 @@
 // O^T = V^T P^T when that product numbers its 16 tokens as the accumulator
 // rows lie.  V^T is read from the row-major LDS tile by transposing reads.
 // FP8 scales multiply the fp32 score and the fp32 weight; the weight is then
-// rounded once to bf16 (relative error 2^-8 at most, each token its own, so
-// the sum's is smaller than the output's own bf16 rounding).
+// rounded once to bf16, by 2^-8 of itself at most, while the row's sum adds it
+// unrounded: an output is off by up to 2^-8 of sum p |v|, as much as its own
+// bf16 rounding, for rows in which few tokens weigh most, and by less where
+// many do, whose errors are independent.  (A second product with the
+// remainder, as for one new token, would double the products with V.)  A row
+// that sees one token has the weight 1 exactly: with bf16 V, or scales that
+// are powers of two, it returns that token's values bit for bit.
 //
 // LDS rows are padded (K by 16 bytes, V by 64) so that the 16-byte reads of
 // 16 K rows, and the transposing reads of 4 V rows, fall into different banks.
@@ -416,10 +421,13 @@ __global__ __launch_bounds__(kThreads, DP <= 128 ? 2 : 1) void k_extend(const Ex
 #pragma unroll
             for (int e = 0; e < 16; ++e) mx = fmaxf(mx, x[t][e]);
             if (__any(mx > limit)) {
-                // m moves by whole powers of two, so everything that depends
-                // on it, the first half's bf16 weights included, scales exactly
+                // The first reference is the largest score itself, so that
+                // the weight of a row's only token is 1 and rounds to itself;
+                // from then on m moves by whole powers of two, so everything
+                // that depends on it, the first half's bf16 weights included,
+                // scales exactly.
                 mx = max_xor32(mx);
-                const float up = mx > limit ? __builtin_ceilf(mx) : 0.0f;
+                const float to = limit == kLowest ? mx : __builtin_ceilf(mx), up = mx > limit ? to : 0.0f;
                 const float f = limit == kLowest ? 1.0f : __builtin_amdgcn_exp2f(-up);  // before the first: o, l are 0
                 limit = mx > limit ? kSlack : limit;
                 m += up;

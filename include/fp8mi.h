@@ -451,7 +451,10 @@ typedef struct fp8_kv_pair {
  * Sums are in fp32 and in a fixed order: results are bit-reproducible run to
  * run; they may differ in the last bits between splits (batch sizes, max_len).
  * Scores, softmax and sums are in fp32; the weights enter the product with V
- * as bf16 pairs (one new token per sequence) or as bf16 (else). */
+ * as bf16 pairs (one new token per sequence) or rounded once to bf16 (else: an
+ * output is off by up to 2^-8 of sum_j exp(s_j - lse) |V_j| beside its own
+ * rounding; a row that sees one token has the weight 1 and no such error where
+ * V is bf16 or its scale a power of two). */
 fp8_status fp8_kv_attention(const fp8_kv_pair* cache, const void* q, int64_t ldq, int64_t total_q, int32_t q_heads,
                             const int32_t* q_offsets, float scale, int32_t window, int32_t sinks, void* out,
                             int64_t ldo, float* lse, float* weights, int64_t ldw, void* workspace,

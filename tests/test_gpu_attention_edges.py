@@ -1,5 +1,5 @@
 """Edges of fp8_kv_attention on the GPU: infinite values and scales of V that
-one new token sees."""
+one new token sees, and rows that see a single token."""
 from __future__ import annotations
 
 import numpy as np
@@ -93,3 +93,52 @@ def test_infinite_scale_of_a_head(n):
     assert np.array_equal(out[n - 1, 2:].float().cpu().numpy(), want, equal_nan=True)
     assert torch.isfinite(out[:n, :2]).all()
     assert (out[:n - 1] == 0).all() and (out[n:] == 0).all() and torch.isneginf(lse[n:]).all()
+
+
+def _single(cache, b, j):
+    """What a row returns that sees token j of sequence b alone: its values
+    times its scale in fp32, rounded once to bf16; [heads, dim]."""
+    row = cache.rows[b][j]
+    v = _codes(cache)[row]
+    if cache.v_storage != "bf16":
+        v = v * (cache.vs[row] if cache.scaling == "token_head" else cache.vs)[:, None]
+    return v.to(torch.bfloat16)
+
+
+def _pow2_scales(cache):
+    if cache.v_storage != "bf16" and cache.scaling == "token_head":
+        cache.vs = torch.exp2(torch.floor(torch.log2(cache.vs)))
+
+
+@pytest.mark.parametrize("dim", [64, 128, 256])
+@pytest.mark.parametrize("v_st, scaling", [("bf16", "token_head"), ("e4m3", "token_head"),
+                                           ("e5m2", "token_head")])
+def test_rows_of_a_single_token_return_it(v_st, scaling, dim):
+    """Several tokens at once: a row's only weight is 1 exactly, so a value
+    (with scales per token: powers of two) comes back bit for bit."""
+    lens = [40, 200]
+    c = ref.Cache(lens, 2, dim, 16, "e4m3", v_st, scaling, seed=dim)
+    _pow2_scales(c)
+    for n, window, ragged in (([40, 40], 1, False), ([40, 133], 1, True), ([40, 200], 0, True)):
+        q, out, lse = _run(c, n, 6, window, 0, ragged)
+        at = 0
+        for b in range(2):
+            for i in range(n[b]):
+                j = lens[b] - n[b] + i
+                if window == 1 or j == 0:
+                    want = _single(c, b, j).repeat_interleave(3, 0)
+                    assert torch.equal(out[at + i].cpu(), want), (b, i)
+            at += n[b]
+
+
+@pytest.mark.parametrize("v_st, scaling", [("bf16", "token_head"), ("e4m3", "token_head")])
+def test_single_token_of_a_split_row(v_st, scaling):
+    """The same where several blocks share a row's tokens, of which one is there."""
+    n, length, there = 5, 2100, 1700
+    c = ref.Cache([length], 2, 64, 1, "e4m3", v_st, scaling, seed=7,
+                  absent=[(0, p) for p in range(length) if p != there])
+    _pow2_scales(c)
+    q, out, lse = _run(c, [n], 4)
+    want = _single(c, 0, there).repeat_interleave(2, 0)
+    for i in range(n):
+        assert torch.equal(out[i].cpu(), want)
