@@ -15,19 +15,20 @@
 // exchange (lanes l and l + 32), and the weights are already the B operand of
 // O^T = V^T P^T when that product numbers its 16 tokens as the accumulator
 // rows lie.  V^T is read from the row-major LDS tile by transposing reads.
-// FP8 scales multiply the fp32 score and the fp32 weight; the weight is then
-// rounded once to bf16, by 2^-8 of itself at most, while the row's sum adds it
-// unrounded: an output is off by up to 2^-8 of sum p |v|, as much as its own
-// bf16 rounding, for rows in which few tokens weigh most, and by less where
-// many do, whose errors are independent.  (A second product with the
-// remainder, as for one new token, would double the products with V.)  A row
-// that sees one token has the weight 1 exactly: with bf16 V, or scales that
-// are powers of two, it returns that token's values bit for bit.
+// FP8 scales per token multiply the fp32 score and the fp32 weight, V's scale
+// per head the fp32 output; the weight is then rounded once to bf16, by 2^-8
+// of itself at most, while the row's sum adds it unrounded: an output is off
+// by up to 2^-8 of sum p |v|, as much as its own bf16 rounding, for rows in
+// which few tokens weigh most, and by less where many do, whose errors are
+// independent.  (A second product with the remainder, as for one new token,
+// would double the products with V.)  A row that sees one token has the weight
+// 1 exactly: with bf16 V, a scale per head, or scales per token that are powers
+// of two, it returns that token's values bit for bit.
 //
 // LDS rows are padded (K by 16 bytes, V by 64) so that the 16-byte reads of
 // 16 K rows, and the transposing reads of 4 V rows, fall into different banks.
 //
-// Values of V that are not finite (and tokens whose V scale is not): a product
+// Values of V that are not finite (and tokens whose own V scale is not): a product
 // with weight 0 would turn a token that one row does not see into NaN for that
 // row.  Staging puts 0 in their place and marks the step; a block that met one
 // goes over its marked steps once more at the end and adds these values, row
@@ -96,6 +97,11 @@ __device__ __forceinline__ void queries_of(const ExtendParams& a, int b, int* fi
         *first = lo;
         *n = hi - lo;
     }
+}
+
+// V's scale of a KV head where it has one for all tokens, else 1.
+__device__ __forceinline__ float v_scale_of(const KvView& kv, int h) {
+    return kv.per_head && kv.v_scale ? kv.v_scale[h] : 1.0f;
 }
 
 // With q_offsets: slot of the first row tile of sequence b.  A sequence's
@@ -285,7 +291,6 @@ __global__ __launch_bounds__(kThreads, DP <= 128 ? 2 : 1) void k_extend(const Ex
     float scale_log2 = a.scale_log2;
     asm volatile("" : "+s"(scale_log2));      // a register: selects below must not pick an argument's address
     const float k_head = (KST == kBf16 || k_tok ? 1.0f : kv.k_scale[h]) * scale_log2;
-    const float v_head = VST == kBf16 || v_tok ? 1.0f : kv.v_scale[h];
 
     // Staging.  No load is conditional, so that a wait for one counts the later
     // ones: tokens that are not there (their score is masked, their weight 0)
@@ -298,7 +303,7 @@ __global__ __launch_bounds__(kThreads, DP <= 128 ? 2 : 1) void k_extend(const Ex
     const float* const k_scales = k_tok ? kv.k_scale : reinterpret_cast<const float*>(table);
     const float* const v_scales = v_tok ? kv.v_scale : reinterpret_cast<const float*>(table);
     const float* const scales = key ? k_scales : v_scales;
-    const float scale_of_head = key ? k_head : v_head, scale_by = key ? scale_log2 : 1.0f;
+    const float scale_of_head = key ? k_head : 1.0f, scale_by = key ? scale_log2 : 1.0f;
     auto entry_of = [&](int i) -> int {         // the page of token tid % kStep of a step
         const int j = steps.token(min(i, s_end - 1)) + (tid & (kStep - 1));
         return table[min(j, p_last) >> kv.page_shift];
@@ -521,7 +526,7 @@ __global__ __launch_bounds__(kThreads, DP <= 128 ? 2 : 1) void k_extend(const Ex
                 const int row = row_of_entry(kv, table[j >> kv.page_shift], j);
                 if (row < 0) continue;
                 const uint8_t* vr = vb + row * v_row;
-                const float s = v_tok ? kv.v_scale[(int64_t)row * kv.heads + h] : v_head;
+                const float s = v_tok ? kv.v_scale[(int64_t)row * kv.heads + h] : 1.0f;
                 bool odd = !__builtin_isfinite(s);
                 for (int d = lane; d < D; d += 64) odd = odd || !__builtin_isfinite(value_at<VST>(vr, d));
                 if (!__any(odd)) continue;
@@ -563,7 +568,7 @@ __global__ __launch_bounds__(kThreads, DP <= 128 ? 2 : 1) void k_extend(const Ex
             }
         return;
     }
-    const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+    const float inv = l == 0.0f ? 0.0f : v_scale_of(kv, h) / l;
     uint16_t* to = a.out + (int64_t)(q_first + tok) * a.ldo + (int64_t)hq * D;
 #pragma unroll
     for (int d = 0; d < DT; ++d)
@@ -606,7 +611,7 @@ __global__ __launch_bounds__(kThreads) void k_extend_join(const ExtendParams a) 
             l += ml[s].y * f;
             acc += *reinterpret_cast<const f4*>(a.part_o + (row * a.splits + s) * D + d) * f;
         }
-        const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+        const float inv = l == 0.0f ? 0.0f : v_scale_of(a.kv, h) / l;
         *reinterpret_cast<uint2*>(a.out + (int64_t)tok * a.ldo + (int64_t)hq * D + d) =
             make_uint2(pack2(acc[0] * inv, acc[1] * inv), pack2(acc[2] * inv, acc[3] * inv));
         if (d == 0 && a.lse) a.lse[row] = l == 0.0f ? -INFINITY : (m + __builtin_amdgcn_logf(l)) * kLn2;

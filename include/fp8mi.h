@@ -454,7 +454,7 @@ typedef struct fp8_kv_pair {
  * as bf16 pairs (one new token per sequence) or rounded once to bf16 (else: an
  * output is off by up to 2^-8 of sum_j exp(s_j - lse) |V_j| beside its own
  * rounding; a row that sees one token has the weight 1 and no such error where
- * V is bf16 or its scale a power of two). */
+ * V is bf16, or its scale is per head or a power of two). */
 fp8_status fp8_kv_attention(const fp8_kv_pair* cache, const void* q, int64_t ldq, int64_t total_q, int32_t q_heads,
                             const int32_t* q_offsets, float scale, int32_t window, int32_t sinks, void* out,
                             int64_t ldo, float* lse, float* weights, int64_t ldw, void* workspace,

@@ -1,5 +1,5 @@
 """Edges of fp8_kv_attention on the GPU: infinite values and scales of V that
-one new token sees, and rows that see a single token."""
+a row sees, and rows that see a single token."""
 from __future__ import annotations
 
 import numpy as np
@@ -82,7 +82,7 @@ def test_one_token_sees_an_infinite_scale(v_st):
     assert torch.isfinite(out[:, :4]).all() and torch.isfinite(lse).all()
 
 
-@pytest.mark.parametrize("n", [1])
+@pytest.mark.parametrize("n", [1, 2])
 def test_infinite_scale_of_a_head(n):
     """Rows that see one token: its signs; a row that sees nothing: 0."""
     c = ref.Cache([1, 0], 2, 64, 16, "e4m3", "e5m2", "head", seed=4)
@@ -112,10 +112,11 @@ def _pow2_scales(cache):
 
 @pytest.mark.parametrize("dim", [64, 128, 256])
 @pytest.mark.parametrize("v_st, scaling", [("bf16", "token_head"), ("e4m3", "token_head"),
-                                           ("e5m2", "token_head")])
+                                           ("e5m2", "token_head"), ("e4m3", "head"), ("e5m2", "head")])
 def test_rows_of_a_single_token_return_it(v_st, scaling, dim):
     """Several tokens at once: a row's only weight is 1 exactly, so a value
-    (with scales per token: powers of two) comes back bit for bit."""
+    (with scales per token: powers of two, any scale per head) comes back bit
+    for bit."""
     lens = [40, 200]
     c = ref.Cache(lens, 2, dim, 16, "e4m3", v_st, scaling, seed=dim)
     _pow2_scales(c)
@@ -131,7 +132,7 @@ def test_rows_of_a_single_token_return_it(v_st, scaling, dim):
             at += n[b]
 
 
-@pytest.mark.parametrize("v_st, scaling", [("bf16", "token_head"), ("e4m3", "token_head")])
+@pytest.mark.parametrize("v_st, scaling", [("bf16", "token_head"), ("e4m3", "token_head"), ("e4m3", "head")])
 def test_single_token_of_a_split_row(v_st, scaling):
     """The same where several blocks share a row's tokens, of which one is there."""
     n, length, there = 5, 2100, 1700
