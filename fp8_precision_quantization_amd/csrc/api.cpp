@@ -583,9 +583,10 @@ static fp8_status attention_args(const fp8_kv_pair* cache, bool sizes, int64_t t
     if (q_heads < 1 || q_heads % cache->heads != 0)
         return fail(FP8_ERR_INVALID_ARG, "q_heads=%d must be a multiple of heads=%d", (int)q_heads,
                     (int)cache->heads);
-    if (total_q >= (int64_t(1) << 30) || total_q >= (int64_t(1) << 31) / q_heads || q_heads > 65535)
+    // rows are counted in 32 bits, rounded up to a tile of 128 and one more
+    if (total_q >= (int64_t(1) << 30) || total_q > ((int64_t(1) << 31) - 256) / q_heads || q_heads > 65535)
         return fail(FP8_ERR_UNSUPPORTED_SHAPE,
-                    "total_q must be < 2^30, total_q * q_heads < 2^31 and q_heads <= 65535");
+                    "total_q must be < 2^30, total_q * q_heads <= 2^31 - 256 and q_heads <= 65535");
     // blocks of the launches
     if ((int64_t)cache->batch * cache->heads >= (int64_t(1) << 30) ||
         (cache->max_len / 128 + 1) * cache->heads >= (int64_t(1) << 31))

@@ -657,7 +657,8 @@ __global__ __launch_bounds__(kThreads, DP <= 128 ? 2 : 1) void k_weights(const E
 
     // rows (token of the call, head in the group) that see any of the block's tokens
     int i_lo = block0 - base, i_hi = n;
-    if (a.window > 0 && block0 >= a.sinks) i_hi = min(i_hi, block0 + kRows - 1 + a.window - base);
+    if (a.window > 0 && block0 >= a.sinks)      // (a window and a position may add up to 2^31)
+        i_hi = (int)std::min<int64_t>(i_hi, (int64_t)block0 + kRows - 1 + a.window - base);
     i_lo = i_lo < 0 ? 0 : i_lo;
     if (i_lo >= i_hi) return;
     const int r_first = i_lo * G, r_end = i_hi * G;
@@ -827,7 +828,7 @@ __global__ __launch_bounds__(kThreads, DP <= 128 ? 2 : 1) void k_weights(const E
     }
 }
 
-// total_q * q_heads < 2^31: a tile count is far inside int
+// total_q * q_heads <= 2^31 - 256: rows, rounded up to a tile, are inside int
 int tiles_of(const ExtendParams& p) {
     return p.q_offsets == nullptr ? p.kv.batch * ((p.each * p.group + kRows - 1) / kRows)
                                   : p.total_q * p.group / kRows + p.kv.batch;

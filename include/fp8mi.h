@@ -433,7 +433,7 @@ typedef struct fp8_kv_pair {
  * q: bf16 [total_q x (q_heads*head_dim)], leading dimension ldq; out: bf16,
  * the same shape, ldo (both multiples of 8, 16-byte aligned); out must not
  * overlap anything the call reads.  q_heads a multiple of heads and <= 65535,
- * total_q < 2^30, total_q * q_heads < 2^31.
+ * total_q < 2^30, total_q * q_heads <= 2^31 - 256.
  * q_offsets: NULL = every sequence has total_q / batch new tokens (total_q a
  * multiple of batch); else DEVICE int32 [batch + 1], non-decreasing, within
  * [0, total_q]: sequence b's queries are rows q_offsets[b]..q_offsets[b+1]-1
