@@ -575,6 +575,8 @@ static fp8_status check_kv_pair(const fp8_kv_pair* c, bool sizes, fp8mi::KvView*
     return FP8_OK;
 }
 
+static bool one_each(const fp8mi::AttnArgs& a, bool ragged) { return !ragged && a.total_q == a.kv.batch; }
+
 static fp8_status attention_args(const fp8_kv_pair* cache, bool sizes, int64_t total_q, int32_t q_heads, bool ragged,
                                  int32_t window, int32_t sinks, bool weighted, fp8mi::AttnArgs* a) {
     fp8_status st = check_kv_pair(cache, sizes, &a->kv);
@@ -604,10 +606,16 @@ static fp8_status attention_args(const fp8_kv_pair* cache, bool sizes, int64_t t
     // a window that reaches every token is none; sinks past the end are all
     a->window = window >= cache->max_len ? 0 : window;
     a->sinks = sinks > cache->max_len ? (int)cache->max_len : sinks;
+    if (total_q > 0) {
+        const int64_t blocks = one_each(*a, ragged) ? fp8mi::decode_blocks(*a) : fp8mi::extend_blocks(*a, ragged);
+        if (blocks > fp8mi::kMaxAttnBlocks)
+            return fail(FP8_ERR_UNSUPPORTED_SHAPE,
+                        "%lld blocks (row tiles * heads, with weights also max_len / 128 * heads) must be < 2^24",
+                        (long long)blocks);
+    }
     return FP8_OK;
 }
 
-static bool one_each(const fp8mi::AttnArgs& a, bool ragged) { return !ragged && a.total_q == a.kv.batch; }
 
 static int64_t attention_bytes(const fp8mi::AttnArgs& a, bool ragged) {
     if (a.total_q == 0) return 0;

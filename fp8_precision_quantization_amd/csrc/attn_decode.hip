@@ -644,6 +644,8 @@ Plan plan_of(const AttnArgs& a) {
     return p;
 }
 
+int64_t weights_tiles(const Plan& p) { return (p.span + kJoinThreads - 1) / kJoinThreads; }
+
 template <int KST, int VST, int DP>
 hipError_t launch_wide(const DecodeParams& p, const Plan& plan, hipStream_t stream) {
     const dim3 grid((unsigned)plan.blocks), block(64 * kWaves);
@@ -691,6 +693,13 @@ int64_t decode_workspace(const AttnArgs& a) {
     return parts.ml + parts.o + parts.scores;
 }
 
+// Of the launch that computes the weights: the others have a few thousand blocks.
+int64_t decode_blocks(const AttnArgs& a) {
+    if (!a.weighted) return 0;
+    const Plan plan = plan_of(a);
+    return plan.scores ? weights_tiles(plan) * a.kv.heads : extend_blocks(a, false);
+}
+
 hipError_t launch_decode(const AttnArgs& a) {
     const Plan plan = plan_of(a);
     DecodeParams p;
@@ -720,7 +729,7 @@ hipError_t launch_decode(const AttnArgs& a) {
     }
     if (e != hipSuccess || !a.weighted) return e;
     if (!plan.scores) return launch_attention_weights(a);
-    const unsigned tiles = (unsigned)((plan.span + kJoinThreads - 1) / kJoinThreads);
+    const unsigned tiles = (unsigned)weights_tiles(plan);
     hipLaunchKernelGGL(k_decode_weights, dim3(tiles * (unsigned)a.kv.heads, (unsigned)a.kv.batch), dim3(kJoinThreads),
                        0, a.stream, p);
     return hipGetLastError();

@@ -828,42 +828,40 @@ __global__ __launch_bounds__(kThreads, DP <= 128 ? 2 : 1) void k_weights(const E
     }
 }
 
-// total_q * q_heads <= 2^31 - 256: rows, rounded up to a tile, are inside int
-int tiles_of(const ExtendParams& p) {
-    return p.q_offsets == nullptr ? p.kv.batch * ((p.each * p.group + kRows - 1) / kRows)
-                                  : p.total_q * p.group / kRows + p.kv.batch;
+// Row tiles of a call, spare slots of a ragged one included.
+int64_t tiles_of(const AttnArgs& a, bool ragged) {
+    const int64_t group = a.q_heads / a.kv.heads, each = a.total_q / a.kv.batch;
+    return ragged ? a.total_q * group / kRows + a.kv.batch : a.kv.batch * ((each * group + kRows - 1) / kRows);
 }
+int64_t weights_tiles(const AttnArgs& a) { return (a.kv.max_len + kRows - 1) / kRows; }
 
 template <int KST, int VST, int DP>
-hipError_t run_extend(const ExtendParams& p, hipStream_t stream) {
+hipError_t run_extend(const ExtendParams& p, unsigned tiles, hipStream_t stream) {
     static_assert(sizeof(Lds<DP>) <= 160 * 1024, "LDS");
     constexpr int bytes = sizeof(Lds<DP>);
     hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(&k_extend<KST, VST, DP>),
                                        hipFuncAttributeMaxDynamicSharedMemorySize, bytes);
     if (e != hipSuccess) return e;
-    const int tiles = tiles_of(p);
-    hipLaunchKernelGGL((k_extend<KST, VST, DP>), dim3((unsigned)(tiles * p.kv.heads * p.splits)), dim3(kThreads), bytes,
-                       stream, p);
+    hipLaunchKernelGGL((k_extend<KST, VST, DP>), dim3(tiles * p.kv.heads * p.splits), dim3(kThreads), bytes, stream, p);
     e = hipGetLastError();
     if (e != hipSuccess || p.splits == 1) return e;
-    hipLaunchKernelGGL(k_extend_join, dim3((unsigned)(tiles * p.kv.heads), kRows / kJoinRows), dim3(kThreads), 0, stream,
-                       p);
+    hipLaunchKernelGGL(k_extend_join, dim3(tiles * p.kv.heads, kRows / kJoinRows), dim3(kThreads), 0, stream, p);
     return hipGetLastError();
 }
 
 template <int KST, int VST>
-hipError_t extend_dim(const ExtendParams& p, hipStream_t stream) {
-    if (p.kv.head_dim <= 64) return run_extend<KST, VST, 64>(p, stream);
-    if (p.kv.head_dim <= 128) return run_extend<KST, VST, 128>(p, stream);
-    return run_extend<KST, VST, 256>(p, stream);
+hipError_t extend_dim(const ExtendParams& p, unsigned tiles, hipStream_t stream) {
+    if (p.kv.head_dim <= 64) return run_extend<KST, VST, 64>(p, tiles, stream);
+    if (p.kv.head_dim <= 128) return run_extend<KST, VST, 128>(p, tiles, stream);
+    return run_extend<KST, VST, 256>(p, tiles, stream);
 }
 
 template <int KST>
-hipError_t extend_v(const ExtendParams& p, hipStream_t stream) {
+hipError_t extend_v(const ExtendParams& p, unsigned tiles, hipStream_t stream) {
     switch (p.kv.v_st) {
-    case FP8_KV_E4M3: return extend_dim<KST, kE4M3>(p, stream);
-    case FP8_KV_E5M2: return extend_dim<KST, kE5M2>(p, stream);
-    default: return extend_dim<KST, kBf16>(p, stream);
+    case FP8_KV_E4M3: return extend_dim<KST, kE4M3>(p, tiles, stream);
+    case FP8_KV_E5M2: return extend_dim<KST, kE5M2>(p, tiles, stream);
+    default: return extend_dim<KST, kBf16>(p, tiles, stream);
     }
 }
 
@@ -879,8 +877,7 @@ hipError_t run_weights(const ExtendParams& p, dim3 grid, hipStream_t stream) {
 }
 
 template <int KST>
-hipError_t weights_dim(const ExtendParams& p, hipStream_t stream) {
-    const unsigned tiles = (unsigned)((p.kv.max_len + kRows - 1) / kRows);
+hipError_t weights_dim(const ExtendParams& p, unsigned tiles, hipStream_t stream) {
     const dim3 grid(tiles * p.kv.heads, (unsigned)p.kv.batch);
     if (p.kv.head_dim <= 64) return run_weights<KST, 64>(p, grid, stream);
     if (p.kv.head_dim <= 128) return run_weights<KST, 128>(p, grid, stream);
@@ -908,10 +905,7 @@ ExtendParams params_of(const AttnArgs& a) {
 // 24 pieces 142 and 32 119).  A tile of up to 8 steps stays whole: the join
 // costs what it saves.
 int splits_of(const AttnArgs& a, bool ragged, int* least) {
-    const int64_t group = a.q_heads / a.kv.heads, each = a.total_q / a.kv.batch;
-    const int64_t tiles = ragged ? a.total_q * group / kRows + a.kv.batch
-                                 : a.kv.batch * ((each * group + kRows - 1) / kRows);
-    const int64_t blocks = tiles * a.kv.heads;
+    const int64_t group = a.q_heads / a.kv.heads, blocks = tiles_of(a, ragged) * a.kv.heads;
     int64_t steps = (a.kv.max_len + kStep - 1) / kStep;
     if (a.window > 0) {
         // a tile's tokens, their window and the sinks
@@ -936,17 +930,24 @@ int64_t extend_workspace(const AttnArgs& a, bool ragged) {
     return s == 1 ? 0 : (rows * s * 8 + 15) / 16 * 16 + rows * s * a.kv.head_dim * 4;
 }
 
+int64_t extend_blocks(const AttnArgs& a, bool ragged) {
+    int least;
+    const int64_t tiles = tiles_of(a, ragged) * splits_of(a, ragged, &least);
+    return std::max(tiles, a.weighted ? weights_tiles(a) : 0) * a.kv.heads;
+}
+
 hipError_t launch_extend(const AttnArgs& a) {
     ExtendParams p = params_of(a);
     p.splits = splits_of(a, a.q_offsets != nullptr, &p.least);
+    const unsigned tiles = (unsigned)tiles_of(a, a.q_offsets != nullptr);
     const int64_t rows = a.total_q * a.q_heads;
     p.part_ml = reinterpret_cast<float2*>(a.workspace);
     p.part_o = reinterpret_cast<float*>(a.workspace + (rows * p.splits * 8 + 15) / 16 * 16);
     hipError_t e;
     switch (a.kv.k_st) {
-    case FP8_KV_E4M3: e = extend_v<kE4M3>(p, a.stream); break;
-    case FP8_KV_E5M2: e = extend_v<kE5M2>(p, a.stream); break;
-    default: e = extend_v<kBf16>(p, a.stream); break;
+    case FP8_KV_E4M3: e = extend_v<kE4M3>(p, tiles, a.stream); break;
+    case FP8_KV_E5M2: e = extend_v<kE5M2>(p, tiles, a.stream); break;
+    default: e = extend_v<kBf16>(p, tiles, a.stream); break;
     }
     return e != hipSuccess || !a.weighted ? e : launch_attention_weights(a);
 }
@@ -954,10 +955,11 @@ hipError_t launch_extend(const AttnArgs& a) {
 hipError_t launch_attention_weights(const AttnArgs& a) {
     if (a.kv.max_len == 0) return hipSuccess;
     const ExtendParams p = params_of(a);
+    const unsigned tiles = (unsigned)weights_tiles(a);
     switch (a.kv.k_st) {
-    case FP8_KV_E4M3: return weights_dim<kE4M3>(p, a.stream);
-    case FP8_KV_E5M2: return weights_dim<kE5M2>(p, a.stream);
-    default: return weights_dim<kBf16>(p, a.stream);
+    case FP8_KV_E4M3: return weights_dim<kE4M3>(p, tiles, a.stream);
+    case FP8_KV_E5M2: return weights_dim<kE5M2>(p, tiles, a.stream);
+    default: return weights_dim<kBf16>(p, tiles, a.stream);
     }
 }
 

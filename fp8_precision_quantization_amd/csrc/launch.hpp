@@ -165,6 +165,11 @@ hipError_t launch_kv_load(const KvLoadArgs& a);
 // same rules as the launch's splits.
 int64_t decode_workspace(const AttnArgs& a);
 int64_t extend_workspace(const AttnArgs& a, bool ragged);
+// Blocks (of 256 threads) of the call's largest launch.  2^32 threads and more
+// are not launched, or wrap to fewer without an error.
+int64_t decode_blocks(const AttnArgs& a);
+int64_t extend_blocks(const AttnArgs& a, bool ragged);
+constexpr int64_t kMaxAttnBlocks = (int64_t(1) << 24) - 1;
 hipError_t launch_decode(const AttnArgs& a);              // weights included
 hipError_t launch_extend(const AttnArgs& a);              // weights included
 hipError_t launch_attention_weights(const AttnArgs& a);   // the weights alone, from the keys and a.lse

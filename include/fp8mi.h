@@ -398,7 +398,10 @@ fp8_status fp8_kv_load(const void* cache, fp8_kv_storage storage, fp8_kv_scaling
  * page_size a power of two <= 2^20; head_dim % 16 == 0, 16 <= head_dim <= 256;
  * capacity < 2^31, max_len < 2^30; heads and batch <= 65535; for the attention
  * also batch * max_len < 2^35, batch * heads < 2^30 and max_len / 128 * heads
- * < 2^31; caches 16-byte aligned. */
+ * < 2^31, and launches of fewer than 2^24 blocks: where a sequence has several
+ * new tokens or q_offsets is given, (total_q * q_heads / heads / 128 + batch) *
+ * heads, and with weights max_len / 128 * heads (each rounded up); caches
+ * 16-byte aligned. */
 typedef struct fp8_kv_pair {
     void* k;
     void* v;

@@ -29,3 +29,33 @@ def test_rows_stay_in_32_bits(group, ragged):
         assert size(p, total, group, ragged) == -1 and "total_q" in L.lib().fp8_last_error().decode()
         check(attention(p, total_q=total, q_heads=group, ldq=16 * 1000, ldo=16 * 1000, q_offsets=0x10000 * ragged or None),
               U, "total_q")
+
+
+@pytest.mark.parametrize("p, q, status", [
+    # sequences of several tokens: a tile of 128 rows each, by every KV head
+    (dict(batch=65535, heads=256), dict(total_q=65535, q_heads=256, ragged=1), U),
+    (dict(batch=65000, heads=255), dict(total_q=65000, q_heads=255, ragged=1), 0),
+    (dict(batch=65535, heads=512), dict(total_q=65535, q_heads=512, ragged=1), U),
+    (dict(batch=32768, heads=512), dict(total_q=65536, q_heads=512), U),
+    (dict(batch=32767, heads=512), dict(total_q=65534, q_heads=512), 0),
+    (dict(batch=65535, heads=512), dict(total_q=65535, q_heads=512), 0),            # one token each
+    # weights: a block for 128 tokens of a KV head, 256 of the last token's stored scores
+    (dict(batch=1, heads=8, max_len=1 << 28), dict(total_q=2, q_heads=8, weighted=1), U),
+    (dict(batch=1, heads=8, max_len=(1 << 28) - 128), dict(total_q=2, q_heads=8, weighted=1), 0),
+    (dict(batch=1, heads=8, max_len=1 << 28), dict(total_q=2, q_heads=8), 0),
+    (dict(batch=1, heads=8, max_len=1 << 28), dict(total_q=1, q_heads=8, weighted=1), 0),
+    (dict(batch=1, heads=8, max_len=1 << 29), dict(total_q=1, q_heads=8, weighted=1), U),
+    (dict(batch=1, heads=8, max_len=1 << 29), dict(total_q=1, q_heads=8, weighted=1, window=4096), 0),
+    (dict(batch=1, heads=8, max_len=1 << 28), dict(total_q=1, q_heads=1024, weighted=1), U),
+])
+def test_launches_stay_below_2_32_threads(p, q, status):
+    """A launch of more is refused by the runtime or wraps to fewer blocks."""
+    c = pair(**{**dict(head_dim=16, page_size=1 << 20, page_ld=512), **p})
+    got = size(c, q["total_q"], q["q_heads"], q.get("ragged", 0), q.get("window", 0), 0, q.get("weighted", 0))
+    if status == 0:
+        assert got >= 0, L.lib().fp8_last_error()
+        return
+    assert got == -1 and "2^24" in L.lib().fp8_last_error().decode()
+    w = c.max_len if q.get("weighted") else 0
+    check(attention(c, total_q=q["total_q"], q_heads=q["q_heads"], ldq=16 * q["q_heads"], ldo=16 * q["q_heads"],
+                    q_offsets=0x10000 if q.get("ragged") else None, weights=0x10000 if w else None, ldw=w), status, "2^24")
