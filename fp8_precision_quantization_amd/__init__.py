@@ -559,11 +559,18 @@ def kv_load(cache: torch.Tensor, scale_inv: Optional[torch.Tensor], n: Optional[
 _PAIR = struct.Struct("PPPPqPqPqiiiiiiii")     # fp8_kv_pair (_lib.Fp8KvPair) as the bytes a call passes
 
 
+def _int32(value: int, name: str) -> None:
+    """A number the library takes as int32: ctypes would pass its low 32 bits."""
+    if not -(1 << 31) <= value < 1 << 31:
+        raise ValueError("%s=%d does not fit in 32 bits" % (name, value))
+
+
 def _kv_pair(k_cache, v_cache, page_table, lens, page_size, k_scale_inv, v_scale_inv, k_storage, v_storage, scaling,
              max_len):
     """The fp8_kv_pair (as bytes) of a layer's K and V caches and a batch's
     pages, and the sizes in it: (pair, heads, head_dim, batch, max_len).
     Raises before any launch if a buffer is not what the library would read."""
+    _int32(page_size, "page_size")
     shape = k_cache.shape
     if len(shape) != 3 or not k_cache.is_cuda:
         raise ValueError("k_cache must be a [capacity, heads, head_dim] device tensor")
@@ -685,6 +692,8 @@ def kv_attention(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor, 
     given) also the fp32 log-sum-exp of the scores [total_q, q_heads]."""
     if v_storage is None:
         v_storage = k_storage
+    _int32(window, "window")
+    _int32(sinks, "sinks")
     pair, heads, head_dim, batch, max_len = _kv_pair(k_cache, v_cache, page_table, lens, page_size, k_scale_inv,
                                                      v_scale_inv, k_storage, v_storage, scaling, max_len)
     dev = k_cache.device
@@ -747,6 +756,8 @@ def kv_evict(k_cache: torch.Tensor, v_cache: torch.Tensor, weights: torch.Tensor
     every layer of a model evicts with the same one."""
     if v_storage is None:
         v_storage = k_storage
+    for value, name in ((budget, "budget"), (sinks, "sinks"), (recent, "recent")):
+        _int32(value, name)
     pair, heads, _, batch, max_len = _kv_pair(k_cache, v_cache, page_table, lens, page_size, k_scale_inv, v_scale_inv,
                                               k_storage, v_storage, scaling, max_len)
     dev = k_cache.device
