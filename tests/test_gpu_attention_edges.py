@@ -1,5 +1,7 @@
-"""Edges of fp8_kv_attention on the GPU: infinite values and scales of V that
-a row sees, and rows that see a single token."""
+"""Edges of fp8_kv_attention and fp8_kv_evict on the GPU: infinite values and
+scales of V that a row sees, rows that see a single token, sequences whose
+neighbours change, weights and evictions in a cache whose offsets pass 32 bits,
+and batches of thousands."""
 from __future__ import annotations
 
 import numpy as np
@@ -143,3 +145,110 @@ def test_single_token_of_a_split_row(v_st, scaling):
     want = _single(c, 0, there).repeat_interleave(2, 0)
     for i in range(n):
         assert torch.equal(out[i].cpu(), want)
+
+
+@pytest.mark.parametrize("n", [[1] * 4, [3, 2, 70, 1]])
+@pytest.mark.parametrize("target", [0, 2])
+def test_neighbours_contents_do_not_matter(n, target):
+    """Other codes, scales and queries in the other sequences, of the same
+    lengths: not a bit of this one's results changes."""
+    lens = [700, 3, 2500, 41]
+    c = ref.Cache(lens, 2, 128, 16, seed=6)
+    ragged = len(set(n)) > 1
+    q = ref.queries(c, n, 8)
+    first = sum(n[:target])
+    mine = slice(first, first + n[target])
+    results = []
+    for other in (False, True):
+        if other:
+            theirs = np.concatenate([c.rows[b] for b in range(4) if b != target])
+            g = torch.Generator().manual_seed(11)
+            for x in (c.k, c.v):
+                x[theirs] = torch.randint(0, 0x7F, x[theirs].shape, generator=g, dtype=torch.uint8)
+            for x in (c.ks, c.vs):
+                x[theirs] *= 1 + torch.rand(x[theirs].shape, generator=g)
+            keep = q[mine].clone()
+            q = ref.queries(c, n, 8, seed=12)
+            q[mine] = keep
+        w = torch.zeros(4, 2, c.max_len, device="cuda")
+        _, out, lse = _run(c, n, 8, ragged=ragged, q=q, weights=w)
+        results.append((out[mine].clone(), lse[mine].clone(), w[target].clone(), out, w))
+    for a, b in zip(results[0][:3], results[1][:3]):
+        assert torch.equal(a, b)
+    assert not torch.equal(results[0][3], results[1][3]) and not torch.equal(results[0][4], results[1][4])
+
+
+class _Long:
+    """A cache of more than 2^32 bytes with a small one's rows at its end."""
+
+    def __init__(self, small):
+        heads, dim, page = small.heads, small.dim, small.page
+        capacity = (1 << 32) // (heads * dim) + 2 * small.capacity
+        self.first = capacity - small.capacity
+        self.first -= self.first % page
+        end = slice(self.first, self.first + small.capacity)
+        self.args = dict(page_size=page, lens=torch.tensor(small.lens, dtype=torch.int32).cuda(),
+                         page_table=torch.from_numpy(small.table + self.first // page).cuda())
+        for name, part in (("k_cache", small.k), ("v_cache", small.v)):
+            t = torch.zeros((capacity, heads, dim), dtype=torch.uint8, device="cuda")
+            t[end] = part.cuda()
+            self.args[name] = t
+        for name, part in (("k_scale_inv", small.ks), ("v_scale_inv", small.vs)):
+            t = torch.ones((capacity, heads), device="cuda")
+            t[end] = part.cuda()
+            self.args[name] = t
+        self.end = end
+
+
+@pytest.mark.parametrize("n", [[1, 1], [9, 30]])
+def test_weights_past_2_31_elements(n):
+    """The keys that the weights are made from lie past 32-bit offsets."""
+    small = ref.Cache([200, 90], 8, 128, 16, seed=9)
+    long = _Long(small)
+    q = ref.queries(small, n, 16)
+    if n[0] > 1:
+        long.args["q_offsets"] = torch.tensor([0, n[0], sum(n)], dtype=torch.int32).cuda()
+    w = torch.zeros(2, 8, small.max_len, device="cuda")
+    say("long cache, weights", n)
+    out, lse = fp8.kv_attention(q.cuda(), weights=w, return_lse=True, **long.args)
+    torch.cuda.synchronize()
+    want, delta, acc = ref.check_attention(small, q, n, out, lse)
+    for b, x in enumerate(want):
+        got = w[b].double().cpu().numpy()
+        bound = (2 * float(delta.max()) + acc + 2.0 ** -20) * (x + 1e-6 * n[b]) + 2.0 ** -23 * x
+        assert (np.abs(got[:, :small.lens[b]] - x) <= bound).all()
+        assert (got[:, small.lens[b]:] == 0).all()
+
+
+@pytest.mark.parametrize("in_place", [True, False])
+def test_evict_past_2_31_elements(in_place):
+    """The same rows move as in a small cache, and nothing below them changes."""
+    small = ref.Cache([700, 333, 60], 8, 128, 16, seed=10, slack_pages=3 * 10)
+    dst = np.setdiff1d(np.arange(small.capacity // 16), small.table.ravel())[:30].reshape(3, 10).astype(np.int32)
+    w = torch.rand(3, 8, small.max_len, generator=torch.Generator().manual_seed(5)).cuda()
+    long = _Long(small)
+    results = []
+    for args, at in ((small.device(), 0), (long.args, long.first)):
+        args = {k: v for k, v in args.items() if k not in ("k_storage", "v_storage", "scaling")}
+        table = None if in_place else torch.from_numpy(dst + at // 16).cuda()
+        ww = w.clone()
+        say("evict, first row", at, "in place", in_place)
+        kept, lens = fp8.kv_evict(weights=ww, budget=160, sinks=4, recent=50, dst_page_table=table, **args)
+        torch.cuda.synchronize()
+        rows = slice(at, at + small.capacity)
+        results.append([kept, lens, ww] + [args[x][rows] for x in ("k_cache", "v_cache", "k_scale_inv", "v_scale_inv")])
+    for a, b in zip(*results):
+        assert torch.equal(a.contiguous().view(torch.uint8), b.contiguous().view(torch.uint8))
+    assert not long.args["k_cache"][:long.first].any() and not long.args["v_cache"][:long.first].any()
+    assert (long.args["k_scale_inv"][:long.first] == 1).all()
+
+
+@pytest.mark.parametrize("ragged", [False, True])
+def test_thousands_of_sequences(ragged):
+    """Shares and row tiles found among 3000 short sequences, empty ones among them."""
+    rng = np.random.default_rng(4)
+    lens = [int(x) for x in rng.integers(0, 40, 3000)]
+    n = [int(x) for x in rng.integers(0, 4, 3000)] if ragged else [1] * 3000
+    c = ref.Cache(lens, 1, 32, 8, seed=25)
+    q, out, lse = _run(c, n, 2, ragged=ragged)
+    ref.check_attention(c, q, n, out, lse, p_bits=8 if ragged else 15)
