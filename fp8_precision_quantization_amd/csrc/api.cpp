@@ -683,6 +683,8 @@ fp8_status fp8_kv_evict(const fp8_kv_pair* cache, float* weights, int64_t ldw, i
     fp8_status st = check_kv_pair(cache, false, &a.kv);
     if (st != FP8_OK) return st;
     if (budget < 1) return fail(FP8_ERR_INVALID_ARG, "budget=%d must be >= 1", (int)budget);
+    // positions advance by whole blocks and grids past the budget in 32 bits
+    if (budget >= 1 << 30) return fail(FP8_ERR_UNSUPPORTED_SHAPE, "budget=%d must be < 2^30", (int)budget);
     if (sinks < 0 || recent < 0 || (int64_t)sinks + recent > budget)
         return fail(FP8_ERR_INVALID_ARG, "sinks=%d and recent=%d must be >= 0 and together <= budget=%d", (int)sinks,
                     (int)recent, (int)budget);

@@ -493,7 +493,7 @@ int64_t fp8_kv_attention_workspace(const fp8_kv_pair* cache, int64_t total_q, in
  *   it).
  * weights_out (unless it is weights), kept and new_lens must not overlap
  * anything else the call reads or writes.
- * 0 <= sinks, 0 <= recent, sinks + recent <= budget, budget >= 1. */
+ * 0 <= sinks, 0 <= recent, sinks + recent <= budget, 1 <= budget < 2^30. */
 fp8_status fp8_kv_evict(const fp8_kv_pair* cache, float* weights, int64_t ldw, int32_t budget, int32_t sinks,
                         int32_t recent, const int32_t* dst_page_table, int64_t dst_page_ld, float* weights_out,
                         int64_t ldwo, int32_t* kept, int32_t* new_lens, void* stream);

@@ -1,6 +1,6 @@
-"""Sizes at the limits of fp8_kv_attention, checked without a GPU through its
-workspace query and its own refusals.  Pointers are fake and never
-dereferenced."""
+"""Sizes at the limits of fp8_kv_attention and fp8_kv_evict, checked without a
+GPU through the workspace query and the calls' own refusals.  Pointers are
+fake and never dereferenced."""
 from __future__ import annotations
 
 import ctypes
@@ -8,7 +8,7 @@ import ctypes
 import pytest
 
 from fp8_precision_quantization_amd import _lib as L
-from tests.test_attention_boundary import U, attention, check, pair
+from tests.test_attention_boundary import U, attention, check, evict, pair
 
 
 def size(p, total, q_heads, ragged=0, window=0, sinks=0, weighted=0):
@@ -59,3 +59,9 @@ def test_launches_stay_below_2_32_threads(p, q, status):
     w = c.max_len if q.get("weighted") else 0
     check(attention(c, total_q=q["total_q"], q_heads=q["q_heads"], ldq=16 * q["q_heads"], ldo=16 * q["q_heads"],
                     q_offsets=0x10000 if q.get("ragged") else None, weights=0x10000 if w else None, ldw=w), status, "2^24")
+
+
+@pytest.mark.parametrize("budget", [1 << 30, (1 << 31) - 1])
+def test_budget_stays_below_2_30(budget):
+    """No sequence is longer; loops over a larger budget would pass 2^31."""
+    check(evict(budget=budget), U, "budget")
