@@ -391,14 +391,20 @@ __global__ __launch_bounds__(kMoveThreads) void k_evict_move(const EvictArgs a, 
                      kv.page_shift, (int)kv.capacity, m, in_place, (int)blockIdx.z, in_place ? 1 : (int)gridDim.z};
     const int kper = kv.head_dim * (kv.k_st == FP8_KV_BF16 ? 2 : 1) / 16;
     const int vper = kv.head_dim * (kv.v_st == FP8_KV_BF16 ? 2 : 1) / 16;
+    // (K and V, or their scales, may be one array: it moves once)
     switch (part) {
-    case 0: move_rows<IN_PLACE>(w, static_cast<attn::u4*>(kv.k) + (int64_t)h * kper, (int64_t)kv.heads * kper, kper); break;
-    case 1: move_rows<IN_PLACE>(w, static_cast<attn::u4*>(kv.v) + (int64_t)h * vper, (int64_t)kv.heads * vper, vper); break;
+    case 0:
+        move_rows<IN_PLACE>(w, static_cast<attn::u4*>(kv.k) + (int64_t)h * kper, (int64_t)kv.heads * kper, kper);
+        break;
+    case 1:
+        if (kv.v != kv.k)
+            move_rows<IN_PLACE>(w, static_cast<attn::u4*>(kv.v) + (int64_t)h * vper, (int64_t)kv.heads * vper, vper);
+        break;
     case 2:
         if (kv.k_scale && !kv.per_head) move_rows<IN_PLACE>(w, kv.k_scale + h, (int64_t)kv.heads, 1);
         break;
     case 3:
-        if (kv.v_scale && !kv.per_head) move_rows<IN_PLACE>(w, kv.v_scale + h, (int64_t)kv.heads, 1);
+        if (kv.v_scale && kv.v_scale != kv.k_scale && !kv.per_head) move_rows<IN_PLACE>(w, kv.v_scale + h, (int64_t)kv.heads, 1);
         break;
     default: {
         const float* src = a.weights + bh * a.ldw;

@@ -492,7 +492,8 @@ int64_t fp8_kv_attention_workspace(const fp8_kv_pair* cache, int64_t total_q, in
  *   min(len_b, budget); lens itself is not changed (a model's layers share
  *   it).
  * weights_out (unless it is weights), kept and new_lens must not overlap
- * anything else the call reads or writes.
+ * anything else the call reads or writes.  K and V, and their scales, may be
+ * one array, which moves once, or do not overlap.
  * 0 <= sinks, 0 <= recent, sinks + recent <= budget, 1 <= budget < 2^30. */
 fp8_status fp8_kv_evict(const fp8_kv_pair* cache, float* weights, int64_t ldw, int32_t budget, int32_t sinks,
                         int32_t recent, const int32_t* dst_page_table, int64_t dst_page_ld, float* weights_out,

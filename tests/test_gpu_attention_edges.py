@@ -252,3 +252,36 @@ def test_thousands_of_sequences(ragged):
     c = ref.Cache(lens, 1, 32, 8, seed=25)
     q, out, lse = _run(c, n, 2, ragged=ragged)
     ref.check_attention(c, q, n, out, lse, p_bits=8 if ragged else 15)
+
+
+@pytest.mark.parametrize("same_cache", [True, False])
+@pytest.mark.parametrize("in_place", [True, False])
+def test_evict_where_k_and_v_share_arrays(same_cache, in_place):
+    """One array for K and V, or for their scales alone, moves once."""
+    lens, budget = [9500, 4097, 60], 4300
+    c = ref.Cache(lens, 2, 32, 16, seed=12, slack_pages=3 * 270)
+    dst = np.setdiff1d(np.arange(c.capacity // 16), c.table.ravel())[:3 * 270].reshape(3, 270).astype(np.int32)
+    args = c.device()
+    args["v_scale_inv"] = args["k_scale_inv"]
+    if same_cache:
+        args["v_cache"] = args["k_cache"]
+    before = {x: args[x].clone() for x in ("k_cache", "v_cache", "k_scale_inv")}
+    w = torch.rand(3, 2, c.max_len, generator=torch.Generator().manual_seed(6))
+    say("evict, shared arrays", same_cache, in_place)
+    kept, new_lens = fp8.kv_evict(weights=w.cuda(), budget=budget, sinks=4, recent=100,
+                                  dst_page_table=None if in_place else torch.from_numpy(dst).cuda(), **args)
+    torch.cuda.synchronize()
+    want = {x: t.clone() for x, t in before.items()}
+    to_table = c.table if in_place else dst
+    for b, n in enumerate(lens):
+        m = min(n, budget)
+        r = np.arange(m)
+        to = torch.from_numpy(to_table[b, r // 16].astype(np.int64) * 16 + r % 16).cuda()
+        for h in range(2):
+            keep = ref.evict(w[b, h].numpy(), n, budget, 4, 100)
+            assert np.array_equal(kept[b, h, :m].cpu().numpy(), keep)
+            src = torch.from_numpy(c.table[b, keep // 16].astype(np.int64) * 16 + keep % 16).cuda()
+            for x in want:
+                want[x][to, h] = before[x][src, h]
+    for x in want:
+        assert torch.equal(args[x].view(torch.uint8), want[x].view(torch.uint8)), x
