@@ -681,7 +681,10 @@ def kv_attention(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor, 
     weights: fp32 [batch, heads, >= max_len], to which the call adds what each
     cached token receives (the input of kv_evict).  workspace: a uint8 device
     tensor for callers that may not allocate (fp8_kv_attention_workspace
-    bytes).
+    bytes; it follows max_len: with weights and one new token per sequence,
+    batch * q_heads * max_len fp32 scores, so a max_len near the longest
+    sequence saves memory where page_table holds more).  out must not overlap
+    anything the call reads, q included.  No gradient is formed.
 
     Scores, softmax and sums are in fp32.  The weights of one new token per
     sequence enter the product with V with 16 significant bits, those of
@@ -748,8 +751,10 @@ def kv_evict(k_cache: torch.Tensor, v_cache: torch.Tensor, weights: torch.Tensor
     Without dst_page_table the cache, its scales and the weights are changed in
     place; with it (int32 [batch, pages] other pages of the same caches) the
     kept tokens are copied there.  Sequences of one call must not share pages
-    that are written: with shared prefixes, evict into other pages.  weights_out [batch, heads, >= budget]: the
-    kept tokens' weights go there instead of into weights.
+    that are written: with shared prefixes, evict into other pages.  A kept
+    token without a page does not move, and its new row stays as it was.
+    weights_out [batch, heads, >= budget]: the kept tokens' weights go there
+    instead of into weights.
 
     Returns (kept, new_lens): int32 [batch, heads, budget] positions kept, -1
     behind the last, and int32 [batch] the new lengths.  lens is not changed:

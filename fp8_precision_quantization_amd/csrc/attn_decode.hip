@@ -34,9 +34,9 @@
 //
 // Bound by HBM: 2 * group operations a code byte.  Measured on one MI355X, 8
 // KV heads of 128, group 4: 8 sequences of 65536 tokens (E5M2, scale per
-// head) 196 us = 5.5 TB/s, a device copy's rate here being 5.2; 64 ragged
-// sequences up to 4096 (E4M3, scale per (token, head), pages of 16) 66 us =
-// 4.2 TB/s, of which the join is 5.  One sequence of 517 tokens takes 15 us:
+// head) 197 us = 5.5 TB/s, where a read-only probe reaches 7.2; 64 ragged
+// sequences up to 4096 (E4M3, scale per (token, head), pages of 16) 65 us =
+// 4.3 TB/s, of which the join is 5.  One sequence of 517 tokens takes 15 us:
 // lens -> page entry -> scales, K and V are dependent reads, then the join.
 #include <hip/hip_runtime.h>
 
@@ -490,7 +490,8 @@ __global__ __launch_bounds__(64 * kWaves, DP <= 128 && NT == 1 ? 2 : 1) void k_d
         if (g == 0) {
             if (!alone) a.part_ml[part] = make_float2(m[nt], sum);
             else if (a.lse)
-                a.lse[(int64_t)b * a.q_heads + hq] = sum == 0.0f ? -INFINITY : (m[nt] + __builtin_amdgcn_logf(sum)) * kLn2;
+                a.lse[(int64_t)b * a.q_heads + hq] =
+                    sum == 0.0f ? -INFINITY : (m[nt] + __builtin_amdgcn_logf(sum)) * kLn2;
         }
 #pragma unroll
         for (int i = 0; i < 4; ++i) {

@@ -326,7 +326,8 @@ __global__ __launch_bounds__(kThreads, DP <= 128 ? 2 : 1) void k_extend(const Ex
         }
     };
     auto mark = [&](int i) { atomicOr(&lds.bad[i % kMarks / 32], 1u << (i % 32)); };
-    auto put = [&](int i, int part) {           // K or V of one unit into a step's LDS buffer, the scales with the first
+    // K or V of one unit into a step's LDS buffer, the scales with the first
+    auto put = [&](int i, int part) {
         typename L::Buf& buf = lds.buf[i & 1];
         const int u = part >> 1, t = (tid + u * kThreads) / UR, e = (tid + u * kThreads) % UR;
         if (part & 1) {
@@ -487,7 +488,8 @@ __global__ __launch_bounds__(kThreads, DP <= 128 ? 2 : 1) void k_extend(const Ex
         // Lane i of 16 points at row i / 4, channels 4 (i % 4).. of a 4 x 16
         // block and receives its column i.
         b8 vf[4];
-        const uint8_t* vp = buf.v + (g * 4 + ((lane & 15) >> 2)) * L::kV + (((lane >> 4) & 1) * 16 + (lane & 3) * 4) * 2;
+        const uint8_t* vp =
+            buf.v + (g * 4 + ((lane & 15) >> 2)) * L::kV + (((lane >> 4) & 1) * 16 + (lane & 3) * 4) * 2;
         auto read_v = [&](int n) {
             const uint8_t* p = vp + n / DT * 16 * L::kV + n % DT * 64;
             const s4 lo = read_tr(p), hi = read_tr(p + 8 * L::kV);
@@ -886,8 +888,8 @@ hipError_t weights_dim(const ExtendParams& p, unsigned tiles, hipStream_t stream
 
 ExtendParams params_of(const AttnArgs& a) {
     ExtendParams p;
-    p.kv = a.kv; p.q = a.q; p.ldq = a.ldq; p.total_q = (int)a.total_q; p.each = (int)(a.total_q / a.kv.batch); p.q_heads = a.q_heads;
-    p.group = a.q_heads / a.kv.heads; p.q_offsets = a.q_offsets; p.scale_log2 = a.scale * kLog2e;
+    p.kv = a.kv; p.q = a.q; p.ldq = a.ldq; p.total_q = (int)a.total_q; p.each = (int)(a.total_q / a.kv.batch);
+    p.q_heads = a.q_heads; p.group = a.q_heads / a.kv.heads; p.q_offsets = a.q_offsets; p.scale_log2 = a.scale * kLog2e;
     p.window = a.window; p.sinks = a.sinks; p.out = a.out; p.ldo = a.ldo; p.lse = a.lse;
     p.weights = a.weights; p.ldw = a.ldw;
     p.splits = 1; p.least = 1; p.part_ml = nullptr; p.part_o = nullptr;
@@ -902,14 +904,16 @@ ExtendParams params_of(const AttnArgs& a) {
 // lengths, 2 x 64 queries over 60000 tokens: 219 us, one round 190).  The join
 // reads all pieces one after the other, which bounds their number (one
 // sequence, 32 queries: over 4096 tokens 24 pieces 23 us and 32 29, over 100000
-// 24 pieces 142 and 32 119).  A tile of up to 8 steps stays whole: the join
-// costs what it saves.
+// 24 pieces 142 and 32 119).  Where max_len is no more than 8 steps every tile
+// stays whole: the join costs what it saves.  (A short tile of a batch whose
+// max_len is larger is cut all the same, into pieces of 2 to 4 steps.)
 int splits_of(const AttnArgs& a, bool ragged, int* least) {
     const int64_t group = a.q_heads / a.kv.heads, blocks = tiles_of(a, ragged) * a.kv.heads;
     int64_t steps = (a.kv.max_len + kStep - 1) / kStep;
     if (a.window > 0) {
         // a tile's tokens, their window and the sinks
-        const int64_t span = kRows / group + 1 + a.window, seen = (span + kStep - 1) / kStep + 1 + (a.sinks + kStep - 1) / kStep;
+        const int64_t span = kRows / group + 1 + a.window;
+        const int64_t seen = (span + kStep - 1) / kStep + 1 + (a.sinks + kStep - 1) / kStep;
         steps = seen < steps ? seen : steps;
     }
     *least = 4;

@@ -404,7 +404,8 @@ __global__ __launch_bounds__(kMoveThreads) void k_evict_move(const EvictArgs a, 
         if (kv.k_scale && !kv.per_head) move_rows<IN_PLACE>(w, kv.k_scale + h, (int64_t)kv.heads, 1);
         break;
     case 3:
-        if (kv.v_scale && kv.v_scale != kv.k_scale && !kv.per_head) move_rows<IN_PLACE>(w, kv.v_scale + h, (int64_t)kv.heads, 1);
+        if (kv.v_scale && kv.v_scale != kv.k_scale && !kv.per_head)
+            move_rows<IN_PLACE>(w, kv.v_scale + h, (int64_t)kv.heads, 1);
         break;
     default: {
         const float* src = a.weights + bh * a.ldw;

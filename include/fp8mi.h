@@ -448,8 +448,9 @@ typedef struct fp8_kv_pair {
  * call ADDS what every cached token receives, summed over the sequence's
  * queries and the query heads of the KV head: weights[b,h,j] += sum exp(s_j -
  * lse).  Needs lse.  Entries of tokens that are not there are left alone.
- * workspace: fp8_kv_attention_workspace() bytes, 16-byte aligned, as the
- * other workspaces (no initialization; not shared by calls that can run at
+ * workspace: fp8_kv_attention_workspace() bytes (they follow max_len, not
+ * lens: with weights and one new token per sequence, batch * q_heads * max_len
+ * fp32 scores), 16-byte aligned, as the other workspaces (no initialization; not shared by calls that can run at
  * the same time, captured graphs included); NULL is fine when that is 0.
  * Sums are in fp32 and in a fixed order: results are bit-reproducible run to
  * run; they may differ in the last bits between splits (batch sizes, max_len).
@@ -484,8 +485,10 @@ int64_t fp8_kv_attention_workspace(const fp8_kv_pair* cache, int64_t total_q, in
  * dst_page_table: NULL = in place; else int32 [batch x dst_page_ld] pages of
  *   the same caches (dst_page_ld * page_size >= budget) that hold no page of
  *   page_table: the kept tokens of every sequence, shorter ones included, are
- *   copied there and the old pages stay as they are.  Tokens whose source or
- *   destination row is outside the cache are left out.
+ *   copied there and the old pages stay as they are.
+ * A kept token whose source or destination row is outside the cache does not
+ *   move: it counts in kept and new_lens, and its new row stays as it was, so a
+ *   sequence that is cut should have pages for the tokens it keeps.
  * Sequences (of one call) must not share pages that are written.
  * kept: int32 [batch x heads x budget], the positions kept (increasing), -1
  *   behind the last of a shorter sequence.  new_lens: int32 [batch],
