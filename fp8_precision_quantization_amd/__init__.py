@@ -25,7 +25,7 @@ from ._lib import Fp8Error  # noqa: F401
 
 __all__ = ["quantize", "quantize_dual", "quantize_tensors", "amax", "scaled_gemm", "blockscaled_gemm", "AmaxHistory", "Diag",
            "QuantResult", "Fp8Error", "FORMATS", "GRANULARITIES", "group_grid", "kv_store", "kv_load",
-           "KVTensorCache", "KVCache", "grouped_gemm", "workspace", "kv_attention", "kv_evict"]
+           "KVTensorCache", "KVCache", "grouped_gemm", "workspace", "kv_attention", "kv_evict", "kv_append"]
 
 FORMATS = {"e4m3": _lib.FP8_E4M3, "e5m2": _lib.FP8_E5M2}
 GRANULARITIES = {"tensor": _lib.FP8_GRAN_TENSOR, "row": _lib.FP8_GRAN_ROW,
@@ -565,6 +565,12 @@ def _int32(value: int, name: str) -> None:
         raise ValueError("%s=%d does not fit in 32 bits" % (name, value))
 
 
+def _len32(t: torch.Tensor, name: str) -> int:
+    """The number of a 1-D tensor's elements, where twice as many still fit in 32 bits."""
+    _int32(2 * t.numel(), name)
+    return t.numel()
+
+
 def _kv_pair(k_cache, v_cache, page_table, lens, page_size, k_scale_inv, v_scale_inv, k_storage, v_storage, scaling,
              max_len):
     """The fp8_kv_pair (as bytes) of a layer's K and V caches and a batch's
@@ -652,6 +658,132 @@ def _call_on(device, func, *args):
         return func(*args, _stream(device))
     with torch.cuda.device(device):
         return func(*args, _stream(device))
+
+
+def _caches(k_cache, v_cache, k_scale_inv, v_scale_inv, k_storage, v_storage, scaling):
+    """The fp8_kv_pair (as bytes) of a layer's K and V caches alone, without pages: (pair, heads, head_dim)."""
+    shape = k_cache.shape
+    if len(shape) != 3 or not k_cache.is_cuda:
+        raise ValueError("k_cache must be a [capacity, heads, head_dim] device tensor")
+    capacity, heads, head_dim = shape
+    dev = k_cache.device
+    if v_cache.shape != shape:
+        raise ValueError("k_cache and v_cache must have one shape, got %s and %s"
+                         % (tuple(shape), tuple(v_cache.shape)))
+    for cache, st, name in ((k_cache, k_storage, "k_cache"), (v_cache, v_storage, "v_cache")):
+        want = torch.bfloat16 if st == "bf16" else torch.uint8
+        if cache.dtype != want or not cache.is_contiguous() or cache.device != dev:
+            raise ValueError("%s must be a contiguous %s tensor on %s" % (name, want, dev))
+    pair = _PAIR.pack(
+        k_cache.data_ptr(), v_cache.data_ptr(), _kv_scales(k_scale_inv, k_storage, scaling, capacity, heads, dev) or 0,
+        _kv_scales(v_scale_inv, v_storage, scaling, capacity, heads, dev) or 0, capacity, 0, 0, 0, 0,
+        KV_STORAGE[k_storage], KV_STORAGE[v_storage], KV_SCALING[scaling], heads, head_dim, 1, 0, 0)
+    return pair, heads, head_dim
+
+
+def kv_append(k: torch.Tensor, v: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
+              slots: Optional[torch.Tensor] = None, q: Optional[torch.Tensor] = None,
+              positions: Optional[torch.Tensor] = None, inv_freq: Optional[torch.Tensor] = None, sections=None,
+              interleaved: bool = False, q_out: Optional[torch.Tensor] = None,
+              k_scale_inv: Optional[torch.Tensor] = None, v_scale_inv: Optional[torch.Tensor] = None,
+              k_storage="e4m3", v_storage=None, scaling="token_head", pow2: bool = False,
+              diag: Optional[Diag] = None) -> Optional[torch.Tensor]:
+    """Append new tokens to one layer's K and V caches in one launch, rotating
+    q and k by their positions on the way (fp8_kv_append).
+
+    k, v: [n, heads, head_dim] or [n, heads * head_dim], q (optional): [n,
+    q_heads, head_dim] or 2-D, all bf16 or all fp32, heads packed within a
+    token (slices of one projection's output are fine).  Caches, scales,
+    storage and scaling as kv_store and kv_attention take them; slots: int64
+    [n] cache rows (None: rows 0..n-1; outside the cache: not stored).
+
+    inv_freq: fp32 [rotary_dim / 2], radians a position, of the pairs of the
+    first rotary_dim channels (None: nothing turns): channels i and i +
+    rotary_dim / 2, with interleaved 2i and 2i + 1.  positions: int64 [n], or
+    [axes, n] with sections, the number of pairs that turn with each axis, in
+    their order (time, height and width of a picture's patches, say).  Angles
+    are formed in 64 bits, the rotation in fp32; k is cast without a rounding
+    between.
+
+    Returns the rotated q in bf16, [n, q_heads, head_dim] (q_out where given,
+    which may be q itself), or None without q."""
+    if v_storage is None:
+        v_storage = k_storage
+    pair, heads, head_dim = _caches(k_cache, v_cache, k_scale_inv, v_scale_inv, k_storage, v_storage, scaling)
+    dev = k_cache.device
+    if k.dtype == torch.bfloat16:
+        in_dt = _lib.FP8_IN_BF16
+    elif k.dtype == torch.float32:
+        in_dt = _lib.FP8_IN_F32
+    else:
+        raise TypeError("k must be bfloat16 or float32, got %s" % k.dtype)
+    if v.dtype != k.dtype:
+        raise TypeError("v must be %s as k, got %s" % (k.dtype, v.dtype))
+    _same_device(k, dev, "k")
+    _same_device(v, dev, "v")
+    n, ldk = _kv_rows(k, heads, head_dim, "k")
+    n2, ldv = _kv_rows(v, heads, head_dim, "v")
+    if n2 != n:
+        raise ValueError("v has %d tokens, k %d" % (n2, n))
+    if slots is not None:
+        _same_device(slots, dev, "slots")
+    q_heads = ldq = ldqo = 0
+    if q is None:
+        if q_out is not None:
+            raise ValueError("q_out needs q")
+    else:
+        if q.dtype != k.dtype:
+            raise TypeError("q must be %s as k, got %s" % (k.dtype, q.dtype))
+        _same_device(q, dev, "q")
+        if q.dim() not in (2, 3) or (q.dim() == 2 and q.shape[1] % head_dim):
+            raise ValueError("q must be [n, q_heads, %d] or [n, q_heads * %d], got shape %s"
+                             % (head_dim, head_dim, tuple(q.shape)))
+        q_heads = q.shape[1] if q.dim() == 3 else q.shape[1] // head_dim
+        nq, ldq = _kv_rows(q, q_heads, head_dim, "q")
+        if nq != n:
+            raise ValueError("q has %d tokens, k %d" % (nq, n))
+        if q_out is None:
+            q_out = torch.empty((n, q_heads, head_dim), dtype=torch.bfloat16, device=dev)
+            ldqo = q_heads * head_dim
+        else:
+            _same_device(q_out, dev, "q_out")
+            if q_out.dtype != torch.bfloat16:
+                raise TypeError("q_out must be torch.bfloat16, got %s" % q_out.dtype)
+            no, ldqo = _kv_rows(q_out, q_heads, head_dim, "q_out")
+            if no != n:
+                raise ValueError("q_out has %d tokens, q %d" % (no, n))
+    rotary, axes, pos_ld, cuts, flags = 0, 1, 0, None, _lib.FP8_SCALE_POW2 if pow2 else 0
+    if inv_freq is None:
+        if positions is not None or sections is not None or interleaved:
+            raise ValueError("positions, sections and interleaved need inv_freq")
+    else:
+        if inv_freq.dim() != 1:
+            raise ValueError("inv_freq must be 1-D, got shape %s" % (tuple(inv_freq.shape),))
+        rotary = 2 * _len32(inv_freq, "inv_freq")
+        _buf(inv_freq, rotary // 2, torch.float32, dev, "inv_freq")
+        axes = 1 if sections is None else len(sections)
+        want = (n,) if sections is None else (axes, n)
+        if positions is None or not isinstance(positions, torch.Tensor):
+            raise ValueError("inv_freq needs positions")
+        if sections is not None:
+            if not 1 <= axes <= 4:
+                raise ValueError("sections must name 1..4 axes, got %d" % axes)
+            for pairs in sections:
+                _int32(pairs, "sections")
+            cuts = (ctypes.c_int32 * axes)(*sections)
+        if positions.dtype != torch.int64 or positions.device != dev:
+            raise TypeError("positions must be torch.int64 on %s, got %s on %s" % (dev, positions.dtype, positions.device))
+        if tuple(positions.shape) != want:
+            raise ValueError("positions must have shape %s, got %s" % (want, tuple(positions.shape)))
+        if (n > 1 and positions.stride(-1) != 1) or (axes > 1 and positions.stride(0) < n):
+            raise ValueError("positions must have a contiguous last dimension")
+        pos_ld = positions.stride(0) if axes > 1 else n
+        flags |= _lib.FP8_ROTARY_INTERLEAVED if interleaved else 0
+    st = _call_on(dev, _lib.lib().fp8_kv_append, pair, k.data_ptr(), ldk, v.data_ptr(), ldv, _ptr(q), ldq, q_heads,
+                  _ptr(q_out), ldqo, in_dt, n, _slots(slots, n), _ptr(positions), pos_ld, cuts, axes, _ptr(inv_freq),
+                  rotary, flags, _ptr(diag.buf) if diag is not None else None)
+    _lib.check(st, "fp8_kv_append")
+    return q_out
 
 
 def kv_attention(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor, page_table: torch.Tensor,
@@ -858,6 +990,10 @@ class KVCache:
               pow2: bool = False) -> None:
         self.k[layer].store(k, slots, pow2)
         self.v[layer].store(v, slots, pow2)
+
+    def append(self, layer: int, k: torch.Tensor, v: torch.Tensor, slots: Optional[torch.Tensor] = None, **options):
+        """kv_append of new tokens to a layer's caches (options: its keywords)."""
+        return kv_append(k, v, self.k[layer].data, self.v[layer].data, slots, **self._layer(layer), **options)
 
     def load(self, layer: int, n: Optional[int] = None, slots: Optional[torch.Tensor] = None,
              out_dtype=torch.bfloat16):

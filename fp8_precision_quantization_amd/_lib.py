@@ -28,6 +28,7 @@ FP8_GRAN_TENSOR, FP8_GRAN_ROW, FP8_GRAN_BLOCK_1x128, FP8_GRAN_BLOCK_128x128 = 0,
 FP8_SCALE_POW2 = 1
 FP8_TRANSPOSE_OUT = 2
 FP8_SPIKE_GUARD = 4
+FP8_ROTARY_INTERLEAVED = 8
 FP8_KV_E4M3, FP8_KV_E5M2, FP8_KV_BF16 = 0, 1, 2
 FP8_KV_PER_TOKEN_HEAD, FP8_KV_PER_HEAD = 0, 1
 FP8_GROUPED_MAX_TILES = 1983
@@ -80,6 +81,8 @@ SIGNATURES = {
                                 _P, _INT, _P, _INT, _I64, _P, _I64, _P]),
     "fp8_kv_store": (_INT, [_P, _INT, _I64, _I64, _I32, _I32, _P, _INT, _INT, _U32, _P, _P, _I64, _P, _P]),
     "fp8_kv_load": (_INT, [_P, _INT, _INT, _P, _I64, _I32, _I32, _P, _I64, _INT, _P, _I64, _P]),
+    "fp8_kv_append": (_INT, [_P, _P, _I64, _P, _I64, _P, _I64, _I32, _P, _I64, _INT, _I64, _P, _P, _I64, _P, _I32, _P,
+                             _I32, _U32, _P, _P]),
     "fp8_kv_attention": (_INT, [_P, _P, _I64, _I64, _I32, _P, ctypes.c_float, _I32, _I32, _P, _I64, _P, _P, _I64,
                                 _P, _I64, _P]),
     "fp8_kv_attention_workspace": (_I64, [_P, _I64, _I32, _I32, _I32, _I32, _I32]),

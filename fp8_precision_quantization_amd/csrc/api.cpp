@@ -575,6 +575,87 @@ static fp8_status check_kv_pair(const fp8_kv_pair* c, bool sizes, fp8mi::KvView*
     return FP8_OK;
 }
 
+fp8_status fp8_kv_append(const fp8_kv_pair* cache, const void* k, int64_t ldk, const void* v, int64_t ldv,
+                         const void* q, int64_t ldq, int32_t q_heads, void* q_out, int64_t ldqo,
+                         fp8_in_dtype in_dtype, int64_t n_tokens, const int64_t* slots, const int64_t* positions,
+                         int64_t pos_ld, const int32_t* sections, int32_t axes, const float* inv_freq,
+                         int32_t rotary_dim, uint32_t flags, fp8_diag* diag, void* stream) {
+    if (cache == nullptr) return fail(FP8_ERR_INVALID_ARG, "cache is NULL");
+    fp8_kv_pair caches = *cache;
+    caches.page_table = nullptr; caches.page_ld = 0; caches.lens = nullptr; caches.max_len = 0;
+    caches.page_size = 1; caches.batch = 0; caches.reserved = 0;
+    fp8mi::KvAppendArgs a;
+    fp8_status st = check_kv_pair(&caches, false, &a.kv);
+    if (st != FP8_OK) return st;
+    if (in_dtype != FP8_IN_F32 && in_dtype != FP8_IN_BF16)
+        return fail(FP8_ERR_INVALID_ARG, "in_dtype %d is not FP8_IN_F32 or FP8_IN_BF16", (int)in_dtype);
+    if (flags & ~(FP8_SCALE_POW2 | FP8_ROTARY_INTERLEAVED))
+        return fail(FP8_ERR_INVALID_ARG, "unknown flag bits 0x%x", flags & ~(FP8_SCALE_POW2 | FP8_ROTARY_INTERLEAVED));
+    if (n_tokens < 0 || q_heads < 0)
+        return fail(FP8_ERR_INVALID_ARG, "negative size n_tokens=%lld q_heads=%d", (long long)n_tokens, (int)q_heads);
+    if (q_heads > 65535) return fail(FP8_ERR_UNSUPPORTED_SHAPE, "q_heads=%d must be <= 65535", (int)q_heads);
+    const int64_t heads = cache->heads, D = cache->head_dim;
+    // a block has 16 rows or more: a launch stays below 2^32 threads
+    if (n_tokens >= (int64_t(1) << 27) / (q_heads + 2 * heads))
+        return fail(FP8_ERR_UNSUPPORTED_SHAPE, "n_tokens * (q_heads + 2 * heads) must be < 2^27");
+    if (ldk < heads * D || ldv < heads * D || (q_heads > 0 && (ldq < q_heads * D || ldqo < q_heads * D)))
+        return fail(FP8_ERR_INVALID_ARG,
+                    "ldk=%lld and ldv=%lld must be >= heads*head_dim=%lld, ldq=%lld and ldqo=%lld >= q_heads*head_dim=%lld",
+                    (long long)ldk, (long long)ldv, (long long)(heads * D), (long long)ldq, (long long)ldqo,
+                    (long long)(q_heads * D));
+    if (ldk % 8 != 0 || ldv % 8 != 0 || (q_heads > 0 && (ldq % 8 != 0 || ldqo % 8 != 0)))
+        return fail(FP8_ERR_MISALIGNED, "ldk=%lld, ldv=%lld, ldq=%lld and ldqo=%lld must be multiples of 8",
+                    (long long)ldk, (long long)ldv, (long long)ldq, (long long)ldqo);
+    if (n_tokens > 0 && (k == nullptr || v == nullptr)) return fail(FP8_ERR_INVALID_ARG, "k or v is NULL");
+    if (q_heads == 0 && (q != nullptr || q_out != nullptr))
+        return fail(FP8_ERR_INVALID_ARG, "q or q_out is given with q_heads=0");
+    if (n_tokens > 0 && q_heads > 0 && (q == nullptr || q_out == nullptr))
+        return fail(FP8_ERR_INVALID_ARG, "q or q_out is NULL");
+    if (q_out != nullptr && q_out == q && (in_dtype != FP8_IN_BF16 || ldqo != ldq))
+        return fail(FP8_ERR_INVALID_ARG, "q_out is q, which needs bf16 and ldqo=%lld equal to ldq=%lld",
+                    (long long)ldqo, (long long)ldq);
+    if (!is_aligned(k, 16) || !is_aligned(v, 16) || !is_aligned(q, 16) || !is_aligned(q_out, 16))
+        return fail(FP8_ERR_MISALIGNED, "q, k, v and q_out must be 16-byte aligned");
+    if (cache->k == cache->v && cache->capacity > 0)
+        return fail(FP8_ERR_INVALID_ARG, "the K and V caches are one array");
+    if (!is_aligned(slots, 8) || !is_aligned(positions, 8))
+        return fail(FP8_ERR_MISALIGNED, "slots and positions must be 8-byte aligned");
+    if (!is_aligned(inv_freq, 4) || !is_aligned(diag, 4))
+        return fail(FP8_ERR_MISALIGNED, "inv_freq and diag must be 4-byte aligned");
+    if (rotary_dim < 0 || rotary_dim > D || rotary_dim % 16 != 0)
+        return fail(FP8_ERR_UNSUPPORTED_SHAPE, "rotary_dim=%d must be a multiple of 16 in 0..head_dim=%lld",
+                    (int)rotary_dim, (long long)D);
+    if (rotary_dim > 0) {
+        if (axes < 1 || axes > 4) return fail(FP8_ERR_UNSUPPORTED_SHAPE, "axes=%d must be in 1..4", (int)axes);
+        if (inv_freq == nullptr) return fail(FP8_ERR_INVALID_ARG, "inv_freq is NULL");
+        if (n_tokens > 0 && positions == nullptr) return fail(FP8_ERR_INVALID_ARG, "positions is NULL");
+        if (axes > 1 && pos_ld < n_tokens)
+            return fail(FP8_ERR_INVALID_ARG, "pos_ld=%lld must be >= n_tokens=%lld", (long long)pos_ld,
+                        (long long)n_tokens);
+        if (sections == nullptr && axes > 1) return fail(FP8_ERR_INVALID_ARG, "sections is NULL with axes=%d", (int)axes);
+        int64_t pairs = 0;
+        for (int i = 0; i < axes; ++i) {
+            a.sections[i] = sections ? sections[i] : rotary_dim / 2;
+            if (a.sections[i] < 0) return fail(FP8_ERR_INVALID_ARG, "sections[%d]=%d must be >= 0", i, a.sections[i]);
+            pairs += a.sections[i];
+        }
+        if (pairs != rotary_dim / 2)
+            return fail(FP8_ERR_INVALID_ARG, "sections hold %lld pairs, rotary_dim/2 is %d", (long long)pairs,
+                        (int)(rotary_dim / 2));
+        a.axes = axes;
+    }
+    int cus = 0;
+    st = check_device(&cus);
+    if (st != FP8_OK) return st;
+    if (n_tokens == 0) return ok();
+    a.q = q; a.k = k; a.v = v; a.in_bf16 = in_dtype == FP8_IN_BF16; a.ldq = ldq; a.ldk = ldk; a.ldv = ldv;
+    a.q_heads = q_heads; a.q_out = static_cast<uint16_t*>(q_out); a.ldqo = ldqo; a.n_tokens = n_tokens;
+    a.slots = slots; a.positions = positions; a.pos_ld = pos_ld; a.inv_freq = inv_freq; a.rotary = rotary_dim;
+    a.interleaved = (flags & FP8_ROTARY_INTERLEAVED) != 0; a.pow2 = (flags & FP8_SCALE_POW2) != 0;
+    a.diag = diag; a.stream = (hipStream_t)stream; a.num_cus = cus;
+    return launch_result(fp8mi::launch_kv_append(a), "fp8_kv_append");
+}
+
 static bool one_each(const fp8mi::AttnArgs& a, bool ragged) { return !ragged && a.total_q == a.kv.batch; }
 
 static fp8_status attention_args(const fp8_kv_pair* cache, bool sizes, int64_t total_q, int32_t q_heads, bool ragged,

@@ -122,6 +122,27 @@ struct KvView {
     int64_t max_len = 0;         // < 2^31, <= pages * page size
 };
 
+// fp8_kv_append: of kv, the caches, their scales, storage and sizes.
+struct KvAppendArgs {
+    KvView kv;
+    const void *q = nullptr, *k = nullptr, *v = nullptr;
+    bool in_bf16 = true;
+    int64_t ldq = 0, ldk = 0, ldv = 0;
+    int q_heads = 0;                      // 0: no queries
+    uint16_t* q_out = nullptr;
+    int64_t ldqo = 0, n_tokens = 0;
+    const int64_t* slots = nullptr;
+    const int64_t* positions = nullptr;   // [axes, pos_ld]
+    int64_t pos_ld = 0;
+    int axes = 1, sections[4] = {};       // pairs of each axis
+    const float* inv_freq = nullptr;
+    int rotary = 0;                       // 0: nothing turns
+    bool interleaved = false, pow2 = false;
+    fp8_diag* diag = nullptr;
+    hipStream_t stream = nullptr;
+    int num_cus = 256;
+};
+
 struct AttnArgs {
     KvView kv;
     const uint16_t* q = nullptr;
@@ -161,6 +182,7 @@ hipError_t launch_quantize_multi(const MultiQuantArgs& a);
 hipError_t static_workspace(uint32_t** out);
 hipError_t launch_kv_store(const KvStoreArgs& a);
 hipError_t launch_kv_load(const KvLoadArgs& a);
+hipError_t launch_kv_append(const KvAppendArgs& a);
 // One query per sequence (decode) or several; the workspace's bytes follow the
 // same rules as the launch's splits.
 int64_t decode_workspace(const AttnArgs& a);

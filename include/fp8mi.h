@@ -422,6 +422,45 @@ typedef struct fp8_kv_pair {
     int32_t reserved;        /* 0 */
 } fp8_kv_pair;
 
+/* Rotation pairs (2i, 2i + 1) instead of (i, i + rotary_dim / 2). */
+#define FP8_ROTARY_INTERLEAVED 8u
+
+/* Append new tokens: rotate q and k by their positions, cast k and v and store
+ * them, in one launch.  cache: the layer's caches (its page_table, page_ld,
+ * lens, max_len, page_size, batch and reserved are not read; K and V must not
+ * be one array).  k, v: [n_tokens x (heads*head_dim)], q: [n_tokens x
+ * (q_heads*head_dim)], all in_dtype, with their leading dimensions, heads
+ * packed within a token (the slices of one projection's output, say).  Token t
+ * goes to cache row slots[t] as with fp8_kv_store (NULL = row t; a slot outside
+ * [0, capacity) stores nothing, its q is still rotated; two tokens with one
+ * slot race).
+ * Rotation: pair i of the first rotary_dim channels of every head of q and k
+ * turns by positions[axis(i)*pos_ld + t] * inv_freq[i]:
+ *   (a, b) -> (a cos - b sin, b cos + a sin), in fp32, the angle in 64 bits;
+ * pair i is channels (i, i + rotary_dim/2), with FP8_ROTARY_INTERLEAVED (2i,
+ * 2i + 1).  positions: DEVICE int64 [axes x pos_ld] (pos_ld >= n_tokens);
+ * inv_freq: DEVICE fp32 [rotary_dim/2], radians a position.  sections: HOST
+ * int32 [axes], the pairs of each axis in their order (>= 0, together
+ * rotary_dim/2; time, height and width, say); NULL with axes = 1.  rotary_dim
+ * 0: nothing turns, positions, sections and inv_freq are not read.
+ * q_out: bf16 [n_tokens x (q_heads*head_dim)], ldqo: q rotated, rounded once.
+ * It may be q itself (bf16, the same pitch), else it overlaps nothing the call
+ * reads.  q NULL and q_heads 0: no queries.
+ * k (rotated, not rounded before the cast) and v are cast as fp8_kv_store
+ * casts them: the codes of v, and of k where nothing turns, are those of
+ * fp8_kv_store.  flags: FP8_SCALE_POW2, FP8_ROTARY_INTERLEAVED.  diag: optional
+ * counters of the FP8 casts (rotated values; inputs of bf16 storage not
+ * counted).
+ * Requirements (else FP8_ERR_UNSUPPORTED_SHAPE / FP8_ERR_MISALIGNED): head_dim
+ * % 16 == 0, 16 <= head_dim <= 256; rotary_dim % 16 == 0, <= head_dim; axes
+ * 1..4; q_heads <= 65535; n_tokens * (q_heads + 2*heads) < 2^27; q, k, v,
+ * q_out and the caches 16-byte aligned, leading dimensions multiples of 8. */
+fp8_status fp8_kv_append(const fp8_kv_pair* cache, const void* k, int64_t ldk, const void* v, int64_t ldv,
+                         const void* q, int64_t ldq, int32_t q_heads, void* q_out, int64_t ldqo,
+                         fp8_in_dtype in_dtype, int64_t n_tokens, const int64_t* slots, const int64_t* positions,
+                         int64_t pos_ld, const int32_t* sections, int32_t axes, const float* inv_freq,
+                         int32_t rotary_dim, uint32_t flags, fp8_diag* diag, void* stream);
+
 /* Attention over the cache ([DeepL] 3.1: K's precision drives the attention
  * scores, V's the mixed output), reading the codes in place.  Sequence b has
  * n_b new tokens (stored in the cache before the call), the last n_b of its

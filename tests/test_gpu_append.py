@@ -1,0 +1,308 @@
+"""fp8_kv_append on the GPU against a float64 reference of the rotation and
+against fp8_kv_store bit for bit where nothing turns: storages, scalings, head
+dimensions, partial and interleaved rotations, several axes, far positions,
+padding slots, slices of one projection, q in place, captured graphs and other
+streams."""
+from __future__ import annotations
+
+import numpy as np
+import pytest
+import torch
+
+from tests.attention_ref import FMAX, TORCH_FP8
+from tests.gpu_util import say
+
+pytestmark = pytest.mark.gpu
+
+fp8 = pytest.importorskip("fp8_precision_quantization_amd")
+
+STEP = {"e4m3": 2.0 ** -4, "e5m2": 2.0 ** -3}           # half a step, relative
+LEAST = {"e4m3": 2.0 ** -10, "e5m2": 2.0 ** -17}        # half a step of the subnormals
+
+
+@pytest.fixture(autouse=True)
+def _need_gpu(gpu):
+    yield
+
+
+def rotated(x, pos, freq, axis_of, interleaved):
+    """float64 [n, heads, dim] of x, positions [axes, n], freq [pairs]; and
+    |a| + |b| of each value's pair (0 where nothing turns)."""
+    x = x.double().cpu().numpy().copy()
+    pairs = len(freq)
+    size = np.zeros_like(x)
+    if pairs == 0:
+        return x, size
+    angle = pos[axis_of].T.astype(np.float64) * freq.astype(np.float64)
+    # numpy reduces a float64 angle exactly, as the angle itself is rounded once
+    c, s = np.cos(angle)[:, None], np.sin(angle)[:, None]
+    i = np.arange(pairs)
+    first, second = (2 * i, 2 * i + 1) if interleaved else (i, i + pairs)
+    a, b = x[:, :, first].copy(), x[:, :, second].copy()
+    x[:, :, first], x[:, :, second] = a * c - b * s, b * c + a * s
+    size[:, :, first] = size[:, :, second] = np.abs(a) + np.abs(b)
+    return x, size
+
+
+class Case:
+    def __init__(self, n=37, heads=4, kv_heads=2, dim=64, rotary=None, sections=None, interleaved=False,
+                 dtype=torch.bfloat16, k_storage="e4m3", v_storage=None, scaling="token_head", first=1000, padding=3,
+                 seed=0, base=10000.0):
+        g = torch.Generator().manual_seed(seed)
+        self.n, self.heads, self.kv_heads, self.dim = n, heads, kv_heads, dim
+        self.storage = {"k": k_storage, "v": v_storage or k_storage}
+        self.scaling, self.interleaved, self.sections = scaling, interleaved, sections
+        rotary = dim if rotary is None else rotary
+        pairs = rotary // 2
+        qkv = torch.randn(n, (heads + 2 * kv_heads) * dim, generator=g) * torch.exp2(
+            torch.rand(n, 1, generator=g) * 6 - 3)
+        self.qkv = qkv.to(dtype).cuda()
+        hd, kd = heads * dim, kv_heads * dim
+        self.q = self.qkv[:, :hd].unflatten(1, (heads, dim)) if heads else None
+        self.k = self.qkv[:, hd:hd + kd].unflatten(1, (kv_heads, dim))
+        self.v = self.qkv[:, hd + kd:]
+        self.capacity = n + 9
+        slots = torch.randperm(self.capacity, generator=g)[:n]
+        pad = torch.randperm(n, generator=g)[:min(padding, n - 1)]
+        slots[pad] = torch.tensor([-1, self.capacity, 1 << 40, -(1 << 40)])[torch.arange(len(pad)) % 4]
+        self.slots = slots
+        self.freq = torch.tensor([base ** (-i / max(pairs, 1)) for i in range(pairs)], dtype=torch.float32)
+        axes = len(sections) if sections else 1
+        self.pos = first + torch.randint(0, 4096, (axes, n), generator=g) * (1 + torch.arange(axes))[:, None]
+        self.axis_of = np.repeat(np.arange(axes), sections) if sections else np.zeros(pairs, int)
+        self.cache, self.scale = {}, {}
+        for w in "kv":
+            st = self.storage[w]
+            self.cache[w] = (torch.full((self.capacity, kv_heads, dim), 7, dtype=torch.uint8).cuda() if st != "bf16"
+                             else torch.full((self.capacity, kv_heads, dim), 7.0, dtype=torch.bfloat16).cuda())
+            self.scale[w] = None
+            if st != "bf16":
+                self.scale[w] = (torch.full((self.capacity, kv_heads), -1.0).cuda() if scaling == "token_head" else
+                                 ((1 + torch.arange(kv_heads)) * 3.7 / FMAX[st]).float().cuda())
+
+    def call(self, **more):
+        args = dict(q=self.q, k_scale_inv=self.scale["k"], v_scale_inv=self.scale["v"], k_storage=self.storage["k"],
+                    v_storage=self.storage["v"], scaling=self.scaling, interleaved=self.interleaved)
+        if len(self.freq):
+            args.update(inv_freq=self.freq.cuda(), sections=self.sections,
+                        positions=(self.pos if self.sections else self.pos[0]).cuda())
+        else:
+            args["interleaved"] = False
+        args.update(more)
+        say("kv_append", dict(n=self.n, heads=self.heads, kv=self.kv_heads, dim=self.dim, pairs=len(self.freq),
+                              sections=self.sections, inter=self.interleaved, st=self.storage, sc=self.scaling))
+        q = fp8.kv_append(self.k, self.v, self.cache["k"], self.cache["v"], self.slots.cuda(), **args)
+        torch.cuda.synchronize()
+        return q
+
+    def check_q(self, got):
+        want, size = rotated(self.q, self.pos.numpy(), self.freq.numpy(), self.axis_of, self.interleaved)
+        g = got.double().cpu().numpy().reshape(want.shape)
+        # cos and sin to 2 ulp, two products and a sum in fp32; then one rounding to bf16
+        fp32 = 6 * 2.0 ** -24 * size
+        assert (np.abs(g - want) <= fp32 + 2.0 ** -8 * (np.abs(want) + fp32)).all()
+
+    def check_cache(self, which, pow2=False):
+        x = self.k if which == "k" else self.v.unflatten(1, (self.kv_heads, self.dim))
+        turn = which == "k"
+        want, size = rotated(x, self.pos.numpy(), self.freq.numpy() if turn else self.freq.numpy()[:0],
+                             self.axis_of, self.interleaved)
+        fp32 = 6 * 2.0 ** -24 * size
+        live = ((self.slots >= 0) & (self.slots < self.capacity)).numpy()
+        rows = self.slots.numpy()[live]
+        untouched = np.setdiff1d(np.arange(self.capacity), rows)
+        cache = self.cache[which].cpu()
+        assert (cache[untouched] == 7).all(), "a row of no token changed"
+        want, fp32 = want[live], fp32[live]
+        st = self.storage[which]
+        if st == "bf16":
+            g = cache[rows].double().numpy()
+            assert (np.abs(g - want) <= fp32 + 2.0 ** -8 * (np.abs(want) + fp32)).all()
+            return
+        sc = self.scale[which].double().cpu().numpy()
+        if self.scaling == "token_head":
+            assert (sc[untouched] == -1).all()
+            sc = sc[rows]
+            amax = np.abs(want).max(2)
+            # the amax to its value's error, a division and a reciprocal rounded
+            off = (fp32.max(2) + 3 * 2.0 ** -24 * amax) / FMAX[st]
+            if pow2:
+                assert (np.exp2(np.round(np.log2(sc))) == sc).all()
+                assert (sc * FMAX[st] >= amax - fp32.max(2) - 2.0 ** -22 * amax).all()
+                assert (sc * FMAX[st] <= 2 * amax * (1 + 2.0 ** -20)).all()
+            else:
+                assert (np.abs(sc - amax / FMAX[st]) <= off).all()
+        else:
+            sc = np.broadcast_to(sc, want.shape[:2])
+        val = cache[rows].view(TORCH_FP8[st]).double().numpy()
+        y = np.clip(want / sc[:, :, None], -FMAX[st], FMAX[st])
+        err = fp32 / sc[:, :, None] + 3 * 2.0 ** -24 * np.abs(y)
+        assert (np.abs(val - y) <= np.maximum(STEP[st] * (np.abs(y) + err), LEAST[st]) + err).all()
+
+    def check(self, q):
+        if self.q is not None:
+            self.check_q(q)
+        self.check_cache("k")
+        self.check_cache("v")
+
+
+STORAGES = [("e4m3", "e4m3", "token_head"), ("e4m3", "e4m3", "head"), ("e5m2", "e5m2", "token_head"),
+            ("e5m2", "e4m3", "head"), ("bf16", "bf16", "token_head"), ("bf16", "e4m3", "token_head"),
+            ("e4m3", "bf16", "head")]
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32], ids=["bf16", "f32"])
+@pytest.mark.parametrize("storage", STORAGES, ids="-".join)
+def test_storages(storage, dtype):
+    c = Case(k_storage=storage[0], v_storage=storage[1], scaling=storage[2], dtype=dtype)
+    c.check(c.call())
+
+
+@pytest.mark.parametrize("interleaved", [False, True])
+@pytest.mark.parametrize("dim, rotary", [(16, 16), (32, 16), (48, 48), (64, 32), (80, 80), (80, 16), (96, 96), (96, 64),
+                                         (112, 48), (128, 128), (128, 32), (144, 144), (192, 128), (240, 240),
+                                         (256, 256), (256, 16), (64, 0)])
+def test_dims(dim, rotary, interleaved):
+    c = Case(n=21, dim=dim, rotary=rotary, interleaved=interleaved, seed=dim + rotary)
+    c.check(c.call())
+
+
+@pytest.mark.parametrize("heads, kv_heads", [(0, 1), (1, 1), (7, 1), (0, 5), (40, 8), (33, 3), (64, 64)])
+@pytest.mark.parametrize("n", [1, 2, 63, 300])
+def test_heads(heads, kv_heads, n):
+    c = Case(n=n, heads=heads, kv_heads=kv_heads, seed=heads + n)
+    c.check(c.call())
+
+
+@pytest.mark.parametrize("interleaved", [False, True])
+@pytest.mark.parametrize("sections", [(32,), (16, 16), (8, 12, 12), (0, 32, 0), (3, 5, 7, 17), (1, 0, 0, 31)])
+def test_axes(sections, interleaved):
+    c = Case(n=65, sections=sections, interleaved=interleaved, seed=len(sections))
+    c.check(c.call())
+
+
+@pytest.mark.parametrize("first", [0, -5000, 131071, 10 ** 6, (1 << 31) - 9, 1 << 36])
+def test_far_positions(first):
+    """The angle is formed in 64 bits: at 2^36 its own rounding is 2^36 * 2^-53
+    = 2^-17 rad on both sides, far below bf16; at 2^31 below 2^-20."""
+    c = Case(n=33, first=first, kv_heads=1, k_storage="bf16")
+    got = c.call()
+    want, size = rotated(c.q, c.pos.numpy(), c.freq.numpy(), c.axis_of, False)
+    off = size * (6 * 2.0 ** -24 + abs(first + 4096.0) * 2.0 ** -52)
+    assert (np.abs(got.double().cpu().numpy() - want) <= off + 2.0 ** -8 * (np.abs(want) + off)).all()
+
+
+def test_large_call():
+    """Several passes a block, the sines of many tokens in one."""
+    c = Case(n=5000, heads=8, kv_heads=2, dim=128, padding=11)
+    c.check(c.call())
+    c = Case(n=20000, heads=0, kv_heads=1, dim=64, padding=4, k_storage="e5m2")
+    c.check(c.call())
+
+
+@pytest.mark.parametrize("scaling", ["token_head", "head"])
+@pytest.mark.parametrize("st", ["e4m3", "e5m2", "bf16"])
+@pytest.mark.parametrize("pow2", [False, True])
+def test_unrotated_is_store(st, scaling, pow2):
+    """Codes, scales and counters are those of kv_store, non-finite values included."""
+    c = Case(n=40, rotary=0, k_storage=st, scaling=scaling, heads=0)
+    c.qkv[3, 5], c.qkv[9, 70], c.qkv[11, 200] = float("inf"), float("nan"), float("-inf")
+    c.qkv[20] = 0
+    d, d2 = fp8.Diag(), fp8.Diag()
+    c.call(pow2=pow2, diag=d)
+    for w, x in (("k", c.k), ("v", c.v)):
+        cache = torch.full_like(c.cache[w], 7)
+        scale = None if c.scale[w] is None else (torch.full_like(c.scale[w], -1.0) if scaling == "token_head"
+                                                 else c.scale[w])
+        fp8.kv_store(x.reshape(c.n, -1), cache, scale, st, scaling, c.slots.cuda(), pow2, d2)
+        torch.cuda.synchronize()
+        a, b = cache.view(torch.uint8 if st != "bf16" else torch.int16), c.cache[w].view(
+            torch.uint8 if st != "bf16" else torch.int16)
+        if st == "bf16":
+            assert torch.equal(cache.isnan(), c.cache[w].isnan())
+            a, b = a[~cache.isnan()], b[~cache.isnan()]
+        assert torch.equal(a, b)
+        if scale is not None:
+            assert torch.equal(scale, c.scale[w])
+    assert d.read() == d2.read()
+
+
+def test_pow2_scales():
+    c = Case(n=50, seed=5)
+    q = c.call(pow2=True)
+    c.check_q(q)
+    c.check_cache("k", pow2=True)
+    c.check_cache("v", pow2=True)
+
+
+def test_q_in_place_and_strided():
+    c = Case(n=45, heads=6)
+    qkv = c.qkv.clone()
+    out = c.call(q_out=c.q)
+    assert out.data_ptr() == c.q.data_ptr()
+    after, c.qkv = c.qkv, qkv
+    assert torch.equal(after[:, 6 * 64:], qkv[:, 6 * 64:]), "k or v changed"
+    c.q = qkv[:, :6 * 64].unflatten(1, (6, 64))
+    c.check_q(out)
+    wide = torch.full((45, 8 * 64), 3.0, dtype=torch.bfloat16, device="cuda")
+    got = c.call(q_out=wide[:, 64:7 * 64])
+    assert torch.equal(got.reshape(45, 6, 64), out) and (wide[:, :64] == 3).all() and (wide[:, 7 * 64:] == 3).all()
+
+
+def test_no_tokens_and_no_slots():
+    c = Case(n=4, padding=0)
+    c.slots = torch.arange(4)
+    args = dict(k_scale_inv=c.scale["k"], v_scale_inv=c.scale["v"])
+    assert fp8.kv_append(c.k, c.v, c.cache["k"], c.cache["v"], **args) is None
+    torch.cuda.synchronize()
+    c.freq = c.freq[:0]
+    c.check_cache("k")
+    c.check_cache("v")
+    q = fp8.kv_append(c.k[:0], c.v[:0], c.cache["k"], c.cache["v"], q=c.q[:0], **args)
+    assert q.shape == (0, 4, 64)
+
+
+def test_graph_and_stream():
+    """A captured call follows slots and positions changed between replays; a call on another stream."""
+    c = Case(n=19, seed=8)
+    slots, pos, freq = c.slots.cuda(), c.pos[0].cuda(), c.freq.cuda()
+    q_out = torch.empty(19, 4, 64, dtype=torch.bfloat16, device="cuda")
+
+    def call():
+        fp8.kv_append(c.k, c.v, c.cache["k"], c.cache["v"], slots, q=c.q, q_out=q_out, positions=pos, inv_freq=freq,
+                      k_scale_inv=c.scale["k"], v_scale_inv=c.scale["v"])
+
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        call()
+    side.synchronize()
+    c.check(q_out)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        call()
+    for step in range(3):
+        c.pos = c.pos + 17
+        c.slots = torch.randperm(c.capacity)[:19]
+        pos.copy_(c.pos[0])
+        slots.copy_(c.slots)
+        for w in "kv":
+            c.cache[w].fill_(7)
+            c.scale[w].fill_(-1.0)
+        graph.replay()
+        torch.cuda.synchronize()
+        c.check(q_out)
+
+
+def test_cache_class():
+    cache = fp8.KVCache(2, 64, 2, 64, bf16_k_layers=(1,))
+    c = Case(n=12, padding=0)
+    c.capacity = 64
+    for layer in (0, 1):
+        q = cache.append(layer, c.k, c.v, c.slots.cuda(), q=c.q, positions=c.pos[0].cuda(), inv_freq=c.freq.cuda())
+        c.check_q(q)
+        want, _ = rotated(c.k, c.pos.numpy(), c.freq.numpy(), c.axis_of, False)
+        got = cache.k[layer].load(slots=c.slots.cuda()).double().cpu().numpy().reshape(want.shape)
+        top = np.abs(want).max(2, keepdims=True)
+        # half a step of the largest binade (448 = 1.75 * 2^8: 16 of 448), and bf16's
+        assert (np.abs(got - want) <= (16.0 / 448 + 2.0 ** -8) * top).all()
