@@ -80,59 +80,89 @@ __device__ __forceinline__ void put_unit(void* cache, int64_t at, int st, const 
     }
 }
 
-// A row of the call and what a lane holds of it.
-template <typename InT>
-struct Row {
-    uint32_t t = 0;              // token
-    int head = 0, role = 0;      // role 0: q, 1: k, 2: v
-    int u0 = 0, u1 = 0, freq = 0;
-    bool on = false, turns = false;
-    int64_t slot = -1;
-    Pack<InT> raw[2];
+// An argument as a register: a choice between two arguments must not become a
+// choice of their addresses, which would put all of them into scratch memory.
+template <typename T>
+__device__ __forceinline__ T held(T x) {
+    asm volatile("" : "+s"(x));
+    return x;
+}
 
-    __device__ __forceinline__ void load(const AppendParams& a, uint32_t r, int j) {
-        const uint32_t width = (uint32_t)(a.q_heads + 2 * a.heads);
-        on = r < a.rows && j < a.head_dim >> 4;
-        if (!on) return;
-        t = r / width;
-        head = (int)(r - t * width);
-        role = head < a.q_heads ? 0 : head < a.q_heads + a.heads ? 1 : 2;
-        head -= role == 0 ? 0 : role == 1 ? a.q_heads : a.q_heads + a.heads;
-        const int pair_units = role == 2 ? 0 : a.rotary >> 4;
-        turns = j < pair_units;
-        u0 = turns ? j : 2 * j;
-        u1 = turns ? j + pair_units : 2 * j + 1;
-        const InT* x = static_cast<const InT*>(role == 0 ? a.q : role == 1 ? a.k : a.v) +
-                       (int64_t)t * (role == 0 ? a.ldq : role == 1 ? a.ldk : a.ldv) + (int64_t)head * a.head_dim;
-        raw[0] = load_unit<InT>(x, (int64_t)u0 * 8, 8, true);
-        raw[1] = load_unit<InT>(x, (int64_t)u1 * 8, 8, true);
-        if (role != 0) slot = a.slots ? a.slots[t] : (int64_t)t;
-    }
+// What differs between q, k and v rows (role 0, 1, 2).
+template <typename T>
+struct ByRole {
+    T q, k, v;
+    __device__ __forceinline__ ByRole(T q_, T k_, T v_) : q(held(q_)), k(held(k_)), v(held(v_)) {}
+    __device__ __forceinline__ T of(int role) const { return role == 0 ? q : role == 1 ? k : v; }
 };
 
 template <typename InT, int LPR, bool DIAG>
 __global__ __launch_bounds__(kThreads) void k_kv_append(const AppendParams a) {
     extern __shared__ __align__(16) f2 s_turn[];        // [tokens of the block][rotary / 2]
     __shared__ uint32_t lds[16];
+    constexpr int kPass = kThreads / LPR;               // rows of a pass
+    typedef const InT __attribute__((address_space(1))) * In;
+    const ByRole<const InT*> in(static_cast<const InT*>(a.q), static_cast<const InT*>(a.k), static_cast<const InT*>(a.v));
+    const ByRole<int64_t> ld(a.ldq, a.ldk, a.ldv);
+    const ByRole<int> before(0, a.q_heads, a.q_heads + a.heads), units(a.rotary >> 4, a.rotary >> 4, 0);
+    const ByRole<int> storage(FP8_KV_BF16, a.k_st, a.v_st);
+    const ByRole<void*> out(nullptr, a.k_cache, a.v_cache);
+    const ByRole<float*> scales(nullptr, a.k_scale, a.v_scale);
+
     const int j = threadIdx.x & (LPR - 1);
-    const uint32_t first = blockIdx.x * a.run, end = min(first + a.run, a.rows);
     const uint32_t width = (uint32_t)(a.q_heads + 2 * a.heads);
-    Row<InT> row;
-    row.load(a, first + threadIdx.x / LPR, j);
-    const uint32_t t0 = first / width;
+    const uint32_t first = blockIdx.x * a.run, end = min(first + a.run, a.rows), t0 = first / width;
+    const uint32_t pass_t = kPass / width, pass_h = kPass - pass_t * width;
+    // the row of this lane: token, place among the token's rows
+    uint32_t r = first + threadIdx.x / LPR, t = r / width, place = r - t * width;
+
+    // What a lane holds of a row that is on its way.
+    struct Row {
+        Pack<InT> raw[2];
+        int64_t slot;
+        uint32_t t;
+        int head, role, u0, u1;
+        bool on, turns;
+    };
+    auto load = [&](Row& row) {
+        row.t = t;
+        row.role = (int)place < before.k ? 0 : (int)place < before.v ? 1 : 2;
+        row.head = (int)place - before.of(row.role);
+        const int pair_units = units.of(row.role);
+        row.turns = j < pair_units;
+        row.u0 = row.turns ? j : 2 * j;
+        row.u1 = row.turns ? j + pair_units : 2 * j + 1;
+        row.on = r < end && j < a.head_dim >> 4;
+        row.slot = -1;
+        if (row.on) {
+            const In x = (In)(in.of(row.role) + (int64_t)t * ld.of(row.role) + (int64_t)row.head * a.head_dim);
+            row.raw[0] = load_unit<InT>((const InT*)(x + row.u0 * 8), 0, 8, true);
+            row.raw[1] = load_unit<InT>((const InT*)(x + row.u1 * 8), 0, 8, true);
+            if (row.role != 0) row.slot = a.slots ? a.slots[t] : (int64_t)t;
+        }
+        r += kPass;
+        t += pass_t;
+        place += pass_h;
+        const bool over = place >= width;
+        t += over ? 1 : 0;
+        place -= over ? width : 0;
+    };
+
+    Row row;
+    load(row);
     const int pairs = a.rotary >> 1;
     if (pairs > 0) {
         const int n = (int)((end - 1) / width - t0 + 1) * pairs;
         for (int i = threadIdx.x; i < n; i += kThreads) {
-            const int t = i / pairs;
-            s_turn[i] = turn_of(a, (int64_t)t0 + t, i - t * pairs);
+            const int token = i / pairs;
+            s_turn[i] = turn_of(a, (int64_t)t0 + token, i - token * pairs);
         }
         __syncthreads();
     }
     Counters cnt;
-    for (uint32_t r = first + threadIdx.x / LPR; r - threadIdx.x / LPR < end; r += kThreads / LPR) {
-        Row<InT> next;
-        next.load(a, r + kThreads / LPR < end ? r + kThreads / LPR : a.rows, j);
+    for (uint32_t at = first; at < end; at += kPass) {
+        Row next;
+        load(next);
         Pack<float> p[2];
         uint32_t m = 0;
         if (row.on) {
@@ -170,22 +200,21 @@ __global__ __launch_bounds__(kThreads) void k_kv_append(const AppendParams a) {
             put_unit<false>(to, row.u0 * 8, FP8_KV_BF16, p[0], 1.0f, cnt);
             put_unit<false>(to, row.u1 * 8, FP8_KV_BF16, p[1], 1.0f, cnt);
         } else if (row.on && row.slot >= 0 && row.slot < a.capacity) {
-            const int st = row.role == 1 ? a.k_st : a.v_st;
-            float* scales = row.role == 1 ? a.k_scale : a.v_scale;
-            const int64_t at = row.slot * a.heads + row.head;
+            const int st = storage.of(row.role);
+            float* const sc = scales.of(row.role);
+            const int64_t vec = row.slot * a.heads + row.head;
             float s = 1.0f;
             if (st != FP8_KV_BF16) {
                 if (a.per_head) {
-                    s = recip_rn(scales[row.head]);
+                    s = recip_rn(sc[row.head]);
                 } else {
                     s = st == FP8_KV_E4M3 ? scale_from_amax_bits<kE4M3>(m, a.pow2)
                                           : scale_from_amax_bits<kE5M2>(m, a.pow2);
-                    if (j == 0) scales[at] = recip_rn(s);
+                    if (j == 0) sc[vec] = recip_rn(s);
                 }
             }
-            void* cache = row.role == 1 ? a.k_cache : a.v_cache;
-            put_unit<DIAG>(cache, at * a.head_dim + row.u0 * 8, st, p[0], s, cnt);
-            put_unit<DIAG>(cache, at * a.head_dim + row.u1 * 8, st, p[1], s, cnt);
+            put_unit<DIAG>(out.of(row.role), vec * a.head_dim + row.u0 * 8, st, p[0], s, cnt);
+            put_unit<DIAG>(out.of(row.role), vec * a.head_dim + row.u1 * 8, st, p[1], s, cnt);
         }
         row = next;
     }
