@@ -25,7 +25,8 @@ from ._lib import Fp8Error  # noqa: F401
 
 __all__ = ["quantize", "quantize_dual", "quantize_tensors", "amax", "scaled_gemm", "blockscaled_gemm", "AmaxHistory", "Diag",
            "QuantResult", "Fp8Error", "FORMATS", "GRANULARITIES", "group_grid", "kv_store", "kv_load",
-           "KVTensorCache", "KVCache", "grouped_gemm", "workspace", "kv_attention", "kv_evict", "kv_append"]
+           "KVTensorCache", "KVCache", "grouped_gemm", "workspace", "kv_attention", "kv_evict", "kv_append",
+           "lora_add"]
 
 FORMATS = {"e4m3": _lib.FP8_E4M3, "e5m2": _lib.FP8_E5M2}
 GRANULARITIES = {"tensor": _lib.FP8_GRAN_TENSOR, "row": _lib.FP8_GRAN_ROW,
@@ -460,6 +461,82 @@ def grouped_gemm(a_q: torch.Tensor, b_q: torch.Tensor, group_offsets: torch.Tens
                                      b_scale_inv.data_ptr(), b_row, out.data_ptr(), _out_dtype(out.dtype), ldc,
                                      ws_ptr, ws_bytes, _stream(a_q.device))
     _lib.check(st, "fp8_grouped_gemm")
+    return out
+
+
+# ------------------------------------------- adapters beside a projection --
+@functools.lru_cache(maxsize=1024)
+def _lora_workspace(rows, columns, inner, rank, adapters, slices) -> int:
+    return _lib.lib().fp8_lora_workspace(rows, columns, inner, rank, adapters, slices)
+
+
+def lora_add(y: torch.Tensor, x: torch.Tensor, a: torch.Tensor, b: torch.Tensor, ids: torch.Tensor,
+             gain: Optional[torch.Tensor] = None, slices=None, out: Optional[torch.Tensor] = None,
+             workspace: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """Add to every row of a projection's output y the product of the row's own
+    low-rank adapter (fp8_lora_add): out[m] = y[m] + gain[l] * B_l (A_l x[m])
+    with l = ids[m]; rows whose id is outside 0..adapters-1 stay as they are.
+
+    y: bf16 or fp32 [rows, columns] (of scaled_gemm, say); x: bf16 [rows,
+    inner], the projection's input before its cast; a: bf16 [adapters, rank,
+    inner]; b: bf16 [adapters, columns, rank]; ids: int32 [rows], in any order
+    (batches of more than 1024 rows are fastest with the rows of an adapter
+    together); gain: fp32 [adapters], default 1.  slices: the columns of each
+    part of a fused projection that has adapters of its own, (q, k, v) say;
+    then a is [adapters, len(slices) * rank, inner].  rank: a multiple of 8 up
+    to 128 (a smaller adapter is padded with zeros).
+
+    out: where to write, y itself included (default: a new tensor).
+    workspace: a uint8 device tensor for callers that may not allocate
+    (fp8_lora_workspace bytes).  No gradient is formed.
+
+    A x is summed and kept in fp32 and enters the second product with 16
+    significant bits (bf16 out) or 24 (fp32 out); one rounding at the end."""
+    rows, columns, ldy = _matrix(y, "y")
+    rows_x, inner, ldx = _matrix(x, "x")
+    dev = y.device
+    _same_device(x, dev, "x")
+    if x.dtype != torch.bfloat16:
+        raise TypeError("x must be torch.bfloat16, got %s" % x.dtype)
+    if rows_x != rows:
+        raise ValueError("x has %d rows, y %d" % (rows_x, rows))
+    dtype = _out_dtype(y.dtype)
+    for t, name in ((a, "a"), (b, "b")):
+        if not isinstance(t, torch.Tensor) or t.dim() != 3:
+            raise ValueError("%s must be a 3-D tensor" % name)
+    parts = 1 if slices is None else len(slices)
+    adapters, width, rank = a.shape[0], a.shape[1], b.shape[2]
+    if slices is not None:
+        if not 1 <= parts <= 4:
+            raise ValueError("slices must name 1..4 parts, got %d" % parts)
+        for n in slices:
+            _int32(n, "slices")
+    if a.shape[2] != inner or width != parts * rank:
+        raise ValueError("a must be [adapters, %d, %d], got shape %s" % (parts * rank, inner, tuple(a.shape)))
+    if tuple(b.shape[:2]) != (adapters, columns):
+        raise ValueError("b must be [%d, %d, rank], got shape %s" % (adapters, columns, tuple(b.shape)))
+    for value, name in ((adapters, "adapters"), (rank, "rank")):
+        _int32(value, name)
+    a_ptr = _buf(a, a.numel(), torch.bfloat16, dev, "a")
+    b_ptr = _buf(b, b.numel(), torch.bfloat16, dev, "b")
+    ids_ptr = _buf(ids, rows, torch.int32, dev, "ids")
+    gain_ptr = None if gain is None else _buf(gain, adapters, torch.float32, dev, "gain")
+    if out is None:
+        out = torch.empty((rows, columns), dtype=y.dtype, device=dev)
+    ldo = _out_matrix(out, rows, columns, y.dtype, dev, "out")
+    if workspace is not None:
+        if not isinstance(workspace, torch.Tensor) or workspace.device != dev or not workspace.is_contiguous():
+            raise ValueError("workspace must be a contiguous tensor on %s" % dev)
+        ws_bytes = workspace.numel() * workspace.element_size()
+    else:
+        ws_bytes = _lora_workspace(rows, columns, inner, rank, adapters, parts)
+        if ws_bytes > 0:
+            workspace = torch.empty(ws_bytes, dtype=torch.uint8, device=dev)
+    cuts = None if slices is None else (ctypes.c_int32 * parts)(*slices)
+    st = _call_on(dev, _lib.lib().fp8_lora_add, y.data_ptr(), ldy, x.data_ptr(), ldx, a_ptr, b_ptr, ids_ptr, gain_ptr,
+                  out.data_ptr(), ldo, dtype, rows, columns, inner, rank, adapters, cuts, parts, _ptr(workspace),
+                  ws_bytes)
+    _lib.check(st, "fp8_lora_add")
     return out
 
 

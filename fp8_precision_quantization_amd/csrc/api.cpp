@@ -803,4 +803,95 @@ fp8_status fp8_kv_evict(const fp8_kv_pair* cache, float* weights, int64_t ldw, i
     return launch_result(fp8mi::launch_evict(a), "fp8_kv_evict");
 }
 
+static fp8_status lora_args(int64_t rows, int64_t columns, int64_t inner, int32_t rank, int32_t adapters, int32_t slices,
+                            fp8mi::LoraArgs* a) {
+    if (rows < 0 || columns < 0 || inner < 0)
+        return fail(FP8_ERR_INVALID_ARG, "negative size rows=%lld columns=%lld inner=%lld", (long long)rows,
+                    (long long)columns, (long long)inner);
+    if (rank < 8 || rank > 128 || rank % 8 != 0)
+        return fail(FP8_ERR_UNSUPPORTED_SHAPE, "rank=%d must be a multiple of 8 in 8..128", (int)rank);
+    if (slices < 1 || slices > 4) return fail(FP8_ERR_UNSUPPORTED_SHAPE, "slices=%d must be in 1..4", (int)slices);
+    if (adapters < 1 || adapters > (1 << 20))
+        return fail(FP8_ERR_UNSUPPORTED_SHAPE, "adapters=%d must be in 1..2^20", (int)adapters);
+    if (inner % 8 != 0 || columns % 8 != 0)
+        return fail(FP8_ERR_UNSUPPORTED_SHAPE, "inner=%lld and columns=%lld must be multiples of 8", (long long)inner,
+                    (long long)columns);
+    if (inner >= (1 << 24) || columns >= (1 << 24) || rows >= (1 << 30))
+        return fail(FP8_ERR_UNSUPPORTED_SHAPE, "inner and columns must be < 2^24 and rows < 2^30");
+    a->rows = rows; a->columns = columns; a->inner = inner; a->rank = rank; a->adapters = adapters; a->slices = slices;
+    if (rows > 0 && fp8mi::lora_blocks(*a) >= (1 << 24))
+        return fail(FP8_ERR_UNSUPPORTED_SHAPE, "rows=%lld times columns=%lld need 2^24 blocks or more", (long long)rows,
+                    (long long)columns);
+    return FP8_OK;
+}
+
+int64_t fp8_lora_workspace(int64_t rows, int64_t columns, int64_t inner, int32_t rank, int32_t adapters,
+                           int32_t slices) {
+    fp8mi::LoraArgs a;
+    if (lora_args(rows, columns, inner, rank, adapters, slices, &a) != FP8_OK) return -1;
+    ok();
+    return fp8mi::lora_workspace(a);
+}
+
+fp8_status fp8_lora_add(const void* y, int64_t ldy, const void* x, int64_t ldx, const void* a_, const void* b,
+                        const int32_t* ids, const float* gain, void* out, int64_t ldo, fp8_out_dtype dtype,
+                        int64_t rows, int64_t columns, int64_t inner, int32_t rank, int32_t adapters,
+                        const int32_t* slice_columns, int32_t slices, void* workspace, int64_t workspace_bytes,
+                        void* stream) {
+    fp8mi::LoraArgs a;
+    fp8_status st = lora_args(rows, columns, inner, rank, adapters, slices, &a);
+    if (st != FP8_OK) return st;
+    if (dtype != FP8_OUT_F32 && dtype != FP8_OUT_BF16)
+        return fail(FP8_ERR_INVALID_ARG, "dtype %d is not FP8_OUT_F32 or FP8_OUT_BF16", (int)dtype);
+    if (slice_columns == nullptr && slices > 1)
+        return fail(FP8_ERR_INVALID_ARG, "slice_columns is NULL with slices=%d", (int)slices);
+    int64_t sum = 0;
+    for (int i = 0; i < slices; ++i) {
+        a.columns_of[i] = slice_columns ? slice_columns[i] : (int)columns;
+        if (a.columns_of[i] < 0 || a.columns_of[i] % 8 != 0)
+            return fail(FP8_ERR_UNSUPPORTED_SHAPE, "slice_columns[%d]=%d must be a multiple of 8, >= 0", i, a.columns_of[i]);
+        sum += a.columns_of[i];
+    }
+    if (sum != columns)
+        return fail(FP8_ERR_INVALID_ARG, "slice_columns add up to %lld, columns is %lld", (long long)sum,
+                    (long long)columns);
+    if (ldx < inner || ldy < columns || ldo < columns)
+        return fail(FP8_ERR_INVALID_ARG, "ldx=%lld must be >= inner=%lld, ldy=%lld and ldo=%lld >= columns=%lld",
+                    (long long)ldx, (long long)inner, (long long)ldy, (long long)ldo, (long long)columns);
+    if (ldx % 8 != 0 || ldy % 8 != 0 || ldo % 8 != 0)
+        return fail(FP8_ERR_MISALIGNED, "ldx=%lld, ldy=%lld and ldo=%lld must be multiples of 8", (long long)ldx,
+                    (long long)ldy, (long long)ldo);
+    if (rows > 0 && columns > 0) {
+        if (y == nullptr || out == nullptr) return fail(FP8_ERR_INVALID_ARG, "y or out is NULL");
+        if (inner > 0 && x == nullptr) return fail(FP8_ERR_INVALID_ARG, "x is NULL");
+        if (inner > 0 && a_ == nullptr) return fail(FP8_ERR_INVALID_ARG, "a is NULL");
+        if (b == nullptr) return fail(FP8_ERR_INVALID_ARG, "b is NULL");
+        if (ids == nullptr) return fail(FP8_ERR_INVALID_ARG, "ids is NULL");
+    }
+    if (out == y && ldo != ldy)
+        return fail(FP8_ERR_INVALID_ARG, "out is y, which needs ldo=%lld equal to ldy=%lld", (long long)ldo,
+                    (long long)ldy);
+    if (!is_aligned(x, 16) || !is_aligned(a_, 16) || !is_aligned(b, 16) || !is_aligned(y, 16) || !is_aligned(out, 16))
+        return fail(FP8_ERR_MISALIGNED, "x, a, b, y and out must be 16-byte aligned");
+    if (!is_aligned(ids, 4) || !is_aligned(gain, 4))
+        return fail(FP8_ERR_MISALIGNED, "ids and gain must be 4-byte aligned");
+    const int64_t need = fp8mi::lora_workspace(a);
+    if (need > 0) {
+        if (workspace == nullptr)
+            return fail(FP8_ERR_INVALID_ARG, "workspace is NULL (this call needs %lld bytes)", (long long)need);
+        if (workspace_bytes < need)
+            return fail(FP8_ERR_INVALID_ARG, "workspace_bytes=%lld is below the %lld this call needs",
+                        (long long)workspace_bytes, (long long)need);
+        if (!is_aligned(workspace, 16)) return fail(FP8_ERR_MISALIGNED, "workspace must be 16-byte aligned");
+    }
+    int cus = 0;
+    st = check_device(&cus);
+    if (st != FP8_OK) return st;
+    if (rows == 0 || columns == 0) return ok();
+    a.x = static_cast<const uint16_t*>(x); a.ldx = ldx; a.a = static_cast<const uint16_t*>(a_);
+    a.b = static_cast<const uint16_t*>(b); a.ids = ids; a.gain = gain; a.y = y; a.ldy = ldy; a.out = out; a.ldo = ldo;
+    a.out_bf16 = dtype == FP8_OUT_BF16; a.workspace = static_cast<uint8_t*>(workspace); a.stream = (hipStream_t)stream;
+    return launch_result(fp8mi::launch_lora(a), "fp8_lora_add");
+}
+
 }  // extern "C"

@@ -161,6 +161,21 @@ struct AttnArgs {
     hipStream_t stream = nullptr;
 };
 
+// fp8_lora_add: out = y + gain[id] * (x A_id^T) B_id^T by rows.
+struct LoraArgs {
+    const uint16_t *x = nullptr, *a = nullptr, *b = nullptr;
+    int64_t ldx = 0, rows = 0, inner = 0, columns = 0;
+    const int32_t* ids = nullptr;
+    const float* gain = nullptr;          // null: 1
+    const void* y = nullptr;
+    void* out = nullptr;
+    int64_t ldy = 0, ldo = 0;
+    bool out_bf16 = true;
+    int rank = 0, adapters = 0, slices = 1, columns_of[4] = {};
+    uint8_t* workspace = nullptr;
+    hipStream_t stream = nullptr;
+};
+
 struct EvictArgs {
     KvView kv;
     const float* weights = nullptr;      // [batch, heads, ldw]
@@ -195,6 +210,9 @@ constexpr int64_t kMaxAttnBlocks = (int64_t(1) << 24) - 1;
 hipError_t launch_decode(const AttnArgs& a);              // weights included
 hipError_t launch_extend(const AttnArgs& a);              // weights included
 hipError_t launch_attention_weights(const AttnArgs& a);   // the weights alone, from the keys and a.lse
+int64_t lora_workspace(const LoraArgs& a);
+int64_t lora_blocks(const LoraArgs& a);                   // as decode_blocks
+hipError_t launch_lora(const LoraArgs& a);
 hipError_t launch_evict(const EvictArgs& a);
 hipError_t launch_history_init(fp8_amax_history* h, int32_t len, hipStream_t stream);
 hipError_t launch_history_set_guard(fp8_amax_history* h, float threshold, hipStream_t stream);

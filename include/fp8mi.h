@@ -541,6 +541,43 @@ fp8_status fp8_kv_evict(const fp8_kv_pair* cache, float* weights, int64_t ldw, i
                         int32_t recent, const int32_t* dst_page_table, int64_t dst_page_ld, float* weights_out,
                         int64_t ldwo, int32_t* kept, int32_t* new_lens, void* stream);
 
+/* Low-rank adapters of many requests beside a shared projection: row m of a
+ * projection's output adds the product of its own adapter l = ids[m],
+ *   out[m, n] = y[m, n] + gain[l] * sum_r B_l[n, r] * (A_l[s(n)*rank + r] . x[m])
+ * where s(n) is the slice column n lies in (the query, key and value parts of
+ * one projection, say).  An id outside [0, adapters) has no adapter: out = y.
+ * x: bf16 [rows x inner] (ldx).  a: bf16 [adapters x (slices*rank) x inner]
+ * packed; b: bf16 [adapters x columns x rank] packed (an adapter of a smaller
+ * rank is padded with zeros).  ids: DEVICE int32 [rows]; rows of one adapter may lie
+ * anywhere (in batches of more than 1024 rows they are fastest together).
+ * gain: DEVICE fp32 [adapters], NULL = 1.  y, out: [rows x columns] of dtype
+ * (ldy, ldo); out may be y (the same pitch), else it overlaps nothing the call
+ * reads.  slice_columns: HOST int32 [slices], the columns of each slice, together
+ * `columns`; NULL with slices = 1.
+ * x A^T is summed and held in fp32 and enters the second product with 16
+ * significant bits where out is bf16, with 24 where it is fp32; the sum with y
+ * is formed in fp32 and rounded once.  Sums are in a fixed order: results are
+ * bit-reproducible run to run; a row's last fp32 bits may depend on the number
+ * of rows and adapters (how the inner dimension is split).
+ * workspace: fp8_lora_workspace() bytes, 16-byte aligned, as the other
+ * workspaces (no initialization; not shared by calls that can run at the same
+ * time, captured graphs included).
+ * Requirements (else FP8_ERR_UNSUPPORTED_SHAPE / FP8_ERR_MISALIGNED): rank a
+ * multiple of 8 in 8..128, slices 1..4, inner and every slice's columns
+ * multiples of 8, columns and inner < 2^24, rows < 2^30, adapters <= 2^20,
+ * launches of fewer than 2^24 blocks; x, a, b, y and out 16-byte aligned,
+ * leading dimensions multiples of 8. */
+fp8_status fp8_lora_add(const void* y, int64_t ldy, const void* x, int64_t ldx, const void* a, const void* b,
+                        const int32_t* ids, const float* gain, void* out, int64_t ldo, fp8_out_dtype dtype,
+                        int64_t rows, int64_t columns, int64_t inner, int32_t rank, int32_t adapters,
+                        const int32_t* slice_columns, int32_t slices, void* workspace, int64_t workspace_bytes,
+                        void* stream);
+
+/* Bytes of workspace fp8_lora_add needs for these sizes; -1 if it would reject
+ * them (see fp8_last_error). */
+int64_t fp8_lora_workspace(int64_t rows, int64_t columns, int64_t inner, int32_t rank, int32_t adapters,
+                           int32_t slices);
+
 #ifdef __cplusplus
 }
 #endif
