@@ -690,11 +690,11 @@ def _kv_pair(k_cache, v_cache, page_table, lens, page_size, k_scale_inv, v_scale
 
 @functools.lru_cache(maxsize=1024)
 def _attention_workspace(k_storage, heads, head_dim, page_size, batch, max_len, total_q, q_heads, ragged, window,
-                         sinks, weighted) -> int:
-    """fp8_kv_attention_workspace of these sizes (it reads nothing else)."""
+                         sinks, weighted, shared) -> int:
+    """fp8_kv_attention_shared_workspace of these sizes (it reads nothing else)."""
     pair = _PAIR.pack(0, 0, 0, 0, 1, 0, max_len, 0, max_len, KV_STORAGE[k_storage], 0, 0, heads, head_dim, page_size,
                       batch, 0)
-    return _lib.lib().fp8_kv_attention_workspace(pair, total_q, q_heads, ragged, window, sinks, weighted)
+    return _lib.lib().fp8_kv_attention_shared_workspace(pair, total_q, q_heads, ragged, window, sinks, weighted, shared)
 
 
 def _kv_weights(weights, batch: int, heads: int, least: int, device, name: str) -> int:
@@ -870,7 +870,7 @@ def kv_attention(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor, 
                  window: int = 0, sinks: int = 0, scale: Optional[float] = None,
                  weights: Optional[torch.Tensor] = None, return_lse: bool = False,
                  out: Optional[torch.Tensor] = None, lse: Optional[torch.Tensor] = None,
-                 workspace: Optional[torch.Tensor] = None):
+                 workspace: Optional[torch.Tensor] = None, shared: int = 0):
     """Attention of a batch's newest tokens over one layer's paged cache,
     read in place (fp8_kv_attention).
 
@@ -895,10 +895,15 @@ def kv_attention(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor, 
     sequence saves memory where page_table holds more).  out must not overlap
     anything the call reads, q included.  No gradient is formed.
 
+    shared: the number of first tokens that all sequences have in the same
+    pages (a common instruction text or document), read once for the batch
+    from the first row's pages (fp8_kv_attention_shared; its workspace is
+    fp8_kv_attention_shared_workspace bytes).
+
     Scores, softmax and sums are in fp32.  The weights of one new token per
     sequence enter the product with V with 16 significant bits, those of
-    several rounded once to bf16 (up to 2^-8 of sum p |v|, beside the output's
-    own rounding).
+    several and of shared tokens rounded once to bf16 (up to 2^-8 of sum p |v|,
+    beside the output's own rounding).
 
     Returns out [total_q, q_heads, head_dim] bf16, with return_lse (or lse
     given) also the fp32 log-sum-exp of the scores [total_q, q_heads]."""
@@ -906,6 +911,7 @@ def kv_attention(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor, 
         v_storage = k_storage
     _int32(window, "window")
     _int32(sinks, "sinks")
+    _int32(shared, "shared")
     pair, heads, head_dim, batch, max_len = _kv_pair(k_cache, v_cache, page_table, lens, page_size, k_scale_inv,
                                                      v_scale_inv, k_storage, v_storage, scaling, max_len)
     dev = k_cache.device
@@ -937,11 +943,11 @@ def kv_attention(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor, 
         ws_bytes = workspace.numel() * workspace.element_size()
     else:
         ws_bytes = _attention_workspace(k_storage, heads, head_dim, page_size, batch, max_len, n, q_heads,
-                                        offsets is not None, window, sinks, weights is not None)
+                                        offsets is not None, window, sinks, weights is not None, shared)
         if ws_bytes > 0:
             workspace = torch.empty(ws_bytes, dtype=torch.uint8, device=dev)
-    st = _call_on(dev, _lib.lib().fp8_kv_attention, pair, q.data_ptr(), ldq, n, q_heads, offsets,
-                  head_dim ** -0.5 if scale is None else scale, window, sinks, out.data_ptr(), ldo, _ptr(lse),
+    st = _call_on(dev, _lib.lib().fp8_kv_attention_shared, pair, q.data_ptr(), ldq, n, q_heads, offsets,
+                  head_dim ** -0.5 if scale is None else scale, window, sinks, shared, out.data_ptr(), ldo, _ptr(lse),
                   _ptr(weights), ldw, _ptr(workspace), ws_bytes)
     _lib.check(st, "fp8_kv_attention")
     return (out, lse) if want_lse else out

@@ -86,6 +86,9 @@ SIGNATURES = {
     "fp8_kv_attention": (_INT, [_P, _P, _I64, _I64, _I32, _P, ctypes.c_float, _I32, _I32, _P, _I64, _P, _P, _I64,
                                 _P, _I64, _P]),
     "fp8_kv_attention_workspace": (_I64, [_P, _I64, _I32, _I32, _I32, _I32, _I32]),
+    "fp8_kv_attention_shared": (_INT, [_P, _P, _I64, _I64, _I32, _P, ctypes.c_float, _I32, _I32, _I64, _P, _I64, _P, _P,
+                                       _I64, _P, _I64, _P]),
+    "fp8_kv_attention_shared_workspace": (_I64, [_P, _I64, _I32, _I32, _I32, _I32, _I32, _I64]),
     "fp8_lora_add": (_INT, [_P, _I64, _P, _I64, _P, _P, _P, _P, _P, _I64, _INT, _I64, _I64, _I64, _I32, _I32, _P, _I32,
                             _P, _I64, _P]),
     "fp8_lora_workspace": (_I64, [_I64, _I64, _I64, _I32, _I32, _I32]),

@@ -20,10 +20,12 @@ CSRC = os.path.join(PKG, "csrc")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libfp8mi.so")
 PROBE_LIB = os.path.join(PKG, "libfp8probe.so")
-SOURCES = ["quantize.hip", "gemm.hip", "kvcache.hip", "kvappend.hip", "attn_decode.hip", "attn_extend.hip", "evict.hip", "lora.hip",
+SOURCES = ["quantize.hip", "gemm.hip", "kvcache.hip", "kvappend.hip", "attn_decode.hip", "attn_extend.hip",
+           "attn_shared.hip", "evict.hip", "lora.hip",
            "api.cpp"]
 PROBE_SOURCES = ["stream_probe.hip"]
-HEADERS = ["device_common.hpp", "cast_unit.hpp", "attention.hpp", "launch.hpp"]
+HEADERS = ["device_common.hpp", "cast_unit.hpp", "attention.hpp", "attn_decode.hpp", "attn_extend.hpp",
+           "launch.hpp"]
 
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 FLAGS = [

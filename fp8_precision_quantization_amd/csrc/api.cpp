@@ -659,7 +659,7 @@ fp8_status fp8_kv_append(const fp8_kv_pair* cache, const void* k, int64_t ldk, c
 static bool one_each(const fp8mi::AttnArgs& a, bool ragged) { return !ragged && a.total_q == a.kv.batch; }
 
 static fp8_status attention_args(const fp8_kv_pair* cache, bool sizes, int64_t total_q, int32_t q_heads, bool ragged,
-                                 int32_t window, int32_t sinks, bool weighted, fp8mi::AttnArgs* a) {
+                                 int32_t window, int32_t sinks, bool weighted, int64_t shared, fp8mi::AttnArgs* a) {
     fp8_status st = check_kv_pair(cache, sizes, &a->kv);
     if (st != FP8_OK) return st;
     if (total_q < 0) return fail(FP8_ERR_INVALID_ARG, "negative size total_q=%lld", (long long)total_q);
@@ -682,13 +682,21 @@ static fp8_status attention_args(const fp8_kv_pair* cache, bool sizes, int64_t t
         return fail(FP8_ERR_INVALID_ARG, "window=%d and sinks=%d must be >= 0", (int)window, (int)sinks);
     if (cache->batch * cache->max_len >= (int64_t(1) << 35))
         return fail(FP8_ERR_UNSUPPORTED_SHAPE, "batch * max_len must be < 2^35");
+    if (shared < 0 || shared > cache->max_len)
+        return fail(FP8_ERR_INVALID_ARG, "shared=%lld must be in 0..max_len=%lld", (long long)shared,
+                    (long long)cache->max_len);
     a->total_q = total_q; a->q_heads = q_heads; a->weighted = weighted;
     if (cache->capacity == 0) a->kv.max_len = 0;    // a cache without rows holds no token
     // a window that reaches every token is none; sinks past the end are all
     a->window = window >= cache->max_len ? 0 : window;
     a->sinks = sinks > cache->max_len ? (int)cache->max_len : sinks;
+    // the prefix in whole steps, the rest of it with the sequences' own tokens; a
+    // window sees little of it, and one sequence has nobody to share it with
+    if (a->window == 0 && cache->batch > 1 && a->kv.max_len > 0) a->from = (int)(shared / 64 * 64);
     if (total_q > 0) {
-        const int64_t blocks = one_each(*a, ragged) ? fp8mi::decode_blocks(*a) : fp8mi::extend_blocks(*a, ragged);
+        const int64_t blocks = a->from > 0           ? fp8mi::shared_blocks(*a, ragged)
+                               : one_each(*a, ragged) ? fp8mi::decode_blocks(*a)
+                                                      : fp8mi::extend_blocks(*a, ragged);
         if (blocks > fp8mi::kMaxAttnBlocks)
             return fail(FP8_ERR_UNSUPPORTED_SHAPE,
                         "%lld blocks (row tiles * heads, with weights also max_len / 128 * heads) must be < 2^24",
@@ -700,25 +708,32 @@ static fp8_status attention_args(const fp8_kv_pair* cache, bool sizes, int64_t t
 
 static int64_t attention_bytes(const fp8mi::AttnArgs& a, bool ragged) {
     if (a.total_q == 0) return 0;
+    if (a.from > 0) return fp8mi::shared_workspace(a, ragged);
     return one_each(a, ragged) ? fp8mi::decode_workspace(a) : fp8mi::extend_workspace(a, ragged);
 }
 
-int64_t fp8_kv_attention_workspace(const fp8_kv_pair* cache, int64_t total_q, int32_t q_heads, int32_t ragged,
-                                   int32_t window, int32_t sinks, int32_t weighted) {
+int64_t fp8_kv_attention_shared_workspace(const fp8_kv_pair* cache, int64_t total_q, int32_t q_heads, int32_t ragged,
+                                          int32_t window, int32_t sinks, int32_t weighted, int64_t shared) {
     fp8mi::AttnArgs a;
-    if (attention_args(cache, true, total_q, q_heads, ragged != 0, window, sinks, weighted != 0, &a) != FP8_OK)
+    if (attention_args(cache, true, total_q, q_heads, ragged != 0, window, sinks, weighted != 0, shared, &a) != FP8_OK)
         return -1;
     ok();
     return attention_bytes(a, ragged != 0);
 }
 
-fp8_status fp8_kv_attention(const fp8_kv_pair* cache, const void* q, int64_t ldq, int64_t total_q, int32_t q_heads,
-                            const int32_t* q_offsets, float scale, int32_t window, int32_t sinks, void* out,
-                            int64_t ldo, float* lse, float* weights, int64_t ldw, void* workspace,
-                            int64_t workspace_bytes, void* stream) {
+int64_t fp8_kv_attention_workspace(const fp8_kv_pair* cache, int64_t total_q, int32_t q_heads, int32_t ragged,
+                                   int32_t window, int32_t sinks, int32_t weighted) {
+    return fp8_kv_attention_shared_workspace(cache, total_q, q_heads, ragged, window, sinks, weighted, 0);
+}
+
+static fp8_status attention(const fp8_kv_pair* cache, const void* q, int64_t ldq, int64_t total_q, int32_t q_heads,
+                            const int32_t* q_offsets, float scale, int32_t window, int32_t sinks, int64_t shared,
+                            void* out, int64_t ldo, float* lse, float* weights, int64_t ldw, void* workspace,
+                            int64_t workspace_bytes, void* stream, const char* what) {
     fp8mi::AttnArgs a;
     const bool ragged = q_offsets != nullptr;
-    fp8_status st = attention_args(cache, false, total_q, q_heads, ragged, window, sinks, weights != nullptr, &a);
+    fp8_status st =
+        attention_args(cache, false, total_q, q_heads, ragged, window, sinks, weights != nullptr, shared, &a);
     if (st != FP8_OK) return st;
     const int64_t width = (int64_t)q_heads * cache->head_dim;
     if (ldq < width || ldo < width)
@@ -754,7 +769,26 @@ fp8_status fp8_kv_attention(const fp8_kv_pair* cache, const void* q, int64_t ldq
     a.q = static_cast<const uint16_t*>(q); a.ldq = ldq; a.q_offsets = q_offsets; a.scale = scale;
     a.out = static_cast<uint16_t*>(out); a.ldo = ldo; a.lse = lse; a.weights = weights; a.ldw = ldw;
     a.workspace = static_cast<uint8_t*>(workspace); a.stream = (hipStream_t)stream;
-    return launch_result(one_each(a, ragged) ? fp8mi::launch_decode(a) : fp8mi::launch_extend(a), "fp8_kv_attention");
+    return launch_result(a.from > 0           ? fp8mi::launch_shared(a)
+                         : one_each(a, ragged) ? fp8mi::launch_decode(a)
+                                               : fp8mi::launch_extend(a),
+                         what);
+}
+
+fp8_status fp8_kv_attention(const fp8_kv_pair* cache, const void* q, int64_t ldq, int64_t total_q, int32_t q_heads,
+                            const int32_t* q_offsets, float scale, int32_t window, int32_t sinks, void* out,
+                            int64_t ldo, float* lse, float* weights, int64_t ldw, void* workspace,
+                            int64_t workspace_bytes, void* stream) {
+    return attention(cache, q, ldq, total_q, q_heads, q_offsets, scale, window, sinks, 0, out, ldo, lse, weights, ldw,
+                     workspace, workspace_bytes, stream, "fp8_kv_attention");
+}
+
+fp8_status fp8_kv_attention_shared(const fp8_kv_pair* cache, const void* q, int64_t ldq, int64_t total_q,
+                                   int32_t q_heads, const int32_t* q_offsets, float scale, int32_t window,
+                                   int32_t sinks, int64_t shared, void* out, int64_t ldo, float* lse, float* weights,
+                                   int64_t ldw, void* workspace, int64_t workspace_bytes, void* stream) {
+    return attention(cache, q, ldq, total_q, q_heads, q_offsets, scale, window, sinks, shared, out, ldo, lse, weights,
+                     ldw, workspace, workspace_bytes, stream, "fp8_kv_attention_shared");
 }
 
 fp8_status fp8_kv_evict(const fp8_kv_pair* cache, float* weights, int64_t ldw, int32_t budget, int32_t sinks,

@@ -117,17 +117,18 @@ __device__ __forceinline__ int row_of_entry(const KvView& kv, int entry, int j) 
 
 // The tokens that queries at positions [first, last] may see, as steps of
 // STEP tokens: first the steps that hold sinks and no window token, then all
-// steps from the first window token to `last`.
+// steps from the first window token to `last`.  With `from` (a multiple of
+// STEP, without a window): those from token `from` on.
 template <int STEP>
 struct Steps {
     int sink_steps, first_step, count;
-    __device__ __forceinline__ Steps(int first, int last, int window, int sinks) {
+    __device__ __forceinline__ Steps(int first, int last, int window, int sinks, int from = 0) {
         int lo = window > 0 ? first - window + 1 : 0;
-        lo = lo < 0 ? 0 : lo;
+        lo = lo < from ? from : lo;
         first_step = lo / STEP;
         const int s = window > 0 ? (sinks + STEP - 1) / STEP : 0;
         sink_steps = s < first_step ? s : first_step;
-        count = last < 0 ? 0 : sink_steps + (last / STEP - first_step + 1);
+        count = last < from ? 0 : sink_steps + (last / STEP - first_step + 1);
     }
     // first token of step i
     __device__ __forceinline__ int token(int i) const {

@@ -1,0 +1,333 @@
+// attn_shared.hip -- attention of a batch whose sequences begin with the same
+// tokens, in the same pages: the shared prefix is read once for all of them.
+//
+// Mathematics: that of attn_decode.hip and attn_extend.hip.  The tokens a row
+// sees are cut at the prefix's end; both parts give (m, l, o), which join by
+// m = max, l and o scaled by 2^(m_s - m) and added.
+//
+// k_shared.  One launch holds two kinds of blocks.  To the prefix, the batch is
+// one sequence without an order: the rows are (query, head in the group) of all
+// sequences, 128 a block, and a KV head's blocks share the prefix's steps in even
+// parts (extend_rows: matrix products against LDS tiles; a row's own position
+// masks only where a sequence ends inside the prefix).  Behind it every sequence
+// has tokens of its own: with one new token each, waves share them evenly whatever
+// their lengths (decode_share, memory bound); with several, as row tiles of
+// their sequence (extend_rows).  The two kinds need different parts of a CU, so
+// they are resident together rather than one after the other.
+//
+// k_shared_join reads a row's pieces of both parts in their order.
+#include <hip/hip_runtime.h>
+
+#include <algorithm>
+
+#include "attn_decode.hpp"
+#include "attn_extend.hpp"
+
+namespace fp8mi {
+namespace {
+
+using namespace attn;
+
+struct SharedParams {
+    extend::ExtendParams e;      // splits: pieces of a row, the prefix's first; least: fewest steps of a tail's piece
+    decode::DecodeParams d;      // the tails where every sequence has one new token
+    int from;                    // tokens of the prefix, a multiple of extend::kStep
+    int blocks;                  // of the prefix
+    int splits, chunk;           // of the prefix: pieces, their steps
+    int tail_splits;             // of a tail's row tile
+    int tail_tiles;
+};
+
+// A query of the call: whether it is in a sequence, its place there, its position.
+struct Place {
+    bool in;
+    int b, i, n, pos;
+    __device__ __forceinline__ Place(const extend::ExtendParams& a, int token) : b(0) {
+        if (a.q_offsets == nullptr) {
+            b = min(token / a.each, a.kv.batch - 1);
+        } else {
+            for (int hi = a.kv.batch; hi - b > 1;) {
+                const int mid = (b + hi) >> 1;
+                if (a.q_offsets[mid] <= token) b = mid; else hi = mid;
+            }
+        }
+        int first;
+        extend::queries_of(a, b, &first, &n);
+        i = token - first;
+        in = i >= 0 && i < n;
+        pos = seq_len(a.kv, b) - n + i;
+    }
+};
+
+template <int KST, int VST, int DP, bool kOne>
+__global__ __launch_bounds__(extend::kThreads, DP <= 128 ? 2 : 1) void k_shared(const SharedParams p) {
+    extern __shared__ __align__(16) uint8_t smem[];
+    const extend::ExtendParams& a = p.e;
+    const KvView& kv = a.kv;
+    const bool prefix = (int)blockIdx.x < p.blocks;
+    if (kOne && !prefix) {
+        decode::decode_share<KST, VST, DP, 1, true>(p.d, (int)blockIdx.x - p.blocks);
+        return;
+    }
+    int block = (int)blockIdx.x - (prefix ? 0 : p.blocks);
+    const int h = block % kv.heads;
+    block /= kv.heads;
+    const int lane_row = (int)(threadIdx.x >> 6) * 32 + (int)(threadIdx.x & 31);
+    extend::Rows at;
+    Steps<extend::kStep> steps(-1, -1, 0, 0);
+    at.partial = true;
+    if (prefix) {
+        const int split = block % p.splits, r = block / p.splits * extend::kRows + lane_row, token = r / a.group;
+        const Place place(a, token);
+        at.live = token < a.total_q && place.in;
+        at.token = token;
+        at.head = h * a.group + (r - token * a.group);
+        at.pos = at.live ? place.pos : -1;
+        // the lowest position of the wave's rows: below the prefix's end they are masked
+        int lowest = at.live ? min(at.pos, p.from - 1) : p.from - 1;
+#pragma unroll
+        for (int off = 1; off < 32; off <<= 1) lowest = min(lowest, __shfl_xor(lowest, off, 64));
+        at.p_first = lowest;
+        at.p_last = p.from - 1;
+        at.table = kv.table;
+        steps = Steps<extend::kStep>(p.from - 1, p.from - 1, 0, 0);
+        at.s_begin = split * p.chunk;
+        at.s_end = min(at.s_begin + p.chunk, steps.count);
+        at.part = split;
+    } else {
+        const int split = block % p.tail_splits;
+        const extend::Tile tile(a, p.tail_tiles - 1 - block / p.tail_splits);
+        if (!tile.any()) return;
+        steps = Steps<extend::kStep>(tile.p_last, tile.p_last, 0, 0, p.from);
+        const int even = (steps.count + p.tail_splits - 1) / p.tail_splits, chunk = max(even, a.least);
+        at.s_begin = split * chunk;
+        at.s_end = min(at.s_begin + chunk, steps.count);
+        if (at.s_begin >= steps.count) return;
+        const int r = tile.row0 + lane_row, tok = r / a.group;
+        at.live = r < tile.rows;
+        at.token = tile.q_first + tok;
+        at.head = h * a.group + (r - tok * a.group);
+        at.pos = at.live ? tile.base + tok : -1;
+        at.p_first = tile.p_first;
+        at.p_last = tile.p_last;
+        at.table = kv.table + tile.b * kv.table_ld;
+        at.part = p.splits + split;
+    }
+    extend::extend_rows<KST, VST, DP>(a, *reinterpret_cast<extend::Lds<DP>*>(smem), h, steps, at);
+}
+
+constexpr int kJoinThreads = 256;
+constexpr int kJoinWaves = kJoinThreads / 64;
+
+// Joins the pieces of a row.  A row takes W waves of a block, a thread 4
+// channels, and what a wave has lanes for goes on to further pieces side by side.
+// piece(i): (m, l) of piece i; values(i): its 4 channels of this thread.
+template <class Ml, class O>
+__device__ __forceinline__ f4 joined(int n, int W, int part_of, int side, int sides, bool on, Ml&& piece, O&& values,
+                                     float2* all) {
+    const int lane = threadIdx.x & 63;
+    float m = kLowest, l = 0.0f;
+    for (int i = lane; i < n; i += 64) m = fmaxf(m, piece(i).x);
+#pragma unroll
+    for (int off = 1; off < 64; off <<= 1) m = fmaxf(m, __shfl_xor(m, off, 64));
+    for (int i = lane; i < n; i += 64) {
+        const float2 ml = piece(i);
+        l += ml.y * __builtin_amdgcn_exp2f(ml.x - m);
+    }
+#pragma unroll
+    for (int off = 1; off < 64; off <<= 1) l += __shfl_xor(l, off, 64);
+    *all = make_float2(m, l);
+    f4 acc = {0, 0, 0, 0};
+    if (on)
+#pragma unroll 4
+        for (int i = part_of * sides + side; i < n; i += W * sides)
+            acc += values(i) * __builtin_amdgcn_exp2f(piece(i).x - m);
+    return acc;
+}
+
+template <bool kOne>
+__global__ __launch_bounds__(kJoinThreads) void k_shared_join(const SharedParams p, int W) {
+    __shared__ f4 s_acc[kJoinThreads];
+    const extend::ExtendParams& a = p.e;
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int64_t row = (int64_t)blockIdx.x * (kJoinWaves / W) + wave / W;   // (token, query head)
+    const int part_of = wave % W;
+    const int D = a.kv.head_dim, quads = D >> 2, sides = 64 / quads, side = lane / quads, d = (lane - side * quads) * 4;
+    const int token = (int)(row / a.q_heads), hq = (int)(row - (int64_t)token * a.q_heads), h = hq / a.group;
+    // the tail's pieces
+    bool there = row < (int64_t)a.total_q * a.q_heads;
+    int n = 0;
+    int64_t tail = 0;
+    if (there) {
+        if constexpr (kOne) {
+            const decode::Work w = decode::work_of<true>(p.d, 0, token, lane);
+            const int i0 = w.before / w.chunk;
+            n = (w.before + decode::steps_of<true>(p.d, w.len) - 1) / w.chunk - i0 + 1;
+            tail = (int64_t)(i0 + token) * a.q_heads + hq;
+        } else {
+            const Place place(a, token);
+            there = place.in;
+            if (there) {
+                // the row tile that this row is in: its last position bounds the steps
+                const int r0 = (place.i * a.group + hq - h * a.group) / extend::kRows * extend::kRows;
+                const int last = place.pos - place.i + (min(r0 + extend::kRows, place.n * a.group) - 1) / a.group;
+                const int steps = Steps<extend::kStep>(last, last, 0, 0, p.from).count;
+                const int even = (steps + p.tail_splits - 1) / p.tail_splits, chunk = max(even, a.least);
+                n = (steps + chunk - 1) / chunk;
+            }
+        }
+    }
+    const float by_head = extend::v_scale_of(a.kv, h);
+    const int pieces = there ? p.splits + n : 0;
+    auto piece = [&](int i) {
+        if (kOne && i >= p.splits) return p.d.part_ml[tail + (int64_t)(i - p.splits) * a.q_heads];
+        return a.part_ml[row * a.splits + i];
+    };
+    auto values = [&](int i) {
+        if (kOne && i >= p.splits)
+            return *reinterpret_cast<const f4*>(p.d.part_o + (tail + (int64_t)(i - p.splits) * a.q_heads) * D + d);
+        return *reinterpret_cast<const f4*>(a.part_o + (row * a.splits + i) * D + d) * by_head;
+    };
+    float2 all;
+    f4 acc = joined(pieces, W, part_of, side, sides, side < sides, piece, values, &all);
+    s_acc[threadIdx.x] = acc;
+    if (W == 1) wave_sync();
+    else __syncthreads();
+    if (side != 0 || part_of != 0 || !there) return;
+    const f4* mine = s_acc + (threadIdx.x - lane);
+    for (int v = 0; v < W; ++v)
+        for (int s = v == 0 ? 1 : 0; s < sides; ++s) acc += mine[v * 64 + s * quads + lane];
+    const float m = all.x, l = all.y, r = l == 0.0f ? 0.0f : 1.0f / l;
+    *reinterpret_cast<uint2*>(a.out + (int64_t)token * a.ldo + (int64_t)hq * D + d) =
+        make_uint2(pack2(acc[0] * r, acc[1] * r), pack2(acc[2] * r, acc[3] * r));
+    if (d == 0 && a.lse) a.lse[row] = l == 0.0f ? -INFINITY : (m + __builtin_amdgcn_logf(l)) * kLn2;
+}
+
+// How a call is shared out.
+struct Plan {
+    bool one;
+    int64_t prefix_blocks, tail_blocks;
+    int splits, chunk;               // of the prefix
+    int tail_splits, least, tail_tiles;
+    int shares;                      // one new token a sequence: as attn_decode.hip's
+    int64_t ml, o, tail_ml, tail_o;  // bytes of the parts of the workspace
+};
+
+int64_t up16(int64_t n) { return (n + 15) / 16 * 16; }
+
+Plan plan_of(const AttnArgs& a, bool ragged) {
+    Plan p = {};
+    const int64_t group = a.q_heads / a.kv.heads, rows = a.total_q * group, heads = a.kv.heads;
+    p.one = !ragged && a.total_q == a.kv.batch;
+    const int64_t tiles = (rows + extend::kRows - 1) / extend::kRows;
+    const int64_t steps = a.from / extend::kStep, tail = std::max<int64_t>(a.kv.max_len - a.from, 0);
+    const int64_t want = 256;
+    int64_t s = std::clamp<int64_t>(want / (tiles * heads), 1, std::min<int64_t>(32, std::max<int64_t>(steps / 2, 1)));
+    p.chunk = (int)((steps + s - 1) / s);
+    p.splits = (int)((steps + p.chunk - 1) / p.chunk);
+    p.prefix_blocks = tiles * heads * p.splits;
+    if (p.one) {
+        const int64_t units = heads * ((group + 15) / 16);
+        const int64_t most = std::max<int64_t>((tail + decode::kStep - 1) / decode::kStep, 1) * a.kv.batch;
+        p.shares = (int)std::max<int64_t>(std::min<int64_t>((1024 + units - 1) / units, most), 1);
+        p.tail_blocks = ((p.shares + 7) / 8 * units + decode::kWaves - 1) / decode::kWaves * 8;
+        const int64_t pieces = (int64_t)(p.shares + a.kv.batch) * a.q_heads;
+        p.tail_ml = up16(pieces * 8);
+        p.tail_o = pieces * a.kv.head_dim * 4;
+    } else {
+        const int64_t each = a.total_q / a.kv.batch;
+        p.tail_tiles = (int)(ragged ? rows / extend::kRows + a.kv.batch
+                                    : a.kv.batch * ((each * group + extend::kRows - 1) / extend::kRows));
+        const int64_t tail_steps = (tail + extend::kStep - 1) / extend::kStep;
+        p.least = 4;
+        p.tail_splits = (int)std::clamp<int64_t>(std::min(512 / (p.tail_tiles * heads), tail_steps / 4), 1, 16);
+        p.tail_blocks = (int64_t)p.tail_tiles * heads * p.tail_splits;
+    }
+    const int64_t pieces = a.total_q * a.q_heads * (p.splits + p.tail_splits);
+    p.ml = up16(pieces * 8);
+    p.o = pieces * a.kv.head_dim * 4;
+    return p;
+}
+
+template <int KST, int VST, int DP, bool kOne>
+hipError_t run(const SharedParams& p, const Plan& plan, hipStream_t stream) {
+    constexpr int bytes = sizeof(extend::Lds<DP>);
+    static_assert(bytes <= 158 * 1024, "LDS");
+    const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(&k_shared<KST, VST, DP, kOne>),
+                                             hipFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    if (e != hipSuccess) return e;
+    hipLaunchKernelGGL((k_shared<KST, VST, DP, kOne>), dim3((unsigned)(plan.prefix_blocks + plan.tail_blocks)),
+                       dim3(extend::kThreads), bytes, stream, p);
+    return hipGetLastError();
+}
+
+template <int KST, int VST, bool kOne>
+hipError_t run_dim(const SharedParams& p, const Plan& plan, hipStream_t stream) {
+    if (p.e.kv.head_dim <= 64) return run<KST, VST, 64, kOne>(p, plan, stream);
+    if (p.e.kv.head_dim <= 128) return run<KST, VST, 128, kOne>(p, plan, stream);
+    return run<KST, VST, 256, kOne>(p, plan, stream);
+}
+
+template <int KST, bool kOne>
+hipError_t run_v(const SharedParams& p, const Plan& plan, hipStream_t stream) {
+    switch (p.e.kv.v_st) {
+    case FP8_KV_E4M3: return run_dim<KST, kE4M3, kOne>(p, plan, stream);
+    case FP8_KV_E5M2: return run_dim<KST, kE5M2, kOne>(p, plan, stream);
+    default: return run_dim<KST, kBf16, kOne>(p, plan, stream);
+    }
+}
+
+template <bool kOne>
+hipError_t run_k(const SharedParams& p, const Plan& plan, hipStream_t stream) {
+    hipError_t e;
+    switch (p.e.kv.k_st) {
+    case FP8_KV_E4M3: e = run_v<kE4M3, kOne>(p, plan, stream); break;
+    case FP8_KV_E5M2: e = run_v<kE5M2, kOne>(p, plan, stream); break;
+    default: e = run_v<kBf16, kOne>(p, plan, stream); break;
+    }
+    if (e != hipSuccess) return e;
+    const int64_t rows = (int64_t)p.e.total_q * p.e.q_heads;
+    const int W = rows < 2048 ? kJoinWaves : 1;
+    hipLaunchKernelGGL((k_shared_join<kOne>), dim3((unsigned)((rows * W + kJoinWaves - 1) / kJoinWaves)),
+                       dim3(kJoinThreads), 0, stream, p, W);
+    return hipGetLastError();
+}
+
+}  // namespace
+
+int64_t shared_workspace(const AttnArgs& a, bool ragged) {
+    const Plan p = plan_of(a, ragged);
+    return p.ml + up16(p.o) + p.tail_ml + p.tail_o;
+}
+
+int64_t shared_blocks(const AttnArgs& a, bool ragged) {
+    const Plan p = plan_of(a, ragged);
+    return std::max({p.prefix_blocks + p.tail_blocks, a.total_q * a.q_heads / (a.total_q * a.q_heads < 2048 ? 1 : 4) + 1,
+                     a.weighted ? extend_blocks(a, ragged) : 0});
+}
+
+hipError_t launch_shared(const AttnArgs& a) {
+    const Plan plan = plan_of(a, a.q_offsets != nullptr);
+    SharedParams p = {};
+    const int group = a.q_heads / a.kv.heads;
+    p.e.kv = a.kv; p.e.q = a.q; p.e.ldq = a.ldq; p.e.total_q = (int)a.total_q; p.e.each = (int)(a.total_q / a.kv.batch);
+    p.e.q_heads = a.q_heads; p.e.group = group; p.e.q_offsets = a.q_offsets; p.e.scale_log2 = a.scale * kLog2e;
+    p.e.out = a.out; p.e.ldo = a.ldo; p.e.lse = a.lse;
+    p.e.splits = plan.splits + plan.tail_splits; p.e.least = plan.least;
+    p.e.part_ml = reinterpret_cast<float2*>(a.workspace);
+    p.e.part_o = reinterpret_cast<float*>(a.workspace + plan.ml);
+    p.from = a.from; p.blocks = (int)plan.prefix_blocks; p.splits = plan.splits; p.chunk = plan.chunk;
+    p.tail_splits = plan.tail_splits; p.tail_tiles = plan.tail_tiles;
+    if (plan.one) {
+        p.d.kv = a.kv; p.d.q = a.q; p.d.ldq = a.ldq; p.d.q_heads = a.q_heads; p.d.group = group;
+        p.d.col_tiles = (group + 15) / 16; p.d.scale_log2 = a.scale * kLog2e; p.d.from = a.from;
+        p.d.shares = plan.shares; p.d.least = 4;
+        uint8_t* tail = a.workspace + plan.ml + up16(plan.o);
+        p.d.part_ml = reinterpret_cast<float2*>(tail);
+        p.d.part_o = reinterpret_cast<float*>(tail + plan.tail_ml);
+    }
+    const hipError_t e = plan.one ? run_k<true>(p, plan, a.stream) : run_k<false>(p, plan, a.stream);
+    return e != hipSuccess || !a.weighted ? e : launch_attention_weights(a);
+}
+
+}  // namespace fp8mi

@@ -151,6 +151,7 @@ struct AttnArgs {
     const int32_t* q_offsets = nullptr;   // null: total_q / batch queries a sequence
     float scale = 0.0f;
     int window = 0, sinks = 0;            // window 0: none; < max_len otherwise
+    int from = 0;                         // first tokens that all sequences share, a multiple of 64; with them no window
     uint16_t* out = nullptr;
     int64_t ldo = 0;
     float* lse = nullptr;
@@ -202,13 +203,16 @@ hipError_t launch_kv_append(const KvAppendArgs& a);
 // same rules as the launch's splits.
 int64_t decode_workspace(const AttnArgs& a);
 int64_t extend_workspace(const AttnArgs& a, bool ragged);
+int64_t shared_workspace(const AttnArgs& a, bool ragged);
 // Blocks (of 256 threads) of the call's largest launch.  2^32 threads and more
 // are not launched, or wrap to fewer without an error.
 int64_t decode_blocks(const AttnArgs& a);
 int64_t extend_blocks(const AttnArgs& a, bool ragged);
+int64_t shared_blocks(const AttnArgs& a, bool ragged);
 constexpr int64_t kMaxAttnBlocks = (int64_t(1) << 24) - 1;
 hipError_t launch_decode(const AttnArgs& a);              // weights included
 hipError_t launch_extend(const AttnArgs& a);              // weights included
+hipError_t launch_shared(const AttnArgs& a);              // a.from > 0, any queries; weights included
 hipError_t launch_attention_weights(const AttnArgs& a);   // the weights alone, from the keys and a.lse
 int64_t lora_workspace(const LoraArgs& a);
 int64_t lora_blocks(const LoraArgs& a);                   // as decode_blocks

@@ -510,6 +510,27 @@ fp8_status fp8_kv_attention(const fp8_kv_pair* cache, const void* q, int64_t ldq
 int64_t fp8_kv_attention_workspace(const fp8_kv_pair* cache, int64_t total_q, int32_t q_heads, int32_t ragged,
                                    int32_t window, int32_t sinks, int32_t weighted);
 
+/* fp8_kv_attention of a batch whose sequences begin with the same tokens in the
+ * same pages (a common instruction text or document): token j < shared of every
+ * sequence is read from the pages of the FIRST row of page_table, once for all
+ * queries.  The other rows' entries of those tokens should name the same pages
+ * (the results are then those of fp8_kv_attention up to rounding); a sequence
+ * shorter than `shared` sees its own length of them.  0 <= shared <= max_len;
+ * whole steps of 64 tokens are shared, what is left of `shared` is read with the
+ * sequences' own tokens.  With a window (of fewer than max_len tokens) or one
+ * sequence the call is fp8_kv_attention.  The weights of shared tokens enter the
+ * product with V rounded once to bf16, as those of several new tokens do; the
+ * sequences' own tokens as in fp8_kv_attention.
+ * workspace: fp8_kv_attention_shared_workspace() bytes.  Everything else as
+ * fp8_kv_attention. */
+fp8_status fp8_kv_attention_shared(const fp8_kv_pair* cache, const void* q, int64_t ldq, int64_t total_q,
+                                   int32_t q_heads, const int32_t* q_offsets, float scale, int32_t window,
+                                   int32_t sinks, int64_t shared, void* out, int64_t ldo, float* lse, float* weights,
+                                   int64_t ldw, void* workspace, int64_t workspace_bytes, void* stream);
+
+int64_t fp8_kv_attention_shared_workspace(const fp8_kv_pair* cache, int64_t total_q, int32_t q_heads, int32_t ragged,
+                                          int32_t window, int32_t sinks, int32_t weighted, int64_t shared);
+
 /* Eviction by accumulated attention weight: a sequence of n = len_b > budget
  * tokens keeps, for every KV head by itself, its first `sinks` tokens, its
  * last `recent`, and of those between the budget - sinks - recent with the

@@ -1,0 +1,355 @@
+"""fp8_kv_attention_shared on the GPU against the float64 reference of
+attention over the paged cache: one and several new tokens per sequence behind
+a shared prefix of whole and cut steps, every storage and scaling, sequences
+that end inside the prefix, empty ones, absent pages, values that are not
+finite, weights, captured graphs and other streams; and a step of a layer as it
+is used, projection, adapters, append and attention one after the other."""
+from __future__ import annotations
+
+import numpy as np
+import pytest
+import torch
+
+from tests import attention_ref as ref
+from tests.gpu_util import say
+
+pytestmark = pytest.mark.gpu
+
+fp8 = pytest.importorskip("fp8_precision_quantization_amd")
+
+
+@pytest.fixture(autouse=True)
+def _need_gpu(gpu):
+    yield
+
+
+class SharedCache(ref.Cache):
+    """A cache whose sequences' first `prefix` tokens (a multiple of the page)
+    lie in the first row's pages, from the first sequence that is long enough.
+    The other rows' entries of these pages name NaN pages: they are not read."""
+
+    def __init__(self, lens, prefix, *args, keep_tables=False, **kw):
+        super().__init__(lens, *args, **kw)
+        assert prefix % self.page == 0
+        self.prefix = prefix
+        owner = int(np.argmax(lens))
+        whole = prefix // self.page
+        assert lens[owner] >= prefix
+        pages = self.table[owner, :whole].copy()
+        for b, n in enumerate(lens):
+            m = min(n, prefix)
+            for w in "kv":
+                getattr(self, w + "64")[b][:m] = getattr(self, w + "64")[owner][:m]
+            if b != owner:
+                self.there[b][:m] = self.there[owner][:m]
+            # what these rows named before belongs to nobody now
+            if b != owner:
+                dead = self.rows[b][:m]
+                for w, st in (("k", self.k_storage), ("v", self.v_storage)):
+                    data = getattr(self, w)
+                    data[torch.from_numpy(dead)] = float("nan") if st == "bf16" else ref.NAN_CODE[st]
+                    if st != "bf16" and self.scaling == "token_head":
+                        getattr(self, w + "s")[torch.from_numpy(dead)] = float("nan")
+        dead_page = self.table[(owner + 1) % len(lens), 0] if len(lens) > 1 else pages[0] if whole else 0
+        for b in range(len(lens)):
+            self.table[b, :whole] = pages if b == 0 or keep_tables else dead_page
+        self.owner = owner
+
+
+def _run(cache, n, q_heads, shared=None, ragged=None, weights=None, scale=None, seed=1, **more):
+    q = ref.queries(cache, n, q_heads, seed)
+    args = cache.device()
+    if ragged is None:
+        ragged = len(set(n)) > 1
+    if ragged:
+        args["q_offsets"] = torch.tensor(np.concatenate([[0], np.cumsum(n)]), dtype=torch.int32).cuda()
+    args.update(more)
+    shared = cache.prefix if shared is None else shared
+    say("shared", shared, dict(lens=cache.lens[:6], n=list(n)[:6], heads=cache.heads, q_heads=q_heads, dim=cache.dim,
+                               page=cache.page, k=cache.k_storage, v=cache.v_storage, scaling=cache.scaling))
+    out, lse = fp8.kv_attention(q.cuda(), shared=shared, weights=weights, scale=scale, return_lse=True, **args)
+    torch.cuda.synchronize()
+    return q, out, lse
+
+
+def _check(cache, n, q_heads, **more):
+    q, out, lse = _run(cache, n, q_heads, **more)
+    ref.check_attention(cache, q, n, out, lse, scale=more.get("scale"))
+    return q, out, lse
+
+
+STORAGES = [("e4m3", "e4m3", "token_head"), ("e4m3", "e4m3", "head"), ("e5m2", "e5m2", "token_head"),
+            ("e5m2", "e4m3", "head"), ("bf16", "bf16", "token_head"), ("bf16", "e4m3", "token_head"),
+            ("e5m2", "bf16", "token_head"), ("e4m3", "e5m2", "token_head"), ("bf16", "e5m2", "head")]
+NEW = {"one": [1] * 5, "each": [3] * 5, "ragged": [1, 40, 7, 2, 64]}
+
+
+@pytest.mark.parametrize("new", NEW)
+@pytest.mark.parametrize("dim", [64, 128, 256])
+@pytest.mark.parametrize("storage", STORAGES, ids="-".join)
+def test_storages(storage, dim, new):
+    k, v, scaling = storage
+    c = SharedCache([140, 333, 200, 131, 192], 128, 2, dim, 16, k, v, scaling, seed=dim)
+    _check(c, NEW[new], 8)
+
+
+@pytest.mark.parametrize("new", NEW)
+@pytest.mark.parametrize("dim", [16, 48, 80, 96, 112, 160, 208, 240])
+def test_odd_dims(dim, new):
+    c = SharedCache([100, 150, 129, 70, 128], 64, 3, dim, 8, seed=dim)
+    _check(c, NEW[new], 6)
+
+
+@pytest.mark.parametrize("new", NEW)
+@pytest.mark.parametrize("group", [1, 3, 5, 8, 16, 17, 33, 71])
+def test_groups(group, new):
+    c = SharedCache([100, 150, 129, 70, 198], 64, 2, 64, 8, seed=group)
+    _check(c, NEW[new], 2 * group)
+
+
+@pytest.mark.parametrize("new", ["one", "ragged"])
+@pytest.mark.parametrize("page, prefix", [(1, 64), (1, 65), (1, 127), (2, 130), (8, 200), (32, 96), (64, 64), (64, 448),
+                                          (128, 128), (256, 512), (1, 63), (16, 16), (512, 512)])
+def test_prefixes(page, prefix, new):
+    """Prefixes that end inside a step of 64 leave the rest to the sequences' own tokens; so do their tables name them."""
+    c = SharedCache([prefix + 70, prefix + 64, prefix + 90, prefix + 66, prefix + 70], prefix, 2, 64, page,
+                    seed=prefix, keep_tables=True)
+    _check(c, NEW[new], 4)
+
+
+@pytest.mark.parametrize("new", ["one", "each"])
+def test_other_rows_are_not_read(new):
+    """With a prefix of whole steps, only the first row's entries of it are."""
+    c = SharedCache([400, 350, 321, 500, 330], 320, 2, 128, 32, seed=5)
+    _check(c, NEW[new], 8)
+
+
+@pytest.mark.parametrize("batch, prefix, tail", [(2, 4096, 5), (3, 10000, 700), (40, 1920, 33), (130, 640, 60), (300, 64, 20)])
+@pytest.mark.parametrize("several", [False, True])
+def test_sizes(batch, prefix, tail, several):
+    rng = np.random.default_rng(batch)
+    n = [1] * batch if not several else [int(x) for x in rng.integers(1, 12, batch)]
+    lens = [prefix + max(a, int(x)) for a, x in zip(n, rng.integers(1, tail + 1, batch))]
+    c = SharedCache(lens, prefix, 2, 64, 16, seed=batch, keep_tables=True)
+    _check(c, n, 4)
+
+
+@pytest.mark.parametrize("new", NEW)
+def test_sequences_inside_the_prefix(new):
+    """Shorter sequences see their own length of it; one of no tokens nothing."""
+    n = NEW[new]
+    c = SharedCache([700, max(40, n[1]), max(257, n[2]), 640, max(300, n[4])], 640, 2, 64, 32, seed=2)
+    _check(c, n, 4)
+    if new == "one":
+        c = SharedCache([700, 0, 1, 640, 0], 640, 2, 64, 32, seed=2)
+        _, out, lse = _check(c, n, 4)
+        for b in (1, 4):
+            assert (out[b] == 0).all() and torch.isneginf(lse[b]).all()
+
+
+def test_more_queries_than_tokens():
+    """Queries before a sequence's first token see nothing: zeros and -inf, as without the prefix."""
+    c = SharedCache([200, 5, 0, 190], 128, 2, 64, 32, seed=9)
+    n = [12] * 4
+    q, out, lse = _run(c, n, 4)
+    args = c.device()
+    args["page_table"] = args["page_table"].clone()
+    args["page_table"][:, :4] = args["page_table"][0, :4]
+    want, z = fp8.kv_attention(q.cuda(), return_lse=True, **args)
+    torch.cuda.synchronize()
+    assert torch.equal(lse.isneginf(), z.isneginf()) and (out[12:19] == 0).all() and (out[24:36] == 0).all()
+    keep = ~z.isneginf()
+    assert (lse[keep] - z[keep]).abs().max() < 1e-4
+    assert ((out - want).float().abs() <= 2.0 ** -6 * want.float().abs() + 2.0 ** -6).all()
+
+
+def test_queries_in_no_sequence_stay():
+    """Rows before the first and behind the last offset are not written."""
+    c = SharedCache([200, 300, 250], 128, 2, 64, 32, seed=4)
+    n = [3, 5, 2]
+    q = ref.queries(c, [14], 4)
+    args = c.device()
+    args["q_offsets"] = torch.tensor([2, 5, 10, 12], dtype=torch.int32).cuda()
+    out = torch.full((14, 4, 64), 9.0, dtype=torch.bfloat16).cuda()
+    lse = torch.full((14, 4), 9.0).cuda()
+    say("rows of no sequence")
+    fp8.kv_attention(q.cuda(), out=out, lse=lse, shared=128, **args)
+    torch.cuda.synchronize()
+    for rows in (slice(0, 2), slice(12, 14)):
+        assert (out[rows] == 9).all() and (lse[rows] == 9).all()
+    ref.check_attention(c, q[2:12], n, out[2:12], lse[2:12])
+
+
+@pytest.mark.parametrize("new", NEW)
+def test_absent_pages(new):
+    c = SharedCache([333, 260, 300, 340, 299], 192, 2, 128, 16, seed=4,
+                    absent=[(3, 1), (3, 7), (1, 13), (2, 12), (4, 18)])
+    assert c.owner == 3
+    _check(c, NEW[new], 8)
+
+
+@pytest.mark.parametrize("new", NEW)
+@pytest.mark.parametrize("storage", [("e4m3", "e4m3"), ("e5m2", "e5m2"), ("bf16", "bf16")], ids="-".join)
+def test_unseen_values_that_are_not_finite(new, storage):
+    """NaN values of the prefix reach the rows that see them, and no row that ends before them."""
+    n = NEW[new]
+    c = SharedCache([500, max(100, n[1]), 470, max(90, n[3]), 450], 448, 2, 64, 64, *storage, seed=11)
+    _, good, _ = _check(c, n, 4)
+    bad = int(c.rows[c.owner][300])
+    c.v[bad] = float("nan") if storage[1] == "bf16" else ref.NAN_CODE[storage[1]]
+    _, out, lse = _run(c, n, 4)
+    ends = np.cumsum([0] + list(n))
+    for b in range(5):
+        rows = slice(ends[b], ends[b + 1])
+        if c.lens[b] - n[b] > 300:
+            assert out[rows].isnan().all()
+        elif c.lens[b] <= 300:
+            assert torch.equal(out[rows], good[rows])
+    assert lse.isfinite().all()
+
+
+@pytest.mark.parametrize("new", NEW)
+def test_weights(new):
+    n = NEW[new]
+    c = SharedCache([400, 350, 389, 500, 384], 320, 2, 64, 32, seed=6, keep_tables=True)
+    start = torch.rand(5, 2, c.max_len).cuda()
+    w = start.clone()
+    q, out, lse = _run(c, n, 4, weights=w)
+    weights, delta, acc = ref.check_attention(c, q, n, out, lse)
+    w, start = w.double().cpu().numpy(), start.double().cpu().numpy()
+    at = 0
+    for b in range(5):
+        L = c.lens[b]
+        d = delta[at:at + n[b]].max()
+        at += n[b]
+        got = w[b, :, :L] - start[b, :, :L]
+        # the score's error in the weight and in the row's lse, an fp32 lse, sums of up to rows terms and the addition
+        bound = weights[b] * (2 * d + 4 * acc + 2.0 ** -18) + (weights[b] + 1) * 64 * 2.0 ** -24
+        assert (np.abs(got - weights[b]) <= bound).all()
+        assert np.array_equal(w[b, :, L:], start[b, :, L:])
+
+
+def test_windows_and_single_sequences_are_plain():
+    c = SharedCache([500, 400, 450], 320, 2, 64, 32, seed=8, keep_tables=True)
+    q = ref.queries(c, [1, 1, 1], 4).cuda()
+    a = fp8.kv_attention(q, shared=320, window=100, sinks=4, **c.device())
+    b = fp8.kv_attention(q, window=100, sinks=4, **c.device())
+    d = fp8.kv_attention(q, shared=63, **c.device())
+    e = fp8.kv_attention(q, **c.device())
+    one = c.device()
+    one["page_table"], one["lens"] = one["page_table"][:1], one["lens"][:1]
+    f = fp8.kv_attention(q[:1], shared=320, **one)
+    g = fp8.kv_attention(q[:1], **one)
+    torch.cuda.synchronize()
+    assert torch.equal(a, b) and torch.equal(d, e) and torch.equal(f, g)
+
+
+@pytest.mark.parametrize("new", NEW)
+def test_same_bits_again(new):
+    c = SharedCache([1400, 1350, 1321, 1500, 1330], 1280, 2, 128, 32, seed=12)
+    _, a, z = _run(c, NEW[new], 8)
+    for _ in range(3):
+        _, b, y = _run(c, NEW[new], 8)
+        assert torch.equal(a, b) and torch.equal(z, y)
+
+
+@pytest.mark.parametrize("new", NEW)
+def test_graph_stream_workspace(new):
+    """A captured call follows lengths that change between replays; a workspace of NaN on another stream."""
+    n = NEW[new]
+    c = SharedCache([400, 350, 389, 500, 384], 320, 2, 64, 32, seed=6, keep_tables=True)
+    args = c.device()
+    if new == "ragged":
+        args["q_offsets"] = torch.tensor(np.concatenate([[0], np.cumsum(n)]), dtype=torch.int32).cuda()
+    q = ref.queries(c, n, 4)
+    qd = q.cuda()
+    need = fp8._attention_workspace("e4m3", 2, 64, 32, 5, c.max_len, sum(n), 4, new == "ragged", 0, 0, False, 320)
+    ws = torch.full((need // 4 + 1,), float("nan"), device="cuda").view(torch.uint8)
+    out, lse = torch.empty_like(qd), torch.empty(sum(n), 4, device="cuda")
+
+    def call():
+        fp8.kv_attention(qd, shared=320, out=out, lse=lse, workspace=ws, **args)
+
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        call()
+    side.synchronize()
+    ref.check_attention(c, q, n, out, lse)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        call()
+    for step in range(3):
+        for b in range(5):
+            c.lens[b] -= 9
+            for name in ("k64", "v64", "there", "rows"):
+                getattr(c, name)[b] = getattr(c, name)[b][:c.lens[b]]
+        args["lens"].copy_(torch.tensor(c.lens, dtype=torch.int32))
+        out.fill_(5)
+        graph.replay()
+        torch.cuda.synchronize()
+        ref.check_attention(c, q, n, out, lse)
+
+
+@pytest.mark.parametrize("new", [1, 4])
+def test_a_layers_step(new):
+    """Projection in FP8, adapters in place, append with rotation, attention behind a shared prefix: each
+    against float64 on what it was given, and the chain's attention against plain kv_attention."""
+    B, H, G, D, inner, prefix = 6, 2, 4, 64, 256, 128
+    g = torch.Generator().manual_seed(3)
+    cache = fp8.KVCache(1, 1024, H, D)
+    width = (G * H + 2 * H) * D
+    w = fp8.quantize((torch.randn(width, inner, generator=g) / 16).to(torch.bfloat16).cuda(), "e4m3", "row")
+    slices = (G * H * D, H * D, H * D)
+    a = (torch.randn(3, 24, inner, generator=g) / 16).to(torch.bfloat16).cuda()
+    b = (torch.randn(3, width, 8, generator=g) / 4).to(torch.bfloat16).cuda()
+    freq = torch.tensor([10000.0 ** (-i / 32) for i in range(32)]).cuda()
+    table = torch.cat([torch.arange(8).expand(B, 8), 8 + torch.arange(B * 4).reshape(B, 4)], 1).to(torch.int32).cuda()
+
+    def project(x, ids):
+        xq = fp8.quantize(x, "e4m3", "row")
+        y = fp8.scaled_gemm(xq.q, w.q, xq.scale_inv, w.scale_inv)
+        y0 = y.clone()
+        fp8.lora_add(y, x, a, b, ids, slices=slices, out=y)
+        for row in range(0, x.shape[0], 5):
+            l = int(ids[row])
+            if l < 0:
+                assert torch.equal(y[row], y0[row])
+                continue
+            t, size = a[l].double() @ x[row].double(), a[l].double().abs() @ x[row].double().abs()
+            # t: sums of `inner` products in fp32, held with 16 bits; sums of 8 of its products
+            off = (inner + 24) * 2.0 ** -24 * size + (2.0 ** -16 + 32 * 2.0 ** -24) * t.abs()
+            parts = torch.repeat_interleave(torch.arange(3), torch.tensor(slices)).cuda()
+            want = y0[row].double() + (b[l].double() * t.reshape(3, 8)[parts]).sum(1)
+            off = (b[l].double().abs() * off.reshape(3, 8)[parts]).sum(1) + 2.0 ** -23 * want.abs()
+            assert ((y[row].double() - want).abs() <= off + 2.0 ** -8 * (want.abs() + off)).all()
+        return y[:, :slices[0]], y[:, slices[0]:slices[0] + H * D], y[:, slices[0] + H * D:]
+
+    # the prefix, once
+    x = torch.randn(prefix, inner, generator=g).to(torch.bfloat16).cuda()
+    q, k, v = project(x, torch.full((prefix,), -1, dtype=torch.int32).cuda())
+    pos = torch.arange(prefix).cuda()
+    cache.append(0, k, v, pos, positions=pos, inv_freq=freq)
+    # the sequences' own first tokens, then a step
+    lens = torch.full((B,), prefix)
+    ids = torch.tensor([0, 2, -1, 1, 0, 2], dtype=torch.int32)
+    for n in (5, new):
+        x = torch.randn(B * n, inner, generator=g).to(torch.bfloat16).cuda()
+        q, k, v = project(x, ids.repeat_interleave(n).cuda())
+        pos = (lens[:, None] + torch.arange(n)).reshape(-1)
+        row = torch.arange(B).repeat_interleave(n)
+        slots = table.cpu().long()[row, pos // 16] * 16 + pos % 16
+        q = cache.append(0, k, v, slots.cuda(), q=q, positions=pos.cuda(), inv_freq=freq)
+        lens = lens + n
+        dl = lens.to(torch.int32).cuda()
+        say("a layer's step", n)
+        out, z = cache.attend(0, q, table, dl, 16, shared=prefix, return_lse=True)
+        want, y = cache.attend(0, q, table, dl, 16, return_lse=True)
+        torch.cuda.synchronize()
+        # each is off its exact value by 2^-8 of itself and of sum p |v| <= max |v|, and what fp32 leaves
+        top = float(cache.v[0].load(prefix + 16 * 4 * B).float().abs().max())
+        assert ((out - want).float().abs() <= 2 * 2.0 ** -8 * (1 + 2.0 ** -7) * (want.float().abs() + top)).all()
+        # scores of 64 products in fp32, twice: |q| |k| / 8 of each
+        kk = cache.k[0].load(prefix + 16 * 4 * B).float().reshape(-1, D).norm(dim=1).max()
+        most = float(q.float().norm(dim=2).max() * kk) / 8
+        assert (z - y).abs().max() <= 2 * ((D + 8) * 2.0 ** -24 * most + 400 * 2.0 ** -24 + 2.0 ** -22 * (1 + y.abs().max()))
