@@ -8,21 +8,27 @@
 // two of them (16 significant bits) for a bf16 output, three (all 24) for an
 // fp32 one; B's values are bf16, so every product is exact in fp32.
 //
-// Two launches.  k_lora_shrink: a block takes a tile of rows that share an
-// adapter and a part of the inner dimension, whose steps go round its four
-// waves, so that neither x nor A is read twice by a block; the parts' sums go to
-// the workspace.  k_lora_expand: a block takes a row tile and a run of columns
-// of one slice, adds up the parts of t (in their order) and adds B t to y.
-// Products are 16x16x32 with ranks (columns of the output) as the matrix rows
-// and batch rows as its columns; a wave's 64 columns of the output are numbered
-// so that a lane gets 16 neighbouring ones of a row.
+// Rows are sorted by adapter first: a tile is up to 16 or 128 rows of one
+// adapter, wherever they are in the batch, so that A and B are read once a tile
+// whatever the order of the ids.  The sort counts ids in 1024 buckets; a tile of
+// a bucket that several adapters share takes them one after the other.
 //
-// Row tiles.  Up to kGathered rows, a tile is up to 16 rows with one adapter,
-// wherever they are in the batch: every wave looks through the ids by itself and
-// block i goes on if its row i is the first, 17th, .. of its adapter.  (A decode
-// step of many users.)  Larger batches hold prompts, whose rows lie together: a
-// tile is 64 neighbouring rows, and the adapters among them are taken one after
-// the other.
+// Up to kSmall rows (a decode step of many users) there are two launches.
+// k_shrink_small: a block (up to kFew rows each of its waves) sorts for itself, takes a tile of 16 rows and a part of
+// the inner dimension, whose steps go round its four waves, so that it reads
+// neither x nor A twice; the parts' sums and the tile's rows go to the workspace.
+// k_expand_small: a block takes a tile and 256 columns of one slice, adds up the
+// parts of t in their order and adds B t to y.  Products are 16x16x32 with ranks
+// (columns of the output) as the matrix rows and batch rows as its columns.
+//
+// Larger batches (prompts) are sorted by a launch of their own and take tiles of
+// 128 rows.  k_shrink_large: x and A go through LDS in three stages of 64 inner
+// elements, loaded past the registers; read as matrix operands directly, four
+// neighbouring lanes touch four rows, which the caches serve at a quarter of the
+// rate (8192 rows, 192 ranks, inner 4096: 105 us).  k_expand_large: a wave takes
+// 32 rows with the batch rows as the matrix rows and columns numbered so that a
+// lane has 16 bytes of a row and 16 lanes 256 neighbouring ones; B goes through
+// LDS, shared by the four waves.
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
@@ -37,9 +43,12 @@ using namespace attn;
 
 constexpr int kWaves = 4;
 constexpr int kThreads = 64 * kWaves;
-constexpr int kGathered = 1024;      // rows up to which a tile's rows may lie anywhere
-constexpr int kStepK = 64;           // inner elements of a wave's step
-constexpr int kChunk = 64;           // output columns of a wave's step
+constexpr int kSmall = 1024;         // rows up to which blocks sort for themselves
+constexpr int kFew = 64;             // rows up to which a wave sorts for itself
+constexpr int kSmallTile = 16, kLargeTile = 128;
+constexpr int kBuckets = 1024;
+constexpr int kStepK = 64;           // inner elements of a step
+constexpr int kChunk = 64;           // small: output columns of a wave
 
 struct LoraParams {
     const uint16_t* x;
@@ -54,8 +63,12 @@ struct LoraParams {
     int slices, width;               // width: slices * rank
     int ends[4];                     // first column behind each slice
     int block_ends[4];               // expand: first column block behind each slice
+    int slots;                       // tiles that the sort may make
     int splits, split_steps;         // parts of the inner dimension, their steps
-    int groups, chunks;              // shrink: blocks that share the ranks; expand: chunks of a wave
+    int groups;                      // shrink: blocks that share the ranks
+    int chunks;                      // expand, large: of a block
+    int2* tiles;                     // [slots][tile]: row and adapter (-1: none); small: row -1 where there is none
+    int* counts;                     // [slots], large: rows of a tile
     float* part;                     // [splits, rows, width]
 };
 
@@ -63,186 +76,92 @@ __device__ __forceinline__ int id_of(const LoraParams& p, int m) {
     const int l = p.ids[m];
     return l >= 0 && l < p.adapters ? l : -1;
 }
+__device__ __forceinline__ int bucket_of(int id) { return (id + 1) & (kBuckets - 1); }
 
-// The rows of a tile: lane i (of the first 16 CT) knows row i's number and its
-// adapter, -1 for a row that is not there (-2) or has none.
-template <int CT>
-struct Tile {
-    int row = 0, id = -2;
-    bool any = false;
-    __device__ __forceinline__ Tile(const LoraParams& p, int slot, int* s_rows) {
-        const int lane = threadIdx.x & 63;
-        if constexpr (CT == 1) {
-            const int mine = id_of(p, slot);
-            if (mine < 0) {                  // a row of its own, to copy
-                row = slot;
-                id = lane == 0 ? -1 : -2;
-                any = true;
-                return;
-            }
-            int ids[kGathered / 64];
+__device__ __forceinline__ int wave_scan(int v, int lane) {
 #pragma unroll
-            for (int i = 0; i < kGathered / 64; ++i) {
-                if (i * 64 >= p.rows) break;
-                ids[i] = id_of(p, min(i * 64 + lane, p.rows - 1));
-            }
-            int before = 0, rank = 0;        // of the rows looked at with this adapter, of row `slot`
-            if (lane < 16) s_rows[lane] = -1;
-            wave_sync();
-            // the rank of row `slot` first: the rows below it
+    for (int off = 1; off < 64; off <<= 1) {
+        const int t = __shfl_up(v, off, 64);
+        if (lane >= off) v += t;
+    }
+    return v;
+}
+
+// The slice of column block cb, its columns [first, end) and the block's place in it.
+struct Slice {
+    int index, first, end, block;
+    __device__ __forceinline__ Slice(const LoraParams& p, int cb) : first(0), end(p.ends[0]), block(cb) {
+        index = (cb >= p.block_ends[0] ? 1 : 0) + (cb >= p.block_ends[1] ? 1 : 0) + (cb >= p.block_ends[2] ? 1 : 0);
 #pragma unroll
-            for (int i = 0; i < kGathered / 64; ++i) {
-                if (i * 64 >= slot) break;
-                const int m = i * 64 + lane;
-                rank += __popcll(__ballot(ids[i] == mine && m < slot));
+        for (int i = 1; i < 4; ++i)
+            if (index == i) {
+                first = p.ends[i - 1];
+                end = p.ends[i];
+                block = cb - p.block_ends[i - 1];
             }
-            if (rank % 16 != 0) return;
-#pragma unroll
-            for (int i = 0; i < kGathered / 64; ++i) {
-                if (i * 64 >= p.rows) break;
-                const int m = i * 64 + lane;
-                const uint64_t same = __ballot(ids[i] == mine && m < p.rows);
-                const int at = before + __popcll(same & ((1ull << lane) - 1)) - rank;
-                if ((same >> lane & 1) && at >= 0 && at < 16) s_rows[at] = m;
-                before += __popcll(same);
-            }
-            wave_sync();
-            row = s_rows[lane & 15];
-            id = row < 0 ? -2 : mine;
-            row = max(row, 0);
-            any = true;
-        } else {
-            row = slot * 16 * CT + lane;
-            id = row < p.rows ? id_of(p, row) : -2;
-            row = min(row, p.rows - 1);
-            any = true;
-        }
     }
 };
 
-template <int CT, int RT>
-__global__ __launch_bounds__(kThreads, 2) void k_lora_shrink(const LoraParams p) {
-    __shared__ int s_rows[kWaves][16];
-    __shared__ f4 s_sum[2][RT * CT * 64];
-    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const int c = lane & 15, g = lane >> 4;
-    int block = blockIdx.x;
-    const int group = block % p.groups;
-    block /= p.groups;
-    const int split = block % p.splits, slot = block / p.splits;
-    const Tile<CT> tile(p, slot, s_rows[wave]);
-    if (!tile.any) return;
-    const int rank0 = group * RT * 16;
-    const int total = (p.inner + kStepK - 1) / kStepK;
-    const int s_begin = split * p.split_steps, s_end = min(s_begin + p.split_steps, total);
+// How t's bf16 terms lie along the matrix steps over the ranks.  With a multiple
+// of 32 ranks the terms follow each other against one piece of B; else terms and
+// ranks are one axis, filled up with zeros.
+struct Ranks {
+    int groups, steps, terms, pitch;     // groups of 8 ranks; bytes of a row of t in LDS
+    bool whole;
+    __host__ __device__ __forceinline__ Ranks(int rank, int terms_) {
+        groups = rank >> 3;
+        whole = rank % 32 == 0;
+        steps = whole ? rank / 32 : (terms_ * groups + 3) / 4;
+        terms = whole ? terms_ : 1;
+        pitch = (whole ? terms_ * rank : steps * 32) * 2 + 16;
+    }
+};
 
-    int rows[CT];                    // this lane's row of each column tile
-#pragma unroll
-    for (int i = 0; i < CT; ++i) rows[i] = __shfl(tile.row, i * 16 + c, 64);
-    uint64_t left = __ballot(tile.id >= 0);
-    while (left) {
-        const int l = __builtin_amdgcn_readlane(tile.id, __builtin_ctzll(left));
-        const uint64_t same = __ballot(tile.id == l);
-        left &= ~same;
-        const uint16_t* const ap = p.a + (int64_t)l * p.width * p.inner;
-        f4 acc[RT][CT];
-#pragma unroll
-        for (int i = 0; i < RT; ++i)
-#pragma unroll
-            for (int k = 0; k < CT; ++k) acc[i][k] = f4{0, 0, 0, 0};
-        struct StepA {
-            uint4 a[RT][2];
-        };
-        struct StepX {
-            uint4 x[CT][2];
-        };
-        // a lane's 16 elements of a step: both operands agree on the order
-        auto piece = [&](const uint16_t* from, int st, int h) {
-            const int e = st * kStepK + g * 16 + h * 8;
-            const bool in = e < p.inner;
-            const uint32_t keep = in ? ~0u : 0u;
-            const uint4 w = *reinterpret_cast<const uint4*>(from + (in ? e : 0));
-            return make_uint4(w.x & keep, w.y & keep, w.z & keep, w.w & keep);
-        };
-        auto load_x = [&](StepX& s, int st) {
-#pragma unroll
-            for (int k = 0; k < CT; ++k)
-#pragma unroll
-                for (int h = 0; h < 2; ++h) s.x[k][h] = piece(p.x + rows[k] * p.ldx, st, h);
-        };
-        auto load_a = [&](StepA& s, int st, int h) {
-            int rank = rank0 + c;
-            asm volatile("" : "+v"(rank));      // addresses anew each step: kept, they take the accumulators' registers
-#pragma unroll
-            for (int i = 0; i < RT; ++i)
-                s.a[i][h] = piece(ap + (int64_t)min(rank + i * 16, p.width - 1) * p.inner, st, h);
-        };
-        auto multiply = [&](const StepA& sa, const StepX& sx, int h) {
-#pragma unroll
-            for (int i = 0; i < RT; ++i)
-#pragma unroll
-                for (int k = 0; k < CT; ++k)
-                    acc[i][k] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
-                        __builtin_bit_cast(b8, sa.a[i][h]), __builtin_bit_cast(b8, sx.x[k][h]), acc[i][k], 0, 0, 0);
-        };
-        int st = s_begin + wave;
-        if (st < s_end) {
-            // x is a step ahead, A (from the caches, shared by the tiles) too
-            // where registers allow
-            constexpr bool kAheadA = RT * (CT + 4) <= 24;
-            StepX x, next_x;
-            StepA a, next_a;
-            load_x(x, st);
-            if (kAheadA) {
-                load_a(a, st, 0);
-                load_a(a, st, 1);
-            }
-            for (; st < s_end; st += kWaves) {
-                if (!kAheadA) load_a(a, st, 0);
-                if (st + kWaves < s_end) {
-                    load_x(next_x, st + kWaves);
-                    if (kAheadA) {
-                        load_a(next_a, st + kWaves, 0);
-                        load_a(next_a, st + kWaves, 1);
-                    }
-                }
-                multiply(a, x, 0);
-                if (!kAheadA) load_a(a, st, 1);
-                multiply(a, x, 1);
-                x = next_x;
-                if (kAheadA) a = next_a;
+// t of a tile's rows (their numbers: row_of(i)) for one adapter, as bf16 terms in LDS.
+template <int kTerms, class RowOf>
+__device__ __forceinline__ void put_t(const LoraParams& p, uint8_t* s_t, const Ranks& ranks, int rows, int slice,
+                                      float gain, RowOf&& row_of) {
+    const int groups = ranks.groups;
+    for (int i = threadIdx.x; i < rows * groups; i += kThreads) {
+        const int r = i / groups, q = i - r * groups, row = row_of(r);
+        f4 lo = {0, 0, 0, 0}, hi = {0, 0, 0, 0};
+        if (row >= 0) {
+            const float* from = p.part + (int64_t)row * p.width + slice * p.rank + q * 8;
+            const int64_t next = (int64_t)p.rows * p.width;
+#pragma unroll 4
+            for (int s = 0; s < p.splits; ++s) {
+                lo += *reinterpret_cast<const f4*>(from + s * next);
+                hi += *reinterpret_cast<const f4*>(from + s * next + 4);
             }
         }
-        // the four waves' sums: 2 and 3 to 0 and 1, then 1 to 0
-        if (wave >= 2)
+        float t[8];
 #pragma unroll
-            for (int i = 0; i < RT * CT; ++i) s_sum[wave - 2][i * 64 + lane] = acc[i / CT][i % CT];
-        __syncthreads();
-        if (wave < 2)
-#pragma unroll
-            for (int i = 0; i < RT * CT; ++i) acc[i / CT][i % CT] += s_sum[wave][i * 64 + lane];
-        __syncthreads();
-        if (wave == 1)
-#pragma unroll
-            for (int i = 0; i < RT * CT; ++i) s_sum[0][i * 64 + lane] = acc[i / CT][i % CT];
-        __syncthreads();
-        if (wave == 0) {
-#pragma unroll
-            for (int i = 0; i < RT; ++i) {
-                const int rank = rank0 + i * 16 + g * 4;
-#pragma unroll
-                for (int k = 0; k < CT; ++k) {
-                    const f4 sum = acc[i][k] + s_sum[0][(i * CT + k) * 64 + lane];
-                    if (rank < p.width && (same >> (k * 16 + c) & 1))
-                        *reinterpret_cast<f4*>(p.part + ((int64_t)split * p.rows + rows[k]) * p.width + rank) = sum;
-                }
-            }
+        for (int e = 0; e < 4; ++e) {
+            t[e] = lo[e] * gain;
+            t[4 + e] = hi[e] * gain;
         }
-        if (left) __syncthreads();
+#pragma unroll
+        for (int k = 0; k < kTerms; ++k) {
+            // one term of two values, which keep what it leaves
+            auto term = [](float& a, float& b) {
+                const uint32_t w = pack2(a, b);
+                a -= as_f32(w << 16);
+                b -= as_f32(w & 0xFFFF0000u);
+                return w;
+            };
+            *reinterpret_cast<uint4*>(s_t + r * ranks.pitch + (k * groups + q) * 16) =
+                make_uint4(term(t[0], t[1]), term(t[2], t[3]), term(t[4], t[5]), term(t[6], t[7]));
+        }
+    }
+    const int fill = ranks.whole ? 0 : ranks.steps * 4 - kTerms * groups;
+    for (int i = threadIdx.x; i < rows * fill; i += kThreads) {
+        const int r = i / fill;
+        *reinterpret_cast<uint4*>(s_t + r * ranks.pitch + (kTerms * groups + i - r * fill) * 16) =
+            make_uint4(0, 0, 0, 0);
     }
 }
 
-// Eight neighbouring values of an output row as fp32, and back.
+// Eight neighbouring values of an output row, to which fp32 ones are added.
 template <typename OutT>
 struct Eight {
     uint4 w[sizeof(OutT) / 2];
@@ -269,221 +188,723 @@ struct Eight {
     }
 };
 
-template <int CT, typename OutT>
-__global__ __launch_bounds__(kThreads, 2) void k_lora_expand(const LoraParams p) {
+// ------------------------------------------------------------ small batches --
+// The rows of tile `slot`, sorted by this block for itself: lane i (and i + 16,
+// i + 32, i + 48) gets row i and its adapter, row -1 where there is none.
+// Returns false where there is no such tile (for the whole block).
+__device__ __forceinline__ bool pick_tile(const LoraParams& p, int slot, int* row, int* id) {
+    if (p.rows <= kFew) {
+        // every wave by itself: the tile of row `slot`, where that is the first,
+        // 17th, .. of its adapter
+        const int lane = threadIdx.x & 63, mine = lane < p.rows ? id_of(p, lane) : -2;
+        const uint64_t same = __ballot(mine == __builtin_amdgcn_readlane(mine, slot));
+        const int rank = __popcll(same & ((1ull << slot) - 1)), n = __popcll(same) - rank;
+        if (rank % kSmallTile != 0) return false;
+        // lane i of the tile's takes the i-th of these rows from row `slot` on
+        const int at = __popcll(same & ((1ull << lane) - 1)) - rank;
+        const bool in = (same >> lane & 1) && at >= 0;
+        const int from = __builtin_amdgcn_ds_permute((in ? at : 63) * 4, lane);
+        *id = __builtin_amdgcn_readlane(mine, slot);
+        *row = __shfl(from, lane & (kSmallTile - 1), 64);
+        if ((lane & (kSmallTile - 1)) >= n) {
+            *row = -1;
+            *id = -2;
+        }
+        return true;
+    }
+    __shared__ int s_count[kBuckets];
+    constexpr int kEach = kSmall / kThreads;
+    __shared__ int s_sum[kWaves], s_found[2], s_in[kEach * kWaves];
+    __shared__ int2 s_rows[kSmallTile];
+    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+    *reinterpret_cast<int4*>(&s_count[tid * 4]) = make_int4(0, 0, 0, 0);
+    if (tid < kSmallTile) s_rows[tid] = make_int2(-1, -1);
+    if (tid == 0) s_found[0] = -1;
+    int ids[kEach];
+#pragma unroll
+    for (int i = 0; i < kEach; ++i) ids[i] = tid + i * kThreads < p.rows ? id_of(p, tid + i * kThreads) : -1;
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < kEach; ++i)
+        if (tid + i * kThreads < p.rows) atomicAdd(&s_count[bucket_of(ids[i])], 1);
+    __syncthreads();
+    static_assert(kBuckets == 4 * kThreads, "four buckets a thread");
+    const int4 n = *reinterpret_cast<const int4*>(&s_count[tid * 4]);
+    const int t0 = (n.x + kSmallTile - 1) / kSmallTile, t1 = t0 + (n.y + kSmallTile - 1) / kSmallTile,
+              t2 = t1 + (n.z + kSmallTile - 1) / kSmallTile, t3 = t2 + (n.w + kSmallTile - 1) / kSmallTile;
+    const int sum = wave_scan(t3, lane);
+    if (lane == 63) s_sum[wave] = sum;
+    __syncthreads();
+    int before = sum - t3;
+#pragma unroll
+    for (int w = 0; w < kWaves - 1; ++w) before += w < wave ? s_sum[w] : 0;
+    const int at = slot - before;
+    if (at >= 0 && at < t3) {
+        const int k = (at >= t0 ? 1 : 0) + (at >= t1 ? 1 : 0) + (at >= t2 ? 1 : 0);
+        s_found[0] = tid * 4 + k;
+        s_found[1] = at - (k == 0 ? 0 : k == 1 ? t0 : k == 2 ? t1 : t2);
+    }
+    __syncthreads();
+    const int bucket = s_found[0], first = s_found[1] * kSmallTile;
+    if (bucket < 0) return false;
+    // the bucket's rows in their order, the same in every block: 64 rows of every
+    // wave after the other
+    uint64_t in[kEach];
+#pragma unroll
+    for (int i = 0; i < kEach; ++i) {
+        in[i] = __ballot(tid + i * kThreads < p.rows && bucket_of(ids[i]) == bucket);
+        if (lane == 0) s_in[i * kWaves + wave] = __popcll(in[i]);
+    }
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < kEach; ++i) {
+        if (i * kThreads >= p.rows) break;
+        int at = __popcll(in[i] & ((1ull << lane) - 1)) - first;
+        for (int k = 0; k < i * kWaves + wave; ++k) at += s_in[k];
+        if ((in[i] >> lane & 1) && at >= 0 && at < kSmallTile) s_rows[at] = make_int2(tid + i * kThreads, ids[i]);
+    }
+    __syncthreads();
+    const int2 mine = s_rows[lane & (kSmallTile - 1)];
+    *row = mine.x;
+    *id = mine.x < 0 ? -2 : mine.y;
+    return true;
+}
+
+template <int RT>
+__global__ __launch_bounds__(kThreads, 2) void k_shrink_small(const LoraParams p) {
+    __shared__ f4 s_sum[2][RT * 64];
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int c = lane & 15, g = lane >> 4;
+    const int group = blockIdx.x % p.groups, split = blockIdx.x / p.groups % p.splits,
+              slot = blockIdx.x / (p.groups * p.splits);
+    int row, id;
+    const bool any = pick_tile(p, slot, &row, &id);
+    if (split == 0 && group == 0 && threadIdx.x < kSmallTile)
+        p.tiles[slot * kSmallTile + threadIdx.x] = any ? make_int2(row, id) : make_int2(-1, -1);
+    if (!any) return;
+    const int rank0 = group * RT * 16;
+    const int total = (p.inner + kStepK - 1) / kStepK;
+    const int s_begin = split * p.split_steps, s_end = min(s_begin + p.split_steps, total);
+    const uint16_t* const xp = p.x + (int64_t)max(row, 0) * p.ldx;
+    uint64_t left = __ballot(id >= 0);
+    while (left) {
+        const int l = __builtin_amdgcn_readlane(id, __builtin_ctzll(left));
+        const uint64_t same = __ballot(id == l);
+        left &= ~same;
+        const uint16_t* const ap = p.a + (int64_t)l * p.width * p.inner;
+        f4 acc[RT];
+#pragma unroll
+        for (int i = 0; i < RT; ++i) acc[i] = f4{0, 0, 0, 0};
+        struct StepA {
+            uint4 a[RT][2];
+        };
+        struct StepX {
+            uint4 x[2];
+        };
+        // a lane's 16 elements of a step: both operands agree on the order
+        auto piece = [&](const uint16_t* from, int st, int h) {
+            const int e = st * kStepK + g * 16 + h * 8;
+            return *reinterpret_cast<const uint4*>(from + (e < p.inner ? e : 0));
+        };
+        auto load_x = [&](StepX& s, int st) {
+#pragma unroll
+            for (int h = 0; h < 2; ++h) s.x[h] = piece(xp, st, h);
+        };
+        auto load_a = [&](StepA& s, int st) {
+            int rank = rank0 + c;
+            asm volatile("" : "+v"(rank));      // addresses anew each step: kept, they take the operands' registers
+#pragma unroll
+            for (int i = 0; i < RT; ++i)
+#pragma unroll
+                for (int h = 0; h < 2; ++h)
+                    s.a[i][h] = piece(ap + (int64_t)min(rank + i * 16, p.width - 1) * p.inner, st, h);
+        };
+        auto multiply = [&](StepA& sa, StepX& sx, int st, int h) {
+            if ((st + 1) * kStepK > p.inner) {      // the last step, cut: nothing behind the end
+                const uint32_t keep = st * kStepK + g * 16 + h * 8 < p.inner ? ~0u : 0u;
+                auto cut = [&](uint4& w) { w = make_uint4(w.x & keep, w.y & keep, w.z & keep, w.w & keep); };
+#pragma unroll
+                for (int i = 0; i < RT; ++i) cut(sa.a[i][h]);
+                cut(sx.x[h]);
+            }
+#pragma unroll
+            for (int i = 0; i < RT; ++i)
+                acc[i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(b8, sa.a[i][h]),
+                                                                 __builtin_bit_cast(b8, sx.x[h]), acc[i], 0, 0, 0);
+        };
+        int st = s_begin + wave;
+        if (st < s_end) {
+            StepX x, next_x;
+            StepA a, next_a;
+            load_x(x, st);
+            load_a(a, st);
+            for (; st < s_end; st += kWaves) {
+                if (st + kWaves < s_end) {
+                    load_x(next_x, st + kWaves);
+                    load_a(next_a, st + kWaves);
+                }
+                multiply(a, x, st, 0);
+                multiply(a, x, st, 1);
+                x = next_x;
+                a = next_a;
+            }
+        }
+        // the four waves' sums: 2 and 3 to 0 and 1, then 1 to 0
+        if (wave >= 2)
+#pragma unroll
+            for (int i = 0; i < RT; ++i) s_sum[wave - 2][i * 64 + lane] = acc[i];
+        __syncthreads();
+        if (wave < 2)
+#pragma unroll
+            for (int i = 0; i < RT; ++i) acc[i] += s_sum[wave][i * 64 + lane];
+        __syncthreads();
+        if (wave == 1)
+#pragma unroll
+            for (int i = 0; i < RT; ++i) s_sum[0][i * 64 + lane] = acc[i];
+        __syncthreads();
+        if (wave == 0) {
+#pragma unroll
+            for (int i = 0; i < RT; ++i) {
+                const int rank = rank0 + i * 16 + g * 4;
+                if (rank < p.width && (same >> c & 1))
+                    *reinterpret_cast<f4*>(p.part + ((int64_t)split * p.rows + row) * p.width + rank) =
+                        acc[i] + s_sum[0][i * 64 + lane];
+            }
+        }
+        if (left) __syncthreads();
+    }
+}
+
+template <typename OutT>
+__global__ __launch_bounds__(kThreads, 5) void k_expand_small(const LoraParams p) {
     constexpr int kTerms = sizeof(OutT) == 2 ? 2 : 3;
-    __shared__ int s_rows[kWaves][16];
-    extern __shared__ __align__(16) uint8_t s_t[];      // [16 CT rows][kTerms * rank, padded] bf16
+    extern __shared__ __align__(16) uint8_t s_t[];      // [16 rows][terms of t, padded] bf16
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int c = lane & 15, g = lane >> 4;
     const int column_blocks = p.block_ends[3], slot = blockIdx.x / column_blocks;
-    int cb = blockIdx.x % column_blocks;
-    const Tile<CT> tile(p, slot, s_rows[wave]);
-    if (!tile.any) return;
-    const int slice = (cb >= p.block_ends[0] ? 1 : 0) + (cb >= p.block_ends[1] ? 1 : 0) + (cb >= p.block_ends[2] ? 1 : 0);
-    int first = 0, end = p.ends[0];
+    const int2* const tile = p.tiles + slot * kSmallTile;
+    const int row = tile[c].x, id = row < 0 ? -2 : tile[c].y;
+    if (__ballot(row >= 0) == 0) return;
+    const Slice slice(p, blockIdx.x % column_blocks);
+    const int n0 = slice.first + (slice.block * kWaves + wave) * kChunk, end = slice.end;
+    const int n = n0 + g * 16;                          // this lane's 16 columns
+    const bool on[2] = {n < end && row >= 0, n + 8 < end && row >= 0};
+    const Ranks ranks(p.rank, kTerms);
+    const OutT* const y = static_cast<const OutT*>(p.y) + (int64_t)max(row, 0) * p.ldy;
+    OutT* const out = static_cast<OutT*>(p.out) + (int64_t)max(row, 0) * p.ldo;
+    Eight<OutT> v[2];
 #pragma unroll
-    for (int i = 1; i < 4; ++i)
-        if (slice >= i) {
-            first = p.ends[i - 1];
-            end = p.ends[i];
-        }
-#pragma unroll
-    for (int i = 0; i < 3; ++i) cb -= slice == i + 1 ? p.block_ends[i] : 0;
-    // this wave's chunks of columns
-    const int n_begin = first + (cb * kWaves + wave) * p.chunks * kChunk, n_end = min(n_begin + p.chunks * kChunk, end);
-
-    int rows[CT];
-#pragma unroll
-    for (int i = 0; i < CT; ++i) rows[i] = __shfl(tile.row, i * 16 + c, 64);
-    const int groups = p.rank >> 3;                     // of 8 ranks
-    // Matrix steps over the ranks.  With a multiple of 32 the terms of t follow
-    // each other against one piece of B; else terms and ranks are one axis.
-    const bool whole = p.rank % 32 == 0;
-    const int steps = whole ? p.rank / 32 : (kTerms * groups + 3) / 4, terms = whole ? kTerms : 1;
-    const int pitch = (whole ? kTerms * p.rank : steps * 32) * 2 + 16;
-    const OutT* y = static_cast<const OutT*>(p.y);
-    OutT* out = static_cast<OutT*>(p.out);
-
-    // rows without an adapter stay as they are
-    const uint64_t bare = __ballot(tile.id == -1);
-    if (bare && out != y) {
-        for (int n = n_begin + g * 16; n < n_end; n += kChunk)
-#pragma unroll
-            for (int k = 0; k < CT; ++k)
-#pragma unroll
-                for (int h = 0; h < 2; ++h)
-                    if ((bare >> (k * 16 + c) & 1) && n + h * 8 < n_end) {
-                        const uint4* from = reinterpret_cast<const uint4*>(y + rows[k] * p.ldy + n + h * 8);
-                        uint4* to = reinterpret_cast<uint4*>(out + rows[k] * p.ldo + n + h * 8);
-#pragma unroll
-                        for (int i = 0; i < (int)sizeof(OutT) / 2; ++i) to[i] = from[i];
-                    }
-    }
-    uint64_t left = __ballot(tile.id >= 0);
+    for (int h = 0; h < 2; ++h) v[h].load(y + (on[h] ? n + h * 8 : 0));
+    uint64_t left = __ballot(id >= 0);
     bool again = false;
     while (left) {
-        const int l = __builtin_amdgcn_readlane(tile.id, __builtin_ctzll(left));
-        const uint64_t same = __ballot(tile.id == l);
+        const int l = __builtin_amdgcn_readlane(id, __builtin_ctzll(left));
+        const uint64_t same = __ballot(id == l);
         left &= ~same;
+        // matrix row rho of piece j is column n0 + 16 (rho / 4) + 4 j + rho % 4
+        const uint16_t* bp[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+            bp[j] = p.b + ((int64_t)l * p.columns + min(n0 + (c >> 2) * 16 + j * 4 + (c & 3), end - 1)) * p.rank;
         if (again) __syncthreads();
         again = true;
-        // t of the tile's rows in bf16 terms
-        const float gain = p.gain ? p.gain[l] : 1.0f;
-        for (int i = threadIdx.x; i < 16 * CT * groups; i += kThreads) {
-            const int r = i / groups, q = i - r * groups;
-            const int row = CT == 1 ? s_rows[wave][r] : min(slot * 16 * CT + r, p.rows - 1);
-            f4 lo = {0, 0, 0, 0}, hi = {0, 0, 0, 0};
-            if (row >= 0) {
-                const float* from = p.part + (int64_t)row * p.width + slice * p.rank + q * 8;
-#pragma unroll 4
-                for (int s = 0; s < p.splits; ++s) {
-                    lo += *reinterpret_cast<const f4*>(from + (int64_t)s * p.rows * p.width);
-                    hi += *reinterpret_cast<const f4*>(from + (int64_t)s * p.rows * p.width + 4);
-                }
-            }
-            float t[8];
+        put_t<kTerms>(p, s_t, ranks, kSmallTile, slice.index, p.gain ? p.gain[l] : 1.0f,
+                      [&](int r) { return tile[r].x; });
+        __syncthreads();
+        f4 acc[4];
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                t[e] = lo[e] * gain;
-                t[4 + e] = hi[e] * gain;
-            }
+        for (int j = 0; j < 4; ++j) acc[j] = f4{0, 0, 0, 0};
+        for (int s = 0; s < ranks.steps; ++s) {
+            const int q = ranks.whole ? s * 4 + g : (s * 4 + g) % ranks.groups;
+            b8 bf[4];
 #pragma unroll
-            for (int k = 0; k < kTerms; ++k) {
-                // one term of two values, which keep what it leaves
-                auto term = [](float& a, float& b) {
-                    const uint32_t w = pack2(a, b);
-                    a -= as_f32(w << 16);
-                    b -= as_f32(w & 0xFFFF0000u);
-                    return w;
-                };
-                *reinterpret_cast<uint4*>(s_t + r * pitch + (k * groups + q) * 16) =
-                    make_uint4(term(t[0], t[1]), term(t[2], t[3]), term(t[4], t[5]), term(t[6], t[7]));
+            for (int j = 0; j < 4; ++j) bf[j] = *reinterpret_cast<const b8*>(bp[j] + q * 8);
+            for (int t = 0; t < ranks.terms; ++t) {
+                const b8 tf = *reinterpret_cast<const b8*>(s_t + c * ranks.pitch + (t * ranks.groups + s * 4 + g) * 16);
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    acc[j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(bf[j], tf, acc[j], 0, 0, 0);
             }
         }
-        if (!whole)
-            for (int i = threadIdx.x; i < 16 * CT * (steps * 4 - kTerms * groups); i += kThreads) {
-                const int n = steps * 4 - kTerms * groups, r = i / n;
-                *reinterpret_cast<uint4*>(s_t + r * pitch + (kTerms * groups + i - r * n) * 16) = make_uint4(0, 0, 0, 0);
-            }
-        __syncthreads();
+        if (id == l) {
+#pragma unroll
+            for (int h = 0; h < 2; ++h) v[h].add(acc[2 * h], acc[2 * h + 1]);
+        }
+    }
+    // (rows without an adapter as they are)
+    if (id >= 0 || (id == -1 && p.out != p.y)) {
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+            if (on[h]) v[h].store(out + n + h * 8);
+    }
+}
 
-        for (int n0 = n_begin; n0 < n_end; n0 += kChunk) {
-            const int n = n0 + g * 16;              // this lane's 16 columns
-            Eight<OutT> v[CT][2];
+// ------------------------------------------------------------ large batches --
+// Sorts the rows into tiles: one block.
+constexpr int kSortThreads = 1024;
+
+// Adds every lane's row to its bucket's counter and returns the row's place: one
+// addition where all 64 agree, which in prompts is most often so (one for each
+// lane, 8192 rows of 8 adapters: 19 us against 11).
+__device__ __forceinline__ int count_in(int* s_count, int bucket, bool on) {
+    const int lane = threadIdx.x & 63;
+    const uint64_t all = __ballot(on);
+    if (all == 0) return 0;
+    const int b = __builtin_amdgcn_readlane(bucket, __builtin_ctzll(all));
+    int place = 0;
+    if (__ballot(on && bucket == b) == all) {
+        if (lane == 0) place = atomicAdd(&s_count[b], __popcll(all));
+        return __builtin_amdgcn_readfirstlane(place) + __popcll(all & ((1ull << lane) - 1));
+    }
+    if (on) place = atomicAdd(&s_count[bucket], 1);
+    return place;
+}
+
+__global__ __launch_bounds__(kSortThreads) void k_sort_rows(const LoraParams p) {
+    constexpr int kRound = 8;               // rows of a thread that are on their way together
+    __shared__ int s_count[kBuckets], s_first[kBuckets + 1];
+    __shared__ int s_sum[kSortThreads / 64];
+    static_assert(kBuckets == kSortThreads, "a bucket a thread");
+    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+    s_count[tid] = 0;
+    __syncthreads();
+    int ids[kRound], place[kRound];
+    auto load = [&](int m0) {
 #pragma unroll
-            for (int k = 0; k < CT; ++k)
+        for (int i = 0; i < kRound; ++i) {
+            const int m = m0 + i * kSortThreads + tid;
+            ids[i] = m < p.rows ? id_of(p, m) : -1;
+        }
+    };
+    for (int m0 = 0; m0 < p.rows; m0 += kRound * kSortThreads) {
+        load(m0);
 #pragma unroll
-                for (int h = 0; h < 2; ++h)
-                    v[k][h].load(y + rows[k] * p.ldy + (n + h * 8 < n_end ? n + h * 8 : n0));
-            // matrix row rho of piece j is column n0 + 16 (rho / 4) + 4 j + rho % 4
-            const uint16_t* bp[4];
+        for (int i = 0; i < kRound; ++i)
+            place[i] = count_in(s_count, bucket_of(ids[i]), m0 + i * kSortThreads + tid < p.rows);
+    }
+    __syncthreads();
+    const int n = s_count[tid], tiles = (n + kLargeTile - 1) / kLargeTile;
+    const int sum = wave_scan(tiles, lane);
+    if (lane == 63) s_sum[wave] = sum;
+    __syncthreads();
+    int first = sum - tiles;
+    for (int w = 0; w < wave; ++w) first += s_sum[w];
+    s_first[tid] = first;
+    if (tid == kBuckets - 1) s_first[kBuckets] = first + tiles;
+    __syncthreads();
+    for (int slot = tid; slot < p.slots; slot += kSortThreads) {
+        // the last bucket whose tiles begin at or before this one
+        int b = 0;
 #pragma unroll
-            for (int j = 0; j < 4; ++j)
-                bp[j] = p.b + ((int64_t)l * p.columns + min(n0 + (c >> 2) * 16 + j * 4 + (c & 3), end - 1)) * p.rank;
-            f4 acc[4][CT];
+        for (int step = kBuckets / 2; step > 0; step >>= 1)
+            if (s_first[b + step] <= slot) b += step;
+        p.counts[slot] =
+            slot < s_first[kBuckets] ? min(s_count[b] - (slot - s_first[b]) * kLargeTile, kLargeTile) : 0;
+    }
+    // (a row's place in its bucket follows the order of the additions; no result does)
+    const bool again = p.rows > kRound * kSortThreads;
+    if (again) {
+        __syncthreads();
+        s_count[tid] = 0;
+        __syncthreads();
+    }
+    for (int m0 = 0; m0 < p.rows; m0 += kRound * kSortThreads) {
+        if (again) load(m0);
 #pragma unroll
-            for (int j = 0; j < 4; ++j)
+        for (int i = 0; i < kRound; ++i) {
+            const int m = m0 + i * kSortThreads + tid, b = bucket_of(ids[i]);
+            if (again) place[i] = count_in(s_count, b, m < p.rows);
+            if (m < p.rows) p.tiles[s_first[b] * kLargeTile + place[i]] = make_int2(m, ids[i]);
+        }
+    }
+}
+
+__device__ __forceinline__ uint32_t lds_address(const void* p) {
+    return (uint32_t)(uintptr_t)(const __attribute__((address_space(3))) void*)p;
+}
+
+// 64 lanes x 16 bytes into LDS [lds, lds + 1024).  No register result: nothing in
+// flight targets a register, and only the explicit waits below order it.
+__device__ __forceinline__ void load_to_lds(uint32_t lds, const void* from) {
+    asm volatile("s_mov_b32 m0, %0\n\tglobal_load_lds_dwordx4 %1, off"
+                 :: "s"(__builtin_amdgcn_readfirstlane(lds)), "v"(from) : "memory", "m0");
+}
+
+// Two waves a SIMD, so that one's reads of LDS stand beside the other's products:
+// two halves of the rows by four quarters of the ranks, RT rank tiles each.
+constexpr int kShrinkWaves = 8;
+
+template <int RT>
+__global__ __launch_bounds__(64 * kShrinkWaves, 1) void k_shrink_large(const LoraParams p) {
+    constexpr int kStages = 3, kRow = kStepK * 2;                   // bytes of a row of a stage
+    constexpr int kX = kLargeTile * kRow, kStage = kX + 4 * RT * 16 * kRow;
+    // 1 KiB loads of a wave: 8 rows each
+    constexpr int kXUnits = kLargeTile / 8 / kShrinkWaves, kAUnits = RT;
+    extern __shared__ __align__(1024) uint8_t smem[];
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int c = lane & 15, g = lane >> 4;
+    // neighbouring tiles, which often share an adapter, on one XCD (blocks go
+    // round the eight) for its L2 to hold A
+    const int unit = blockIdx.x >> 3, each = p.groups * p.splits;
+    const int group = unit % p.groups, split = unit / p.groups % p.splits;
+    const int slot = (int)(blockIdx.x & 7) * ((p.slots + 7) / 8) + unit / each;
+    if (slot >= p.slots || unit / each >= (p.slots + 7) / 8) return;
+    const int2* const tile = p.tiles + (int64_t)slot * kLargeTile;
+    const int count = p.counts[slot];
+    if (count == 0) return;
+    const int id_a = lane < count ? tile[lane].y : -2, id_b = 64 + lane < count ? tile[64 + lane].y : -2;
+    const int rank0 = group * RT * 64;
+    const int total = (p.inner + kStepK - 1) / kStepK;
+    const int s_begin = split * p.split_steps, s_end = min(s_begin + p.split_steps, total);
+    const int quarter = wave & 3, rows0 = (wave >> 2) * 64;         // this wave's ranks and rows
+
+    // What a lane loads: of row lane / 8 of a unit the 16-byte piece that belongs
+    // at place lane % 8, pieces being turned by the row so that 16 rows' reads of
+    // one piece fall into different banks.
+    const int piece = ((lane & 7) ^ (lane >> 3)) * 8;
+    const uint16_t* xp[kXUnits];
 #pragma unroll
-                for (int k = 0; k < CT; ++k) acc[j][k] = f4{0, 0, 0, 0};
-            for (int s = 0; s < steps; ++s) {
-                const int q = whole ? s * 4 + g : (s * 4 + g) % groups;
-                b8 bf[4];
+    for (int i = 0; i < kXUnits; ++i) {
+        const int row = tile[min((wave * kXUnits + i) * 8 + (lane >> 3), count - 1)].x;
+        xp[i] = p.x + (int64_t)row * p.ldx;
+    }
+    uint64_t left_a = __ballot(id_a >= 0), left_b = __ballot(id_b >= 0);
+    while (left_a | left_b) {
+        const int l = left_a ? __builtin_amdgcn_readlane(id_a, __builtin_ctzll(left_a))
+                             : __builtin_amdgcn_readlane(id_b, __builtin_ctzll(left_b));
+        const uint64_t same_a = __ballot(id_a == l), same_b = __ballot(id_b == l);
+        left_a &= ~same_a;
+        left_b &= ~same_b;
+        const uint16_t* ap[kAUnits];
 #pragma unroll
-                for (int j = 0; j < 4; ++j) bf[j] = *reinterpret_cast<const b8*>(bp[j] + q * 8);
-                for (int t = 0; t < terms; ++t) {
-                    const uint8_t* tp = s_t + c * pitch + (t * groups + s * 4 + g) * 16;
+        for (int i = 0; i < kAUnits; ++i) {
+            const int rank = min(rank0 + (wave * kAUnits + i) * 8 + (lane >> 3), p.width - 1);
+            ap[i] = p.a + ((int64_t)l * p.width + rank) * p.inner;
+        }
+        auto stage = [&](int st) {
+            const uint32_t to = lds_address(smem) + (uint32_t)((st - s_begin) % kStages) * kStage;
+            const int e = st * kStepK + piece, at = e < p.inner ? e : 0;
 #pragma unroll
-                    for (int k = 0; k < CT; ++k) {
-                        const b8 tf = *reinterpret_cast<const b8*>(tp + k * 16 * pitch);
+            for (int i = 0; i < kXUnits; ++i) load_to_lds(to + (wave * kXUnits + i) * 1024, xp[i] + at);
 #pragma unroll
-                        for (int j = 0; j < 4; ++j)
-                            acc[j][k] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(bf[j], tf, acc[j][k], 0, 0, 0);
-                    }
+            for (int i = 0; i < kAUnits; ++i) load_to_lds(to + kX + (wave * kAUnits + i) * 1024, ap[i] + at);
+        };
+        f4 acc[RT][4];
+#pragma unroll
+        for (int i = 0; i < RT; ++i)
+#pragma unroll
+            for (int k = 0; k < 4; ++k) acc[i][k] = f4{0, 0, 0, 0};
+        // everything loaded before is here, so the counts below are of the stages alone
+        asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
+        if (s_begin < s_end) stage(s_begin);
+        if (s_begin + 1 < s_end) stage(s_begin + 1);
+        for (int st = s_begin; st < s_end; ++st) {
+            // this stage has arrived, in all waves; the one read last is free for the next but one
+            if (st + 1 < s_end)
+                asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"(kXUnits + kAUnits) : "memory");
+            else
+                asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
+            if (st + 2 < s_end) stage(st + 2);
+            const uint8_t* const from = smem + (st - s_begin) % kStages * kStage;
+            const bool cut = (st + 1) * kStepK > p.inner;
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const int at = ((h * 4 + g) ^ (c & 7)) * 16;
+                uint4 xf[4], af[RT];
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+                    xf[k] = *reinterpret_cast<const uint4*>(from + (rows0 + k * 16 + c) * kRow + at);
+#pragma unroll
+                for (int i = 0; i < RT; ++i)
+                    af[i] = *reinterpret_cast<const uint4*>(from + kX + ((quarter * RT + i) * 16 + c) * kRow + at);
+                if (cut) {                                          // nothing behind the end
+                    const uint32_t keep = st * kStepK + h * 32 + g * 8 < p.inner ? ~0u : 0u;
+                    auto clear = [&](uint4& w) { w = make_uint4(w.x & keep, w.y & keep, w.z & keep, w.w & keep); };
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) clear(xf[k]);
+#pragma unroll
+                    for (int i = 0; i < RT; ++i) clear(af[i]);
                 }
+#pragma unroll
+                for (int i = 0; i < RT; ++i)
+#pragma unroll
+                    for (int k = 0; k < 4; ++k)
+                        acc[i][k] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
+                            __builtin_bit_cast(b8, af[i]), __builtin_bit_cast(b8, xf[k]), acc[i][k], 0, 0, 0);
             }
+        }
+        const uint64_t same = rows0 ? same_b : same_a;
 #pragma unroll
-            for (int k = 0; k < CT; ++k)
+        for (int k = 0; k < 4; ++k) {
+            if (!(same >> (k * 16 + c) & 1)) continue;
+            float* const to = p.part + ((int64_t)split * p.rows + tile[rows0 + k * 16 + c].x) * p.width;
 #pragma unroll
-                for (int h = 0; h < 2; ++h)
-                    if ((same >> (k * 16 + c) & 1) && n + h * 8 < n_end) {
-                        v[k][h].add(acc[2 * h][k], acc[2 * h + 1][k]);
-                        v[k][h].store(out + rows[k] * p.ldo + n + h * 8);
+            for (int i = 0; i < RT; ++i) {
+                const int rank = rank0 + (quarter * RT + i) * 16 + g * 4;
+                if (rank < p.width) *reinterpret_cast<f4*>(to + rank) = acc[i][k];
+            }
+        }
+    }
+}
+
+// Columns of a step: 8 neighbouring ones a lane in bf16, 4 in fp32.
+template <typename OutT> constexpr int kEach = sizeof(OutT) == 2 ? 8 : 4;
+
+template <typename OutT>
+__global__ __launch_bounds__(kThreads, 2) void k_expand_large(const LoraParams p) {
+    constexpr int kTerms = sizeof(OutT) == 2 ? 2 : 3, J = kEach<OutT>, kCols = 16 * J;
+    extern __shared__ __align__(16) uint8_t smem[];     // t of 128 rows, then two steps' B
+    const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int c = lane & 15, g = lane >> 4;
+    const int column_blocks = p.block_ends[3], slot = blockIdx.x / column_blocks;
+    const int2* const tile = p.tiles + (int64_t)slot * kLargeTile;
+    const int count = p.counts[slot];
+    if (count == 0) return;
+    const Slice slice(p, blockIdx.x % column_blocks);
+    const int n_begin = slice.first + slice.block * p.chunks * kCols, n_end = min(n_begin + p.chunks * kCols, slice.end);
+    const Ranks ranks(p.rank, kTerms);
+    uint8_t* const s_b = smem + kLargeTile * ranks.pitch;
+    const int b_bytes = kCols * p.rank * 2, pieces = J * 16 * ranks.groups;
+    const OutT* const y = static_cast<const OutT*>(p.y);
+    OutT* const out = static_cast<OutT*>(p.out);
+
+    // this lane's rows: 4 g + i of the wave's two matrix tiles
+    int rows[2][4], ids[2][4];
+#pragma unroll
+    for (int k = 0; k < 2; ++k)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int at = wave * 32 + k * 16 + g * 4 + i;
+            const int2 e = tile[min(at, count - 1)];
+            rows[k][i] = e.x;
+            ids[k][i] = at < count ? e.y : -2;
+        }
+    auto load_y = [&](uint4 (&v)[2][4], int n0) {
+        const int n = n0 + c * J < n_end ? n0 + c * J : n_begin;
+        int none = 0;
+        asm volatile("" : "+v"(none));              // addresses anew each step, not kept in registers
+#pragma unroll
+        for (int k = 0; k < 2; ++k)
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                v[k][i] = *reinterpret_cast<const uint4*>(y + (rows[k][i] + none) * p.ldy + n);
+    };
+    auto store = [&](const uint4& v, int k, int i, int n0) {
+        int none = 0;
+        asm volatile("" : "+v"(none));
+        if (n0 + c * J < n_end) *reinterpret_cast<uint4*>(out + (rows[k][i] + none) * p.ldo + n0 + c * J) = v;
+    };
+
+    const int id_a = lane < count ? tile[lane].y : -2, id_b = 64 + lane < count ? tile[64 + lane].y : -2;
+    // rows without an adapter stay as they are
+    if (p.out != p.y && __any(id_a == -1 || id_b == -1))
+        for (int n = n_begin + c * J; n < n_end; n += kCols)
+#pragma unroll
+            for (int k = 0; k < 2; ++k)
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    if (ids[k][i] == -1)
+                        *reinterpret_cast<uint4*>(out + rows[k][i] * p.ldo + n) =
+                            *reinterpret_cast<const uint4*>(y + rows[k][i] * p.ldy + n);
+    uint64_t left_a = __ballot(id_a >= 0), left_b = __ballot(id_b >= 0);
+    bool again = false;
+    while (left_a | left_b) {
+        const int l = left_a ? __builtin_amdgcn_readlane(id_a, __builtin_ctzll(left_a))
+                             : __builtin_amdgcn_readlane(id_b, __builtin_ctzll(left_b));
+        left_a &= ~__ballot(id_a == l);
+        left_b &= ~__ballot(id_b == l);
+        const uint16_t* const b = p.b + (int64_t)l * p.columns * p.rank;
+        // B of a step into LDS: piece (j, q, c) is ranks 8 q.. of column n0 + c J + j
+        auto stage_b = [&](int n0, int buf) {
+            for (int i = tid; i < pieces; i += kThreads) {          // (whole waves)
+                const int jq = i >> 4, j = jq / ranks.groups, q = jq - j * ranks.groups;
+                const int n = min(n0 + (i & 15) * J + j, slice.end - 1);
+                load_to_lds(lds_address(s_b) + buf * b_bytes + (i & ~63) * 16, b + (int64_t)n * p.rank + q * 8);
+            }
+        };
+        if (again) __syncthreads();
+        again = true;
+        uint4 v[2][4];                              // y, on its way during the step before
+        stage_b(n_begin, 0);
+        load_y(v, n_begin);
+        put_t<kTerms>(p, smem, ranks, kLargeTile, slice.index, p.gain ? p.gain[l] : 1.0f,
+                      [&](int r) { return r < count ? tile[r].x : -1; });
+        asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
+        int buf = 0;
+        for (int n0 = n_begin; n0 < n_end; n0 += kCols, buf ^= 1) {
+            const bool more = n0 + kCols < n_end;
+            if (more) stage_b(n0 + kCols, buf ^ 1);
+            f4 acc[2][J];
+#pragma unroll
+            for (int k = 0; k < 2; ++k)
+#pragma unroll
+                for (int j = 0; j < J; ++j) acc[k][j] = f4{0, 0, 0, 0};
+            for (int s = 0; s < ranks.steps; ++s) {
+                const int q = ranks.whole ? s * 4 + g : (s * 4 + g) % ranks.groups;
+                b8 bf[J];
+#pragma unroll
+                for (int j = 0; j < J; ++j)
+                    bf[j] = *reinterpret_cast<const b8*>(s_b + buf * b_bytes + ((j * ranks.groups + q) * 16 + c) * 16);
+                for (int t = 0; t < ranks.terms; ++t)
+#pragma unroll
+                    for (int k = 0; k < 2; ++k) {
+                        const b8 tf = *reinterpret_cast<const b8*>(smem + (wave * 32 + k * 16 + c) * ranks.pitch +
+                                                                   (t * ranks.groups + s * 4 + g) * 16);
+#pragma unroll
+                        for (int j = 0; j < J; ++j)
+                            acc[k][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(tf, bf[j], acc[k][j], 0, 0, 0);
                     }
+            }
+            // y of this step and B of the next are here
+            asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+#pragma unroll
+            for (int k = 0; k < 2; ++k)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    if (ids[k][i] != l) continue;
+                    uint4 w = v[k][i];
+                    if constexpr (sizeof(OutT) == 2) {
+                        auto two = [&](uint32_t v, float a, float d) {
+                            return pack2(as_f32(v << 16) + a, as_f32(v & 0xFFFF0000u) + d);
+                        };
+                        w = make_uint4(two(w.x, acc[k][0][i], acc[k][1][i]), two(w.y, acc[k][2][i], acc[k][3][i]),
+                                       two(w.z, acc[k][J - 4][i], acc[k][J - 3][i]),
+                                       two(w.w, acc[k][J - 2][i], acc[k][J - 1][i]));
+                    } else {
+                        auto one = [](uint32_t v, float a) { return __builtin_bit_cast(uint32_t, as_f32(v) + a); };
+                        w = make_uint4(one(w.x, acc[k][0][i]), one(w.y, acc[k][1][i]), one(w.z, acc[k][2][i]),
+                                       one(w.w, acc[k][3][i]));
+                    }
+                    store(w, k, i, n0);
+                }
+            if (more) load_y(v, n0 + kCols);
+            asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
         }
     }
 }
 
 // How a call is shared out.
 struct Plan {
-    bool gathered;
-    int slots, tiles;                // blocks of rows; about as many have work
+    bool small;
+    int slots, tile;                 // tiles that the sort may make, rows of one
     int rank_tiles, groups, splits, split_steps;
     int64_t shrink_blocks;
 };
 
 Plan plan_of(const LoraArgs& a) {
     Plan p;
-    p.gathered = a.rows <= kGathered;
-    const int width = a.slices * a.rank, all = (width + 15) / 16;
-    p.slots = p.gathered ? (int)a.rows : (int)((a.rows + 63) / 64);
-    p.tiles = p.gathered ? (int)std::min<int64_t>(a.rows, (a.rows + 15) / 16 + a.adapters) : p.slots;
-    p.groups = (all + 5) / 6;
-    const int each = (all + p.groups - 1) / p.groups;
-    p.rank_tiles = each == 5 ? 6 : each;
-    const int steps = (int)((a.inner + kStepK - 1) / kStepK);
-    // Parts of the inner dimension: about two blocks a CU, every wave with a
-    // step or more, and no more than 16 rows of t for the second launch to add.
-    int splits = 512 / (p.tiles * p.groups);
-    splits = std::clamp(splits, 1, 16);
+    p.small = a.rows <= kSmall;
+    p.tile = p.small ? kSmallTile : kLargeTile;
+    p.slots = a.rows <= kFew ? (int)a.rows
+                             : (int)(a.rows / p.tile + std::min<int64_t>({a.rows, (int64_t)a.adapters + 1, kBuckets}));
+    const int ranks = (a.slices * a.rank + 15) / 16, steps = (int)((a.inner + kStepK - 1) / kStepK);
+    int splits;
+    if (p.small) {
+        p.groups = (ranks + 5) / 6;
+        p.rank_tiles = (ranks + p.groups - 1) / p.groups;
+        if (p.rank_tiles == 5) p.rank_tiles = 6;
+        // Parts of the inner dimension: about a block a CU, every wave with a step
+        // or more, and no more than 16 rows of t for the second launch to add (331
+        // rows of 12 adapters, 14336 columns: half as many 20.4 us, twice 19.5, so 18.5).
+        const int tiles = std::min(p.slots, (int)std::min<int64_t>(a.rows, (a.rows + 15) / 16 + a.adapters));
+        splits = std::clamp(256 / (tiles * p.groups), 1, 16);
+    } else {
+        p.groups = (ranks + 11) / 12;
+        p.rank_tiles = ((ranks + p.groups - 1) / p.groups + 3) / 4;
+        // Blocks take a CU each: whole rounds of 256, and one round where it can be.
+        const int64_t blocks = (int64_t)p.slots * p.groups;
+        splits = (int)std::clamp<int64_t>((blocks <= 128 ? 256 : 512) / blocks, 1, 8);
+    }
     p.split_steps = std::max((steps + splits - 1) / splits, kWaves);
     p.splits = std::max(1, (steps + p.split_steps - 1) / p.split_steps);
-    p.shrink_blocks = (int64_t)p.slots * p.splits * p.groups;
+    p.shrink_blocks = (int64_t)(p.small ? p.slots : (p.slots + 7) / 8 * 8) * p.splits * p.groups;
     return p;
 }
 
-template <int CT>
+int64_t tile_bytes(const Plan& p) { return (int64_t)p.slots * p.tile * 8; }
+int64_t count_bytes(const Plan& p) { return p.small ? 0 : ((int64_t)p.slots * 4 + 15) / 16 * 16; }
+
+// Column blocks of the second launch.
+template <typename OutT>
+int64_t column_blocks(const LoraArgs& a, const Plan& plan, int* chunks, int (&ends)[4]) {
+    const int cols = plan.small ? kWaves * kChunk : 16 * kEach<OutT>;
+    auto count = [&](int run) {
+        int blocks = 0;
+        for (int i = 0; i < 4; ++i) {
+            const int n = i < a.slices ? a.columns_of[i] : 0;
+            blocks += (n + run - 1) / run;
+            ends[i] = blocks;
+        }
+        return (int64_t)blocks * plan.slots;
+    };
+    *chunks = 1;
+    if (!plan.small) {
+        // One resident round of two blocks a CU where runs of up to 16 steps allow
+        // (a block's rows of t are read once for its run): 8192 rows of 6144
+        // columns in 438 blocks 51 us, in 657 63, in 876 63, in 365 61.
+        const int most = 16;
+        while (*chunks < most && count(cols * *chunks) > 512) ++*chunks;
+    }
+    return count(cols * *chunks);
+}
+
+template <int RT>
+hipError_t shrink_large(const LoraParams& p, const Plan& plan, hipStream_t stream) {
+    constexpr int bytes = 3 * (kLargeTile + 64 * RT) * kStepK * 2;
+    static_assert(bytes <= 160 * 1024, "LDS");
+    const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(&k_shrink_large<RT>),
+                                             hipFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    if (e != hipSuccess) return e;
+    hipLaunchKernelGGL((k_shrink_large<RT>), dim3((unsigned)plan.shrink_blocks), dim3(64 * kShrinkWaves), bytes, stream,
+                       p);
+    return hipGetLastError();
+}
+
 hipError_t run_shrink(const LoraParams& p, const Plan& plan, hipStream_t stream) {
+    if (!plan.small)
+        return plan.rank_tiles == 1   ? shrink_large<1>(p, plan, stream)
+               : plan.rank_tiles == 2 ? shrink_large<2>(p, plan, stream)
+                                      : shrink_large<3>(p, plan, stream);
     const dim3 grid((unsigned)plan.shrink_blocks), block(kThreads);
     switch (plan.rank_tiles) {
-    case 1: hipLaunchKernelGGL((k_lora_shrink<CT, 1>), grid, block, 0, stream, p); break;
-    case 2: hipLaunchKernelGGL((k_lora_shrink<CT, 2>), grid, block, 0, stream, p); break;
-    case 3: hipLaunchKernelGGL((k_lora_shrink<CT, 3>), grid, block, 0, stream, p); break;
-    case 4: hipLaunchKernelGGL((k_lora_shrink<CT, 4>), grid, block, 0, stream, p); break;
-    default: hipLaunchKernelGGL((k_lora_shrink<CT, 6>), grid, block, 0, stream, p); break;
+    case 1: hipLaunchKernelGGL((k_shrink_small<1>), grid, block, 0, stream, p); break;
+    case 2: hipLaunchKernelGGL((k_shrink_small<2>), grid, block, 0, stream, p); break;
+    case 3: hipLaunchKernelGGL((k_shrink_small<3>), grid, block, 0, stream, p); break;
+    case 4: hipLaunchKernelGGL((k_shrink_small<4>), grid, block, 0, stream, p); break;
+    default: hipLaunchKernelGGL((k_shrink_small<6>), grid, block, 0, stream, p); break;
     }
     return hipGetLastError();
 }
 
-template <int CT, typename OutT>
-hipError_t run_expand(LoraParams& p, const Plan& plan, hipStream_t stream) {
-    constexpr int kTerms = sizeof(OutT) == 2 ? 2 : 3;
-    int ends[4], from = 0, blocks = 0;
-    p.chunks = CT == 1 ? 1 : 2;
-    for (int i = 0; i < 4; ++i) {
-        const int run = kWaves * p.chunks * kChunk;
-        blocks += (p.ends[i] - from + run - 1) / run;
-        from = p.ends[i];
-        ends[i] = blocks;
+template <typename OutT>
+hipError_t run_expand(const LoraArgs& a, LoraParams& p, const Plan& plan, hipStream_t stream) {
+    const int64_t blocks = column_blocks<OutT>(a, plan, &p.chunks, p.block_ends);
+    const Ranks ranks(p.rank, sizeof(OutT) == 2 ? 2 : 3);
+    const dim3 grid((unsigned)blocks), block(kThreads);
+    if (plan.small) {
+        hipLaunchKernelGGL((k_expand_small<OutT>), grid, block, kSmallTile * ranks.pitch, stream, p);
+        return hipGetLastError();
     }
-    for (int i = 0; i < 4; ++i) p.block_ends[i] = ends[i];
-    const int kv = p.rank % 32 == 0 ? kTerms * p.rank : (kTerms * p.rank + 31) / 32 * 32;
-    const int bytes = 16 * CT * (kv * 2 + 16);
-    hipLaunchKernelGGL((k_lora_expand<CT, OutT>), dim3((unsigned)((int64_t)plan.slots * blocks)), dim3(kThreads), bytes,
-                       stream, p);
+    const int bytes = kLargeTile * ranks.pitch + 2 * 16 * kEach<OutT> * p.rank * 2;
+    const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(&k_expand_large<OutT>),
+                                             hipFuncAttributeMaxDynamicSharedMemorySize, 160 * 1024);
+    if (e != hipSuccess) return e;
+    hipLaunchKernelGGL((k_expand_large<OutT>), grid, block, bytes, stream, p);
     return hipGetLastError();
 }
 
 }  // namespace
 
 int64_t lora_workspace(const LoraArgs& a) {
-    return a.rows == 0 ? 0 : (int64_t)plan_of(a).splits * a.rows * a.slices * a.rank * 4;
+    if (a.rows == 0) return 0;
+    const Plan p = plan_of(a);
+    return tile_bytes(p) + count_bytes(p) + (int64_t)p.splits * a.rows * a.slices * a.rank * 4;
 }
 
-// Blocks of the larger launch: 2^32 threads and more are not launched.
+// Blocks of the largest launch: 2^32 threads and more are not launched.
 int64_t lora_blocks(const LoraArgs& a) {
     const Plan plan = plan_of(a);
-    return std::max(plan.shrink_blocks, (int64_t)plan.slots * ((a.columns + kWaves * kChunk - 1) / (kWaves * kChunk) + 4));
+    return std::max(plan.shrink_blocks, (int64_t)plan.slots * (a.columns / 64 + a.slices));
 }
 
 hipError_t launch_lora(const LoraArgs& a) {
@@ -497,13 +918,18 @@ hipError_t launch_lora(const LoraArgs& a) {
         end += i < a.slices ? a.columns_of[i] : 0;
         p.ends[i] = end;
     }
-    p.splits = plan.splits; p.split_steps = plan.split_steps; p.groups = plan.groups;
-    p.part = reinterpret_cast<float*>(a.workspace);
-    hipError_t e = plan.gathered ? run_shrink<1>(p, plan, a.stream) : run_shrink<4>(p, plan, a.stream);
+    p.slots = plan.slots; p.splits = plan.splits; p.split_steps = plan.split_steps; p.groups = plan.groups;
+    p.tiles = reinterpret_cast<int2*>(a.workspace);
+    p.counts = reinterpret_cast<int*>(a.workspace + tile_bytes(plan));
+    p.part = reinterpret_cast<float*>(a.workspace + tile_bytes(plan) + count_bytes(plan));
+    if (!plan.small) {
+        hipLaunchKernelGGL(k_sort_rows, dim3(1), dim3(kSortThreads), 0, a.stream, p);
+        const hipError_t e = hipGetLastError();
+        if (e != hipSuccess) return e;
+    }
+    const hipError_t e = run_shrink(p, plan, a.stream);
     if (e != hipSuccess) return e;
-    if (plan.gathered)
-        return a.out_bf16 ? run_expand<1, uint16_t>(p, plan, a.stream) : run_expand<1, float>(p, plan, a.stream);
-    return a.out_bf16 ? run_expand<4, uint16_t>(p, plan, a.stream) : run_expand<4, float>(p, plan, a.stream);
+    return a.out_bf16 ? run_expand<uint16_t>(a, p, plan, a.stream) : run_expand<float>(a, p, plan, a.stream);
 }
 
 }  // namespace fp8mi
