@@ -73,6 +73,13 @@ __device__ __forceinline__ uint32_t pack2(float a, float b) {
 
 __device__ __forceinline__ float as_f32(uint32_t bits) { return __builtin_bit_cast(float, bits); }
 
+// One value of the cache as fp32.
+template <int ST>
+__device__ __forceinline__ float value_at(const uint8_t* p, int d) {
+    if constexpr (ST == kBf16) return as_f32((uint32_t)reinterpret_cast<const uint16_t*>(p)[d] << 16);
+    else return as_f32(decode2<ST>(p[d], false) << 16);
+}
+
 // max / sum over lanes l and l ^ 32, and over l and l ^ 16 (register moves)
 __device__ __forceinline__ float max_xor32(float v) {
     const uint32_t u = __builtin_bit_cast(uint32_t, v);

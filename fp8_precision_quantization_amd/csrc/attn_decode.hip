@@ -52,7 +52,7 @@ constexpr int kMaxScored = 64;  // query heads of a KV head up to which scores a
 
 template <int KST, int VST, int DP, int NT>
 __global__ __launch_bounds__(64 * kWaves, DP <= 128 && NT == 1 ? 2 : 1) void k_decode(const DecodeParams a) {
-    decode_share<KST, VST, DP, NT, false>(a, (int)blockIdx.x);
+    decode_share<KST, VST, DP, NT, kWhole>(a, (int)blockIdx.x, [](int) { return 0; });
 }
 
 constexpr int kJoinThreads = 256;
@@ -87,8 +87,8 @@ __global__ __launch_bounds__(kJoinThreads) void k_decode_join(const DecodeParams
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), b = blockIdx.y;
     const int W = a.join_waves, part_of = wave % W;
     const int hq = blockIdx.x * (kJoinWaves / W) + wave / W;
-    const Work w = work_of<false>(a, 0, b, lane);
-    const int i0 = w.before / w.chunk, n = (w.before + steps_of<false>(a, w.len) - 1) / w.chunk - i0 + 1;
+    const Work w = work_of<kWhole>(a, 0, b, lane);
+    const int i0 = w.before / w.chunk, n = (w.before + steps_of<kWhole>(a, w.len) - 1) / w.chunk - i0 + 1;
     if (n <= 1 || hq >= a.q_heads) return;              // the same for all W waves
     const int D = a.kv.head_dim, quads = D >> 2;
     const int64_t part = (int64_t)(i0 + b) * a.q_heads + hq, next = a.q_heads;

@@ -26,7 +26,8 @@ struct DecodeParams {
     int q_heads, group, col_tiles;
     float scale_log2;
     int window, sinks;
-    int from;                    // the first token (a multiple of 64; those before it are another kernel's)
+    int from;                    // kTail: the first token, a multiple of 64; kPrefix: the prefix's length
+    int columns, pieces;         // kPrefix: query heads of a KV head over the whole batch, pieces of a row
     int shares, least;           // waves that share the batch's steps, per KV head and column tile
     uint16_t* out;
     int64_t ldo;
@@ -51,15 +52,21 @@ struct Work {
     int b = 0, len = 0, before = 0;      // a sequence, its tokens and the steps before it
 };
 
-// The steps of a sequence's newest token: all it sees, or with kTail those from a.from on.
-template <bool kTail>
+// What a launch's waves read: every sequence (kWhole), of every sequence the
+// tokens from a.from on (kTail), or the first a.from tokens of the first row's
+// pages for the queries of all sequences at once (kPrefix).
+enum Part { kWhole, kTail, kPrefix };
+
+// The steps of a sequence's newest token.
+template <Part kPart>
 __device__ __forceinline__ Steps<kStep> steps_at(const DecodeParams& a, int pos) {
-    return Steps<kStep>(pos, pos, kTail ? 0 : a.window, kTail ? 0 : a.sinks, kTail ? a.from : 0);
+    constexpr bool all = kPart == kWhole;
+    return Steps<kStep>(pos, pos, all ? a.window : 0, all ? a.sinks : 0, kPart == kTail ? a.from : 0);
 }
 
-template <bool kTail>
+template <Part kPart>
 __device__ __forceinline__ int steps_of(const DecodeParams& a, int len) {
-    const int n = steps_at<kTail>(a, len - 1).count;
+    const int n = steps_at<kPart>(a, len - 1).count;
     return n < 1 ? 1 : n;
 }
 
@@ -75,14 +82,14 @@ __device__ __forceinline__ int wave_scan(int v, int lane) {
 // The total and the chunk, then the sequence that step `at` of the whole (or,
 // with seq >= 0, the sequence `seq`) lies in.  Every wave computes it for
 // itself, 64 sequences at a time.
-template <bool kTail>
+template <Part kPart>
 __device__ __forceinline__ Work work_of(const DecodeParams& a, int share, int seq, int lane) {
     Work w;
     const int B = a.kv.batch;
     int sum = 0, mine = 0, len = 0;      // of the last 64 sequences looked at
     auto look = [&](int b0) {
         len = b0 + lane < B ? seq_len(a.kv, b0 + lane) : 0;
-        mine = b0 + lane < B ? steps_of<kTail>(a, len) : 0;
+        mine = b0 + lane < B ? steps_of<kPart>(a, len) : 0;
         sum = wave_scan(mine, lane);
     };
     for (int b0 = 0; b0 < B; b0 += 64) {
@@ -107,6 +114,14 @@ __device__ __forceinline__ Work work_of(const DecodeParams& a, int share, int se
         w.before += __builtin_amdgcn_readlane(sum, 63);
     }
     return w;
+}
+
+template <int N>
+__device__ __forceinline__ int min_of(const int (&v)[N]) {
+    int r = v[0];
+#pragma unroll
+    for (int i = 1; i < N; ++i) r = min(r, v[i]);
+    return r;
 }
 
 // VD values of one token (one lane's channels) as raw words
@@ -145,9 +160,10 @@ struct Loads {
 };
 
 // One worker's (a wave's) share of the steps, for its KV head and columns.
-// kTail: tokens from a.from on, every piece into the partial results.
-template <int KST, int VST, int DP, int NT, bool kTail>
-__device__ __forceinline__ void decode_share(const DecodeParams& a, int block) {
+// kTail and kPrefix: every piece into the partial results.  pos_of(token), kPrefix:
+// a query's position, which masks where its sequence ends inside the prefix.
+template <int KST, int VST, int DP, int NT, Part kPart, class PosOf>
+__device__ __forceinline__ void decode_share(const DecodeParams& a, int block, PosOf&& pos_of) {
     constexpr int VD = DP / 16;                         // channels of V a lane holds
     constexpr int KC = DP * kElemBytes<KST> / 64;       // 16-byte pieces of K a lane holds per token
     constexpr int KM = DP / 32;                         // matrix steps over the channels
@@ -167,26 +183,43 @@ __device__ __forceinline__ void decode_share(const DecodeParams& a, int block) {
     const int hc = worker % units, share = (worker / units) * 8 + (block & 7);
     if (share >= a.shares) return;
     const int h = hc % kv.heads, ct = hc / kv.heads;
-    const Work work = work_of<kTail>(a, share, -1, lane);
+    Work work;
+    if constexpr (kPart == kPrefix) {
+        work.total = a.from / kStep;
+        work.chunk = (work.total + a.shares - 1) / a.shares;
+        work.len = a.from;
+    } else {
+        work = work_of<kPart>(a, share, -1, lane);
+    }
     const int share_end = min(work.total, (share + 1) * work.chunk);
     for (int at = share * work.chunk, b = work.b, len = work.len, before = work.before; at < share_end;) {
     const int pos = len - 1;
-    const Steps<kStep> steps = steps_at<kTail>(a, pos);
+    const Steps<kStep> steps = steps_at<kPart>(a, pos);
     const int seq_steps = steps.count < 1 ? 1 : steps.count;
     const int s_begin = at - before, s_end = min(steps.count, share_end - before);
 
     const int D = kv.head_dim;
     const int head0 = ct * 16 * NT;                     // first query head of this block within the group
+    // (kPrefix: the columns are (query, head in the group))
+    const int columns = kPart == kPrefix ? a.columns : a.group;
     b8 qf[NT][KM];
+    int ends[NT];                                       // kPrefix: the last token a column sees
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
         const int hq = head0 + nt * 16 + c;
-        const uint16_t* qr = a.q + b * a.ldq + (int64_t)(h * a.group + hq) * D;
+        const uint16_t* qr;
+        if constexpr (kPart == kPrefix) {
+            const int col = min(hq, columns - 1), token = col / a.group;
+            qr = a.q + token * a.ldq + (int64_t)(h * a.group + col - token * a.group) * D;
+            ends[nt] = pos_of(token);
+        } else {
+            qr = a.q + b * a.ldq + (int64_t)(h * a.group + hq) * D;
+        }
 #pragma unroll
         for (int s = 0; s < KM; ++s) {
             const int e = KST == kBf16 ? s * 32 + g * 8 : (s >> 1) * 64 + g * 16 + (s & 1) * 8;
             uint4 t = make_uint4(0, 0, 0, 0);
-            if (hq < a.group && e < D) t = *reinterpret_cast<const uint4*>(qr + e);
+            if (hq < columns && e < D) t = *reinterpret_cast<const uint4*>(qr + e);
             qf[nt][s] = __builtin_bit_cast(b8, t);
         }
     }
@@ -218,7 +251,7 @@ __device__ __forceinline__ void decode_share(const DecodeParams& a, int block) {
     };
     auto row_of = [&](int st, int entry) -> int {
         const int j = steps.token(st) + half;
-        return st < s_end && sees(j, pos, kTail ? 0 : a.window, kTail ? 0 : a.sinks) ? row_of_entry(kv, entry, j) : -1;
+        return st < s_end && sees(j, pos, kPart == kWhole ? a.window : 0, kPart == kWhole ? a.sinks : 0) ? row_of_entry(kv, entry, j) : -1;
     };
     // A step's loads.  None of them is conditional, so a wait for one step's
     // does not wait for the next one's: a token that is not seen reads row 0.
@@ -263,7 +296,7 @@ __device__ __forceinline__ void decode_share(const DecodeParams& a, int block) {
         entry = entry_of(st + 2);
         if (kAhead) load(next, row);
         if (cur.there == 0) {
-            if (!kTail && a.scores && lane < kStep)
+            if (kPart == kWhole && a.scores && lane < kStep)
                 for (int col = head0; col < min(head0 + 16 * NT, a.group); ++col)
                     a.scores[((int64_t)b * a.q_heads + h * a.group + col) * a.span + st * kStep + lane] = -INFINITY;
             if (!kAhead) load(next, row);
@@ -322,7 +355,34 @@ __device__ __forceinline__ void decode_share(const DecodeParams& a, int block) {
                 for (int w = 0; w < VW; ++w) cur.v[i].w[w] = hidden ? 0 : cur.v[i].w[w];
             }
         }
-        if (!kTail && a.scores) {
+        // kPrefix: where a column's sequence ends before this step does, tokens that
+        // it does not see and others do; what these hold that is not finite
+        // must not meet its weights of 0, and is added apart.
+        bool cut = false;
+        uint32_t odd_tokens = 0;            // of this lane's 8
+        if constexpr (kPart == kPrefix) {
+            const int first = steps.token(st);
+            cut = __any(min_of(ends) < first + kStep - 1);
+            if (cut) {
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                    for (int i = 0; i < 8; ++i)
+                        x[nt][i] = first + (i >> 2) * 16 + 4 * g + (i & 3) <= ends[nt] ? x[nt][i] : -INFINITY;
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    uint32_t any = 0;
+#pragma unroll
+                    for (int w = 0; w < VW; ++w) {
+                        const uint32_t t = not_finite<VST>(cur.v[i].w[w]);
+                        any |= t;
+                        cur.v[i].w[w] = cleared<VST>(cur.v[i].w[w], t);
+                    }
+                    odd_tokens |= (any ? 1u : 0u) << i;
+                }
+            }
+        }
+        if (kPart == kWhole && a.scores) {
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) {
                 const int col = head0 + nt * 16 + c;
@@ -353,6 +413,7 @@ __device__ __forceinline__ void decode_share(const DecodeParams& a, int block) {
             for (int i = 0; i < 4; ++i) { vs[i] = v0[i]; vs[4 + i] = v1[i]; }
         }
         b8 ph[NT], pl[NT];
+        float weight[NT][8];                // kPrefix
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
             float mx = x[nt][0];
@@ -372,6 +433,10 @@ __device__ __forceinline__ void decode_share(const DecodeParams& a, int block) {
                 p[i] = __builtin_amdgcn_exp2f(x[nt][i] - m[nt]);
                 l[nt] += p[i];
                 p[i] *= vs[i];      // a scale that is not seen is 0
+                if constexpr (kPart == kPrefix) {
+                    if (cut && x[nt][i] == -INFINITY) p[i] = 0.0f;
+                    weight[nt][i] = p[i];
+                }
             }
             u4 hi, lo;
 #pragma unroll
@@ -454,18 +519,52 @@ __device__ __forceinline__ void decode_share(const DecodeParams& a, int block) {
                 o[nt][d] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(vf, pl[nt], o[nt][d], 0, 0, 0);
             }
         });
+        if constexpr (kPart == kPrefix) {
+            if (cut && __any(odd_tokens != 0)) [[unlikely]] {
+                for (int i = 0; i < 8; ++i) {
+                    const uint64_t lanes = __ballot(odd_tokens >> i & 1);
+                    for (int gt = 0; gt < 4; ++gt) {
+                        if (!(lanes >> (16 * gt) & 0xFFFF)) continue;
+                        const int j = steps.token(st) + (i >> 2) * 16 + 4 * gt + (i & 3);
+                        const int row = row_of_entry(kv, table[j >> kv.page_shift], j);
+                        const uint8_t* vr = static_cast<const uint8_t*>(kv.v) +
+                                            (max(row, 0) * v_row + (int64_t)h * D * kElemBytes<VST>);
+#pragma unroll
+                        for (int nt = 0; nt < NT; ++nt) {
+                            float mine = 0.0f;
+#pragma unroll
+                            for (int k = 0; k < 8; ++k) mine = k == i ? weight[nt][k] : mine;
+                            const float w = __shfl(mine, c + 16 * gt, 64);
+                            if (row < 0 || j > ends[nt]) continue;
+#pragma unroll
+                            for (int k = 0; k < 4; ++k)
+#pragma unroll
+                                for (int d = 0; d < VD; ++d) {
+                                    const int ch = VD * (4 * g + k) + d;
+                                    const float v = ch < D ? value_at<VST>(vr, ch) : 0.0f;
+                                    if (!__builtin_isfinite(v)) o[nt][d][k] += w * v;
+                                }
+                        }
+                    }
+                }
+            }
+        }
         if (!kAhead) load(next, row);
     }
     }
 
-    const bool alone = !kTail && s_begin == 0 && share_end - before >= seq_steps;      // the sequence's only piece
+    const bool alone = kPart == kWhole && s_begin == 0 && share_end - before >= seq_steps;      // the sequence's only piece
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
         const int col = head0 + nt * 16 + c, hq = h * a.group + col;
         const float sum = sum_xor16(sum_xor32(l[nt]));
-        if (col >= a.group) continue;
+        if (col >= columns) continue;
         const float f = !alone ? 1.0f : sum == 0.0f ? 0.0f : 1.0f / sum;
-        const int64_t part = (int64_t)(share + b) * a.q_heads + hq;
+        int64_t part = (int64_t)(share + b) * a.q_heads + hq;
+        if constexpr (kPart == kPrefix) {
+            const int token = col / a.group;
+            part = ((int64_t)token * a.q_heads + h * a.group + col - token * a.group) * a.pieces + share;
+        }
         if (g == 0) {
             if (!alone) a.part_ml[part] = make_float2(m[nt], sum);
             else if (a.lse)
@@ -489,7 +588,7 @@ __device__ __forceinline__ void decode_share(const DecodeParams& a, int block) {
     }
     before += seq_steps;
     at = before;
-    if (at < share_end) len = seq_len(kv, ++b);
+    if (kPart != kPrefix && at < share_end) len = seq_len(kv, ++b);
     }
 }
 

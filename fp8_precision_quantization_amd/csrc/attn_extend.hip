@@ -87,7 +87,7 @@ __global__ __launch_bounds__(kThreads, DP <= 128 ? 2 : 1) void k_extend(const Ex
     at.table = kv.table + tile.b * kv.table_ld;
     at.partial = chunk < steps.count;
     at.part = split;
-    extend_rows<KST, VST, DP>(a, *reinterpret_cast<Lds<DP>*>(smem), h, steps, at);
+    extend_rows<KST, VST, DP, false>(a, *reinterpret_cast<Lds<DP>*>(smem), h, steps, at);
 }
 
 // Joins the blocks of a row tile in their order; threads take 4 channels of a

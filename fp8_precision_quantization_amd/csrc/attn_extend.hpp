@@ -127,13 +127,6 @@ struct Lds {
     uint32_t bad[kMarks / 32];      // step i marks bit i % kMarks
 };
 
-// One value of the cache as fp32.
-template <int ST>
-__device__ __forceinline__ float value_at(const uint8_t* p, int d) {
-    if constexpr (ST == kBf16) return as_f32((uint32_t)reinterpret_cast<const uint16_t*>(p)[d] << 16);
-    else return as_f32(decode2<ST>(p[d], false) << 16);
-}
-
 // 16 values of a cache row: 16 bytes of codes or 32 of bf16
 template <int ST>
 struct Unit {
@@ -198,7 +191,7 @@ __device__ __forceinline__ s4 read_tr(const uint8_t* p) {
 struct Rows {
     bool live;
     int token, head, pos;
-    int p_first, p_last;            // of the block: lowest position, last token that any row sees
+    int p_first, p_last;            // of the block: lowest position (-1: to be found), last token that any row sees
     const int32_t* table;
     int s_begin, s_end;             // this block's steps
     bool partial;                   // one of several blocks of these rows: the results are joined
@@ -206,7 +199,7 @@ struct Rows {
 };
 
 // One block's rows of one KV head over its steps of the cached tokens.
-template <int KST, int VST, int DP>
+template <int KST, int VST, int DP, bool kFind>
 __device__ __forceinline__ void extend_rows(const ExtendParams& a, Lds<DP>& lds, int h, const Steps<kStep>& steps,
                                             const Rows& at) {
     constexpr int KM = DP / 16;                     // matrix steps over the channels of K
@@ -218,7 +211,8 @@ __device__ __forceinline__ void extend_rows(const ExtendParams& a, Lds<DP>& lds,
     const KvView& kv = a.kv;
     const int tid = threadIdx.x, lane = tid & 63;
     const int g = lane >> 5, c = lane & 31;
-    const int p_first = at.p_first, p_last = at.p_last, s_begin = at.s_begin, s_end = at.s_end;
+    int p_first = at.p_first;
+    const int p_last = at.p_last, s_begin = at.s_begin, s_end = at.s_end;
     const int D = kv.head_dim, hq = at.head, pos = at.pos;
     const bool live = at.live;
     const int32_t* const table = at.table;
@@ -322,6 +316,11 @@ __device__ __forceinline__ void extend_rows(const ExtendParams& a, Lds<DP>& lds,
 #pragma unroll
         for (int s = 0; s < KM; ++s) asm volatile("" : "+v"(qf[s]));
         __syncthreads();
+    }
+    if (kFind && p_first < 0) {         // of the wave's rows, whose positions have been on their way until here
+        p_first = live ? min(pos, p_last) : p_last;
+#pragma unroll
+        for (int off = 1; off < 32; off <<= 1) p_first = min(p_first, __shfl_xor(p_first, off, 64));
     }
     for (int i = s_begin; i < s_end; ++i) {
         const typename L::Buf& buf = lds.buf[i & 1];

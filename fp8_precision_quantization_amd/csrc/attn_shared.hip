@@ -19,6 +19,7 @@
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
+#include <cstdlib>
 
 #include "attn_decode.hpp"
 #include "attn_extend.hpp"
@@ -31,8 +32,10 @@ using namespace attn;
 struct SharedParams {
     extend::ExtendParams e;      // splits: pieces of a row, the prefix's first; least: fewest steps of a tail's piece
     decode::DecodeParams d;      // the tails where every sequence has one new token
+    decode::DecodeParams few;    // the prefix where the queries are few
     int from;                    // tokens of the prefix, a multiple of extend::kStep
     int blocks;                  // of the prefix
+    bool is_few;                 // the prefix is read by k_shared_few
     int splits, chunk;           // of the prefix: pieces, their steps
     int tail_splits;             // of a tail's row tile
     int tail_tiles;
@@ -66,7 +69,7 @@ __global__ __launch_bounds__(extend::kThreads, DP <= 128 ? 2 : 1) void k_shared(
     const KvView& kv = a.kv;
     const bool prefix = (int)blockIdx.x < p.blocks;
     if (kOne && !prefix) {
-        decode::decode_share<KST, VST, DP, 1, true>(p.d, (int)blockIdx.x - p.blocks);
+        decode::decode_share<KST, VST, DP, 1, decode::kTail>(p.d, (int)blockIdx.x - p.blocks, [](int) { return 0; });
         return;
     }
     int block = (int)blockIdx.x - (prefix ? 0 : p.blocks);
@@ -83,11 +86,7 @@ __global__ __launch_bounds__(extend::kThreads, DP <= 128 ? 2 : 1) void k_shared(
         at.token = token;
         at.head = h * a.group + (r - token * a.group);
         at.pos = at.live ? place.pos : -1;
-        // the lowest position of the wave's rows: below the prefix's end they are masked
-        int lowest = at.live ? min(at.pos, p.from - 1) : p.from - 1;
-#pragma unroll
-        for (int off = 1; off < 32; off <<= 1) lowest = min(lowest, __shfl_xor(lowest, off, 64));
-        at.p_first = lowest;
+        at.p_first = -1;            // a sequence may end inside the prefix
         at.p_last = p.from - 1;
         at.table = kv.table;
         steps = Steps<extend::kStep>(p.from - 1, p.from - 1, 0, 0);
@@ -108,96 +107,121 @@ __global__ __launch_bounds__(extend::kThreads, DP <= 128 ? 2 : 1) void k_shared(
         at.token = tile.q_first + tok;
         at.head = h * a.group + (r - tok * a.group);
         at.pos = at.live ? tile.base + tok : -1;
-        at.p_first = tile.p_first;
+        at.p_first = max(tile.p_first, 0);
         at.p_last = tile.p_last;
         at.table = kv.table + tile.b * kv.table_ld;
         at.part = p.splits + split;
     }
-    extend::extend_rows<KST, VST, DP>(a, *reinterpret_cast<extend::Lds<DP>*>(smem), h, steps, at);
+    extend::extend_rows<KST, VST, DP, true>(a, *reinterpret_cast<extend::Lds<DP>*>(smem), h, steps, at);
+}
+
+// Few queries, one new token a sequence: waves read the prefix as they read the
+// tails, its columns being the query heads of all sequences, 16 a wave.
+template <int KST, int VST, int DP>
+__global__ __launch_bounds__(64 * decode::kWaves, DP <= 128 ? 2 : 1) void k_shared_few(const SharedParams p) {
+    const int block = (int)blockIdx.x - p.blocks;
+    if (block < 0)
+        decode::decode_share<KST, VST, DP, 1, decode::kPrefix>(
+            p.few, (int)blockIdx.x, [&](int token) { return seq_len(p.few.kv, token) - 1; });
+    else
+        decode::decode_share<KST, VST, DP, 1, decode::kTail>(p.d, block, [](int) { return 0; });
 }
 
 constexpr int kJoinThreads = 256;
 constexpr int kJoinWaves = kJoinThreads / 64;
 
-// Joins the pieces of a row.  A row takes W waves of a block, a thread 4
-// channels, and what a wave has lanes for goes on to further pieces side by side.
-// piece(i): (m, l) of piece i; values(i): its 4 channels of this thread.
-template <class Ml, class O>
-__device__ __forceinline__ f4 joined(int n, int W, int part_of, int side, int sides, bool on, Ml&& piece, O&& values,
-                                     float2* all) {
-    const int lane = threadIdx.x & 63;
-    float m = kLowest, l = 0.0f;
-    for (int i = lane; i < n; i += 64) m = fmaxf(m, piece(i).x);
-#pragma unroll
-    for (int off = 1; off < 64; off <<= 1) m = fmaxf(m, __shfl_xor(m, off, 64));
-    for (int i = lane; i < n; i += 64) {
-        const float2 ml = piece(i);
-        l += ml.y * __builtin_amdgcn_exp2f(ml.x - m);
-    }
-#pragma unroll
-    for (int off = 1; off < 64; off <<= 1) l += __shfl_xor(l, off, 64);
-    *all = make_float2(m, l);
-    f4 acc = {0, 0, 0, 0};
-    if (on)
-#pragma unroll 4
-        for (int i = part_of * sides + side; i < n; i += W * sides)
-            acc += values(i) * __builtin_amdgcn_exp2f(piece(i).x - m);
-    return acc;
-}
-
+// Joins the pieces of a row, the prefix's first, in their order.  A row takes W
+// waves of a block, a thread 4 channels, and what a wave has lanes for goes on to
+// further pieces side by side.  The prefix's first pieces are on their way while
+// the tail's are looked up.
 template <bool kOne>
 __global__ __launch_bounds__(kJoinThreads) void k_shared_join(const SharedParams p, int W) {
+    constexpr int kFirst = 8;
     __shared__ f4 s_acc[kJoinThreads];
     const extend::ExtendParams& a = p.e;
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const int64_t row = (int64_t)blockIdx.x * (kJoinWaves / W) + wave / W;   // (token, query head)
+    const int rows = a.total_q * a.q_heads, mine = (int)blockIdx.x * (kJoinWaves / W) + wave / W;
+    const int row = min(mine, rows - 1);                // (token, query head)
     const int part_of = wave % W;
     const int D = a.kv.head_dim, quads = D >> 2, sides = 64 / quads, side = lane / quads, d = (lane - side * quads) * 4;
-    const int token = (int)(row / a.q_heads), hq = (int)(row - (int64_t)token * a.q_heads), h = hq / a.group;
-    // the tail's pieces
-    bool there = row < (int64_t)a.total_q * a.q_heads;
-    int n = 0;
-    int64_t tail = 0;
-    if (there) {
-        if constexpr (kOne) {
-            const decode::Work w = decode::work_of<true>(p.d, 0, token, lane);
-            const int i0 = w.before / w.chunk;
-            n = (w.before + decode::steps_of<true>(p.d, w.len) - 1) / w.chunk - i0 + 1;
-            tail = (int64_t)(i0 + token) * a.q_heads + hq;
-        } else {
-            const Place place(a, token);
-            there = place.in;
-            if (there) {
-                // the row tile that this row is in: its last position bounds the steps
-                const int r0 = (place.i * a.group + hq - h * a.group) / extend::kRows * extend::kRows;
-                const int last = place.pos - place.i + (min(r0 + extend::kRows, place.n * a.group) - 1) / a.group;
-                const int steps = Steps<extend::kStep>(last, last, 0, 0, p.from).count;
-                const int even = (steps + p.tail_splits - 1) / p.tail_splits, chunk = max(even, a.least);
-                n = (steps + chunk - 1) / chunk;
-            }
-        }
+    const int token = row / a.q_heads, hq = row - token * a.q_heads, h = hq / a.group;
+    const int at = part_of * sides + side, apart = W * sides;
+    const float2* const pre_ml = a.part_ml + (int64_t)row * a.splits;
+    const float* const pre_o = a.part_o + (int64_t)row * a.splits * D + d;
+    const bool on = side < sides;
+    f4 o[kFirst];
+    float o_m[kFirst];
+#pragma unroll
+    for (int i = 0; i < kFirst; ++i) {
+        const int piece = min(at + i * apart, p.splits - 1);
+        o[i] = *reinterpret_cast<const f4*>(pre_o + (int64_t)piece * D);
+        o_m[i] = pre_ml[piece].x;
     }
-    const float by_head = extend::v_scale_of(a.kv, h);
-    const int pieces = there ? p.splits + n : 0;
-    auto piece = [&](int i) {
-        if (kOne && i >= p.splits) return p.d.part_ml[tail + (int64_t)(i - p.splits) * a.q_heads];
-        return a.part_ml[row * a.splits + i];
-    };
-    auto values = [&](int i) {
-        if (kOne && i >= p.splits)
-            return *reinterpret_cast<const f4*>(p.d.part_o + (tail + (int64_t)(i - p.splits) * a.q_heads) * D + d);
-        return *reinterpret_cast<const f4*>(a.part_o + (row * a.splits + i) * D + d) * by_head;
-    };
-    float2 all;
-    f4 acc = joined(pieces, W, part_of, side, sides, side < sides, piece, values, &all);
+    const float2 ml = pre_ml[min(lane, p.splits - 1)];
+    // (a wave's V scale of the head is in its weights already)
+    const float by_head = p.is_few ? 1.0f : extend::v_scale_of(a.kv, h);
+
+    // the tail's pieces: where they are, how far apart, how many
+    bool there = mine < rows;
+    int n = 0;
+    const float2* tail_ml = nullptr;
+    const float* tail_o = nullptr;
+    int64_t next = 1;
+    float tail_head = 1.0f;
+    if constexpr (kOne) {
+        const decode::Work w = decode::work_of<decode::kTail>(p.d, 0, token, lane);
+        const int i0 = w.before / w.chunk;
+        n = (w.before + decode::steps_of<decode::kTail>(p.d, w.len) - 1) / w.chunk - i0 + 1;
+        const int64_t first = (int64_t)(i0 + token) * a.q_heads + hq;
+        tail_ml = p.d.part_ml + first;
+        tail_o = p.d.part_o + first * D + d;
+        next = a.q_heads;
+    } else {
+        const Place place(a, token);
+        there = there && place.in;
+        if (place.in) {
+            // the row tile that this row is in: its last position bounds the steps
+            const int r0 = (place.i * a.group + hq - h * a.group) / extend::kRows * extend::kRows;
+            const int last = place.pos - place.i + (min(r0 + extend::kRows, place.n * a.group) - 1) / a.group;
+            const int steps = Steps<extend::kStep>(last, last, 0, 0, p.from).count;
+            const int even = (steps + p.tail_splits - 1) / p.tail_splits, chunk = max(even, a.least);
+            n = (steps + chunk - 1) / chunk;
+        }
+        tail_ml = pre_ml + p.splits;
+        tail_o = pre_o + (int64_t)p.splits * D;
+        tail_head = by_head;
+    }
+    float m = ml.x;
+    for (int i = lane + 64; i < p.splits; i += 64) m = fmaxf(m, pre_ml[i].x);
+    for (int i = lane; i < n; i += 64) m = fmaxf(m, tail_ml[i * next].x);
+#pragma unroll
+    for (int off = 1; off < 64; off <<= 1) m = fmaxf(m, __shfl_xor(m, off, 64));
+    float l = lane < p.splits ? ml.y * __builtin_amdgcn_exp2f(ml.x - m) : 0.0f;
+    for (int i = lane + 64; i < p.splits; i += 64) l += pre_ml[i].y * __builtin_amdgcn_exp2f(pre_ml[i].x - m);
+    for (int i = lane; i < n; i += 64) l += tail_ml[i * next].y * __builtin_amdgcn_exp2f(tail_ml[i * next].x - m);
+#pragma unroll
+    for (int off = 1; off < 64; off <<= 1) l += __shfl_xor(l, off, 64);
+
+    f4 acc = {0, 0, 0, 0};
+#pragma unroll
+    for (int i = 0; i < kFirst; ++i)
+        if (at + i * apart < p.splits) acc += o[i] * __builtin_amdgcn_exp2f(o_m[i] - m);
+#pragma unroll 4
+    for (int i = at + kFirst * apart; i < p.splits; i += apart)
+        acc += *reinterpret_cast<const f4*>(pre_o + (int64_t)i * D) * __builtin_amdgcn_exp2f(pre_ml[i].x - m);
+    acc *= by_head;
+#pragma unroll 2
+    for (int i = at; i < n; i += apart)
+        acc += *reinterpret_cast<const f4*>(tail_o + i * next * D) *
+               (tail_head * __builtin_amdgcn_exp2f(tail_ml[i * next].x - m));
     s_acc[threadIdx.x] = acc;
     if (W == 1) wave_sync();
     else __syncthreads();
-    if (side != 0 || part_of != 0 || !there) return;
-    const f4* mine = s_acc + (threadIdx.x - lane);
+    if (!on || side != 0 || part_of != 0 || !there) return;
+    const f4* const others = s_acc + (threadIdx.x - lane);
     for (int v = 0; v < W; ++v)
-        for (int s = v == 0 ? 1 : 0; s < sides; ++s) acc += mine[v * 64 + s * quads + lane];
-    const float m = all.x, l = all.y, r = l == 0.0f ? 0.0f : 1.0f / l;
+        for (int s = v == 0 ? 1 : 0; s < sides; ++s) acc += others[v * 64 + s * quads + lane];
+    const float r = l == 0.0f ? 0.0f : 1.0f / l;
     *reinterpret_cast<uint2*>(a.out + (int64_t)token * a.ldo + (int64_t)hq * D + d) =
         make_uint2(pack2(acc[0] * r, acc[1] * r), pack2(acc[2] * r, acc[3] * r));
     if (d == 0 && a.lse) a.lse[row] = l == 0.0f ? -INFINITY : (m + __builtin_amdgcn_logf(l)) * kLn2;
@@ -205,7 +229,7 @@ __global__ __launch_bounds__(kJoinThreads) void k_shared_join(const SharedParams
 
 // How a call is shared out.
 struct Plan {
-    bool one;
+    bool one, few;
     int64_t prefix_blocks, tail_blocks;
     int splits, chunk;               // of the prefix
     int tail_splits, least, tail_tiles;
@@ -221,15 +245,23 @@ Plan plan_of(const AttnArgs& a, bool ragged) {
     p.one = !ragged && a.total_q == a.kv.batch;
     const int64_t tiles = (rows + extend::kRows - 1) / extend::kRows;
     const int64_t steps = a.from / extend::kStep, tail = std::max<int64_t>(a.kv.max_len - a.from, 0);
-    const int64_t want = 256;
-    int64_t s = std::clamp<int64_t>(want / (tiles * heads), 1, std::min<int64_t>(32, std::max<int64_t>(steps / 2, 1)));
+    const int64_t want = getenv("X_WANT") ? atoi(getenv("X_WANT")) : 256; const int64_t tw = getenv("X_TAIL") ? atoi(getenv("X_TAIL")) : 1024;
+    int64_t s = std::clamp<int64_t>(want / (tiles * heads), 1, std::min<int64_t>(64, std::max<int64_t>(steps / 2, 1)));
     p.chunk = (int)((steps + s - 1) / s);
     p.splits = (int)((steps + p.chunk - 1) / p.chunk);
     p.prefix_blocks = tiles * heads * p.splits;
+    p.few = p.one && rows <= (getenv("X_FEW") ? atoi(getenv("X_FEW")) : 32);
+    if (p.few) {
+        const int64_t units = heads * ((rows + 15) / 16), all = a.from / decode::kStep;
+        s = std::clamp<int64_t>((getenv("X_FW") ? atoi(getenv("X_FW")) : 1024) / units, 1, std::max<int64_t>(all / 4, 1));
+        p.chunk = (int)((all + s - 1) / s);
+        p.splits = (int)((all + p.chunk - 1) / p.chunk);
+        p.prefix_blocks = ((p.splits + 7) / 8 * units + decode::kWaves - 1) / decode::kWaves * 8;
+    }
     if (p.one) {
         const int64_t units = heads * ((group + 15) / 16);
         const int64_t most = std::max<int64_t>((tail + decode::kStep - 1) / decode::kStep, 1) * a.kv.batch;
-        p.shares = (int)std::max<int64_t>(std::min<int64_t>((1024 + units - 1) / units, most), 1);
+        p.shares = (int)std::max<int64_t>(std::min<int64_t>((tw + units - 1) / units, most), 1);
         p.tail_blocks = ((p.shares + 7) / 8 * units + decode::kWaves - 1) / decode::kWaves * 8;
         const int64_t pieces = (int64_t)(p.shares + a.kv.batch) * a.q_heads;
         p.tail_ml = up16(pieces * 8);
@@ -261,11 +293,23 @@ hipError_t run(const SharedParams& p, const Plan& plan, hipStream_t stream) {
     return hipGetLastError();
 }
 
+template <int KST, int VST, int DP>
+hipError_t run_few(const SharedParams& p, const Plan& plan, hipStream_t stream) {
+    hipLaunchKernelGGL((k_shared_few<KST, VST, DP>), dim3((unsigned)(plan.prefix_blocks + plan.tail_blocks)),
+                       dim3(64 * decode::kWaves), 0, stream, p);
+    return hipGetLastError();
+}
+
 template <int KST, int VST, bool kOne>
 hipError_t run_dim(const SharedParams& p, const Plan& plan, hipStream_t stream) {
-    if (p.e.kv.head_dim <= 64) return run<KST, VST, 64, kOne>(p, plan, stream);
-    if (p.e.kv.head_dim <= 128) return run<KST, VST, 128, kOne>(p, plan, stream);
-    return run<KST, VST, 256, kOne>(p, plan, stream);
+    const int D = p.e.kv.head_dim;
+    if (kOne && plan.few)
+        return D <= 64    ? run_few<KST, VST, 64>(p, plan, stream)
+               : D <= 128 ? run_few<KST, VST, 128>(p, plan, stream)
+                          : run_few<KST, VST, 256>(p, plan, stream);
+    return D <= 64    ? run<KST, VST, 64, kOne>(p, plan, stream)
+           : D <= 128 ? run<KST, VST, 128, kOne>(p, plan, stream)
+                      : run<KST, VST, 256, kOne>(p, plan, stream);
 }
 
 template <int KST, bool kOne>
@@ -325,6 +369,15 @@ hipError_t launch_shared(const AttnArgs& a) {
         uint8_t* tail = a.workspace + plan.ml + up16(plan.o);
         p.d.part_ml = reinterpret_cast<float2*>(tail);
         p.d.part_o = reinterpret_cast<float*>(tail + plan.tail_ml);
+    }
+    if (plan.few) {
+        p.is_few = true;
+        p.few = p.d;
+        p.few.columns = (int)a.total_q * group;
+        p.few.col_tiles = (p.few.columns + 15) / 16;
+        p.few.shares = p.few.pieces = plan.splits;
+        p.few.part_ml = p.e.part_ml;
+        p.few.part_o = p.e.part_o;
     }
     const hipError_t e = plan.one ? run_k<true>(p, plan, a.stream) : run_k<false>(p, plan, a.stream);
     return e != hipSuccess || !a.weighted ? e : launch_attention_weights(a);

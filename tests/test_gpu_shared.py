@@ -81,7 +81,12 @@ def _check(cache, n, q_heads, **more):
 STORAGES = [("e4m3", "e4m3", "token_head"), ("e4m3", "e4m3", "head"), ("e5m2", "e5m2", "token_head"),
             ("e5m2", "e4m3", "head"), ("bf16", "bf16", "token_head"), ("bf16", "e4m3", "token_head"),
             ("e5m2", "bf16", "token_head"), ("e4m3", "e5m2", "token_head"), ("bf16", "e5m2", "head")]
-NEW = {"one": [1] * 5, "each": [3] * 5, "ragged": [1, 40, 7, 2, 64]}
+NEW = {"one": [1] * 5, "many": [1] * 5, "each": [3] * 5, "ragged": [1, 40, 7, 2, 64]}
+
+
+def _heads(new, q_heads):
+    """Query heads: with "many", more of one new token each than a few columns."""
+    return 8 * q_heads if new == "many" else q_heads
 
 
 @pytest.mark.parametrize("new", NEW)
@@ -90,38 +95,38 @@ NEW = {"one": [1] * 5, "each": [3] * 5, "ragged": [1, 40, 7, 2, 64]}
 def test_storages(storage, dim, new):
     k, v, scaling = storage
     c = SharedCache([140, 333, 200, 131, 192], 128, 2, dim, 16, k, v, scaling, seed=dim)
-    _check(c, NEW[new], 8)
+    _check(c, NEW[new], _heads(new, 8))
 
 
 @pytest.mark.parametrize("new", NEW)
 @pytest.mark.parametrize("dim", [16, 48, 80, 96, 112, 160, 208, 240])
 def test_odd_dims(dim, new):
     c = SharedCache([100, 150, 129, 70, 128], 64, 3, dim, 8, seed=dim)
-    _check(c, NEW[new], 6)
+    _check(c, NEW[new], _heads(new, 6))
 
 
 @pytest.mark.parametrize("new", NEW)
 @pytest.mark.parametrize("group", [1, 3, 5, 8, 16, 17, 33, 71])
 def test_groups(group, new):
     c = SharedCache([100, 150, 129, 70, 198], 64, 2, 64, 8, seed=group)
-    _check(c, NEW[new], 2 * group)
+    _check(c, NEW[new], _heads(new, 2 * group))
 
 
-@pytest.mark.parametrize("new", ["one", "ragged"])
+@pytest.mark.parametrize("new", ["one", "many", "ragged"])
 @pytest.mark.parametrize("page, prefix", [(1, 64), (1, 65), (1, 127), (2, 130), (8, 200), (32, 96), (64, 64), (64, 448),
                                           (128, 128), (256, 512), (1, 63), (16, 16), (512, 512)])
 def test_prefixes(page, prefix, new):
     """Prefixes that end inside a step of 64 leave the rest to the sequences' own tokens; so do their tables name them."""
     c = SharedCache([prefix + 70, prefix + 64, prefix + 90, prefix + 66, prefix + 70], prefix, 2, 64, page,
                     seed=prefix, keep_tables=True)
-    _check(c, NEW[new], 4)
+    _check(c, NEW[new], _heads(new, 4))
 
 
-@pytest.mark.parametrize("new", ["one", "each"])
+@pytest.mark.parametrize("new", ["one", "many", "each"])
 def test_other_rows_are_not_read(new):
     """With a prefix of whole steps, only the first row's entries of it are."""
     c = SharedCache([400, 350, 321, 500, 330], 320, 2, 128, 32, seed=5)
-    _check(c, NEW[new], 8)
+    _check(c, NEW[new], _heads(new, 8))
 
 
 @pytest.mark.parametrize("batch, prefix, tail", [(2, 4096, 5), (3, 10000, 700), (40, 1920, 33), (130, 640, 60), (300, 64, 20)])
@@ -139,10 +144,10 @@ def test_sequences_inside_the_prefix(new):
     """Shorter sequences see their own length of it; one of no tokens nothing."""
     n = NEW[new]
     c = SharedCache([700, max(40, n[1]), max(257, n[2]), 640, max(300, n[4])], 640, 2, 64, 32, seed=2)
-    _check(c, n, 4)
-    if new == "one":
+    _check(c, n, _heads(new, 4))
+    if len(set(n)) == 1 and n[0] == 1:
         c = SharedCache([700, 0, 1, 640, 0], 640, 2, 64, 32, seed=2)
-        _, out, lse = _check(c, n, 4)
+        _, out, lse = _check(c, n, _heads(new, 4))
         for b in (1, 4):
             assert (out[b] == 0).all() and torch.isneginf(lse[b]).all()
 
@@ -185,7 +190,7 @@ def test_absent_pages(new):
     c = SharedCache([333, 260, 300, 340, 299], 192, 2, 128, 16, seed=4,
                     absent=[(3, 1), (3, 7), (1, 13), (2, 12), (4, 18)])
     assert c.owner == 3
-    _check(c, NEW[new], 8)
+    _check(c, NEW[new], _heads(new, 8))
 
 
 @pytest.mark.parametrize("new", NEW)
@@ -194,10 +199,10 @@ def test_unseen_values_that_are_not_finite(new, storage):
     """NaN values of the prefix reach the rows that see them, and no row that ends before them."""
     n = NEW[new]
     c = SharedCache([500, max(100, n[1]), 470, max(90, n[3]), 450], 448, 2, 64, 64, *storage, seed=11)
-    _, good, _ = _check(c, n, 4)
+    _, good, _ = _check(c, n, _heads(new, 4))
     bad = int(c.rows[c.owner][300])
     c.v[bad] = float("nan") if storage[1] == "bf16" else ref.NAN_CODE[storage[1]]
-    _, out, lse = _run(c, n, 4)
+    _, out, lse = _run(c, n, _heads(new, 4))
     ends = np.cumsum([0] + list(n))
     for b in range(5):
         rows = slice(ends[b], ends[b + 1])
@@ -214,7 +219,7 @@ def test_weights(new):
     c = SharedCache([400, 350, 389, 500, 384], 320, 2, 64, 32, seed=6, keep_tables=True)
     start = torch.rand(5, 2, c.max_len).cuda()
     w = start.clone()
-    q, out, lse = _run(c, n, 4, weights=w)
+    q, out, lse = _run(c, n, _heads(new, 4), weights=w)
     weights, delta, acc = ref.check_attention(c, q, n, out, lse)
     w, start = w.double().cpu().numpy(), start.double().cpu().numpy()
     at = 0
@@ -247,9 +252,9 @@ def test_windows_and_single_sequences_are_plain():
 @pytest.mark.parametrize("new", NEW)
 def test_same_bits_again(new):
     c = SharedCache([1400, 1350, 1321, 1500, 1330], 1280, 2, 128, 32, seed=12)
-    _, a, z = _run(c, NEW[new], 8)
+    _, a, z = _run(c, NEW[new], _heads(new, 8))
     for _ in range(3):
-        _, b, y = _run(c, NEW[new], 8)
+        _, b, y = _run(c, NEW[new], _heads(new, 8))
         assert torch.equal(a, b) and torch.equal(z, y)
 
 
@@ -261,11 +266,12 @@ def test_graph_stream_workspace(new):
     args = c.device()
     if new == "ragged":
         args["q_offsets"] = torch.tensor(np.concatenate([[0], np.cumsum(n)]), dtype=torch.int32).cuda()
-    q = ref.queries(c, n, 4)
+    heads = _heads(new, 4)
+    q = ref.queries(c, n, heads)
     qd = q.cuda()
-    need = fp8._attention_workspace("e4m3", 2, 64, 32, 5, c.max_len, sum(n), 4, new == "ragged", 0, 0, False, 320)
+    need = fp8._attention_workspace("e4m3", 2, 64, 32, 5, c.max_len, sum(n), heads, new == "ragged", 0, 0, False, 320)
     ws = torch.full((need // 4 + 1,), float("nan"), device="cuda").view(torch.uint8)
-    out, lse = torch.empty_like(qd), torch.empty(sum(n), 4, device="cuda")
+    out, lse = torch.empty_like(qd), torch.empty(sum(n), heads, device="cuda")
 
     def call():
         fp8.kv_attention(qd, shared=320, out=out, lse=lse, workspace=ws, **args)
