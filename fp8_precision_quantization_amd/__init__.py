@@ -66,26 +66,29 @@ def _same_device(t: torch.Tensor, device: torch.device, name: str) -> None:
 
 
 def _matrix(x: torch.Tensor, name: str):
-    if x.dim() != 2:
-        raise ValueError("%s must be 2-D, got shape %s" % (name, tuple(x.shape)))
+    shape = x.shape
+    if len(shape) != 2:
+        raise ValueError("%s must be 2-D, got shape %s" % (name, tuple(shape)))
     if not x.is_cuda:
         raise ValueError("%s must be a device tensor" % name)
-    if x.stride(1) != 1 and x.shape[1] > 1:
+    rows, cols = shape
+    stride = x.stride()
+    if stride[1] != 1 and cols > 1:
         raise ValueError("%s must have a contiguous last dimension" % name)
-    return x.shape[0], x.shape[1], max(x.stride(0), 1) if x.shape[0] > 1 else max(x.shape[1], 1)
+    return rows, cols, max(stride[0], 1) if rows > 1 else max(cols, 1)
 
 
 def _buf(t: torch.Tensor, n: int, dtype, device: torch.device, name: str) -> int:
     """Pointer of a buffer the library reads or writes as n packed elements
     of dtype on device; raises before any launch if t is not one."""
+    if (isinstance(t, torch.Tensor) and t.dtype is dtype and t.numel() == n and t.device == device
+            and t.is_contiguous()):
+        return t.data_ptr()
     if not isinstance(t, torch.Tensor) or t.device != device:
         raise ValueError("%s must be a tensor on %s" % (name, device))
     if t.dtype != dtype:
         raise TypeError("%s must be %s, got %s" % (name, dtype, t.dtype))
-    if t.numel() != n or not t.is_contiguous():
-        raise ValueError("%s must be a contiguous tensor of %d elements, got shape %s"
-                         % (name, n, tuple(t.shape)))
-    return t.data_ptr()
+    raise ValueError("%s must be a contiguous tensor of %d elements, got shape %s" % (name, n, tuple(t.shape)))
 
 
 def _out_matrix(out: torch.Tensor, rows: int, cols: int, dtype, device: torch.device, name: str) -> int:
@@ -532,7 +535,7 @@ def lora_add(y: torch.Tensor, x: torch.Tensor, a: torch.Tensor, b: torch.Tensor,
         ws_bytes = _lora_workspace(rows, columns, inner, rank, adapters, parts)
         if ws_bytes > 0:
             workspace = torch.empty(ws_bytes, dtype=torch.uint8, device=dev)
-    cuts = None if slices is None else (ctypes.c_int32 * parts)(*slices)
+    cuts = None if slices is None else _INTS[parts](*slices)
     st = _call_on(dev, _lib.lib().fp8_lora_add, y.data_ptr(), ldy, x.data_ptr(), ldx, a_ptr, b_ptr, ids_ptr, gain_ptr,
                   out.data_ptr(), ldo, dtype, rows, columns, inner, rank, adapters, cuts, parts, _ptr(workspace),
                   ws_bytes)
@@ -550,16 +553,17 @@ def _kv_rows(x: torch.Tensor, heads: int, head_dim: int, name: str):
     whose heads are packed back to back within a token."""
     if not x.is_cuda:
         raise ValueError("%s must be a device tensor" % name)
-    if x.dim() == 3:
-        if tuple(x.shape[1:]) != (heads, head_dim) or x.stride(2) != 1 or (heads > 1 and x.stride(1) != head_dim):
+    shape, stride = x.shape, x.stride()
+    if len(shape) == 3:
+        if shape[1] != heads or shape[2] != head_dim or stride[2] != 1 or (heads > 1 and stride[1] != head_dim):
             raise ValueError("%s [n, heads, head_dim] must have packed heads" % name)
-    elif x.dim() == 2:
-        if x.shape[1] != heads * head_dim or (x.shape[1] > 1 and x.stride(1) != 1):
+    elif len(shape) == 2:
+        if shape[1] != heads * head_dim or (shape[1] > 1 and stride[1] != 1):
             raise ValueError("%s must be [n, %d] with a contiguous last dimension" % (name, heads * head_dim))
     else:
         raise ValueError("%s must be 2-D or 3-D" % name)
-    n = x.shape[0]
-    return n, (x.stride(0) if n > 1 else heads * head_dim)
+    n = shape[0]
+    return n, (stride[0] if n > 1 else heads * head_dim)
 
 
 def _kv_scales(scale_inv: Optional[torch.Tensor], storage: str, scaling: str, capacity: int, heads: int,
@@ -642,10 +646,31 @@ def _int32(value: int, name: str) -> None:
         raise ValueError("%s=%d does not fit in 32 bits" % (name, value))
 
 
-def _len32(t: torch.Tensor, name: str) -> int:
-    """The number of a 1-D tensor's elements, where twice as many still fit in 32 bits."""
-    _int32(2 * t.numel(), name)
-    return t.numel()
+# int32 arrays a call passes, by length
+_INTS = [ctypes.c_int32 * n for n in range(5)]
+
+
+_CACHE_DTYPE = {"e4m3": torch.uint8, "e5m2": torch.uint8, "bf16": torch.bfloat16}
+
+
+def _caches(k_cache, v_cache, k_scale_inv, v_scale_inv, k_storage, v_storage, scaling):
+    """A layer's K and V caches: (capacity, heads, head_dim, device, pointers of K's and V's scales).  Raises if one
+    is not what the library would read."""
+    shape = k_cache.shape
+    if len(shape) != 3 or not k_cache.is_cuda:
+        raise ValueError("k_cache must be a [capacity, heads, head_dim] device tensor")
+    dev = k_cache.device
+    if v_cache.shape != shape:
+        raise ValueError("k_cache and v_cache must have one shape, got %s and %s"
+                         % (tuple(shape), tuple(v_cache.shape)))
+    if k_cache.dtype is not _CACHE_DTYPE[k_storage] or not k_cache.is_contiguous():
+        raise ValueError("k_cache must be a contiguous %s tensor on %s" % (_CACHE_DTYPE[k_storage], dev))
+    if v_cache.dtype is not _CACHE_DTYPE[v_storage] or not v_cache.is_contiguous() or v_cache.device != dev:
+        raise ValueError("v_cache must be a contiguous %s tensor on %s" % (_CACHE_DTYPE[v_storage], dev))
+    capacity, heads, head_dim = shape
+    return (capacity, heads, head_dim, dev,
+            _kv_scales(k_scale_inv, k_storage, scaling, capacity, heads, dev) or 0,
+            _kv_scales(v_scale_inv, v_storage, scaling, capacity, heads, dev) or 0)
 
 
 def _kv_pair(k_cache, v_cache, page_table, lens, page_size, k_scale_inv, v_scale_inv, k_storage, v_storage, scaling,
@@ -654,18 +679,8 @@ def _kv_pair(k_cache, v_cache, page_table, lens, page_size, k_scale_inv, v_scale
     pages, and the sizes in it: (pair, heads, head_dim, batch, max_len).
     Raises before any launch if a buffer is not what the library would read."""
     _int32(page_size, "page_size")
-    shape = k_cache.shape
-    if len(shape) != 3 or not k_cache.is_cuda:
-        raise ValueError("k_cache must be a [capacity, heads, head_dim] device tensor")
-    capacity, heads, head_dim = shape
-    dev = k_cache.device
-    if v_cache.shape != shape:
-        raise ValueError("k_cache and v_cache must have one shape, got %s and %s"
-                         % (tuple(shape), tuple(v_cache.shape)))
-    for cache, st, name in ((k_cache, k_storage, "k_cache"), (v_cache, v_storage, "v_cache")):
-        want = torch.bfloat16 if st == "bf16" else torch.uint8
-        if cache.dtype != want or not cache.is_contiguous() or cache.device != dev:
-            raise ValueError("%s must be a contiguous %s tensor on %s" % (name, want, dev))
+    capacity, heads, head_dim, dev, k_scale, v_scale = _caches(k_cache, v_cache, k_scale_inv, v_scale_inv, k_storage,
+                                                               v_storage, scaling)
     if page_table.dim() != 2 or page_table.dtype != torch.int32 or page_table.device != dev:
         raise ValueError("page_table must be an int32 [batch, pages] tensor on %s" % dev)
     batch, pages = page_table.shape
@@ -681,8 +696,7 @@ def _kv_pair(k_cache, v_cache, page_table, lens, page_size, k_scale_inv, v_scale
     elif max_len > pages * page_size:
         raise ValueError("max_len=%d needs more than the %d pages of page_table" % (max_len, pages))
     pair = _PAIR.pack(
-        k_cache.data_ptr(), v_cache.data_ptr(), _kv_scales(k_scale_inv, k_storage, scaling, capacity, heads, dev) or 0,
-        _kv_scales(v_scale_inv, v_storage, scaling, capacity, heads, dev) or 0, capacity, page_table.data_ptr(),
+        k_cache.data_ptr(), v_cache.data_ptr(), k_scale, v_scale, capacity, page_table.data_ptr(),
         page_ld, _buf(lens, batch, torch.int32, dev, "lens"), max_len, KV_STORAGE[k_storage], KV_STORAGE[v_storage],
         KV_SCALING[scaling], heads, head_dim, page_size, batch, 0)
     return pair, heads, head_dim, batch, max_len
@@ -729,33 +743,16 @@ def _heads_matrix(x, head_dim: int, name: str):
     return n, heads, x.stride(0) if n > 1 else heads * head_dim
 
 
+# the current device's index, without the checks of a device that is in use already
+_current = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
+
+
 def _call_on(device, func, *args):
     """func(*args, stream) on the device's current stream, whatever the current device is."""
-    if device.index == torch.cuda.current_device():
+    if device.index == _current():
         return func(*args, _stream(device))
     with torch.cuda.device(device):
         return func(*args, _stream(device))
-
-
-def _caches(k_cache, v_cache, k_scale_inv, v_scale_inv, k_storage, v_storage, scaling):
-    """The fp8_kv_pair (as bytes) of a layer's K and V caches alone, without pages: (pair, heads, head_dim)."""
-    shape = k_cache.shape
-    if len(shape) != 3 or not k_cache.is_cuda:
-        raise ValueError("k_cache must be a [capacity, heads, head_dim] device tensor")
-    capacity, heads, head_dim = shape
-    dev = k_cache.device
-    if v_cache.shape != shape:
-        raise ValueError("k_cache and v_cache must have one shape, got %s and %s"
-                         % (tuple(shape), tuple(v_cache.shape)))
-    for cache, st, name in ((k_cache, k_storage, "k_cache"), (v_cache, v_storage, "v_cache")):
-        want = torch.bfloat16 if st == "bf16" else torch.uint8
-        if cache.dtype != want or not cache.is_contiguous() or cache.device != dev:
-            raise ValueError("%s must be a contiguous %s tensor on %s" % (name, want, dev))
-    pair = _PAIR.pack(
-        k_cache.data_ptr(), v_cache.data_ptr(), _kv_scales(k_scale_inv, k_storage, scaling, capacity, heads, dev) or 0,
-        _kv_scales(v_scale_inv, v_storage, scaling, capacity, heads, dev) or 0, capacity, 0, 0, 0, 0,
-        KV_STORAGE[k_storage], KV_STORAGE[v_storage], KV_SCALING[scaling], heads, head_dim, 1, 0, 0)
-    return pair, heads, head_dim
 
 
 def kv_append(k: torch.Tensor, v: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
@@ -786,36 +783,39 @@ def kv_append(k: torch.Tensor, v: torch.Tensor, k_cache: torch.Tensor, v_cache: 
     which may be q itself), or None without q."""
     if v_storage is None:
         v_storage = k_storage
-    pair, heads, head_dim = _caches(k_cache, v_cache, k_scale_inv, v_scale_inv, k_storage, v_storage, scaling)
-    dev = k_cache.device
-    if k.dtype == torch.bfloat16:
+    capacity, heads, head_dim, dev, k_scale, v_scale = _caches(k_cache, v_cache, k_scale_inv, v_scale_inv, k_storage,
+                                                               v_storage, scaling)
+    pair = _PAIR.pack(k_cache.data_ptr(), v_cache.data_ptr(), k_scale, v_scale, capacity, 0, 0, 0, 0,
+                      KV_STORAGE[k_storage], KV_STORAGE[v_storage], KV_SCALING[scaling], heads, head_dim, 1, 0, 0)
+    dtype = k.dtype
+    if dtype is torch.bfloat16:
         in_dt = _lib.FP8_IN_BF16
-    elif k.dtype == torch.float32:
+    elif dtype is torch.float32:
         in_dt = _lib.FP8_IN_F32
     else:
-        raise TypeError("k must be bfloat16 or float32, got %s" % k.dtype)
-    if v.dtype != k.dtype:
-        raise TypeError("v must be %s as k, got %s" % (k.dtype, v.dtype))
-    _same_device(k, dev, "k")
-    _same_device(v, dev, "v")
+        raise TypeError("k must be bfloat16 or float32, got %s" % dtype)
+    if v.dtype is not dtype:
+        raise TypeError("v must be %s as k, got %s" % (dtype, v.dtype))
+    for t, name in ((k, "k"), (v, "v"), (q, "q"), (q_out, "q_out"), (slots, "slots")):
+        if t is not None and t.device != dev:
+            raise ValueError("%s must be on %s, got %s" % (name, dev, t.device))
     n, ldk = _kv_rows(k, heads, head_dim, "k")
     n2, ldv = _kv_rows(v, heads, head_dim, "v")
     if n2 != n:
         raise ValueError("v has %d tokens, k %d" % (n2, n))
-    if slots is not None:
-        _same_device(slots, dev, "slots")
     q_heads = ldq = ldqo = 0
+    q_ptr = out_ptr = None
     if q is None:
         if q_out is not None:
             raise ValueError("q_out needs q")
     else:
-        if q.dtype != k.dtype:
-            raise TypeError("q must be %s as k, got %s" % (k.dtype, q.dtype))
-        _same_device(q, dev, "q")
-        if q.dim() not in (2, 3) or (q.dim() == 2 and q.shape[1] % head_dim):
+        if q.dtype is not dtype:
+            raise TypeError("q must be %s as k, got %s" % (dtype, q.dtype))
+        shape = q.shape
+        if len(shape) not in (2, 3) or (len(shape) == 2 and shape[1] % head_dim):
             raise ValueError("q must be [n, q_heads, %d] or [n, q_heads * %d], got shape %s"
-                             % (head_dim, head_dim, tuple(q.shape)))
-        q_heads = q.shape[1] if q.dim() == 3 else q.shape[1] // head_dim
+                             % (head_dim, head_dim, tuple(shape)))
+        q_heads = shape[1] if len(shape) == 3 else shape[1] // head_dim
         nq, ldq = _kv_rows(q, q_heads, head_dim, "q")
         if nq != n:
             raise ValueError("q has %d tokens, k %d" % (nq, n))
@@ -823,42 +823,48 @@ def kv_append(k: torch.Tensor, v: torch.Tensor, k_cache: torch.Tensor, v_cache: 
             q_out = torch.empty((n, q_heads, head_dim), dtype=torch.bfloat16, device=dev)
             ldqo = q_heads * head_dim
         else:
-            _same_device(q_out, dev, "q_out")
-            if q_out.dtype != torch.bfloat16:
+            if q_out.dtype is not torch.bfloat16:
                 raise TypeError("q_out must be torch.bfloat16, got %s" % q_out.dtype)
             no, ldqo = _kv_rows(q_out, q_heads, head_dim, "q_out")
             if no != n:
                 raise ValueError("q_out has %d tokens, q %d" % (no, n))
+        q_ptr, out_ptr = q.data_ptr(), q_out.data_ptr()
     rotary, axes, pos_ld, cuts, flags = 0, 1, 0, None, _lib.FP8_SCALE_POW2 if pow2 else 0
+    pos_ptr = freq_ptr = None
     if inv_freq is None:
         if positions is not None or sections is not None or interleaved:
             raise ValueError("positions, sections and interleaved need inv_freq")
     else:
         if inv_freq.dim() != 1:
             raise ValueError("inv_freq must be 1-D, got shape %s" % (tuple(inv_freq.shape),))
-        rotary = 2 * _len32(inv_freq, "inv_freq")
-        _buf(inv_freq, rotary // 2, torch.float32, dev, "inv_freq")
-        axes = 1 if sections is None else len(sections)
-        want = (n,) if sections is None else (axes, n)
-        if positions is None or not isinstance(positions, torch.Tensor):
+        rotary = 2 * inv_freq.shape[0]
+        _int32(rotary, "rotary_dim")
+        freq_ptr = _buf(inv_freq, rotary // 2, torch.float32, dev, "inv_freq")
+        if not isinstance(positions, torch.Tensor):
             raise ValueError("inv_freq needs positions")
-        if sections is not None:
+        if sections is None:
+            want = (n,)
+        else:
+            axes = len(sections)
             if not 1 <= axes <= 4:
                 raise ValueError("sections must name 1..4 axes, got %d" % axes)
             for pairs in sections:
                 _int32(pairs, "sections")
-            cuts = (ctypes.c_int32 * axes)(*sections)
-        if positions.dtype != torch.int64 or positions.device != dev:
+            cuts = _INTS[axes](*sections)
+            want = (axes, n)
+        if positions.dtype is not torch.int64 or positions.device != dev:
             raise TypeError("positions must be torch.int64 on %s, got %s on %s" % (dev, positions.dtype, positions.device))
-        if tuple(positions.shape) != want:
+        if positions.shape != want:
             raise ValueError("positions must have shape %s, got %s" % (want, tuple(positions.shape)))
-        if (n > 1 and positions.stride(-1) != 1) or (axes > 1 and positions.stride(0) < n):
+        stride = positions.stride()
+        if (n > 1 and stride[-1] != 1) or (axes > 1 and stride[0] < n):
             raise ValueError("positions must have a contiguous last dimension")
-        pos_ld = positions.stride(0) if axes > 1 else n
-        flags |= _lib.FP8_ROTARY_INTERLEAVED if interleaved else 0
-    st = _call_on(dev, _lib.lib().fp8_kv_append, pair, k.data_ptr(), ldk, v.data_ptr(), ldv, _ptr(q), ldq, q_heads,
-                  _ptr(q_out), ldqo, in_dt, n, _slots(slots, n), _ptr(positions), pos_ld, cuts, axes, _ptr(inv_freq),
-                  rotary, flags, _ptr(diag.buf) if diag is not None else None)
+        pos_ptr, pos_ld = positions.data_ptr(), stride[0] if axes > 1 else n
+        if interleaved:
+            flags |= _lib.FP8_ROTARY_INTERLEAVED
+    st = _call_on(dev, _lib.lib().fp8_kv_append, pair, k.data_ptr(), ldk, v.data_ptr(), ldv, q_ptr, ldq, q_heads,
+                  out_ptr, ldqo, in_dt, n, _slots(slots, n), pos_ptr, pos_ld, cuts, axes, freq_ptr, rotary, flags,
+                  _ptr(diag.buf) if diag is not None else None)
     _lib.check(st, "fp8_kv_append")
     return q_out
 

@@ -19,7 +19,6 @@
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
-#include <cstdlib>
 
 #include "attn_decode.hpp"
 #include "attn_extend.hpp"
@@ -245,15 +244,15 @@ Plan plan_of(const AttnArgs& a, bool ragged) {
     p.one = !ragged && a.total_q == a.kv.batch;
     const int64_t tiles = (rows + extend::kRows - 1) / extend::kRows;
     const int64_t steps = a.from / extend::kStep, tail = std::max<int64_t>(a.kv.max_len - a.from, 0);
-    const int64_t want = getenv("X_WANT") ? atoi(getenv("X_WANT")) : 256; const int64_t tw = getenv("X_TAIL") ? atoi(getenv("X_TAIL")) : 1024;
+    const int64_t want = p.one ? 256 : 384;
     int64_t s = std::clamp<int64_t>(want / (tiles * heads), 1, std::min<int64_t>(64, std::max<int64_t>(steps / 2, 1)));
     p.chunk = (int)((steps + s - 1) / s);
     p.splits = (int)((steps + p.chunk - 1) / p.chunk);
     p.prefix_blocks = tiles * heads * p.splits;
-    p.few = p.one && rows <= (getenv("X_FEW") ? atoi(getenv("X_FEW")) : 32);
+    p.few = p.one && rows <= 32;
     if (p.few) {
         const int64_t units = heads * ((rows + 15) / 16), all = a.from / decode::kStep;
-        s = std::clamp<int64_t>((getenv("X_FW") ? atoi(getenv("X_FW")) : 1024) / units, 1, std::max<int64_t>(all / 4, 1));
+        s = std::clamp<int64_t>(1024 / units, 1, std::max<int64_t>(all / 2, 1));
         p.chunk = (int)((all + s - 1) / s);
         p.splits = (int)((all + p.chunk - 1) / p.chunk);
         p.prefix_blocks = ((p.splits + 7) / 8 * units + decode::kWaves - 1) / decode::kWaves * 8;
@@ -261,7 +260,7 @@ Plan plan_of(const AttnArgs& a, bool ragged) {
     if (p.one) {
         const int64_t units = heads * ((group + 15) / 16);
         const int64_t most = std::max<int64_t>((tail + decode::kStep - 1) / decode::kStep, 1) * a.kv.batch;
-        p.shares = (int)std::max<int64_t>(std::min<int64_t>((tw + units - 1) / units, most), 1);
+        p.shares = (int)std::max<int64_t>(std::min<int64_t>((1024 + units - 1) / units, most), 1);
         p.tail_blocks = ((p.shares + 7) / 8 * units + decode::kWaves - 1) / decode::kWaves * 8;
         const int64_t pieces = (int64_t)(p.shares + a.kv.batch) * a.q_heads;
         p.tail_ml = up16(pieces * 8);
@@ -365,7 +364,7 @@ hipError_t launch_shared(const AttnArgs& a) {
     if (plan.one) {
         p.d.kv = a.kv; p.d.q = a.q; p.d.ldq = a.ldq; p.d.q_heads = a.q_heads; p.d.group = group;
         p.d.col_tiles = (group + 15) / 16; p.d.scale_log2 = a.scale * kLog2e; p.d.from = a.from;
-        p.d.shares = plan.shares; p.d.least = 4;
+        p.d.shares = plan.shares; p.d.least = 2;
         uint8_t* tail = a.workspace + plan.ml + up16(plan.o);
         p.d.part_ml = reinterpret_cast<float2*>(tail);
         p.d.part_o = reinterpret_cast<float*>(tail + plan.tail_ml);
