@@ -236,6 +236,10 @@ struct Plan {
     int64_t ml, o, tail_ml, tail_o;  // bytes of the parts of the workspace
 };
 
+// Waves of the join that share a row: 128 rows 13.3 us a call with four, 15.0 with
+// one; 512 rows 23.1 and 21.7, 2048 rows 38.3 and 36.7.
+int join_waves(int64_t rows) { return rows < 512 ? kJoinWaves : 1; }
+
 int64_t up16(int64_t n) { return (n + 15) / 16 * 16; }
 
 Plan plan_of(const AttnArgs& a, bool ragged) {
@@ -330,7 +334,7 @@ hipError_t run_k(const SharedParams& p, const Plan& plan, hipStream_t stream) {
     }
     if (e != hipSuccess) return e;
     const int64_t rows = (int64_t)p.e.total_q * p.e.q_heads;
-    const int W = rows < 2048 ? kJoinWaves : 1;
+    const int W = join_waves(rows);
     hipLaunchKernelGGL((k_shared_join<kOne>), dim3((unsigned)((rows * W + kJoinWaves - 1) / kJoinWaves)),
                        dim3(kJoinThreads), 0, stream, p, W);
     return hipGetLastError();
@@ -345,7 +349,7 @@ int64_t shared_workspace(const AttnArgs& a, bool ragged) {
 
 int64_t shared_blocks(const AttnArgs& a, bool ragged) {
     const Plan p = plan_of(a, ragged);
-    return std::max({p.prefix_blocks + p.tail_blocks, a.total_q * a.q_heads / (a.total_q * a.q_heads < 2048 ? 1 : 4) + 1,
+    return std::max({p.prefix_blocks + p.tail_blocks, a.total_q * a.q_heads * join_waves(a.total_q * a.q_heads) / kJoinWaves + 1,
                      a.weighted ? extend_blocks(a, ragged) : 0});
 }
 

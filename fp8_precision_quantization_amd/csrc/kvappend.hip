@@ -225,10 +225,12 @@ template <typename InT, int LPR>
 hipError_t launch_rows(AppendParams& p, bool diag, int num_cus, hipStream_t stream) {
     constexpr int kPass = kThreads / LPR;
     const uint32_t width = (uint32_t)(p.q_heads + 2 * p.heads);
-    // As many rows a block as leave 8 blocks a CU (a whole resident round), so
-    // that a token's sines serve many heads, up to 8 passes and 16 KiB of them.
-    uint32_t passes = p.rows / kPass / (8u * (uint32_t)num_cus);
-    passes = passes < 1 ? 1 : passes > 8 ? 8 : passes;
+    // As many rows a block as make up one round of 8 blocks a CU, so that a
+    // token's sines serve many heads, up to 8 passes and 16 KiB of them (8192
+    // tokens of 32 + 8 + 8 heads 31 us; rounds of 2 blocks a CU 36).
+    const uint32_t round = kPass * 8u * (uint32_t)num_cus;
+    uint32_t passes = (p.rows + round - 1) / round;
+    passes = passes > 8 ? 8 : passes;
     auto turns = [&](uint32_t n) {
         return ((n * kPass - 1) / width + 2) * (uint32_t)(p.rotary >> 1) * (uint32_t)sizeof(f2);
     };
