@@ -687,12 +687,15 @@ __global__ __launch_bounds__(kThreads, 2) void k_expand_large(const LoraParams p
         for (int k = 0; k < 2; ++k)
 #pragma unroll
             for (int i = 0; i < 4; ++i)
-                v[k][i] = *reinterpret_cast<const uint4*>(y + (rows[k][i] + none) * p.ldy + n);
+                v[k][i] = __builtin_bit_cast(
+                    uint4, __builtin_nontemporal_load(reinterpret_cast<const u4*>(y + (rows[k][i] + none) * p.ldy + n)));
     };
     auto store = [&](const uint4& v, int k, int i, int n0) {
         int none = 0;
         asm volatile("" : "+v"(none));
-        if (n0 + c * J < n_end) *reinterpret_cast<uint4*>(out + (rows[k][i] + none) * p.ldo + n0 + c * J) = v;
+        if (n0 + c * J < n_end)
+            __builtin_nontemporal_store(__builtin_bit_cast(u4, v),
+                                        reinterpret_cast<u4*>(out + (rows[k][i] + none) * p.ldo + n0 + c * J));
     };
 
     const int id_a = lane < count ? tile[lane].y : -2, id_b = 64 + lane < count ? tile[64 + lane].y : -2;
