@@ -306,3 +306,29 @@ def test_cache_class():
         top = np.abs(want).max(2, keepdims=True)
         # half a step of the largest binade (448 = 1.75 * 2^8: 16 of 448), and bf16's
         assert (np.abs(got - want) <= (16.0 / 448 + 2.0 ** -8) * top).all()
+
+
+def test_offsets_past_32_bits():
+    """Cache rows and inputs that lie more than 2^32 bytes from the first."""
+    heads, dim, capacity = 8, 256, (1 << 32) // (8 * 256) + 64
+    caches = [torch.empty((capacity, heads, dim), dtype=torch.uint8, device="cuda") for _ in "kv"]
+    scales = [torch.empty((capacity, heads), device="cuda") for _ in "kv"]
+    n, pitch = 70, (1 << 31) // 60 // 8 * 8
+    x = torch.empty(n * pitch, dtype=torch.bfloat16, device="cuda").view(n, pitch)
+    width = heads * dim
+    x[:, :3 * width] = torch.randn(n, 3 * width, device="cuda")
+    q, k, v = (x[:, i * width:(i + 1) * width] for i in range(3))
+    slots = capacity - 1 - torch.arange(n, device="cuda")
+    pos = torch.arange(n, device="cuda")
+    freq = torch.tensor([10000.0 ** (-i / 128) for i in range(128)], device="cuda")
+    say("offsets past 32 bits", capacity, pitch)
+    got = fp8.kv_append(k, v, caches[0], caches[1], slots, q=q, positions=pos, inv_freq=freq, k_scale_inv=scales[0],
+                        v_scale_inv=scales[1])
+    small = [torch.empty((n, heads, dim), dtype=torch.uint8, device="cuda") for _ in "kv"]
+    small_scales = [torch.empty((n, heads), device="cuda") for _ in "kv"]
+    want = fp8.kv_append(k.contiguous(), v.contiguous(), small[0], small[1], q=q.contiguous(), positions=pos, inv_freq=freq,
+                         k_scale_inv=small_scales[0], v_scale_inv=small_scales[1])
+    torch.cuda.synchronize()
+    assert torch.equal(got, want)
+    for a, b, sa, sb in zip(caches, small, scales, small_scales):
+        assert torch.equal(a[slots], b) and torch.equal(sa[slots], sb)

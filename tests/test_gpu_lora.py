@@ -130,10 +130,27 @@ def test_wide_slices(rows, rank, parts):
     c.check(c.run())
 
 
-@pytest.mark.parametrize("adapters, rows", [(1, 300), (1, 1), (300, 300), (1000, 64), (2, 1024), (40, 1300)])
-def test_adapters(adapters, rows):
-    c = Case(rows, inner=72, columns=(40,), rank=8, adapters=adapters, seed=adapters)
+@pytest.mark.parametrize("adapters, rows", [(1, 300), (1, 1), (300, 300), (1000, 64), (2, 1024), (40, 1300), (3000, 400),
+                                            (3000, 1500), (1500, 9000), (3, 8192), (5, 8193), (9, 20000)])
+@pytest.mark.parametrize("order", ["mixed", "sorted"])
+def test_adapters(adapters, rows, order):
+    """More adapters than the sort has buckets share them; more rows than its threads hold are read twice."""
+    c = Case(rows, inner=72, columns=(40,), rank=8, adapters=adapters, seed=adapters, order=order)
     c.check(c.run())
+
+
+@pytest.mark.parametrize("rows", [600, 2100])
+def test_offsets_past_32_bits(rows):
+    """Rows of x, y and out that lie more than 2^32 bytes apart."""
+    c = Case(rows, inner=64, columns=(24,), rank=8, adapters=3, seed=rows)
+    want = c.run()
+    pitch = (1 << 32) // rows // 8 * 8 + 64
+    x = torch.empty(rows * pitch, dtype=torch.bfloat16, device="cuda").view(rows, pitch)
+    assert x.numel() * 2 > 1 << 32
+    x[:, :64], x[:, 64:88] = c.x, c.y
+    c.x, c.y = x[:, :64], x[:, 64:88]
+    got = c.run(out=x[:, 96:120])
+    assert torch.equal(got, want)
 
 
 @pytest.mark.parametrize("rows", [30, 1100])

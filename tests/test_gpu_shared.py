@@ -250,6 +250,28 @@ def test_windows_and_single_sequences_are_plain():
 
 
 @pytest.mark.parametrize("new", NEW)
+def test_offsets_past_32_bits(new):
+    """The shared pages and the sequences' own at rows more than 2^32 bytes from the first."""
+    n, heads = NEW[new], _heads(new, 16)
+    c = SharedCache([400, 350, 389, 500, 384], 320, 8, 256, 32, seed=6, keep_tables=True)
+    args = c.device()
+    q = ref.queries(c, n, heads)
+    shift = (1 << 32) // (8 * 256 * 32)             # pages
+    for name in ("k_cache", "v_cache", "k_scale_inv", "v_scale_inv"):
+        t = args[name]
+        big = torch.empty((shift * 32 + t.shape[0],) + tuple(t.shape[1:]), dtype=t.dtype, device="cuda")
+        big[shift * 32:] = t
+        args[name] = big
+    args["page_table"] = args["page_table"] + shift
+    if new == "ragged":
+        args["q_offsets"] = torch.tensor(np.concatenate([[0], np.cumsum(n)]), dtype=torch.int32).cuda()
+    say("offsets past 32 bits", new)
+    out, lse = fp8.kv_attention(q.cuda(), shared=320, return_lse=True, **args)
+    torch.cuda.synchronize()
+    ref.check_attention(c, q, n, out, lse)
+
+
+@pytest.mark.parametrize("new", NEW)
 def test_same_bits_again(new):
     c = SharedCache([1400, 1350, 1321, 1500, 1330], 1280, 2, 128, 32, seed=12)
     _, a, z = _run(c, NEW[new], _heads(new, 8))
