@@ -13,10 +13,12 @@
 // whatever the order of the ids.  The sort counts ids in 1024 buckets; a tile of
 // a bucket that several adapters share takes them one after the other.
 //
-// Up to kSmall rows (a decode step of many users) there are two launches.
-// k_shrink_small: a block (up to kFew rows each of its waves) sorts for itself, takes a tile of 16 rows and a part of
-// the inner dimension, whose steps go round its four waves, so that it reads
-// neither x nor A twice; the parts' sums and the tile's rows go to the workspace.
+// Up to kFew rows (a decode step) there is one launch, k_lora_few, where the sizes
+// let it gain.  Up to kSmall rows there are otherwise two.  k_shrink_small: a block
+// (up to kFew rows each of its waves) sorts for itself, takes a tile of 16 rows and
+// a part of the inner dimension, whose steps go round its four waves, so that it
+// reads neither x nor A twice; the parts' sums and the tile's rows go to the
+// workspace.
 // k_expand_small: a block takes a tile and 256 columns of one slice, adds up the
 // parts of t in their order and adds B t to y.  Products are 16x16x32 with ranks
 // (columns of the output) as the matrix rows and batch rows as its columns.
@@ -45,6 +47,7 @@ constexpr int kWaves = 4;
 constexpr int kThreads = 64 * kWaves;
 constexpr int kSmall = 1024;         // rows up to which blocks sort for themselves
 constexpr int kFew = 64;             // rows up to which a wave sorts for itself
+constexpr int kFewRank = 64;         // ranks up to which these take one launch
 constexpr int kSmallTile = 16, kLargeTile = 128;
 constexpr int kBuckets = 1024;
 constexpr int kStepK = 64;           // inner elements of a step
@@ -189,29 +192,31 @@ struct Eight {
 };
 
 // ------------------------------------------------------------ small batches --
+// The rows of tile `slot` where a wave holds all ids: the tile of row `slot`, if
+// that is the first, 17th, .. of its adapter.  As pick_tile, every wave by itself.
+__device__ __forceinline__ bool pick_few(const LoraParams& p, int slot, int* row, int* id) {
+    const int lane = threadIdx.x & 63, mine = lane < p.rows ? id_of(p, lane) : -2;
+    const uint64_t same = __ballot(mine == __builtin_amdgcn_readlane(mine, slot));
+    const int rank = __popcll(same & ((1ull << slot) - 1)), n = __popcll(same) - rank;
+    if (rank % kSmallTile != 0) return false;
+    // lane i of the tile's takes the i-th of these rows from row `slot` on
+    const int at = __popcll(same & ((1ull << lane) - 1)) - rank;
+    const bool in = (same >> lane & 1) && at >= 0;
+    const int from = __builtin_amdgcn_ds_permute((in ? at : 63) * 4, lane);
+    *id = __builtin_amdgcn_readlane(mine, slot);
+    *row = __shfl(from, lane & (kSmallTile - 1), 64);
+    if ((lane & (kSmallTile - 1)) >= n) {
+        *row = -1;
+        *id = -2;
+    }
+    return true;
+}
+
 // The rows of tile `slot`, sorted by this block for itself: lane i (and i + 16,
 // i + 32, i + 48) gets row i and its adapter, row -1 where there is none.
 // Returns false where there is no such tile (for the whole block).
 __device__ __forceinline__ bool pick_tile(const LoraParams& p, int slot, int* row, int* id) {
-    if (p.rows <= kFew) {
-        // every wave by itself: the tile of row `slot`, where that is the first,
-        // 17th, .. of its adapter
-        const int lane = threadIdx.x & 63, mine = lane < p.rows ? id_of(p, lane) : -2;
-        const uint64_t same = __ballot(mine == __builtin_amdgcn_readlane(mine, slot));
-        const int rank = __popcll(same & ((1ull << slot) - 1)), n = __popcll(same) - rank;
-        if (rank % kSmallTile != 0) return false;
-        // lane i of the tile's takes the i-th of these rows from row `slot` on
-        const int at = __popcll(same & ((1ull << lane) - 1)) - rank;
-        const bool in = (same >> lane & 1) && at >= 0;
-        const int from = __builtin_amdgcn_ds_permute((in ? at : 63) * 4, lane);
-        *id = __builtin_amdgcn_readlane(mine, slot);
-        *row = __shfl(from, lane & (kSmallTile - 1), 64);
-        if ((lane & (kSmallTile - 1)) >= n) {
-            *row = -1;
-            *id = -2;
-        }
-        return true;
-    }
+    if (p.rows <= kFew) return pick_few(p, slot, row, id);
     __shared__ int s_count[kBuckets];
     constexpr int kEach = kSmall / kThreads;
     __shared__ int s_sum[kWaves], s_found[2], s_in[kEach * kWaves];
@@ -439,6 +444,174 @@ __global__ __launch_bounds__(kThreads, 5) void k_expand_small(const LoraParams p
     }
 }
 
+__device__ __forceinline__ uint32_t lds_address(const void* p) {
+    return (uint32_t)(uintptr_t)(const __attribute__((address_space(3))) void*)p;
+}
+
+// 64 lanes x 16 bytes into LDS [lds, lds + 1024).  No register result: nothing in
+// flight targets a register, and only the explicit waits below order it.
+__device__ __forceinline__ void load_to_lds(uint32_t lds, const void* from) {
+    asm volatile("s_mov_b32 m0, %0\n\tglobal_load_lds_dwordx4 %1, off"
+                 :: "s"(__builtin_amdgcn_readfirstlane(lds)), "v"(from) : "memory", "m0");
+}
+
+// Up to kFew rows, ranks of RT tiles of 16: one launch.  A block takes a tile and
+// 512 columns of one slice and forms the slice's t itself, its eight waves going
+// through the inner dimension side by side: A is read by every column block again
+// (from the caches), which costs less than a second launch and the partial sums'
+// way through memory.  Each wave stages steps of x and A in LDS of its own, several
+// on their way, in the layout that k_shrink_large explains.
+constexpr int few_waves(int rt) { return rt <= 2 ? 16 : 8; }
+constexpr int few_stages(int rt) { return rt == 1 ? 2 : 1; }
+constexpr int few_lds(int rt) { return few_waves(rt) * few_stages(rt) * (rt + 1) * 2048; }
+
+template <int RT, typename OutT>
+__global__ __launch_bounds__(64 * few_waves(RT), 1) void k_lora_few(const LoraParams p) {
+    constexpr int kTerms = sizeof(OutT) == 2 ? 2 : 3;
+    constexpr int kFewWaves = few_waves(RT), kStages = few_stages(RT), kStage = (RT + 1) * 2048, kUnits = (RT + 1) * 2;
+    extern __shared__ __align__(1024) uint8_t smem[];   // the waves' stages, then
+    uint8_t* const s_t = smem + few_lds(RT);            // [16 rows][terms of t, padded] bf16
+    const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int c = lane & 15, g = lane >> 4;
+    const int column_blocks = p.block_ends[3], slot = blockIdx.x / column_blocks;
+    int row, id;
+    if (!pick_few(p, slot, &row, &id)) return;
+    const Slice slice(p, blockIdx.x % column_blocks);
+    const int n0 = slice.first + (slice.block * kFewWaves + wave) * kChunk, end = slice.end;
+    const int n = n0 + g * 16;                          // this lane's 16 columns
+    const bool on[2] = {n < end && row >= 0, n + 8 < end && row >= 0};
+    const OutT* const y = static_cast<const OutT*>(p.y) + (int64_t)max(row, 0) * p.ldy;
+    OutT* const out = static_cast<OutT*>(p.out) + (int64_t)max(row, 0) * p.ldo;
+    Eight<OutT> v[2];
+#pragma unroll
+    for (int h = 0; h < 2; ++h) v[h].load(y + (on[h] ? n + h * 8 : 0));
+    const int l = __builtin_amdgcn_readfirstlane(id);   // (the tile's first row's, all rows')
+    if (l < 0) {                                        // without an adapter: as they are
+        if (p.out != p.y) {
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+                if (on[h]) v[h].store(out + n + h * 8);
+        }
+        return;
+    }
+    const Ranks ranks(p.rank, kTerms);
+    // matrix row rho of piece j is column n0 + 16 (rho / 4) + 4 j + rho % 4
+    const uint16_t* bp[4];
+    b8 bf[4];
+    auto load_b = [&](int s) {
+        const int q = ranks.whole ? s * 4 + g : (s * 4 + g) % ranks.groups;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) bf[j] = *reinterpret_cast<const b8*>(bp[j] + q * 8);
+    };
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+        bp[j] = p.b + ((int64_t)l * p.columns + min(n0 + (c >> 2) * 16 + j * 4 + (c & 3), end - 1)) * p.rank;
+    load_b(0);
+    const float gain = p.gain ? p.gain[l] : 1.0f;
+
+    const uint16_t *xp[2], *ap[RT * 2];                 // of row lane / 8 of a load of 1 KiB
+#pragma unroll
+    for (int i = 0; i < 2; ++i) xp[i] = p.x + (int64_t)max(__shfl(row, i * 8 + (lane >> 3), 64), 0) * p.ldx;
+#pragma unroll
+    for (int i = 0; i < RT * 2; ++i)
+        ap[i] = p.a + ((int64_t)l * p.width + slice.index * p.rank + min(i * 8 + (lane >> 3), p.rank - 1)) * p.inner;
+    uint8_t* const mine = smem + wave * kStages * kStage;
+    const int total = (p.inner + kStepK - 1) / kStepK;
+    const int steps = (total - wave + kFewWaves - 1) / kFewWaves;   // this wave's: wave, wave + 8, ..
+    const int piece = ((lane & 7) ^ (lane >> 3)) * 8;
+    auto stage = [&](int i) {
+        const uint32_t to = lds_address(mine) + (uint32_t)(i % kStages) * kStage;
+        const int e = (wave + i * kFewWaves) * kStepK + piece, at = e < p.inner ? e : 0;
+#pragma unroll
+        for (int k = 0; k < 2; ++k) load_to_lds(to + k * 1024, xp[k] + at);
+#pragma unroll
+        for (int k = 0; k < RT * 2; ++k) load_to_lds(to + 2048 + k * 1024, ap[k] + at);
+    };
+    f4 acc[RT];
+#pragma unroll
+    for (int i = 0; i < RT; ++i) acc[i] = f4{0, 0, 0, 0};
+    for (int i = 0; i < min(kStages, steps); ++i) stage(i);
+    for (int i = 0; i < steps; ++i) {
+        // stage i is here when no more than the loads of those after it are left
+        if (i + kStages <= steps) asm volatile("s_waitcnt vmcnt(%0)" ::"n"((kStages - 1) * kUnits) : "memory");
+        else asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+        const uint8_t* const from = mine + i % kStages * kStage;
+        const int st = wave + i * kFewWaves;
+        uint4 xf[2], af[RT][2];
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const int at = c * 128 + ((h * 4 + g) ^ (c & 7)) * 16;
+            xf[h] = *reinterpret_cast<const uint4*>(from + at);
+#pragma unroll
+            for (int k = 0; k < RT; ++k) af[k][h] = *reinterpret_cast<const uint4*>(from + (k + 1) * 2048 + at);
+        }
+        if (i + kStages < steps) {                      // the stage is read: free for the next
+            asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+            stage(i + kStages);
+        }
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            if ((st + 1) * kStepK > p.inner) {          // nothing behind the end
+                const uint32_t keep = st * kStepK + h * 32 + g * 8 < p.inner ? ~0u : 0u;
+                auto cut = [&](uint4& w) { w = make_uint4(w.x & keep, w.y & keep, w.z & keep, w.w & keep); };
+                cut(xf[h]);
+#pragma unroll
+                for (int k = 0; k < RT; ++k) cut(af[k][h]);
+            }
+#pragma unroll
+            for (int k = 0; k < RT; ++k)
+                acc[k] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(b8, af[k][h]),
+                                                                 __builtin_bit_cast(b8, xf[h]), acc[k], 0, 0, 0);
+        }
+    }
+    // this wave's sums, over its own stages
+    asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+#pragma unroll
+    for (int i = 0; i < RT; ++i) reinterpret_cast<f4*>(mine)[i * 64 + lane] = acc[i];
+    // zeros behind t's last term
+    const int fill = ranks.whole ? 0 : ranks.steps * 4 - kTerms * ranks.groups;
+    if (tid < 16 * fill) {
+        const int r = tid / fill;
+        *reinterpret_cast<uint4*>(s_t + r * ranks.pitch + (kTerms * ranks.groups + tid - r * fill) * 16) =
+            make_uint4(0, 0, 0, 0);
+    }
+    __syncthreads();
+    // four ranks of a row a thread: the waves' sums, in bf16 terms
+    if (tid < RT * 64) {
+        f4 t = reinterpret_cast<const f4*>(smem)[tid];
+#pragma unroll
+        for (int w = 1; w < kFewWaves; ++w) t += reinterpret_cast<const f4*>(smem + w * kStages * kStage)[tid];
+        t *= gain;
+        const int rank = (tid >> 6) * 16 + g * 4;       // (of row c)
+        if (rank < p.rank) {
+#pragma unroll
+            for (int k = 0; k < kTerms; ++k) {
+                const uint32_t w0 = pack2(t[0], t[1]), w1 = pack2(t[2], t[3]);
+                *reinterpret_cast<uint2*>(s_t + c * ranks.pitch + (k * p.rank + rank) * 2) = make_uint2(w0, w1);
+                t -= f4{as_f32(w0 << 16), as_f32(w0 & 0xFFFF0000u), as_f32(w1 << 16), as_f32(w1 & 0xFFFF0000u)};
+            }
+        }
+    }
+    __syncthreads();
+    if (n0 >= end) return;
+    f4 sum[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) sum[j] = f4{0, 0, 0, 0};
+    for (int s = 0; s < ranks.steps; ++s) {
+        if (s > 0) load_b(s);
+        for (int t = 0; t < ranks.terms; ++t) {
+            const b8 tf = *reinterpret_cast<const b8*>(s_t + c * ranks.pitch + (t * ranks.groups + s * 4 + g) * 16);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) sum[j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(bf[j], tf, sum[j], 0, 0, 0);
+        }
+    }
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+        v[h].add(sum[2 * h], sum[2 * h + 1]);
+        if (on[h]) v[h].store(out + n + h * 8);
+    }
+}
+
 // ------------------------------------------------------------ large batches --
 // Sorts the rows into tiles: one block.
 constexpr int kSortThreads = 1024;
@@ -517,17 +690,6 @@ __global__ __launch_bounds__(kSortThreads) void k_sort_rows(const LoraParams p) 
             if (m < p.rows) p.tiles[s_first[b] * kLargeTile + place[i]] = make_int2(m, ids[i]);
         }
     }
-}
-
-__device__ __forceinline__ uint32_t lds_address(const void* p) {
-    return (uint32_t)(uintptr_t)(const __attribute__((address_space(3))) void*)p;
-}
-
-// 64 lanes x 16 bytes into LDS [lds, lds + 1024).  No register result: nothing in
-// flight targets a register, and only the explicit waits below order it.
-__device__ __forceinline__ void load_to_lds(uint32_t lds, const void* from) {
-    asm volatile("s_mov_b32 m0, %0\n\tglobal_load_lds_dwordx4 %1, off"
-                 :: "s"(__builtin_amdgcn_readfirstlane(lds)), "v"(from) : "memory", "m0");
 }
 
 // Two waves a SIMD, so that one's reads of LDS stand beside the other's products:
@@ -788,7 +950,7 @@ __global__ __launch_bounds__(kThreads, 2) void k_expand_large(const LoraParams p
 
 // How a call is shared out.
 struct Plan {
-    bool small;
+    bool few, small;
     int slots, tile;                 // tiles that the sort may make, rows of one
     int rank_tiles, groups, splits, split_steps;
     int64_t shrink_blocks;
@@ -797,6 +959,16 @@ struct Plan {
 Plan plan_of(const LoraArgs& a) {
     Plan p;
     p.small = a.rows <= kSmall;
+    // One launch where its blocks are resident together and a block's pass over the
+    // inner dimension, which grows with the rows of A and x, is shorter than a
+    // second launch (1 .. 64 rows, 6144 columns; 16 ranks of inner 4096: 5.9 .. 7.0
+    // us against 8.1 .. 11.0, of 14336: 10.7 .. 13 against 8.3 .. 11; 32 ranks of
+    // 4096: 7.4 .. 11.6 against 9.2 .. 14.8, 64 ranks: 9.5 .. 32 against 9.8 .. 25,
+    // and of 1024: 6.1 .. 6.7 against 7.7 .. 8.4; in two rounds of blocks 13 .. 15
+    // against 11 .. 13).
+    const int tiles_of_16 = (int)std::min<int64_t>(a.rows, (a.rows + 15) / 16 + a.adapters), rt = (a.rank + 15) / 16;
+    p.few = a.rows <= kFew && a.rank <= kFewRank && a.inner * (rt == 3 ? 5 : rt + 1) <= 16384 &&
+            tiles_of_16 * (a.columns / (few_waves(rt) * kChunk) + a.slices) <= 256;
     p.tile = p.small ? kSmallTile : kLargeTile;
     p.slots = a.rows <= kFew ? (int)a.rows
                              : (int)(a.rows / p.tile + std::min<int64_t>({a.rows, (int64_t)a.adapters + 1, kBuckets}));
@@ -830,7 +1002,7 @@ int64_t count_bytes(const Plan& p) { return p.small ? 0 : ((int64_t)p.slots * 4 
 // Column blocks of the second launch.
 template <typename OutT>
 int64_t column_blocks(const LoraArgs& a, const Plan& plan, int* chunks, int (&ends)[4]) {
-    const int cols = plan.small ? kWaves * kChunk : 16 * kEach<OutT>;
+    const int cols = plan.few ? few_waves((a.rank + 15) / 16) * kChunk : plan.small ? kWaves * kChunk : 16 * kEach<OutT>;
     auto count = [&](int run) {
         int blocks = 0;
         for (int i = 0; i < 4; ++i) {
@@ -880,6 +1052,23 @@ hipError_t run_shrink(const LoraParams& p, const Plan& plan, hipStream_t stream)
 }
 
 template <typename OutT>
+hipError_t run_few(const LoraArgs& a, LoraParams& p, const Plan& plan, hipStream_t stream) {
+    const dim3 grid((unsigned)column_blocks<OutT>(a, plan, &p.chunks, p.block_ends));
+    const auto launch = [&](auto rt) {
+        constexpr int kRT = decltype(rt)::value;
+        const int bytes = few_lds(kRT) + kSmallTile * Ranks(p.rank, sizeof(OutT) == 2 ? 2 : 3).pitch;
+        const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(&k_lora_few<kRT, OutT>),
+                                                 hipFuncAttributeMaxDynamicSharedMemorySize, bytes);
+        if (e != hipSuccess) return e;
+        hipLaunchKernelGGL((k_lora_few<kRT, OutT>), grid, dim3(64 * few_waves(kRT)), bytes, stream, p);
+        return hipGetLastError();
+    };
+    if (p.rank <= 16) return launch(std::integral_constant<int, 1>());
+    if (p.rank <= 32) return launch(std::integral_constant<int, 2>());
+    return launch(std::integral_constant<int, 4>());
+}
+
+template <typename OutT>
 hipError_t run_expand(const LoraArgs& a, LoraParams& p, const Plan& plan, hipStream_t stream) {
     const int64_t blocks = column_blocks<OutT>(a, plan, &p.chunks, p.block_ends);
     const Ranks ranks(p.rank, sizeof(OutT) == 2 ? 2 : 3);
@@ -901,6 +1090,7 @@ hipError_t run_expand(const LoraArgs& a, LoraParams& p, const Plan& plan, hipStr
 int64_t lora_workspace(const LoraArgs& a) {
     if (a.rows == 0) return 0;
     const Plan p = plan_of(a);
+    if (p.few) return 0;
     return tile_bytes(p) + count_bytes(p) + (int64_t)p.splits * a.rows * a.slices * a.rank * 4;
 }
 
@@ -925,6 +1115,8 @@ hipError_t launch_lora(const LoraArgs& a) {
     p.tiles = reinterpret_cast<int2*>(a.workspace);
     p.counts = reinterpret_cast<int*>(a.workspace + tile_bytes(plan));
     p.part = reinterpret_cast<float*>(a.workspace + tile_bytes(plan) + count_bytes(plan));
+    if (plan.few)
+        return a.out_bf16 ? run_few<uint16_t>(a, p, plan, a.stream) : run_few<float>(a, p, plan, a.stream);
     if (!plan.small) {
         hipLaunchKernelGGL(k_sort_rows, dim3(1), dim3(kSortThreads), 0, a.stream, p);
         const hipError_t e = hipGetLastError();

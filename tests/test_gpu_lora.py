@@ -130,6 +130,15 @@ def test_wide_slices(rows, rank, parts):
     c.check(c.run())
 
 
+@pytest.mark.parametrize("rank, inner", [(8, 2048), (16, 8192), (16, 8200), (32, 5456), (32, 5472), (48, 3264),
+                                         (64, 3272), (64, 3280)])
+@pytest.mark.parametrize("rows, adapters", [(1, 1), (33, 2), (64, 64)])
+def test_few_rows(rows, adapters, rank, inner):
+    """Both sides of the rule that takes one launch for few rows."""
+    c = Case(rows, inner=inner, columns=(1032, 8, 520), rank=rank, adapters=adapters, seed=inner, order="mixed")
+    c.check(c.run())
+
+
 @pytest.mark.parametrize("adapters, rows", [(1, 300), (1, 1), (300, 300), (1000, 64), (2, 1024), (40, 1300), (3000, 400),
                                             (3000, 1500), (1500, 9000), (3, 8192), (5, 8193), (9, 20000)])
 @pytest.mark.parametrize("order", ["mixed", "sorted"])
@@ -204,7 +213,7 @@ def test_empty():
     assert torch.equal(out, c.y)
 
 
-@pytest.mark.parametrize("rows", [33, 1500])
+@pytest.mark.parametrize("rows", [33, 90, 1500])
 def test_graph_stream_workspace(rows):
     """A captured call follows new ids and inputs; a workspace full of NaN, on another stream, gives the same bits."""
     c = Case(rows, columns=(136, 64), seed=rows)
