@@ -275,9 +275,81 @@ __device__ __forceinline__ bool pick_tile(const LoraParams& p, int slot, int* ro
     return true;
 }
 
+__device__ __forceinline__ uint32_t lds_address(const void* p) {
+    return (uint32_t)(uintptr_t)(const __attribute__((address_space(3))) void*)p;
+}
+
+// 64 lanes x 16 bytes into LDS [lds, lds + 1024).  No register result: nothing in
+// flight targets a register, and only the explicit waits below order it.
+__device__ __forceinline__ void load_to_lds(uint32_t lds, const void* from) {
+    asm volatile("s_mov_b32 m0, %0\n\tglobal_load_lds_dwordx4 %1, off"
+                 :: "s"(__builtin_amdgcn_readfirstlane(lds)), "v"(from) : "memory", "m0");
+}
+
+// acc[k] += rank tile k of A times a tile of x^T over this wave's steps of 64 inner
+// elements (first, first + stride, ..).  The steps go through kStages stages of LDS
+// of the wave's own, past the registers: a load takes 8 rows of 128 bytes (xp, ap:
+// row lane / 8 of each), where read as matrix operands directly neighbouring lanes
+// would touch different rows, which the caches serve at a quarter of the rate.  Of
+// its row a lane loads the 16-byte piece that belongs at place lane % 8, pieces
+// being turned by the row so that 16 rows' reads of one fall into different banks.
+template <int RT, int kStages>
+__device__ __forceinline__ void multiply_staged(uint8_t* mine, const uint16_t* const (&xp)[2],
+                                                const uint16_t* const (&ap)[RT * 2], int first, int stride, int steps,
+                                                int inner, f4 (&acc)[RT]) {
+    constexpr int kStage = (RT + 1) * 2048, kUnits = (RT + 1) * 2;
+    const int lane = threadIdx.x & 63, c = lane & 15, g = lane >> 4;
+    const int piece = ((lane & 7) ^ (lane >> 3)) * 8;
+    auto stage = [&](int i) {
+        const uint32_t to = lds_address(mine) + (uint32_t)(i % kStages) * kStage;
+        const int e = (first + i * stride) * kStepK + piece, at = e < inner ? e : 0;
+#pragma unroll
+        for (int k = 0; k < 2; ++k) load_to_lds(to + k * 1024, xp[k] + at);
+#pragma unroll
+        for (int k = 0; k < RT * 2; ++k) load_to_lds(to + 2048 + k * 1024, ap[k] + at);
+    };
+    for (int i = 0; i < min(kStages, steps); ++i) stage(i);
+    for (int i = 0; i < steps; ++i) {
+        // stage i is here when no more than the loads of those after it are left
+        if (i + kStages <= steps) asm volatile("s_waitcnt vmcnt(%0)" ::"n"((kStages - 1) * kUnits) : "memory");
+        else asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+        const uint8_t* const from = mine + i % kStages * kStage;
+        const int st = first + i * stride;
+        uint4 xf[2], af[RT][2];
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const int at = c * 128 + ((h * 4 + g) ^ (c & 7)) * 16;
+            xf[h] = *reinterpret_cast<const uint4*>(from + at);
+#pragma unroll
+            for (int k = 0; k < RT; ++k) af[k][h] = *reinterpret_cast<const uint4*>(from + (k + 1) * 2048 + at);
+        }
+        if (i + kStages < steps) {                  // the stage is read: free for the next
+            asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+            stage(i + kStages);
+        }
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            if ((st + 1) * kStepK > inner) {        // nothing behind the end
+                const uint32_t keep = st * kStepK + h * 32 + g * 8 < inner ? ~0u : 0u;
+                auto cut = [&](uint4& w) { w = make_uint4(w.x & keep, w.y & keep, w.z & keep, w.w & keep); };
+                cut(xf[h]);
+#pragma unroll
+                for (int k = 0; k < RT; ++k) cut(af[k][h]);
+            }
+#pragma unroll
+            for (int k = 0; k < RT; ++k)
+                acc[k] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(b8, af[k][h]),
+                                                                 __builtin_bit_cast(b8, xf[h]), acc[k], 0, 0, 0);
+        }
+    }
+}
+
+constexpr int kSmallStages = 2;
+constexpr int small_lds(int rt) { return kWaves * kSmallStages * (rt + 1) * 2048; }
+
 template <int RT>
 __global__ __launch_bounds__(kThreads, 2) void k_shrink_small(const LoraParams p) {
-    __shared__ f4 s_sum[2][RT * 64];
+    extern __shared__ __align__(1024) uint8_t smem[];   // the waves' stages
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int c = lane & 15, g = lane >> 4;
     const int group = blockIdx.x % p.groups, split = blockIdx.x / p.groups % p.splits,
@@ -290,91 +362,39 @@ __global__ __launch_bounds__(kThreads, 2) void k_shrink_small(const LoraParams p
     const int rank0 = group * RT * 16;
     const int total = (p.inner + kStepK - 1) / kStepK;
     const int s_begin = split * p.split_steps, s_end = min(s_begin + p.split_steps, total);
-    const uint16_t* const xp = p.x + (int64_t)max(row, 0) * p.ldx;
+    uint8_t* const mine = smem + wave * (small_lds(RT) / kWaves);
+    const uint16_t* xp[2];                              // of row lane / 8 of a load of 1 KiB
+#pragma unroll
+    for (int i = 0; i < 2; ++i) xp[i] = p.x + (int64_t)max(__shfl(row, i * 8 + (lane >> 3), 64), 0) * p.ldx;
     uint64_t left = __ballot(id >= 0);
     while (left) {
         const int l = __builtin_amdgcn_readlane(id, __builtin_ctzll(left));
         const uint64_t same = __ballot(id == l);
         left &= ~same;
-        const uint16_t* const ap = p.a + (int64_t)l * p.width * p.inner;
+        const uint16_t* ap[RT * 2];
+#pragma unroll
+        for (int i = 0; i < RT * 2; ++i)
+            ap[i] = p.a + ((int64_t)l * p.width + min(rank0 + i * 8 + (lane >> 3), p.width - 1)) * p.inner;
         f4 acc[RT];
 #pragma unroll
         for (int i = 0; i < RT; ++i) acc[i] = f4{0, 0, 0, 0};
-        struct StepA {
-            uint4 a[RT][2];
-        };
-        struct StepX {
-            uint4 x[2];
-        };
-        // a lane's 16 elements of a step: both operands agree on the order
-        auto piece = [&](const uint16_t* from, int st, int h) {
-            const int e = st * kStepK + g * 16 + h * 8;
-            return *reinterpret_cast<const uint4*>(from + (e < p.inner ? e : 0));
-        };
-        auto load_x = [&](StepX& s, int st) {
+        // everything before is done, so the counts of the stages are of their loads alone
+        asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+        multiply_staged<RT, kSmallStages>(mine, xp, ap, s_begin + wave, kWaves,
+                                          max(s_end - s_begin - wave + kWaves - 1, 0) / kWaves, p.inner, acc);
+        // the waves' sums, each over its own stages
+        asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
 #pragma unroll
-            for (int h = 0; h < 2; ++h) s.x[h] = piece(xp, st, h);
-        };
-        auto load_a = [&](StepA& s, int st) {
-            int rank = rank0 + c;
-            asm volatile("" : "+v"(rank));      // addresses anew each step: kept, they take the operands' registers
-#pragma unroll
-            for (int i = 0; i < RT; ++i)
-#pragma unroll
-                for (int h = 0; h < 2; ++h)
-                    s.a[i][h] = piece(ap + (int64_t)min(rank + i * 16, p.width - 1) * p.inner, st, h);
-        };
-        auto multiply = [&](StepA& sa, StepX& sx, int st, int h) {
-            if ((st + 1) * kStepK > p.inner) {      // the last step, cut: nothing behind the end
-                const uint32_t keep = st * kStepK + g * 16 + h * 8 < p.inner ? ~0u : 0u;
-                auto cut = [&](uint4& w) { w = make_uint4(w.x & keep, w.y & keep, w.z & keep, w.w & keep); };
-#pragma unroll
-                for (int i = 0; i < RT; ++i) cut(sa.a[i][h]);
-                cut(sx.x[h]);
-            }
-#pragma unroll
-            for (int i = 0; i < RT; ++i)
-                acc[i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(b8, sa.a[i][h]),
-                                                                 __builtin_bit_cast(b8, sx.x[h]), acc[i], 0, 0, 0);
-        };
-        int st = s_begin + wave;
-        if (st < s_end) {
-            StepX x, next_x;
-            StepA a, next_a;
-            load_x(x, st);
-            load_a(a, st);
-            for (; st < s_end; st += kWaves) {
-                if (st + kWaves < s_end) {
-                    load_x(next_x, st + kWaves);
-                    load_a(next_a, st + kWaves);
-                }
-                multiply(a, x, st, 0);
-                multiply(a, x, st, 1);
-                x = next_x;
-                a = next_a;
-            }
-        }
-        // the four waves' sums: 2 and 3 to 0 and 1, then 1 to 0
-        if (wave >= 2)
-#pragma unroll
-            for (int i = 0; i < RT; ++i) s_sum[wave - 2][i * 64 + lane] = acc[i];
+        for (int i = 0; i < RT; ++i) reinterpret_cast<f4*>(mine)[i * 64 + lane] = acc[i];
         __syncthreads();
-        if (wave < 2)
+        for (int i = wave; i < RT; i += kWaves) {
+            const int rank = rank0 + i * 16 + g * 4;
+            if (rank >= p.width || !(same >> c & 1)) continue;
+            f4 sum = reinterpret_cast<const f4*>(smem)[i * 64 + lane];
 #pragma unroll
-            for (int i = 0; i < RT; ++i) acc[i] += s_sum[wave][i * 64 + lane];
-        __syncthreads();
-        if (wave == 1)
-#pragma unroll
-            for (int i = 0; i < RT; ++i) s_sum[0][i * 64 + lane] = acc[i];
-        __syncthreads();
-        if (wave == 0) {
-#pragma unroll
-            for (int i = 0; i < RT; ++i) {
-                const int rank = rank0 + i * 16 + g * 4;
-                if (rank < p.width && (same >> c & 1))
-                    *reinterpret_cast<f4*>(p.part + ((int64_t)split * p.rows + row) * p.width + rank) =
-                        acc[i] + s_sum[0][i * 64 + lane];
-            }
+            for (int w = 1; w < kWaves; ++w)
+                sum += reinterpret_cast<const f4*>(smem + w * (small_lds(RT) / kWaves))[i * 64 + lane];
+            *reinterpret_cast<f4*>(p.part + ((int64_t)split * p.rows + row) * p.width + rank) = sum;
         }
         if (left) __syncthreads();
     }
@@ -444,17 +464,6 @@ __global__ __launch_bounds__(kThreads, 5) void k_expand_small(const LoraParams p
     }
 }
 
-__device__ __forceinline__ uint32_t lds_address(const void* p) {
-    return (uint32_t)(uintptr_t)(const __attribute__((address_space(3))) void*)p;
-}
-
-// 64 lanes x 16 bytes into LDS [lds, lds + 1024).  No register result: nothing in
-// flight targets a register, and only the explicit waits below order it.
-__device__ __forceinline__ void load_to_lds(uint32_t lds, const void* from) {
-    asm volatile("s_mov_b32 m0, %0\n\tglobal_load_lds_dwordx4 %1, off"
-                 :: "s"(__builtin_amdgcn_readfirstlane(lds)), "v"(from) : "memory", "m0");
-}
-
 // Up to kFew rows, ranks of RT tiles of 16: one launch.  A block takes a tile and
 // 512 columns of one slice and forms the slice's t itself, its eight waves going
 // through the inner dimension side by side: A is read by every column block again
@@ -468,7 +477,7 @@ constexpr int few_lds(int rt) { return few_waves(rt) * few_stages(rt) * (rt + 1)
 template <int RT, typename OutT>
 __global__ __launch_bounds__(64 * few_waves(RT), 1) void k_lora_few(const LoraParams p) {
     constexpr int kTerms = sizeof(OutT) == 2 ? 2 : 3;
-    constexpr int kFewWaves = few_waves(RT), kStages = few_stages(RT), kStage = (RT + 1) * 2048, kUnits = (RT + 1) * 2;
+    constexpr int kFewWaves = few_waves(RT), kStages = few_stages(RT), kStage = (RT + 1) * 2048;
     extern __shared__ __align__(1024) uint8_t smem[];   // the waves' stages, then
     uint8_t* const s_t = smem + few_lds(RT);            // [16 rows][terms of t, padded] bf16
     const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -515,55 +524,12 @@ __global__ __launch_bounds__(64 * few_waves(RT), 1) void k_lora_few(const LoraPa
 #pragma unroll
     for (int i = 0; i < RT * 2; ++i)
         ap[i] = p.a + ((int64_t)l * p.width + slice.index * p.rank + min(i * 8 + (lane >> 3), p.rank - 1)) * p.inner;
-    uint8_t* const mine = smem + wave * kStages * kStage;
-    const int total = (p.inner + kStepK - 1) / kStepK;
-    const int steps = (total - wave + kFewWaves - 1) / kFewWaves;   // this wave's: wave, wave + 8, ..
-    const int piece = ((lane & 7) ^ (lane >> 3)) * 8;
-    auto stage = [&](int i) {
-        const uint32_t to = lds_address(mine) + (uint32_t)(i % kStages) * kStage;
-        const int e = (wave + i * kFewWaves) * kStepK + piece, at = e < p.inner ? e : 0;
-#pragma unroll
-        for (int k = 0; k < 2; ++k) load_to_lds(to + k * 1024, xp[k] + at);
-#pragma unroll
-        for (int k = 0; k < RT * 2; ++k) load_to_lds(to + 2048 + k * 1024, ap[k] + at);
-    };
     f4 acc[RT];
 #pragma unroll
     for (int i = 0; i < RT; ++i) acc[i] = f4{0, 0, 0, 0};
-    for (int i = 0; i < min(kStages, steps); ++i) stage(i);
-    for (int i = 0; i < steps; ++i) {
-        // stage i is here when no more than the loads of those after it are left
-        if (i + kStages <= steps) asm volatile("s_waitcnt vmcnt(%0)" ::"n"((kStages - 1) * kUnits) : "memory");
-        else asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
-        const uint8_t* const from = mine + i % kStages * kStage;
-        const int st = wave + i * kFewWaves;
-        uint4 xf[2], af[RT][2];
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            const int at = c * 128 + ((h * 4 + g) ^ (c & 7)) * 16;
-            xf[h] = *reinterpret_cast<const uint4*>(from + at);
-#pragma unroll
-            for (int k = 0; k < RT; ++k) af[k][h] = *reinterpret_cast<const uint4*>(from + (k + 1) * 2048 + at);
-        }
-        if (i + kStages < steps) {                      // the stage is read: free for the next
-            asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
-            stage(i + kStages);
-        }
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            if ((st + 1) * kStepK > p.inner) {          // nothing behind the end
-                const uint32_t keep = st * kStepK + h * 32 + g * 8 < p.inner ? ~0u : 0u;
-                auto cut = [&](uint4& w) { w = make_uint4(w.x & keep, w.y & keep, w.z & keep, w.w & keep); };
-                cut(xf[h]);
-#pragma unroll
-                for (int k = 0; k < RT; ++k) cut(af[k][h]);
-            }
-#pragma unroll
-            for (int k = 0; k < RT; ++k)
-                acc[k] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(b8, af[k][h]),
-                                                                 __builtin_bit_cast(b8, xf[h]), acc[k], 0, 0, 0);
-        }
-    }
+    const int total = (p.inner + kStepK - 1) / kStepK;
+    uint8_t* const mine = smem + wave * kStages * kStage;
+    multiply_staged<RT, kStages>(mine, xp, ap, wave, kFewWaves, (total - wave + kFewWaves - 1) / kFewWaves, p.inner, acc);
     // this wave's sums, over its own stages
     asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
 #pragma unroll
@@ -1035,20 +1001,28 @@ hipError_t shrink_large(const LoraParams& p, const Plan& plan, hipStream_t strea
     return hipGetLastError();
 }
 
+template <int RT>
+hipError_t shrink_small(const LoraParams& p, const Plan& plan, hipStream_t stream) {
+    constexpr int bytes = small_lds(RT);
+    const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(&k_shrink_small<RT>),
+                                             hipFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    if (e != hipSuccess) return e;
+    hipLaunchKernelGGL((k_shrink_small<RT>), dim3((unsigned)plan.shrink_blocks), dim3(kThreads), bytes, stream, p);
+    return hipGetLastError();
+}
+
 hipError_t run_shrink(const LoraParams& p, const Plan& plan, hipStream_t stream) {
     if (!plan.small)
         return plan.rank_tiles == 1   ? shrink_large<1>(p, plan, stream)
                : plan.rank_tiles == 2 ? shrink_large<2>(p, plan, stream)
                                       : shrink_large<3>(p, plan, stream);
-    const dim3 grid((unsigned)plan.shrink_blocks), block(kThreads);
     switch (plan.rank_tiles) {
-    case 1: hipLaunchKernelGGL((k_shrink_small<1>), grid, block, 0, stream, p); break;
-    case 2: hipLaunchKernelGGL((k_shrink_small<2>), grid, block, 0, stream, p); break;
-    case 3: hipLaunchKernelGGL((k_shrink_small<3>), grid, block, 0, stream, p); break;
-    case 4: hipLaunchKernelGGL((k_shrink_small<4>), grid, block, 0, stream, p); break;
-    default: hipLaunchKernelGGL((k_shrink_small<6>), grid, block, 0, stream, p); break;
+    case 1: return shrink_small<1>(p, plan, stream);
+    case 2: return shrink_small<2>(p, plan, stream);
+    case 3: return shrink_small<3>(p, plan, stream);
+    case 4: return shrink_small<4>(p, plan, stream);
+    default: return shrink_small<6>(p, plan, stream);
     }
-    return hipGetLastError();
 }
 
 template <typename OutT>
