@@ -927,11 +927,12 @@ Plan plan_of(const LoraArgs& a) {
     p.small = a.rows <= kSmall;
     // One launch where its blocks are resident together and a block's pass over the
     // inner dimension, which grows with the rows of A and x, is shorter than a
-    // second launch (1 .. 64 rows, 6144 columns; 16 ranks of inner 4096: 5.9 .. 7.0
-    // us against 8.1 .. 11.0, of 14336: 10.7 .. 13 against 8.3 .. 11; 32 ranks of
-    // 4096: 7.4 .. 11.6 against 9.2 .. 14.8, 64 ranks: 9.5 .. 32 against 9.8 .. 25,
-    // and of 1024: 6.1 .. 6.7 against 7.7 .. 8.4; in two rounds of blocks 13 .. 15
-    // against 11 .. 13).
+    // second launch (1 .. 64 rows, 6144 columns: 16 ranks of inner 4096 in 6.0 .. 6.8
+    // us against 7.8 .. 9.1, of 8192 in 8.0 .. 11.7 against 8.1 .. 10.8; 32 ranks of
+    // 4096 in 7.4 .. 11.9 against 8.5 .. 10.4, of 8192 in 10 .. 18 against 9 .. 16; 64
+    // ranks of 2048 in 7.3 .. 8.6 against 8.4 .. 9.2, of 8192 in 14 .. 23 against 10
+    // .. 13; in two rounds of blocks, 14336 columns, 13 against 11).  A second launch
+    // costs the host 3 us more.
     const int tiles_of_16 = (int)std::min<int64_t>(a.rows, (a.rows + 15) / 16 + a.adapters), rt = (a.rank + 15) / 16;
     p.few = a.rows <= kFew && a.rank <= kFewRank && a.inner * (rt == 3 ? 5 : rt + 1) <= 16384 &&
             tiles_of_16 * (a.columns / (few_waves(rt) * kChunk) + a.slices) <= 256;
