@@ -15,7 +15,22 @@
 // their sequence (extend_rows).  The two kinds need different parts of a CU, so
 // they are resident together rather than one after the other.
 //
+// k_shared_few.  Up to 32 rows of one new token each read the prefix as waves read
+// the tails, 16 rows a wave against 32-token steps in registers: less parallel
+// work in a row (4 sequences, 2000 + up to 130 tokens: 13.2 us), but an eighth of
+// a block tile's products and none of its partial results' 64 KiB (4 sequences on
+// 32768 tokens 28 us against 42, 8 sequences 33 against 42, 16 sequences 50
+// against 44).
+//
 // k_shared_join reads a row's pieces of both parts in their order.
+//
+// Measured (8 KV heads of 128 and 32 query heads; in brackets every sequence by
+// itself, kv_attention without a prefix): 64 sequences on 8192 shared tokens of
+// E4M3 and up to 600 of their own 28 us and 7 for the join (138 together); 24 with
+// six new tokens each on 32768 of E5M2 and up to 1000, 90 and 7 (481).  A block of
+// the prefix takes 11 us (three dependent reads, then 64 KiB of partial results,
+// 3 us of them) and 1.8 us a step of 64 tokens, bound by the decoding and softmax
+// beside the products; the tails hide behind it (27.0 us without them, 28.2 with).
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
