@@ -34,6 +34,7 @@
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
+#include <cmath>
 
 #include "attention.hpp"
 #include "launch.hpp"
@@ -945,11 +946,17 @@ Plan plan_of(const LoraArgs& a) {
         p.groups = (ranks + 5) / 6;
         p.rank_tiles = (ranks + p.groups - 1) / p.groups;
         if (p.rank_tiles == 5) p.rank_tiles = 6;
-        // Parts of the inner dimension: about a block a CU, every wave with a step
-        // or more, and no more than 16 rows of t for the second launch to add (331
-        // rows of 12 adapters, 14336 columns: half as many 20.4 us, twice 19.5, so 18.5).
-        const int tiles = std::min(p.slots, (int)std::min<int64_t>(a.rows, (a.rows + 15) / 16 + a.adapters));
+        // Parts of the inner dimension: about a block a CU for the tiles that rows
+        // spread evenly over the adapters make, every wave with a step or more, and
+        // no more than 16 rows of t for the second launch to add.  A power of two:
+        // blocks go round the eight XCDs, so that each one's L2 then holds the same
+        // part of A for all tiles (700 rows of 8 adapters, 32 ranks, inner 14336:
+        // four parts 16.8 us, five 20.7; 331 rows of 12: eight 12.2, six 14.9).
+        const double each = (double)a.rows / a.adapters;            // rows of an adapter, spread evenly
+        const int64_t expected = (int64_t)(a.adapters * std::max(1 - std::exp(-each), each / 16 + 0.5));
+        const int tiles = (int)std::clamp<int64_t>(expected, 1, std::min(p.slots, tiles_of_16));
         splits = std::clamp(256 / (tiles * p.groups), 1, 16);
+        while (splits & (splits - 1)) splits &= splits - 1;
     } else {
         p.groups = (ranks + 11) / 12;
         p.rank_tiles = ((ranks + p.groups - 1) / p.groups + 3) / 4;
@@ -957,7 +964,8 @@ Plan plan_of(const LoraArgs& a) {
         const int64_t blocks = (int64_t)p.slots * p.groups;
         splits = (int)std::clamp<int64_t>((blocks <= 128 ? 256 : 512) / blocks, 1, 8);
     }
-    p.split_steps = std::max((steps + splits - 1) / splits, kWaves);
+    const int waves = p.small ? kWaves : 1, turn = splits * waves;     // whole turns of the waves
+    p.split_steps = std::max((steps + turn - 1) / turn * waves, kWaves);
     p.splits = std::max(1, (steps + p.split_steps - 1) / p.split_steps);
     p.shrink_blocks = (int64_t)(p.small ? p.slots : (p.slots + 7) / 8 * 8) * p.splits * p.groups;
     return p;
