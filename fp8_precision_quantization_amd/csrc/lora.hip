@@ -1081,10 +1081,13 @@ int64_t lora_workspace(const LoraArgs& a) {
     return tile_bytes(p) + count_bytes(p) + (int64_t)p.splits * a.rows * a.slices * a.rank * 4;
 }
 
-// Blocks of the largest launch: 2^32 threads and more are not launched.
+// The largest launch in blocks of kThreads threads (2^32 threads and more are
+// not launched): k_shrink_large has twice as many, k_lora_few's few blocks are far
+// below their count here.
 int64_t lora_blocks(const LoraArgs& a) {
     const Plan plan = plan_of(a);
-    return std::max(plan.shrink_blocks, (int64_t)plan.slots * (a.columns / 64 + a.slices));
+    return std::max(plan.shrink_blocks * (plan.small ? 1 : kShrinkWaves / kWaves),
+                    (int64_t)plan.slots * (a.columns / 64 + a.slices));
 }
 
 hipError_t launch_lora(const LoraArgs& a) {

@@ -586,8 +586,8 @@ fp8_status fp8_kv_evict(const fp8_kv_pair* cache, float* weights, int64_t ldw, i
  * Requirements (else FP8_ERR_UNSUPPORTED_SHAPE / FP8_ERR_MISALIGNED): rank a
  * multiple of 8 in 8..128, slices 1..4, inner and every slice's columns
  * multiples of 8, columns and inner < 2^24, rows < 2^30, adapters <= 2^20,
- * launches of fewer than 2^24 blocks; x, a, b, y and out 16-byte aligned,
- * leading dimensions multiples of 8. */
+ * launches of fewer than 2^24 blocks of 256 threads; x, a, b, y and out 16-byte
+ * aligned, leading dimensions multiples of 8. */
 fp8_status fp8_lora_add(const void* y, int64_t ldy, const void* x, int64_t ldx, const void* a, const void* b,
                         const int32_t* ids, const float* gain, void* out, int64_t ldo, fp8_out_dtype dtype,
                         int64_t rows, int64_t columns, int64_t inner, int32_t rank, int32_t adapters,
