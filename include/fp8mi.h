@@ -576,8 +576,10 @@ fp8_status fp8_kv_evict(const fp8_kv_pair* cache, float* weights, int64_t ldw, i
  * reads.  slice_columns: HOST int32 [slices], the columns of each slice, together
  * `columns`; NULL with slices = 1.
  * x A^T is summed and held in fp32 and enters the second product with 16
- * significant bits where out is bf16, with 24 where it is fp32; the sum with y
- * is formed in fp32 and rounded once.  Sums are in a fixed order: results are
+ * significant bits where out is bf16, with 24 where it is fp32; the gain multiplies
+ * it there, in fp32; the sum with y is formed in fp32 and rounded once.  Infinite
+ * values of x, a and b give the infinities (and NaN) of the formula, in their rows
+ * and columns alone.  Sums are in a fixed order: results are
  * bit-reproducible run to run; a row's last fp32 bits may depend on the number
  * of rows and adapters (how the inner dimension is split).
  * workspace: fp8_lora_workspace() bytes, 16-byte aligned, as the other
