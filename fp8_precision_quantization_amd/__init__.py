@@ -775,9 +775,9 @@ def kv_append(k: torch.Tensor, v: torch.Tensor, k_cache: torch.Tensor, v_cache: 
     first rotary_dim channels (None: nothing turns): channels i and i +
     rotary_dim / 2, with interleaved 2i and 2i + 1.  positions: int64 [n], or
     [axes, n] with sections, the number of pairs that turn with each axis, in
-    their order (time, height and width of a picture's patches, say).  Angles
-    are formed in 64 bits, the rotation in fp32; k is cast without a rounding
-    between.
+    their order (time, height and width of a picture's patches, say); one row
+    expanded over the axes will do (text beside pictures).  Angles are formed
+    in 64 bits, the rotation in fp32; k is cast without a rounding between.
 
     Returns the rotated q in bf16, [n, q_heads, head_dim] (q_out where given,
     which may be q itself), or None without q."""
@@ -857,8 +857,11 @@ def kv_append(k: torch.Tensor, v: torch.Tensor, k_cache: torch.Tensor, v_cache: 
         if positions.shape != want:
             raise ValueError("positions must have shape %s, got %s" % (want, tuple(positions.shape)))
         stride = positions.stride()
-        if (n > 1 and stride[-1] != 1) or (axes > 1 and stride[0] < n):
+        if n > 1 and stride[-1] != 1:
             raise ValueError("positions must have a contiguous last dimension")
+        if axes > 1 and 0 < stride[0] < n:
+            raise ValueError("positions of several axes must lie %d apart or more, or be one row for all (stride 0), "
+                             "got stride %d" % (n, stride[0]))
         pos_ptr, pos_ld = positions.data_ptr(), stride[0] if axes > 1 else n
         if interleaved:
             flags |= _lib.FP8_ROTARY_INTERLEAVED

@@ -629,8 +629,8 @@ fp8_status fp8_kv_append(const fp8_kv_pair* cache, const void* k, int64_t ldk, c
         if (axes < 1 || axes > 4) return fail(FP8_ERR_UNSUPPORTED_SHAPE, "axes=%d must be in 1..4", (int)axes);
         if (inv_freq == nullptr) return fail(FP8_ERR_INVALID_ARG, "inv_freq is NULL");
         if (n_tokens > 0 && positions == nullptr) return fail(FP8_ERR_INVALID_ARG, "positions is NULL");
-        if (axes > 1 && pos_ld < n_tokens)
-            return fail(FP8_ERR_INVALID_ARG, "pos_ld=%lld must be >= n_tokens=%lld", (long long)pos_ld,
+        if (axes > 1 && pos_ld != 0 && pos_ld < n_tokens)
+            return fail(FP8_ERR_INVALID_ARG, "pos_ld=%lld must be 0 or >= n_tokens=%lld", (long long)pos_ld,
                         (long long)n_tokens);
         if (sections == nullptr && axes > 1) return fail(FP8_ERR_INVALID_ARG, "sections is NULL with axes=%d", (int)axes);
         int64_t pairs = 0;

@@ -438,11 +438,11 @@ typedef struct fp8_kv_pair {
  * turns by positions[axis(i)*pos_ld + t] * inv_freq[i]:
  *   (a, b) -> (a cos - b sin, b cos + a sin), in fp32, the angle in 64 bits;
  * pair i is channels (i, i + rotary_dim/2), with FP8_ROTARY_INTERLEAVED (2i,
- * 2i + 1).  positions: DEVICE int64 [axes x pos_ld] (pos_ld >= n_tokens);
- * inv_freq: DEVICE fp32 [rotary_dim/2], radians a position.  sections: HOST
- * int32 [axes], the pairs of each axis in their order (>= 0, together
- * rotary_dim/2; time, height and width, say); NULL with axes = 1.  rotary_dim
- * 0: nothing turns, positions, sections and inv_freq are not read.
+ * 2i + 1).  positions: DEVICE int64 [axes x pos_ld] (pos_ld >= n_tokens, or 0:
+ * one row for all axes); inv_freq: DEVICE fp32 [rotary_dim/2], radians a
+ * position.  sections: HOST int32 [axes], the pairs of each axis in their order
+ * (>= 0, together rotary_dim/2; time, height and width, say); NULL with axes = 1.
+ * rotary_dim 0: nothing turns, positions, sections and inv_freq are not read.
  * q_out: bf16 [n_tokens x (q_heads*head_dim)], ldqo: q rotated, rounded once.
  * It may be q itself (bf16, the same pitch), else it overlaps nothing the call
  * reads.  q NULL and q_heads 0: no queries.
