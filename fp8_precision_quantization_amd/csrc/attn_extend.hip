@@ -224,7 +224,7 @@ __global__ __launch_bounds__(kThreads, DP <= 128 ? 2 : 1) void k_weights(const E
 
     const int j = j0 + c;
     int row = -1;
-    if (j < len) row = row_of_entry(kv, kv.table[b * kv.table_ld + (j >> kv.page_shift)], j);
+    if (j < len) row = row_of_entry(kv, kv.table[(j < a.from ? 0 : b * kv.table_ld) + (j >> kv.page_shift)], j);
     uint4 kr[KC];
 #pragma unroll
     for (int i = 0; i < KC; ++i) {
@@ -395,7 +395,7 @@ ExtendParams params_of(const AttnArgs& a) {
     ExtendParams p;
     p.kv = a.kv; p.q = a.q; p.ldq = a.ldq; p.total_q = (int)a.total_q; p.each = (int)(a.total_q / a.kv.batch);
     p.q_heads = a.q_heads; p.group = a.q_heads / a.kv.heads; p.q_offsets = a.q_offsets; p.scale_log2 = a.scale * kLog2e;
-    p.window = a.window; p.sinks = a.sinks; p.out = a.out; p.ldo = a.ldo; p.lse = a.lse;
+    p.window = a.window; p.sinks = a.sinks; p.from = a.from; p.out = a.out; p.ldo = a.ldo; p.lse = a.lse;
     p.weights = a.weights; p.ldw = a.ldw;
     p.splits = 1; p.least = 1; p.part_ml = nullptr; p.part_o = nullptr;
     return p;

@@ -32,6 +32,7 @@ struct ExtendParams {
     const int32_t* q_offsets;
     float scale_log2;
     int window, sinks;
+    int from;                    // k_weights: the first tokens, read from the first row's pages by every sequence
     uint16_t* out;
     int64_t ldo;
     float* lse;
