@@ -494,7 +494,8 @@ def lora_add(y: torch.Tensor, x: torch.Tensor, a: torch.Tensor, b: torch.Tensor,
     (fp8_lora_workspace bytes).  No gradient is formed.
 
     A x is summed and kept in fp32 and enters the second product with 16
-    significant bits (bf16 out) or 24 (fp32 out); one rounding at the end."""
+    significant bits (bf16 out) or 24 (fp32 out); one rounding at the end.
+    Infinities are the formula's, in their rows and columns alone."""
     rows, columns, ldy = _matrix(y, "y")
     rows_x, inner, ldx = _matrix(x, "x")
     dev = y.device
@@ -906,13 +907,17 @@ def kv_attention(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor, 
 
     shared: the number of first tokens that all sequences have in the same
     pages (a common instruction text or document), read once for the batch
-    from the first row's pages (fp8_kv_attention_shared; its workspace is
-    fp8_kv_attention_shared_workspace bytes).
+    from the first row's pages, whatever that row's own length
+    (fp8_kv_attention_shared; its workspace is
+    fp8_kv_attention_shared_workspace bytes).  It pays for decode batches and
+    drafted tokens; prompts (some 64 new tokens a sequence and more) are as
+    fast or faster without it, and one new token with weights three times.
 
     Scores, softmax and sums are in fp32.  The weights of one new token per
     sequence enter the product with V with 16 significant bits, those of
-    several and of shared tokens rounded once to bf16 (up to 2^-8 of sum p |v|,
-    beside the output's own rounding).
+    several, and of shared tokens with more than 32 rows (sequences * q_heads /
+    heads), rounded once to bf16 (up to 2^-8 of sum p |v|, beside the output's
+    own rounding).
 
     Returns out [total_q, q_heads, head_dim] bf16, with return_lse (or lse
     given) also the fp32 log-sum-exp of the scores [total_q, q_heads]."""

@@ -257,6 +257,23 @@ int join_waves(int64_t rows) { return rows < 512 ? kJoinWaves : 1; }
 
 int64_t up16(int64_t n) { return (n + 15) / 16 * 16; }
 
+// Numbers that the plan aims at, of 256 CUs, E4M3 with 32 query heads on 8 KV heads
+// of 128 unless named otherwise, us a call:
+// - blocks of the prefix: 64 sequences of one token on 8192 and up to 600 of their
+//   own with 128, 256, 384, 512 of them 47, 36, 44, 51 (200 on 16384: 249, 139, 127,
+//   104); of several tokens, 24 times 6 on 32768 of E5M2, 311, 172, 152, 132, but 8
+//   times 4 on 4096 21, 28, 28, 28;
+// - parts of a row: 16 to 128 at most differ nowhere but there (16: 22);
+// - waves of few queries' prefix: 8 sequences on 32768 with 512, 1024, 2048 of them
+//   47, 34, 38;
+// - waves of tails of one token: 64 sequences up to 600 behind 8192 with 512, 1024,
+//   2048 39, 36, 38, 32 up to 8000 behind 2048 156, 112, 118;
+// - steps of such a wave, at least: 4 sequences up to 130 behind 2000 with 1, 2, 4
+//   15, 15, 17;
+// - blocks of tails of several tokens: 8 times 4 on 1024 and up to 12000 with 256,
+//   512, 1024 98, 79, 82; parts of a row tile, 24 times 6 as above with 8, 16, 32 at
+//   most 157, 151, 151; steps of a part, 8 times 4 on 4096 with 2, 4, 8 at least 24,
+//   28, 28, elsewhere the same.
 Plan plan_of(const AttnArgs& a, bool ragged) {
     Plan p = {};
     const int64_t group = a.q_heads / a.kv.heads, rows = a.total_q * group, heads = a.kv.heads;

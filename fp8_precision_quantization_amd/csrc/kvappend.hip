@@ -22,9 +22,9 @@
 // us from cold caches (4.6 TB/s; a copy of 2 GiB reaches 5.1) and in 31 with what
 // the caches hold; 1531 tokens of 48 heads of 96 on three axes 9.3 us; one token 3.5
 // us, a launch and three dependent reads.  The blocks' tables of sines cost least
-// with eight passes of rows a block (two blocks a CU for 8192 tokens: 36 us); with
-// pointers and pitches chosen by a row's kind from the arguments in memory, not in
-// registers, 8192 tokens took 66 us.
+// in one round of eight blocks a CU (six passes of rows a block for 8192 tokens; in
+// rounds of two blocks a CU 36 us); with pointers and pitches chosen by a row's kind
+// from the arguments in memory, not in registers, 8192 tokens took 66 us.
 #include <hip/hip_runtime.h>
 
 #include "cast_unit.hpp"

@@ -529,11 +529,13 @@ __global__ __launch_bounds__(kThreads, 5) void k_expand_small(const LoraParams p
 }
 
 // Up to kFew rows, ranks of RT tiles of 16: one launch.  A block takes a tile and
-// 512 columns of one slice and forms the slice's t itself, its eight waves going
-// through the inner dimension side by side: A is read by every column block again
-// (from the caches), which costs less than a second launch and the partial sums'
-// way through memory.  Each wave stages steps of x and A in LDS of its own, several
-// on their way, in the layout that k_shrink_large explains.
+// 64 columns a wave of one slice (1024 with 16 waves up to 32 ranks, 512 with eight
+// above) and forms the slice's t itself, its waves going through the inner dimension
+// side by side: A is read by every column block again (from the caches), which costs
+// less than a second launch and the partial sums' way through memory.  Each wave
+// stages steps of x and A in LDS of its own, in the layout that multiply_staged
+// explains: two steps up to 16 ranks, one above, where the other waves' loads stand
+// beside a wave's wait.
 constexpr int few_waves(int rt) { return rt <= 2 ? 16 : 8; }
 constexpr int few_stages(int rt) { return rt == 1 ? 2 : 1; }
 constexpr int few_lds(int rt) { return few_waves(rt) * few_stages(rt) * (rt + 1) * 2048; }
@@ -1015,7 +1017,10 @@ Plan plan_of(const LoraArgs& a) {
     // 4096 in 7.4 .. 11.9 against 8.5 .. 10.4, of 8192 in 10 .. 18 against 9 .. 16; 64
     // ranks of 2048 in 7.3 .. 8.6 against 8.4 .. 9.2, of 8192 in 14 .. 23 against 10
     // .. 13; in two rounds of blocks, 14336 columns, 13 against 11).  A second launch
-    // costs the host 3 us more.
+    // costs the host 3 us more.  The grid has blocks for a tile of every row, most of
+    // them empty: where an adapter's first row is among the last, its blocks wait for
+    // empty ones of the first round (64 rows of 24 adapters 7.0 .. 8.0 us by the order
+    // of the ids, 11.5 with one adapter in the last row alone).
     const int tiles_of_16 = (int)std::min<int64_t>(a.rows, (a.rows + 15) / 16 + a.adapters), rt = (a.rank + 15) / 16;
     p.few = a.rows <= kFew && a.rank <= kFewRank && a.inner * (rt == 3 ? 5 : rt + 1) <= 16384 &&
             tiles_of_16 * (a.columns / (few_waves(rt) * kChunk) + a.slices) <= 256;

@@ -512,15 +512,21 @@ int64_t fp8_kv_attention_workspace(const fp8_kv_pair* cache, int64_t total_q, in
 
 /* fp8_kv_attention of a batch whose sequences begin with the same tokens in the
  * same pages (a common instruction text or document): token j < shared of every
- * sequence is read from the pages of the FIRST row of page_table, once for all
- * queries.  The other rows' entries of those tokens should name the same pages
- * (the results are then those of fp8_kv_attention up to rounding); a sequence
- * shorter than `shared` sees its own length of them.  0 <= shared <= max_len;
- * whole steps of 64 tokens are shared, what is left of `shared` is read with the
- * sequences' own tokens.  With a window (of fewer than max_len tokens) or one
- * sequence the call is fp8_kv_attention.  The weights of shared tokens enter the
- * product with V rounded once to bf16, as those of several new tokens do; the
- * sequences' own tokens as in fp8_kv_attention.
+ * sequence is read from the pages of the FIRST row of page_table (whatever lens[0]
+ * is), once for all queries.  The other rows' entries of those tokens should name
+ * the same pages (the results are then those of fp8_kv_attention up to rounding); a
+ * sequence shorter than `shared` sees its own length of them.  0 <= shared <=
+ * max_len; whole steps of 64 tokens are shared, what is left of `shared` is read
+ * with the sequences' own tokens.  With a window (of fewer than max_len tokens) or one
+ * sequence the call is fp8_kv_attention.  The softmax weights of shared tokens
+ * enter the product with V rounded once to bf16, as those of several new tokens do;
+ * with up to 32 rows (sequences * q_heads / heads) of one new token each they keep
+ * 16 significant bits, as the sequences' own tokens do in fp8_kv_attention.
+ * Sharing pays where the prefix's bytes bound the call: a decode batch, drafted
+ * tokens.  From some 64 new tokens a sequence on the products bound it, and the
+ * call without `shared` is as fast or faster; with `weights` and one new token it
+ * is three times as fast, since here the accumulated weights are formed by a pass
+ * of their own over the keys (of the prefix too, for every sequence).
  * workspace: fp8_kv_attention_shared_workspace() bytes.  Everything else as
  * fp8_kv_attention. */
 fp8_status fp8_kv_attention_shared(const fp8_kv_pair* cache, const void* q, int64_t ldq, int64_t total_q,
